@@ -72,7 +72,10 @@ enum gemm_status {
     GEMM_ERR_LAUNCH = -4,  /* a CUDA runtime call failed (see gemm_last_cuda_error)   */
     GEMM_ERR_TIMEOUT = -5, /* a bounded in-kernel wait ran out; the kernel returned
                               early and C is incomplete (see gemm_last_device_error) */
-    GEMM_ERR_NOMEM = -6    /* host or device allocation failed (create, run_host)     */
+    GEMM_ERR_NOMEM = -6,   /* host or device allocation failed (create, run_host)     */
+    GEMM_ERR_INDEX = -7    /* a length or page number that a call of gemm_serving.h read
+                              from device memory was out of range (reported by
+                              gemm_last_device_error; no access was made with it)     */
 };
 
 /* Create a context for CUDA device `device` (0-based). Checks that the device has compute
@@ -133,7 +136,8 @@ int gemm_run_host(gemm_ctx *ctx, int64_t M, int64_t N, int64_t K, const void *A,
                   const void *B, const void *bias, void *C, int epilogue, void *stream);
 
 /* After the caller has synchronised the stream(s) that ran this context's GEMMs: return
- * GEMM_OK, or GEMM_ERR_TIMEOUT if a bounded in-kernel wait ran out since the last call.
+ * GEMM_OK, or GEMM_ERR_TIMEOUT if a bounded in-kernel wait ran out since the last call
+ * (GEMM_ERR_INDEX, detail 8, if what came first was a bad index in a paged batch).
  * `detail` (may be NULL) receives the raw error word (which wait ran out: 1 producer
  * slot, 2 MMA operands, 3 MMA accumulator, 4 epilogue accumulator, 5 teardown drain,
  * 6 stream-K partial sum from another SM, 7 row statistics from the other CTAs of a

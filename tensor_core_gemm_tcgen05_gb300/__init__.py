@@ -19,7 +19,11 @@ import ctypes
 import os
 import threading
 
+from . import serving as _serving
 from .inputs import EPI_GELU, EPI_NONE, EPI_RELU, EPI_SOFTMAX  # noqa: F401  (C ABI epilogue codes)
+from .serving import (  # noqa: F401  (include/gemm_serving.h)
+    GEMM_BF16, GEMM_F16, GEMM_ROPE_LINEAR, GEMM_ROPE_NTK, GEMM_ROPE_PLAIN, GEMM_ROPE_YARN, SERVING_EXPORTS, kv_append,
+    paged_attention, paged_attention_workspace, qk_rope, rope_table)
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libgb300gemm.so")
@@ -32,6 +36,7 @@ GEMM_ERR_DEVICE = -3
 GEMM_ERR_LAUNCH = -4
 GEMM_ERR_TIMEOUT = -5
 GEMM_ERR_NOMEM = -6
+GEMM_ERR_INDEX = -7
 GEMM_DEBUG_NONE = 0
 GEMM_DEBUG_WITHHOLD_FIRST_LOAD = 1
 GEMM_DEBUG_FORCE_SINGLE = 2
@@ -92,6 +97,7 @@ def lib() -> ctypes.CDLL:
             for name in EXPORTS:
                 if name != "gemm_status_string":
                     getattr(L, name).restype = i32
+            _serving._declare(L)
             _lib = L
     return _lib
 
@@ -181,10 +187,10 @@ def gemm_run_noalloc(M, N, K, A, B, bias, C, epilogue=EPI_NONE, stream=None, dev
 
 
 def gemm_last_device_error(ctx) -> tuple[int, int]:
-    """Returns ``(status, detail)``; status is GEMM_OK or GEMM_ERR_TIMEOUT."""
+    """Returns ``(status, detail)``; status is GEMM_OK, GEMM_ERR_TIMEOUT or GEMM_ERR_INDEX."""
     d = ctypes.c_uint32(0)
     rc = lib().gemm_last_device_error(_h(ctx), ctypes.byref(d))
-    if rc not in (GEMM_OK, GEMM_ERR_TIMEOUT):
+    if rc not in (GEMM_OK, GEMM_ERR_TIMEOUT, GEMM_ERR_INDEX):
         raise GemmError(rc, "gemm_last_device_error")
     return rc, int(d.value)
 

@@ -1,5 +1,5 @@
-"""Build step of the CUDA library: compiles ``csrc/gemm_api.cu`` (with the kernel header)
-into ``libgb300gemm.so`` inside the package, for sm_103a only."""
+"""Build step of the CUDA library: compiles the translation units of ``csrc/`` (with the kernel
+headers) into ``libgb300gemm.so`` inside the package, for sm_103a only."""
 from __future__ import annotations
 
 import glob
@@ -9,13 +9,15 @@ import subprocess
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libgb300gemm.so")
-SOURCES = [os.path.join(PKG, "csrc", "gemm_api.cu"), os.path.join(PKG, "csrc", "gemm_noalloc.cu")]
-DEPS = SOURCES + glob.glob(os.path.join(PKG, "csrc", "*.cuh")) + [os.path.join(ROOT, "include", "gemm.h")]
+SOURCES = [os.path.join(PKG, "csrc", name) for name in ("gemm_api.cu", "gemm_noalloc.cu", "serving_api.cu")]
+DEPS = (SOURCES + glob.glob(os.path.join(PKG, "csrc", "*.cuh")) + glob.glob(os.path.join(PKG, "csrc", "*.h"))
+        + glob.glob(os.path.join(ROOT, "include", "*.h")))
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",
     "-O3", "-lineinfo", "-std=c++17",
     "-Xcompiler", "-fPIC", "-shared",
+    "-t", "0",   # the translation units in parallel
 ]
 
 

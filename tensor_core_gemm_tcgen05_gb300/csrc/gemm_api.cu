@@ -11,12 +11,15 @@
 #include <new>
 
 #include "gemm.h"
+#include "gemm_ctx.h"
 #include "gemm_kernel.cuh"
 #include "gemm_kernel_pair.cuh"
 #include "softmax_gemm_kernel.cuh"
 #include "softmax_kernel.cuh"
 #include "attention_kernel.cuh"
 #include "clock_probe.cuh"
+
+using namespace gb300_host;
 
 namespace {
 
@@ -92,13 +95,7 @@ void raster_groups(int m_blocks, int rows_per_block, int K, int &group_m, int &b
     group_m = m_blocks / count;
     big = m_blocks % count;
 }
-constexpr uint64_t kDefaultTimeoutNs = 2000000000ull;
 constexpr int64_t kSoftmaxMaxCtas = int64_t(1) << 20;   // row softmax grid cap (CTAs loop past it)
-constexpr int kSoftmaxClusterMax = 8;   // softmax: clusters of 1, 2, 4 or 8 CTAs per row block
-// gemm_run_host splits C into at most this many bands (column bands: also two row halves of
-// A when A is at least kHostChunkMinBytes) whose uploads, GEMMs and downloads overlap;
-// outputs smaller than kHostChunkMinBytes are not split.
-constexpr int kHostChunksMax = 8;
 constexpr size_t kHostChunkMinBytes = size_t(32) << 20;
 constexpr uint64_t kMinTimeoutNs = 1000000ull;
 // Stream-K (one-CTA kernel): each CTA gets at least this many (tile, k-block) units, and
@@ -114,92 +111,6 @@ constexpr int kSplitKMinBlocks = 8;   // split-K: k-blocks per CTA at least
 #endif
 constexpr int kPairLongK = GB300_PAIR_LONG_K;   // pairs for a one-wave problem from this K on
 constexpr int kStreamKMinSpread = 2;
-
-}  // namespace
-
-struct gemm_ctx {
-    int device = -1;
-    int num_sms = 0;
-    PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
-    bool pair1w_ok = false;   // the one-wave pair instance runs as many clusters at once
-    uint32_t *d_err = nullptr;
-    uint64_t timeout_ns = kDefaultTimeoutNs;
-    int debug = 0;
-    int last_cuda_error = 0;
-    int max_clusters = 0;   // co-resident CTA pairs of the pair kernel (0: pair kernel unusable)
-    // stream-K workspace: one FP32 128 x 256 partial accumulator per SM, and per SM one
-    // ready flag per epilogue warp (zero between launches)
-    float *sk_ws = nullptr;
-    uint32_t *sk_flags = nullptr;
-    // softmax kernel: co-resident clusters of cs = 1, 2, 4, 8 CTAs (0: that size cannot be
-    // scheduled; cs = 1 must be possible for the softmax epilogue to be offered at all)
-    int softmax_clusters[kSoftmaxClusterMax + 1] = {};
-    // split-K: co-resident clusters of 2, 4 and 8 CTAs of the split-K instance, per size
-    int split_clusters[9] = {};
-    // gemm_run_host: device staging buffers, two copy streams and the events that order
-    // the chunked pipeline (created on first use)
-    void *stage = nullptr;
-    size_t stage_bytes = 0;
-    cudaStream_t copy_in = nullptr, copy_out = nullptr;
-    cudaEvent_t ev_start = nullptr, ev_done = nullptr;
-    cudaEvent_t ev_in[2 * kHostChunksMax] = {}, ev_mm[2 * kHostChunksMax] = {};
-};
-
-namespace {
-
-// Make `device` current for the lifetime of the guard, then restore the caller's device.
-class DeviceGuard {
-  public:
-    explicit DeviceGuard(int device)
-    {
-        if (cudaGetDevice(&prev_) != cudaSuccess) {
-            cudaGetLastError();
-            prev_ = -1;
-        }
-        if (prev_ != device)
-            cudaSetDevice(device);
-    }
-    ~DeviceGuard()
-    {
-        int cur = -1;
-        if (prev_ >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev_)
-            cudaSetDevice(prev_);
-    }
-
-  private:
-    int prev_ = -1;
-};
-
-int cuda_fail(gemm_ctx *ctx, cudaError_t e, int code)
-{
-    if (ctx)
-        ctx->last_cuda_error = static_cast<int>(e);
-    cudaGetLastError();   // clear the sticky-free error state
-    return code;
-}
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-// True when p is device (or managed) memory that `device` can address directly.
-bool on_device(const void *p, int device)
-{
-    cudaPointerAttributes a;
-    if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
-        cudaGetLastError();
-        return false;
-    }
-    if (a.type == cudaMemoryTypeManaged)
-        return true;
-    return a.type == cudaMemoryTypeDevice && a.device == device;
-}
-
-bool overlaps(const void *a, size_t na, const void *b, size_t nb)
-{
-    if (!a || !b || na == 0 || nb == 0)
-        return false;
-    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-    return a0 < b0 + nb && b0 < a0 + na;
-}
 
 // Size and epilogue rules (no pointers): GEMM_OK also for the empty problems M = 0 or N = 0.
 int check_shape(const gemm_ctx *ctx, int64_t M, int64_t N, int64_t K, int epilogue)
@@ -619,6 +530,11 @@ int gemm_create(gemm_ctx **out, int device)
         delete ctx;
         return cuda_fail(nullptr, e, GEMM_ERR_DEVICE);
     }
+    e = serving_init(ctx);
+    if (e != cudaSuccess) {
+        delete ctx;
+        return cuda_fail(nullptr, e, GEMM_ERR_DEVICE);
+    }
     // The clock sampler shares an SM with the kernels it watches: with the default
     // preference a CTA without shared memory may configure its SM for a small shared-memory
     // carve-out, and no CTA needing 200+ KB can join that SM until it exits (a persistent
@@ -925,7 +841,7 @@ int gemm_last_device_error(gemm_ctx *ctx, uint32_t *detail)
         return cuda_fail(ctx, e, GEMM_ERR_LAUNCH);
     if (detail)
         *detail = w;
-    return w ? GEMM_ERR_TIMEOUT : GEMM_OK;
+    return w == gb300::ERR_BATCH_INDEX ? GEMM_ERR_INDEX : w ? GEMM_ERR_TIMEOUT : GEMM_OK;
 }
 
 int gemm_last_cuda_error(gemm_ctx *ctx) { return ctx ? ctx->last_cuda_error : 0; }
@@ -974,6 +890,7 @@ const char *gemm_status_string(int status)
     case GEMM_ERR_LAUNCH: return "GEMM_ERR_LAUNCH: a CUDA call failed";
     case GEMM_ERR_TIMEOUT: return "GEMM_ERR_TIMEOUT: an in-kernel wait ran out";
     case GEMM_ERR_NOMEM: return "GEMM_ERR_NOMEM: allocation failed";
+    case GEMM_ERR_INDEX: return "GEMM_ERR_INDEX: a length or page number in device memory is out of range";
     default: return "unknown gemm status";
     }
 }

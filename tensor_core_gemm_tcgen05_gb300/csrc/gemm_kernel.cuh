@@ -54,6 +54,7 @@ enum : uint32_t {
     ERR_TEARDOWN_DRAIN = 5,
     ERR_STREAMK_PARTIAL = 6,   // a stream-K owner waited too long for another CTA's partial
     ERR_ROW_EXCHANGE = 7,      // a row cluster waited too long for the other CTAs' row statistics
+    ERR_BATCH_INDEX = 8,       // not a wait: a length or page number of a paged batch is out of range
 };
 
 // How a launch maps work to CTAs (the kernel's SCHED template argument).

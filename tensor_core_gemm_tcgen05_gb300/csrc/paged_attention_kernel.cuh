@@ -1,0 +1,1098 @@
+// Attention of a ragged batch's new queries over a paged key/value cache (gemm_serving.h):
+//
+//     out[t][h] = sum_j p_j V[j][h'] / sum_j p_j,   p_j = 2^(s_j - m),  s_j = scale log2(e) q[t][h] . K[j][h']
+//
+// over the keys j at positions up to the token's own, in one pass over the keys with a running
+// maximum m and sum l per row (FP32), on the fifth-generation tensor cores.
+//
+//  * Rows. The G query heads of a key head and consecutive tokens of a sequence are the rows of
+//    one 128-row tile (row = token * G + head, 128 / G tokens), so a key block is read once for
+//    all of them; one TMA box (64 dims x G heads x tokens) loads a tile from any strides. A
+//    decoding token fills G rows and leaves the others idle: the tensor work of a block (two
+//    128-row products) still takes less time than reading it (64 keys: 1024 clocks of two
+//    products against about 1400 at an SM's share of HBM).
+//  * Keys. A block of BKV keys is gathered by one TMA box per page (and 64 dims) at the page
+//    table's page number; pages past the last key, and numbers out of range, are addressed one
+//    past the last page, which TMA fills with zeros. Rows of a page past the last key hold
+//    anything (NaN too): their scores are masked, and their rows of V are zeroed in shared
+//    memory before the product (0 x NaN would be NaN).
+//  * Work. An item is (sequence, key head, tile or pair of tiles), its cost its key blocks. The
+//    blocks of all items in order (units) are cut into one equal range per CTA (every CTA adds
+//    up the lengths itself, on the device, so a captured graph follows them): no CTA waits for
+//    another, and long and short sequences balance. An item cut by a range boundary leaves one
+//    part per CTA, (m, l, O) in FP32 in the workspace, joined by paged_combine_kernel; an item
+//    inside one range is finished here.
+//  * Two forms. NT = 1: one tile, blocks of 64 keys, two score buffers, two CTAs per SM (for
+//    few rows: bound by HBM; one CTA's latencies overlap the other's). NT = 2: two tiles share
+//    each block of 128 keys, one CTA per SM (for many rows: bound by the tensor cores; one
+//    tile's softmax runs during the other's products).
+//  * Warps: 0 producer (TMA), 1 MMA issuer, then four softmax warps per tile, a row per thread,
+//    as in attention_fwd_kernel. Every wait is bounded.
+#pragma once
+
+#include <type_traits>
+
+#include "serving_common.cuh"
+
+namespace gb300 {
+
+// Which keys a launch covers.
+enum : int {
+    KEYS_ALL = 0,     // the prefix (if any), then the sequence's own
+    KEYS_OWN = 1,     // the sequence's own (the prefix is another launch's)
+    KEYS_PREFIX = 2,  // the prefix, for the tokens of all sequences together
+};
+// Which sequences a launch takes, by their new tokens against a tile's.
+enum : int { SEQS_ALL = 0, SEQS_SHORT = 1, SEQS_LONG = 2 };
+
+// Parts of the workspace of one launch: what a CTA leaves of items that are cut.
+struct PartsView {
+    float *o;        // [2 * CTAs][tiles * rows][D]: part 0: began in an earlier CTA; 1: goes on in the next
+    float2 *ml;      // [2 * CTAs][tiles * rows] (m, l)
+    int rows;        // rows kept per tile
+    int tiles;
+};
+
+// Where a token's result is, per key head: CTA of the first part, number of parts, the item's
+// first token, the launch (index of its PartsView).
+using PartInfo = int4;
+
+struct PagedParams {
+    BatchView batch;
+    const int *prefix_pages;
+    int n_prefix_pages;
+    int kv_heads, group, tile_tokens;   // G and 128 / G
+    int keys, seqs;                     // KEYS_*, SEQS_*
+    int launch;                         // index for PartInfo
+    float scale_log2;                   // scale * log2(e)
+    void *out;
+    int64_t out_token, out_head;
+    float *lse;
+    int64_t lse_token;
+    PartsView parts;
+    PartInfo *info;                     // [num_tokens][kv_heads]
+    float *row_o;                       // KEYS_OWN / KEYS_PREFIX: whole items, [num_tokens][heads][D]
+    float2 *row_ml;
+    uint32_t *err;
+    uint64_t timeout_ns;
+    int debug;                          // DEBUG_WITHHOLD_FIRST_LOAD
+};
+
+template <typename T, int D_, int NT_>
+struct PagedConfig {
+    using Type = T;
+    static constexpr int D = D_;
+    static constexpr int NT = NT_;                  // query tiles per item
+    static constexpr int BQ = 128;                  // rows per tile (= TMEM lanes)
+    static constexpr int BKV = NT == 1 ? 64 : 128;  // keys per block
+    static constexpr int ATOMS = D / 64;            // 128-byte-swizzled atoms of 64 dims
+    static constexpr int Q_ATOM = BQ * 128, Q_TILE = ATOMS * Q_ATOM;
+    static constexpr int KV_ATOM = BKV * 128, KV_TILE = ATOMS * KV_ATOM;
+    // ring of K and V tiles (K0 V0 K1 V1 ...): what fits beside Q in half of (NT = 1) or all of
+    // an SM's shared memory
+    static constexpr int STAGES = NT == 1 ? (D == 128 ? 4 : 8) : (D == 128 ? 5 : 8);
+    static constexpr int Q_OFF = 0, RING_OFF = NT * Q_TILE;
+    static constexpr int BAR_OFF = RING_OFF + STAGES * KV_TILE;
+    // q_full, q_empty, drain, full[], empty[], s_full and pv_done (NT = 2: of the first tile),
+    // then NT = 1: p_full[block mod 2]; NT = 2: p_half[tile], p_full[tile]
+    static constexpr int NUM_BARS = 3 + 2 * STAGES + 2 + 2 * NT;
+    static constexpr int SMEM_BYTES = 1024 + BAR_OFF + NUM_BARS * 8 + 16;
+    static constexpr int NUM_THREADS = 64 + NT * 128;
+    static constexpr int CTAS_PER_SM = NT == 1 ? 2 : 1;
+    // TMEM: NT = 1: two score buffers of 64 columns, O; NT = 2: S_A S_B O_A O_B. P (16-bit pairs)
+    // over the first half of its scores.
+    static constexpr int S_COL = 0, O_COL = 2 * BKV;
+    static constexpr int TMEM_COLS = NT == 1 ? 256 : 512;
+    static_assert(O_COL + NT * D <= TMEM_COLS, "Tensor Memory columns");
+    static_assert(SMEM_BYTES + 1024 <= (NT == 1 ? 116736 : 233472), "shared memory of an SM");
+    static constexpr uint32_t TYPE_BITS = std::is_same<T, __nv_bfloat16>::value ? (1u << 7) | (1u << 10) : 0u;
+    // FP32 accumulation, M = 128, A K-major; S: N = BKV, B (keys) K-major; PV: N = D, B (values)
+    // MN-major
+    static constexpr uint32_t ID_S = (1u << 4) | TYPE_BITS | (static_cast<uint32_t>(BKV >> 3) << 17) | (128u >> 4 << 24);
+    static constexpr uint32_t ID_PV = (1u << 4) | TYPE_BITS | (1u << 16) | (static_cast<uint32_t>(D >> 3) << 17) | (128u >> 4 << 24);
+};
+
+// A row's running maximum is raised (and its row of O rescaled) only when a block's maximum
+// exceeds it by more than this many base-2 units: probabilities stay below 2^8.
+constexpr float kPagedRescale = 8.0f;
+
+// ---- work units --------------------------------------------------------------------------------
+
+// sum over i < n of floor((a i + b) / m), a, b >= 0, m > 0 (by reducing a and b modulo m and
+// counting lattice points the other way round, as in the Euclidean algorithm).
+__device__ inline int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b)
+{
+    int64_t sum = 0;
+    while (n > 0) {
+        if (a >= m) {
+            sum += n * (n - 1) / 2 * (a / m);
+            a %= m;
+        }
+        if (b >= m) {
+            sum += n * (b / m);
+            b %= m;
+        }
+        const int64_t top = a * n + b;
+        if (top < m)
+            break;
+        n = top / m;
+        b = top % m;
+        const int64_t t = m;
+        m = a;
+        a = t;
+    }
+    return sum;
+}
+
+// The items of one sequence (or, KEYS_PREFIX, of all tokens together): tiles of NT * tile_tokens
+// tokens for each key head. `edge`: keys that the token before the first would see, counted from
+// the launch's first key (token i sees the edge + i + 1 first of them); fixed >= 0: every tile
+// has `fixed` blocks instead.
+struct SeqItems {
+    int q0, n, kv, tiles, fixed;
+    int edge;
+    bool bad;
+};
+
+template <class Cfg>
+__device__ __forceinline__ SeqItems seq_items(const PagedParams &p, int s)
+{
+    SeqItems q;
+    const int step = Cfg::NT * p.tile_tokens;
+    if (p.keys == KEYS_PREFIX) {
+        const int a = min(max(__ldg(p.batch.q_start), 0), p.batch.num_tokens);
+        const int b = min(max(__ldg(p.batch.q_start + p.batch.num_seqs), a), p.batch.num_tokens);
+        q.q0 = a;
+        q.n = b - a;
+        q.kv = 0;
+        q.fixed = (p.batch.prefix_len + Cfg::BKV - 1) / Cfg::BKV;
+        q.edge = 0;
+        q.bad = false;
+        q.tiles = (q.n + step - 1) / step;
+        return q;
+    }
+    const SeqView v = load_seq(p.batch, s);
+    q.q0 = v.q0;
+    q.n = v.n;
+    q.kv = v.kv;
+    q.fixed = -1;
+    q.edge = (p.keys == KEYS_ALL ? p.batch.prefix_len : 0) + v.kv - v.n;
+    q.bad = v.bad;
+    const bool mine = p.seqs == SEQS_ALL || (v.n > p.tile_tokens) == (p.seqs == SEQS_LONG);
+    q.tiles = mine ? (v.n + step - 1) / step : 0;
+    return q;
+}
+
+// Key blocks of the tokens [.., last] (at least one, so that rows that see nothing are written).
+template <class Cfg>
+__device__ __forceinline__ int blocks_upto(const SeqItems &q, int last)
+{
+    if (q.fixed >= 0)
+        return q.fixed;
+    return max(1, (q.edge + last + Cfg::BKV) / Cfg::BKV);
+}
+
+// Blocks of the first `tiles` tiles together.
+template <class Cfg>
+__device__ inline int64_t blocks_of_tiles(const SeqItems &q, int step, int tiles)
+{
+    if (q.fixed >= 0)
+        return static_cast<int64_t>(tiles) * q.fixed;
+    int64_t sum = 0;
+    int whole = tiles;                            // tiles whose last token is not cut by the sequence's end
+    if (tiles > 0 && tiles * static_cast<int64_t>(step) > q.n) {
+        sum += blocks_upto<Cfg>(q, q.n - 1);
+        --whole;
+    }
+    // tile t < whole: last token (t + 1) step - 1; one block while edge + (t + 1) step <= BKV
+    const int ones = min(whole, max(0, (Cfg::BKV - q.edge) / step));
+    sum += ones;
+    if (whole > ones)
+        sum += floor_sum(whole - ones, Cfg::BKV, step, static_cast<int64_t>(q.edge) + static_cast<int64_t>(ones + 1) * step + Cfg::BKV - 1);
+    return sum;
+}
+
+// A CTA's walk over the units of its range.
+struct Walk {
+    int s;            // sequence (KEYS_PREFIX: 0)
+    SeqItems q;
+    int head, tile, block;
+    int64_t left;     // units left in the range
+};
+
+// One stretch of an item: key blocks [b0, b1) of `blocks`.
+struct Segment {
+    int s, head, tok0, toks;   // tokens [tok0, tok0 + toks) of the flat dimension
+    int q0, n, kv, edge;       // of the sequence
+    int b0, b1, blocks;
+    int64_t left;              // units left in the range, this stretch included
+};
+
+template <class Cfg>
+__device__ __forceinline__ bool next_segment(const PagedParams &p, Walk &w, Segment &g)
+{
+    if (w.left <= 0)
+        return false;
+    const int step = Cfg::NT * p.tile_tokens;
+    while (w.tile >= w.q.tiles) {   // on to the next head or the next sequence with items (units are left)
+        if (w.q.tiles > 0 && w.head + 1 < p.kv_heads) {
+            ++w.head;
+        } else {
+            w.head = 0;
+            if (++w.s >= p.batch.num_seqs)
+                return false;
+            w.q = seq_items<Cfg>(p, w.s);
+        }
+        w.tile = 0;
+    }
+    const int first = w.tile * step, toks = min(step, w.q.n - first);
+    g.s = w.s;
+    g.head = w.head;
+    g.tok0 = w.q.q0 + first;
+    g.toks = toks;
+    g.q0 = w.q.q0;
+    g.n = w.q.n;
+    g.kv = w.q.kv;
+    g.edge = w.q.edge;
+    g.blocks = blocks_upto<Cfg>(w.q, first + toks - 1);
+    g.b0 = w.block;
+    g.b1 = static_cast<int>(min(static_cast<int64_t>(g.blocks), w.block + w.left));
+    g.left = w.left;
+    w.left -= g.b1 - g.b0;
+    if (g.b1 == g.blocks) {
+        ++w.tile;
+        w.block = 0;
+    } else {
+        w.block = g.b1;   // the range ends here
+    }
+    return true;
+}
+
+// What the CTAs agree on: `total` units over `ctas` non-empty ranges.
+struct Shares {
+    int64_t total;
+    int ctas;
+    __device__ int64_t begin(int c) const { return total * c / ctas; }
+    // the range that holds unit u
+    __device__ int owner(int64_t u) const { return static_cast<int>(((u + 1) * ctas + total - 1) / total) - 1; }
+};
+
+// Ring position of the K/V tiles.
+template <int N>
+struct RingPos {
+    int slot = 0;
+    uint32_t parity = 0;
+    __device__ void step()
+    {
+        if (++slot == N) {
+            slot = 0;
+            parity ^= 1u;
+        }
+    }
+};
+
+// ---- softmax warp ------------------------------------------------------------------------------
+
+// Reads the columns addr .. addr + 32 N - 1 of this warp's TMEM lanes in chunks of 32 and hands
+// each to fn(registers, chunk); the next chunk's load is in flight meanwhile. Warp-collective.
+template <int N, class Fn>
+__device__ __forceinline__ void tmem_chunks(uint32_t addr, uint32_t (&va)[32], uint32_t (&vb)[32], Fn &&fn)
+{
+    tmem_ld_32x32b_x32(addr, va);
+#pragma unroll
+    for (int c = 0; c < N; ++c) {
+        uint32_t(&cur)[32] = (c & 1) ? vb : va;
+        uint32_t(&nxt)[32] = (c & 1) ? va : vb;
+        tmem_ld_wait_regs(cur);
+        if (c + 1 < N)
+            tmem_ld_32x32b_x32(addr + 32u * (c + 1), nxt);
+        fn(cur, c);
+    }
+}
+
+struct PagedBars {
+    uint32_t q_full, q_empty, drain, full0, empty0, s_full, pv_done, p_half0, p_full0;
+};
+
+template <class Cfg>
+__device__ __forceinline__ void paged_softmax_warp(const PagedParams &p, const PagedBars &bar, const WaitCtl &wc, uint32_t tmem,
+                                                   uint32_t ring, Walk walk, const Shares &shares, int tile, int warp, int lane)
+{
+    using T = typename Cfg::Type;
+    constexpr int D = Cfg::D, BKV = Cfg::BKV, CH = BKV / 32;
+    // The last tile's scores and products complete the ring's barriers (its K or V tile is free
+    // then, too); the first of two tiles has barriers of its own.
+    const bool last_tile = tile == Cfg::NT - 1;
+    const int quarter = warp & 3;
+    const int r = quarter * 32 + lane;
+    const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t o_addr = tmem + lane_base + static_cast<uint32_t>(Cfg::O_COL + tile * D);
+    const int row_tok = r / p.group, row_head = r - row_tok * p.group;
+    const float sl2 = p.scale_log2;
+    const uint32_t p_half = bar.p_half0 + 8u * tile;
+    RingPos<Cfg::STAGES> ring_k;   // this block's K tile (its V tile is the next position)
+    uint32_t count = 0;            // blocks this tile has worked on
+    uint32_t va[32], vb[32];
+    Segment g;
+    while (next_segment<Cfg>(p, walk, g)) {
+        // ---- rows and masks of the stretch
+        const int first = tile * p.tile_tokens;              // of the item's tokens
+        const int toks = min(p.tile_tokens, g.toks - first); // of this tile (<= 0: none)
+        const bool row_ok = row_tok < toks;
+        const int token = g.tok0 + first + row_tok;
+        int seen = INT32_MAX;   // keys of this launch that the row sees (idle rows: as if all)
+        if (p.keys == KEYS_PREFIX) {
+            // normally all of the prefix; a token that stands inside it sees less
+            int s = find_seq<32>(p.batch.q_start, p.batch.num_seqs, __shfl_sync(0xffffffffu, token, 0), lane);
+            if (row_ok) {
+                while (s + 1 < p.batch.num_seqs && __ldg(p.batch.q_start + s + 1) <= token)
+                    ++s;
+                const SeqView v = load_seq(p.batch, s);
+                seen = min(p.batch.prefix_len, max(0, p.batch.prefix_len + v.kv - v.n + (token - v.q0) + 1));
+            }
+        } else if (row_ok) {
+            seen = max(0, g.edge + (token - g.q0) + 1);
+        }
+        const bool active = __any_sync(0xffffffffu, row_ok);
+        // keys that any row of the item sees: rows of V past them are zeroed
+        const int alive = p.keys == KEYS_PREFIX ? p.batch.prefix_len : max(0, g.edge + (g.tok0 + g.toks - g.q0));
+        // this tile's last block (the first tile of a pair may see fewer keys than the second)
+        int mine = g.blocks;
+        if (!last_tile && p.keys != KEYS_PREFIX && g.toks > p.tile_tokens)
+            mine = max(1, (g.edge + (g.tok0 + p.tile_tokens - 1 - g.q0) + BKV) / BKV);
+        float m = -INFINITY, l = 0.0f;
+        bool any_block = false;
+        RingPos<Cfg::STAGES> prev_v = ring_k;
+        for (int b = g.b0; b < g.b1; ++b) {
+            RingPos<Cfg::STAGES> ring_v = ring_k;
+            ring_v.step();
+            if (b >= mine) {   // the other tile's blocks only
+                ring_k = ring_v;
+                ring_k.step();
+                continue;
+            }
+            if (!(last_tile ? wait_warp(bar.empty0 + 8u * ring_k.slot, ring_k.parity, wc, ERR_EPILOGUE_ACCUMULATOR, lane)
+                            : wait_warp(bar.s_full, count & 1u, wc, ERR_EPILOGUE_ACCUMULATOR, lane)))
+                return;
+            tc_fence_after_sync();
+            const int k0 = b * BKV;
+            if (k0 + BKV > alive) {
+                // rows of V that no row sees: zero them once the tile has landed
+                if (!wait_warp(bar.full0 + 8u * ring_v.slot, ring_v.parity, wc, ERR_EPILOGUE_ACCUMULATOR, lane))
+                    return;
+                const uint32_t v_tile = ring + static_cast<uint32_t>(ring_v.slot) * Cfg::KV_TILE;
+                const int from = max(0, alive - k0);
+                for (int i = from * 8 + r; i < BKV * 8; i += 128)
+#pragma unroll
+                    for (int a = 0; a < Cfg::ATOMS; ++a)
+                        st_shared_v4(v_tile + static_cast<uint32_t>(a) * Cfg::KV_ATOM + static_cast<uint32_t>(i) * 16u,
+                                     make_uint4(0, 0, 0, 0));
+                fence_proxy_async_shared();
+            }
+            const uint32_t s_addr =
+                tmem + lane_base + static_cast<uint32_t>(Cfg::S_COL + (Cfg::NT == 1 ? static_cast<int>(count & 1u) : tile) * BKV);
+            if (active) {
+                const bool all_seen = __all_sync(0xffffffffu, k0 + BKV <= seen);
+                auto block = [&](auto full_tag) -> bool {
+                    constexpr bool full = decltype(full_tag)::value;
+                    // Block maximum of scale * s: on unmasked blocks the extreme of the raw scores in
+                    // four independent chains, scaled once.
+                    float mb = -INFINITY;
+                    float r0 = sl2 >= 0.0f ? -INFINITY : INFINITY, r1 = r0, r2 = r0, r3 = r0;
+                    tmem_chunks<CH>(s_addr, va, vb, [&](const uint32_t(&x)[32], int c) {
+                        if constexpr (full) {
+                            if (sl2 >= 0.0f) {
+#pragma unroll
+                                for (int e = 0; e < 32; e += 8) {
+                                    r0 = fmax3(r0, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+                                    r1 = fmax3(r1, __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
+                                    r2 = fmax3(r2, __uint_as_float(x[e + 4]), __uint_as_float(x[e + 5]));
+                                    r3 = fmax3(r3, __uint_as_float(x[e + 6]), __uint_as_float(x[e + 7]));
+                                }
+                            } else {
+#pragma unroll
+                                for (int e = 0; e < 32; e += 8) {
+                                    r0 = fmin3(r0, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+                                    r1 = fmin3(r1, __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
+                                    r2 = fmin3(r2, __uint_as_float(x[e + 4]), __uint_as_float(x[e + 5]));
+                                    r3 = fmin3(r3, __uint_as_float(x[e + 6]), __uint_as_float(x[e + 7]));
+                                }
+                            }
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (k0 + 32 * c + e < seen)
+                                    mb = fmaxf(mb, __uint_as_float(x[e]) * sl2);
+                        }
+                    });
+                    if constexpr (full)
+                        mb = (sl2 >= 0.0f ? fmax3(fmaxf(r0, r1), r2, r3) : fmin3(fminf(r0, r1), r2, r3)) * sl2;
+                    const bool raise = mb > m + kPagedRescale || m == -INFINITY;
+                    const float m_new = raise ? mb : m;
+                    const float m_use = m_new == -INFINITY ? 0.0f : m_new;
+                    const float alpha = raise && row_ok ? ex2_approx(m - m_use) : 1.0f;   // 0 on the first block
+                    if (any_block && __any_sync(0xffffffffu, alpha != 1.0f)) {
+                        // O holds the blocks before: once their product is complete, rescale the rows
+                        if (!(last_tile ? wait_warp(bar.empty0 + 8u * prev_v.slot, prev_v.parity, wc, ERR_EPILOGUE_ACCUMULATOR, lane)
+                                        : wait_warp(bar.pv_done, (count - 1u) & 1u, wc, ERR_EPILOGUE_ACCUMULATOR, lane)))
+                            return false;
+                        tc_fence_after_sync();
+#pragma unroll 1
+                        for (int c = 0; c < D / 32; ++c) {
+                            tmem_ld_32x32b_x32(o_addr + 32u * c, va);
+                            tmem_ld_wait_regs(va);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                va[e] = __float_as_uint(__uint_as_float(va[e]) * alpha);
+                            tmem_st_32x32b_x32(o_addr + 32u * c, va);
+                        }
+                        tmem_st_wait();
+                    }
+                    uint64_t sum2[4] = {f32x2_pack(0.0f, 0.0f), f32x2_pack(0.0f, 0.0f), f32x2_pack(0.0f, 0.0f),
+                                        f32x2_pack(0.0f, 0.0f)};
+                    const uint64_t scale2 = f32x2_pack(sl2, sl2), neg_m2 = f32x2_pack(-m_use, -m_use);
+                    tmem_chunks<CH>(s_addr, va, vb, [&](const uint32_t(&x)[32], int c) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            float t0, t1;
+                            f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), scale2,
+                                                   neg_m2),
+                                         t0, t1);
+                            float p0 = ex2_approx(t0), p1 = ex2_approx(t1);
+                            if constexpr (!full) {
+                                const int k = k0 + 32 * c + 2 * i;
+                                p0 = k < seen ? p0 : 0.0f;
+                                p1 = k + 1 < seen ? p1 : 0.0f;
+                            }
+                            sum2[i & 3] = f32x2_add(sum2[i & 3], f32x2_pack(p0, p1));
+                            pk[i] = pack2<T>(p0, p1);
+                        }
+                        tmem_st_32x32b_x16(s_addr + 16u * static_cast<uint32_t>(c), pk);   // over scores already read
+                        if (Cfg::NT == 2 && c == CH / 2 - 1) {
+                            // the first half of the keys: their product can start
+                            tmem_st_wait();
+                            tc_fence_before_sync();
+                            __syncwarp();
+                            if (lane == 0)
+                                mbar_arrive(p_half);
+                        }
+                    });
+                    float s0, s1;
+                    f32x2_unpack(f32x2_add(f32x2_add(sum2[0], sum2[1]), f32x2_add(sum2[2], sum2[3])), s0, s1);
+                    l = l * alpha + (s0 + s1);
+                    m = m_new;
+                    tmem_st_wait();
+                    return true;
+                };
+                if (!(all_seen ? block(std::true_type{}) : block(std::false_type{})))
+                    return;
+            } else if (Cfg::NT == 2) {
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(p_half);
+            }
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(Cfg::NT == 1 ? bar.p_half0 + 8u * (count & 1u) : bar.p_full0 + 8u * tile);
+            any_block = true;
+            ++count;
+            prev_v = ring_v;
+            ring_k = ring_v;
+            ring_k.step();
+        }
+        // ---- the stretch's result
+        const bool starts = g.b0 == 0, ends = g.b1 == g.blocks;
+        const bool whole = starts && ends;
+        if (starts && tile == 0 && quarter == 0) {
+            const int64_t u0 = shares.begin(blockIdx.x + 1) - g.left;
+            const int parts = shares.owner(u0 + g.blocks - 1) - static_cast<int>(blockIdx.x) + 1;
+            for (int t = lane; t < g.toks; t += 32)
+                p.info[static_cast<int64_t>(g.tok0 + t) * p.kv_heads + g.head] =
+                    make_int4(static_cast<int>(blockIdx.x), parts, g.tok0, p.launch);
+        }
+        if (!active)
+            continue;
+        if (any_block) {
+            if (!(last_tile ? wait_warp(bar.empty0 + 8u * prev_v.slot, prev_v.parity, wc, ERR_EPILOGUE_ACCUMULATOR, lane)
+                            : wait_warp(bar.pv_done, (count - 1u) & 1u, wc, ERR_EPILOGUE_ACCUMULATOR, lane)))
+                return;
+            tc_fence_after_sync();
+        }
+        const int head = g.head * p.group + row_head;
+        if (whole && p.keys == KEYS_ALL) {
+            const float inv = 1.0f / l;
+            T *dst = static_cast<T *>(p.out) + token * p.out_token + head * p.out_head;
+            tmem_chunks<D / 32>(o_addr, va, vb, [&](const uint32_t(&x)[32], int c) {
+                if (row_ok) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float a = __uint_as_float(x[8 * i + 2 * e]), bb = __uint_as_float(x[8 * i + 2 * e + 1]);
+                            w[e] = l == 0.0f ? 0u : pack2<T>(a * inv, bb * inv);
+                        }
+                        *reinterpret_cast<uint4 *>(dst + 32 * c + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+            });
+            if (row_ok && p.lse)
+                p.lse[token * p.lse_token + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+            continue;
+        }
+        float *dst;
+        float2 *ml;
+        if (whole) {
+            const int64_t row = static_cast<int64_t>(token) * (p.kv_heads * p.group) + head;
+            dst = p.row_o + row * D;
+            ml = p.row_ml + row;
+        } else {
+            const int64_t row = (static_cast<int64_t>(2 * blockIdx.x + (starts ? 1 : 0)) * p.parts.tiles + tile) * p.parts.rows + r;
+            dst = p.parts.o + row * D;
+            ml = p.parts.ml + row;
+        }
+        if (any_block) {
+            tmem_chunks<D / 32>(o_addr, va, vb, [&](const uint32_t(&x)[32], int c) {
+                if (row_ok) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        *reinterpret_cast<uint4 *>(dst + 32 * c + 4 * i) = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                }
+            });
+        }
+        if (row_ok)
+            *ml = make_float2(m, l);
+    }
+}
+
+// ---- kernel ------------------------------------------------------------------------------------
+
+template <class Cfg>
+__global__ void __launch_bounds__(Cfg::NUM_THREADS, Cfg::CTAS_PER_SM)
+    paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
+                           const __grid_constant__ CUtensorMap tmap_v, const PagedParams p)
+{
+    constexpr int NT = Cfg::NT, ATOMS = Cfg::ATOMS, BKV = Cfg::BKV, STAGES = Cfg::STAGES;
+    constexpr int WARPS = Cfg::NUM_THREADS / 32;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ int64_t warp_sum[WARPS];
+    __shared__ Walk start;
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t *sp = smem_raw + (base - raw);
+    const uint32_t sQ = base + Cfg::Q_OFF, ring = base + Cfg::RING_OFF;
+    PagedBars bar;
+    bar.q_full = base + Cfg::BAR_OFF;
+    bar.q_empty = bar.q_full + 8u;
+    bar.drain = bar.q_full + 16u;
+    bar.full0 = bar.q_full + 24u;
+    bar.empty0 = bar.full0 + 8u * STAGES;
+    bar.s_full = bar.empty0 + 8u * STAGES;
+    bar.pv_done = bar.s_full + 8u;
+    bar.p_half0 = bar.pv_done + 8u;
+    bar.p_full0 = bar.p_half0 + 8u * NT;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sp + Cfg::BAR_OFF + Cfg::NUM_BARS * 8);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        mbar_init(bar.q_full, 1);
+        mbar_init(bar.q_empty, 1);
+        mbar_init(bar.drain, 1);
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(bar.full0 + 8u * s, 1);
+            mbar_init(bar.empty0 + 8u * s, 1);
+        }
+        mbar_init(bar.s_full, 1);
+        mbar_init(bar.pv_done, 1);
+        for (int t = 0; t < NT; ++t) {
+            mbar_init(bar.p_half0 + 8u * t, 4);   // the four softmax warps
+            mbar_init(bar.p_full0 + 8u * t, 4);
+        }
+        *abort_flag = 0;
+        start.left = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&tmap_q);
+        tma_prefetch_desc(&tmap_k);
+        tma_prefetch_desc(&tmap_v);
+    }
+    if (warp == 1) {
+        tmem_alloc<1>(smem_u32(tmem_slot), Cfg::TMEM_COLS);
+        tmem_relinquish<1>();
+    }
+    grid_dependency_wait();   // nothing above touched global memory
+
+    // ---- this CTA's share of the units
+    const int step = NT * p.tile_tokens;
+    const int seqs = p.keys == KEYS_PREFIX ? 1 : p.batch.num_seqs;
+    auto units_of = [&](int s) -> int64_t {
+        if (s >= seqs)
+            return 0;
+        const SeqItems q = seq_items<Cfg>(p, s);
+        if (q.bad)
+            atomicCAS(p.err, 0u, static_cast<uint32_t>(ERR_BATCH_INDEX));
+        return p.kv_heads * blocks_of_tiles<Cfg>(q, step, q.tiles);
+    };
+    int64_t mine = 0;
+    for (int s = threadIdx.x; s < seqs; s += Cfg::NUM_THREADS)
+        mine += units_of(s);
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2)
+        mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    if (lane == 0)
+        warp_sum[warp] = mine;
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    grid_dependents_launch();
+    Shares shares;
+    shares.total = 0;
+    for (int w = 0; w < WARPS; ++w)
+        shares.total += warp_sum[w];
+    shares.ctas = static_cast<int>(min(static_cast<int64_t>(gridDim.x), shares.total));
+    const bool works = static_cast<int>(blockIdx.x) < shares.ctas;
+    if (works) {   // (the same answer in every thread)
+        const int64_t u0 = shares.begin(blockIdx.x), u1 = shares.begin(blockIdx.x + 1);
+        int64_t before = 0;   // units of the sequences before this chunk
+        for (int s0 = 0; s0 < seqs && before <= u0; s0 += Cfg::NUM_THREADS) {
+            const int s = s0 + static_cast<int>(threadIdx.x);
+            const int64_t own = units_of(s);
+            int64_t scan = own;
+#pragma unroll
+            for (int o = 1; o < 32; o *= 2) {
+                const int64_t v = __shfl_up_sync(0xffffffffu, scan, o);
+                scan += lane >= o ? v : 0;
+            }
+            __syncthreads();   // warp_sum was read
+            if (lane == 31)
+                warp_sum[warp] = scan;
+            __syncthreads();
+            int64_t ahead = before;
+            for (int w = 0; w < WARPS; ++w) {
+                if (w < warp)
+                    ahead += warp_sum[w];
+                before += warp_sum[w];
+            }
+            const int64_t from = ahead + scan - own;
+            if (own > 0 && from <= u0 && u0 < from + own) {   // one thread: unit u0 is in its sequence
+                Walk w;
+                w.s = s;
+                w.q = seq_items<Cfg>(p, s);
+                const int64_t per_head = own / p.kv_heads;
+                w.head = static_cast<int>((u0 - from) / per_head);
+                const int64_t at = (u0 - from) - w.head * per_head;
+                int lo = 0, hi = w.q.tiles;   // blocks of the first lo tiles <= at
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) / 2;
+                    if (blocks_of_tiles<Cfg>(w.q, step, mid) <= at)
+                        lo = mid;
+                    else
+                        hi = mid;
+                }
+                w.tile = lo;
+                w.block = static_cast<int>(at - blocks_of_tiles<Cfg>(w.q, step, lo));
+                w.left = u1 - u0;
+                start = w;
+            }
+        }
+        __syncthreads();
+    }
+    Walk walk = {};
+    if (works)
+        walk = start;
+    const WaitCtl wc{abort_flag, p.err, p.timeout_ns};
+
+    if (!works) {
+        // fewer units than CTAs
+    } else if (warp == 0) {
+        // ---------------------------------------------------------------- TMA producer
+        // Lane i fetches the page number of page i of a block and, with the others, issues the
+        // boxes of its K and V tiles.
+        const int page_rows = 1 << p.batch.page_shift;
+        const int box_rows = min(page_rows, BKV), boxes = BKV / box_rows;   // boxes per atom of a tile
+        const int key_base = p.keys == KEYS_OWN ? p.batch.prefix_len : 0;
+        RingPos<STAGES> pos;
+        uint32_t issued = 0, issued_parity = 0, q_loads = 0;
+        bool ok = true;
+        Segment g;
+        while (ok && next_segment<Cfg>(p, walk, g)) {
+            if (q_loads > 0)   // the previous item's scores are complete
+                ok = wait_warp(bar.q_empty, (q_loads - 1u) & 1u, wc, ERR_PRODUCER_SLOT, lane);
+            if (!ok)
+                break;
+            if (lane == 0)
+                mbar_arrive_expect_tx(bar.q_full, static_cast<uint32_t>(NT * ATOMS * p.tile_tokens * p.group * 128));
+            __syncwarp();
+            if (lane < NT * ATOMS) {
+                const int t = lane / ATOMS, a = lane % ATOMS;
+                tma_load_4d(sQ + static_cast<uint32_t>(t * Cfg::Q_TILE + a * Cfg::Q_ATOM), &tmap_q, bar.q_full, 64 * a, 0, g.head,
+                            g.tok0 + t * p.tile_tokens);
+            }
+            ++q_loads;
+            // pages of this stretch: numbers past the last key's page (and bad ones) become
+            // num_pages, which TMA reads as zeros
+            const int own_pages = (g.kv + page_rows - 1) >> p.batch.page_shift;
+            auto page_of = [&](int b) -> int {
+                if (lane >= boxes || b >= g.b1)
+                    return 0;
+                const int lp = (key_base + b * BKV + lane * box_rows) >> p.batch.page_shift;
+                int id;
+                if (lp < p.n_prefix_pages)
+                    id = __ldg(p.prefix_pages + lp);
+                else if (p.keys != KEYS_PREFIX && lp - p.n_prefix_pages < own_pages)
+                    id = __ldg(p.batch.table + g.s * p.batch.table_stride + (lp - p.n_prefix_pages));
+                else
+                    return p.batch.num_pages;
+                if (id < 0 || id >= p.batch.num_pages) {
+                    atomicCAS(p.err, 0u, static_cast<uint32_t>(ERR_BATCH_INDEX));
+                    id = p.batch.num_pages;
+                }
+                return id;
+            };
+            int id_next = page_of(g.b0);
+            for (int b = g.b0; ok && b < g.b1; ++b) {
+                const int id = id_next;
+                id_next = page_of(b + 1);
+                const int box = lane % boxes, atom = lane / boxes;
+                const int page = __shfl_sync(0xffffffffu, id, box);
+                const int row = (key_base + b * BKV) & (page_rows - 1);   // 0 unless a page holds several blocks
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv) {
+                    if (!wait_warp(bar.empty0 + 8u * pos.slot, pos.parity ^ 1u, wc, ERR_PRODUCER_SLOT, lane)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t fb = bar.full0 + 8u * pos.slot;
+                    if ((p.debug & DEBUG_WITHHOLD_FIRST_LOAD) && issued == 0) {   // test hook: never loaded
+                        ok = false;
+                        break;
+                    }
+                    if (lane == 0)
+                        mbar_arrive_expect_tx(fb, Cfg::KV_TILE);
+                    __syncwarp();
+                    if (lane < boxes * ATOMS)
+                        tma_load_4d(ring + static_cast<uint32_t>(pos.slot * Cfg::KV_TILE + atom * Cfg::KV_ATOM + box * box_rows * 128),
+                                    kv == 0 ? &tmap_k : &tmap_v, fb, 64 * atom, row, g.head, page);
+                    issued |= 1u << pos.slot;
+                    issued_parity = (issued_parity & ~(1u << pos.slot)) | (pos.parity << pos.slot);
+                    pos.step();
+                }
+            }
+        }
+        if (!ok && lane == 0) {   // let every copy this warp started land before the CTA exits
+            if (q_loads > 0)
+                wait_until(bar.q_full, (q_loads - 1u) & 1u, p.timeout_ns, p.err);
+            for (int s = 0; s < STAGES; ++s)
+                if (issued & (1u << s))
+                    wait_until(bar.full0 + 8u * s, (issued_parity >> s) & 1u, p.timeout_ns, p.err);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ---------------------------------------------------------------- MMA issuer
+        if (lane == 0) {
+            // descriptors: Q and K K-major (atoms of 64 dims, 32 bytes per 16), V MN-major (atoms of
+            // 64 dims apart by KV_ATOM, 16 keys per 2048 bytes)
+            const uint64_t q_desc = sw128_desc(sQ, 16, 1024), k_desc = sw128_desc(ring, 16, 1024);
+            const uint64_t v_desc = sw128_desc(ring, Cfg::KV_ATOM, 1024);
+            auto issue_s = [&](int t, int slot, uint32_t d) {   // S = Q_t K^T
+                const uint64_t qd = q_desc + static_cast<uint64_t>((t * Cfg::Q_TILE) >> 4);
+                const uint64_t kd = k_desc + static_cast<uint64_t>((slot * Cfg::KV_TILE) >> 4);
+#pragma unroll
+                for (int kk = 0; kk < Cfg::D / 16; ++kk) {
+                    const uint64_t qo = static_cast<uint64_t>(((kk >> 2) * Cfg::Q_ATOM + (kk & 3) * 32) >> 4);
+                    const uint64_t ko = static_cast<uint64_t>(((kk >> 2) * Cfg::KV_ATOM + (kk & 3) * 32) >> 4);
+                    umma_f16<1>(d, qd + qo, kd + ko, Cfg::ID_S, kk != 0 ? 1u : 0u);
+                }
+            };
+            auto issue_pv = [&](int slot, uint32_t a, uint32_t d, int k0, int k1, bool add) {   // O += P V, 16-key steps
+                const uint64_t vd = v_desc + static_cast<uint64_t>((slot * Cfg::KV_TILE) >> 4);
+#pragma unroll
+                for (int kk = k0; kk < k1; ++kk)
+                    umma_f16_tmem_a(d, a + 8u * static_cast<uint32_t>(kk), vd + static_cast<uint64_t>(kk * (2048 >> 4)), Cfg::ID_PV,
+                                    add || kk > 0 ? 1u : 0u);
+            };
+            bool ok = true;
+            uint32_t q_uses = 0;
+            if constexpr (NT == 1) {
+                // One tile, score buffers taken in turn: the scores of the next block are issued
+                // ahead of this block's product, except that a new item's scores, which wait for
+                // its queries, come after it.
+                Walk ahead = walk;
+                Segment gs, gp;
+                RingPos<STAGES> ks, kp;          // K tile of the next scores, of the next product
+                RingPos<STAGES> freed;           // V tile of the product two blocks back
+                uint32_t ns = 0, np = 0;         // blocks whose scores / products are issued
+                bool more_s = next_segment<Cfg>(p, ahead, gs), more_p = next_segment<Cfg>(p, walk, gp);
+                int bs = gs.b0, bp = gp.b0;
+                freed.step();
+                auto scores = [&]() -> bool {
+                    if (bs == gs.b0) {
+                        if (!wait_bounded(bar.q_full, q_uses & 1u, wc, ERR_MMA_OPERANDS))
+                            return false;
+                        ++q_uses;
+                    }
+                    if (!wait_bounded(bar.full0 + 8u * ks.slot, ks.parity, wc, ERR_MMA_OPERANDS))
+                        return false;
+                    if (ns >= 2) {   // this buffer's P has been multiplied
+                        if (!wait_bounded(bar.empty0 + 8u * freed.slot, freed.parity, wc, ERR_MMA_ACCUMULATOR))
+                            return false;
+                        freed.step();
+                        freed.step();
+                    }
+                    tc_fence_after_sync();
+                    issue_s(0, ks.slot, tmem + static_cast<uint32_t>(Cfg::S_COL + static_cast<int>(ns & 1u) * BKV));
+                    umma_commit(bar.empty0 + 8u * ks.slot);   // K read, scores complete
+                    if (bs + 1 == gs.b1)
+                        umma_commit(bar.q_empty);
+                    ks.step();
+                    ks.step();
+                    ++ns;
+                    if (++bs == gs.b1) {
+                        more_s = next_segment<Cfg>(p, ahead, gs);
+                        bs = gs.b0;
+                    }
+                    return true;
+                };
+                auto product = [&]() -> bool {
+                    RingPos<STAGES> kv = kp;
+                    kv.step();
+                    // (a barrier per score buffer: the softmax may finish the next block, whose
+                    // scores are issued, before this thread looks)
+                    if (!wait_bounded(bar.full0 + 8u * kv.slot, kv.parity, wc, ERR_MMA_OPERANDS) ||
+                        !wait_bounded(bar.p_half0 + 8u * (np & 1u), (np >> 1) & 1u, wc, ERR_MMA_OPERANDS))
+                        return false;
+                    tc_fence_after_sync();
+                    issue_pv(kv.slot, tmem + static_cast<uint32_t>(Cfg::S_COL + static_cast<int>(np & 1u) * BKV),
+                             tmem + static_cast<uint32_t>(Cfg::O_COL), 0, BKV / 16, bp != gp.b0);
+                    umma_commit(bar.empty0 + 8u * kv.slot);   // V read, product complete
+                    kp = kv;
+                    kp.step();
+                    ++np;
+                    if (++bp == gp.b1) {
+                        more_p = next_segment<Cfg>(p, walk, gp);
+                        bp = gp.b0;
+                    }
+                    return true;
+                };
+                ok = more_s && scores();
+                while (ok && more_p) {
+                    const bool same_item = more_s && bs != gs.b0;
+                    if (same_item)
+                        ok = scores();
+                    ok = ok && product();
+                    if (ok && !same_item && more_s)
+                        ok = scores();
+                }
+            } else {
+                // Two tiles share each block; as in attention_fwd_kernel: P_A V, S_A of the next
+                // block, P_B V, S_B of the next block. The second tile's scores and product complete
+                // the barriers that free their K and V tiles.
+                RingPos<STAGES> pos;       // K tile of the current block
+                uint32_t na = 0, nb = 0;   // blocks of the first and of the second tile so far
+                Segment g;
+                const uint32_t sA = tmem + static_cast<uint32_t>(Cfg::S_COL), sB = sA + BKV;
+                const uint32_t oA = tmem + static_cast<uint32_t>(Cfg::O_COL), oB = oA + Cfg::D;
+                while (ok && next_segment<Cfg>(p, walk, g)) {
+                    int mine = g.blocks;   // the first tile's blocks
+                    if (p.keys != KEYS_PREFIX && g.toks > p.tile_tokens)
+                        mine = max(1, (g.edge + (g.tok0 + p.tile_tokens - 1 - g.q0) + BKV) / BKV);
+                    ok = wait_bounded(bar.q_full, q_uses & 1u, wc, ERR_MMA_OPERANDS);
+                    ++q_uses;
+                    auto product = [&](int t, int slot, bool add) -> bool {
+                        const uint32_t n = t == 0 ? na : nb, s = t == 0 ? sA : sB, o = t == 0 ? oA : oB;
+#pragma unroll
+                        for (int part = 0; part < 2; ++part) {
+                            if (!wait_bounded((part == 0 ? bar.p_half0 : bar.p_full0) + 8u * t, n & 1u, wc, ERR_MMA_OPERANDS))
+                                return false;
+                            tc_fence_after_sync();
+                            if (part == 0)
+                                issue_pv(slot, s, o, 0, BKV / 32, add);
+                            else
+                                issue_pv(slot, s, o, BKV / 32, BKV / 16, true);
+                        }
+                        return true;
+                    };
+                    // scores of the block whose K tile is at `at`
+                    auto scores = [&](int t, const RingPos<STAGES> &at, bool last) {
+                        issue_s(t, at.slot, t == 0 ? sA : sB);
+                        umma_commit(t == 0 ? bar.s_full : bar.empty0 + 8u * at.slot);
+                        if (t == 1 && last)
+                            umma_commit(bar.q_empty);
+                    };
+                    if (ok && (ok = wait_bounded(bar.full0 + 8u * pos.slot, pos.parity, wc, ERR_MMA_OPERANDS))) {
+                        tc_fence_after_sync();
+                        if (g.b0 < mine)
+                            scores(0, pos, false);
+                        scores(1, pos, g.b0 + 1 == g.b1);
+                    }
+                    for (int b = g.b0; ok && b < g.b1; ++b) {
+                        RingPos<STAGES> v = pos, k_next;
+                        v.step();
+                        k_next = v;
+                        k_next.step();
+                        if (!(ok = wait_bounded(bar.full0 + 8u * v.slot, v.parity, wc, ERR_MMA_OPERANDS)))
+                            break;
+                        if (b < mine) {
+                            if (!(ok = product(0, v.slot, b != g.b0)))
+                                break;
+                            umma_commit(bar.pv_done);
+                            ++na;
+                        }
+                        if (b + 1 < g.b1) {
+                            if (!(ok = wait_bounded(bar.full0 + 8u * k_next.slot, k_next.parity, wc, ERR_MMA_OPERANDS)))
+                                break;
+                            if (b + 1 < mine) {   // over P_A of this block
+                                if (!(ok = wait_bounded(bar.pv_done, (na - 1u) & 1u, wc, ERR_MMA_ACCUMULATOR)))
+                                    break;
+                                tc_fence_after_sync();
+                                scores(0, k_next, false);
+                            }
+                        }
+                        if (!(ok = product(1, v.slot, b != g.b0)))
+                            break;
+                        umma_commit(bar.empty0 + 8u * v.slot);
+                        ++nb;
+                        // the next scores of this tile go over P_B (of this item's next block, or of
+                        // the next item: also then P has to have been read)
+                        if (!(ok = wait_bounded(bar.empty0 + 8u * v.slot, v.parity, wc, ERR_MMA_ACCUMULATOR)))
+                            break;
+                        tc_fence_after_sync();
+                        if (b + 1 < g.b1)
+                            scores(1, k_next, b + 2 == g.b1);
+                        pos = k_next;
+                    }
+                }
+            }
+            if (!ok) {
+                umma_commit(bar.drain);
+                wait_until(bar.drain, 0, p.timeout_ns, p.err);
+            }
+        }
+        __syncwarp();
+    } else {
+        // ---------------------------------------------------------------- softmax
+        paged_softmax_warp<Cfg>(p, bar, wc, tmem, ring, walk, shares, (warp - 2) >> 2, warp, lane);
+    }
+
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after_sync();
+        tmem_dealloc<1>(tmem, Cfg::TMEM_COLS);
+    }
+}
+
+// ---- joining the parts ---------------------------------------------------------------------------
+
+struct CombineParams {
+    int num_tokens, kv_heads, group, num_seqs;
+    const int *q_start;
+    PartsView parts[3];
+    int ctas[3];                 // grid sizes of the launches
+    int tile_tokens;
+    const PartInfo *own, *prefix;   // prefix: nullptr when all keys were one launch's
+    const float *row_o[2];       // whole items of the own (0) and prefix (1) keys
+    const float2 *row_ml[2];
+    void *out;
+    int64_t out_token, out_head;
+    float *lse;
+    int64_t lse_token;
+};
+
+// One warp per token and head: out = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i over its parts,
+// in the order of the keys (the same bits whichever CTA was first). Lane i of a step of 32 holds
+// part i's (m, l); every lane then adds up its D / 32 dimensions.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) paged_combine_kernel(const CombineParams p)
+{
+    constexpr int V = D / 32;
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const int lane = threadIdx.x & 31;
+    const int heads = p.kv_heads * p.group;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    if (row >= static_cast<int64_t>(p.num_tokens) * heads)
+        return;
+    const int token = static_cast<int>(row / heads), head = static_cast<int>(row - static_cast<int64_t>(token) * heads);
+    if (token < __ldg(p.q_start) || token >= __ldg(p.q_start + p.num_seqs))
+        return;   // of no sequence: nothing was written for it
+    const int kv_head = head / p.group, g = head - kv_head * p.group;
+    const bool joint = p.prefix != nullptr;
+    float m = -INFINITY, l = 0.0f;
+    float acc[V] = {};
+    for (int side = joint ? 1 : 0; side >= 0; --side) {
+        const PartInfo info = (side == 1 ? p.prefix : p.own)[static_cast<int64_t>(token) * p.kv_heads + kv_head];
+        // (a token of an unsorted q_start may have no entry: what is not a possible one is left out)
+        if (info.w < 0 || info.w > 2 || info.y < 1 || info.x < 0 || info.y > p.ctas[info.w] - info.x)
+            continue;
+        if (!joint && info.y == 1)
+            return;   // finished by its CTA
+        const PartsView &parts = p.parts[info.w];
+        const int at = token - info.z;
+        if (at < 0 || at >= parts.tiles * p.tile_tokens)
+            continue;
+        const int tile = at / p.tile_tokens, r = (at - tile * p.tile_tokens) * p.group + g;
+        auto part_row = [&](int i) -> int64_t {   // the first part is its CTA's last stretch, the others their CTAs' first
+            return (static_cast<int64_t>(2 * (info.x + i) + (i == 0 ? 1 : 0)) * parts.tiles + tile) * parts.rows + r;
+        };
+        for (int i0 = 0; i0 < info.y; i0 += 32) {
+            const int n = min(32, info.y - i0);
+            float2 ml = make_float2(-INFINITY, 0.0f);
+            if (lane < n)
+                ml = info.y == 1 ? p.row_ml[side][row] : parts.ml[part_row(i0 + lane)];
+            float top = ml.x;
+#pragma unroll
+            for (int o = 16; o > 0; o /= 2)
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const float m_new = fmaxf(m, top);
+            const float keep = m == -INFINITY ? 0.0f : exp2f(m - m_new);
+            float w = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - m_new);
+            if (ml.y != ml.y)
+                w = ml.y;   // NaN stays NaN
+            float sum = ml.y == 0.0f ? 0.0f : w * ml.y;
+#pragma unroll
+            for (int o = 16; o > 0; o /= 2)
+                sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            l = l * keep + sum;
+            m = m_new;
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                acc[e] *= keep;
+            const bool none = ml.y == 0.0f;   // a part without a key: its O may not be written
+            for (int i = 0; i < n; ++i) {
+                const float wi = __shfl_sync(0xffffffffu, w, i);
+                if (__shfl_sync(0xffffffffu, none, i))
+                    continue;
+                const float *o = (info.y == 1 ? p.row_o[side] + row * D : parts.o + part_row(i0 + i) * D) + lane * V;
+                if constexpr (V == 4) {
+                    const float4 x = *reinterpret_cast<const float4 *>(o);
+                    acc[0] = fmaf(wi, x.x, acc[0]);
+                    acc[1] = fmaf(wi, x.y, acc[1]);
+                    acc[2] = fmaf(wi, x.z, acc[2]);
+                    acc[3] = fmaf(wi, x.w, acc[3]);
+                } else {
+                    const float2 x = *reinterpret_cast<const float2 *>(o);
+                    acc[0] = fmaf(wi, x.x, acc[0]);
+                    acc[1] = fmaf(wi, x.y, acc[1]);
+                }
+            }
+        }
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    T *dst = static_cast<T *>(p.out) + token * p.out_token + head * p.out_head + lane * V;
+    uint32_t w[V / 2];
+#pragma unroll
+    for (int e = 0; e < V / 2; ++e)
+        w[e] = pack2<T>(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    if constexpr (V == 4)
+        *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
+    else
+        *reinterpret_cast<uint32_t *>(dst) = w[0];
+    if (p.lse && lane == 0)
+        p.lse[token * p.lse_token + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+}
+
+}  // namespace gb300

@@ -197,6 +197,17 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *map, uint3
         : "memory");
 }
 
+// 4-D tiled load of the box at (c0, c1, c2, c3) into shared memory, counted on `bar`.
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void *map, uint32_t bar, int32_t c0, int32_t c1,
+                                            int32_t c2, int32_t c3)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+        : "memory");
+}
+
 // Same, for a CTA pair: the data lands in this CTA's shared memory, the transaction bytes
 // are counted on `bar`, which may be the peer CTA's barrier (a shared::cluster address).
 __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void *map, uint32_t bar_cluster,

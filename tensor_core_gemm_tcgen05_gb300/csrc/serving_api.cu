@@ -1,0 +1,748 @@
+// Host side of the C ABI declared in include/gemm_serving.h: argument checks, the choice of
+// kernels and their launches.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+#include <utility>
+
+#include "gemm_ctx.h"
+#include "gemm_serving.h"
+#include "paged_attention_kernel.cuh"
+#include "rope_kernel.cuh"
+
+using namespace gb300_host;
+
+namespace {
+
+using i128 = __int128;
+constexpr int64_t kMaxStride = (int64_t(1) << 39) - 8;   // elements: tensor maps hold strides below 2^40 bytes
+constexpr int64_t kMaxHeads = 1 << 16;
+
+// ---- strided operands ------------------------------------------------------------------------
+
+// Vectors of `inner` contiguous elements at base + sum_i index_i * stride_i, index_i < count_i.
+struct Layout {
+    const void *base;
+    int64_t inner;
+    int dims;
+    int64_t count[3], stride[3];
+};
+
+int64_t span(const Layout &a)   // elements from the first to the last
+{
+    int64_t s = a.inner;
+    for (int i = 0; i < a.dims; ++i)
+        s += (a.count[i] - 1) * a.stride[i];
+    return s;
+}
+
+// Sorted by stride, largest first, without the dimensions of one element.
+Layout sorted(Layout a)
+{
+    int n = 0;
+    for (int i = 0; i < a.dims; ++i)
+        if (a.count[i] > 1) {
+            a.count[n] = a.count[i];
+            a.stride[n++] = a.stride[i];
+        }
+    a.dims = n;
+    for (int i = 0; i < n; ++i)
+        for (int j = i + 1; j < n; ++j)
+            if (a.stride[j] > a.stride[i]) {
+                std::swap(a.stride[i], a.stride[j]);
+                std::swap(a.count[i], a.count[j]);
+            }
+    return a;
+}
+
+// No two vectors of a (sorted) share an element: every stride covers what lies inside it.
+bool self_disjoint(const Layout &a)
+{
+    int64_t s = a.inner;
+    for (int i = a.dims - 1; i >= 0; --i) {
+        if (a.stride[i] < s)
+            return false;
+        s += (a.count[i] - 1) * a.stride[i];
+    }
+    return true;
+}
+
+// a and b (dimension by dimension of the same strides, largest first, each covering what lies
+// inside it) share no element in the dimensions i.., b moved by `delta` elements against a.
+bool moved_disjoint(const Layout &a, const Layout &b, int i, int64_t delta)
+{
+    if (i == a.dims)
+        return delta >= a.inner || delta <= -a.inner;
+    int64_t wa = a.inner, wb = b.inner;   // width of one step of dimension i
+    for (int k = i + 1; k < a.dims; ++k) {
+        wa += (a.count[k] - 1) * a.stride[k];
+        wb += (b.count[k] - 1) * b.stride[k];
+    }
+    const int64_t s = a.stride[i];
+    if (delta >= wa + (a.count[i] - 1) * s || -delta >= wb + (b.count[i] - 1) * s)
+        return true;
+    // modulo the stride, b's steps begin at r and (the ones before) at r - s
+    const int64_t r = ((delta % s) + s) % s;
+    return (r >= wa || moved_disjoint(a, b, i + 1, r)) && (r - s + wb <= 0 || moved_disjoint(a, b, i + 1, r - s));
+}
+
+// a and b may share an element (both of 2-byte elements; exact where their strides agree, by
+// their extents otherwise).
+bool may_overlap(Layout a, Layout b)
+{
+    if (!overlaps(a.base, static_cast<size_t>(span(a)) * 2, b.base, static_cast<size_t>(span(b)) * 2))
+        return false;
+    if (a.dims != b.dims || a.inner != b.inner)
+        return true;
+    for (int i = 0; i < a.dims; ++i) {   // (the stride of a dimension of one element does not matter)
+        if (a.count[i] <= 1)
+            a.stride[i] = b.stride[i];
+        if (b.count[i] <= 1)
+            b.stride[i] = a.stride[i];
+        if (a.stride[i] != b.stride[i])
+            return true;
+    }
+    int n = 0;
+    for (int i = 0; i < a.dims; ++i)
+        if (a.count[i] > 1 || b.count[i] > 1) {
+            a.count[n] = a.count[i];
+            b.count[n] = b.count[i];
+            a.stride[n] = b.stride[n] = a.stride[i];
+            ++n;
+        }
+    a.dims = b.dims = n;
+    for (int i = 0; i < n; ++i)
+        for (int j = i + 1; j < n; ++j)
+            if (a.stride[j] > a.stride[i]) {
+                std::swap(a.stride[i], a.stride[j]);
+                std::swap(a.count[i], a.count[j]);
+                std::swap(b.count[i], b.count[j]);
+                b.stride[i] = a.stride[i];
+                b.stride[j] = a.stride[j];
+            }
+    if (!self_disjoint(a) || !self_disjoint(b))
+        return true;
+    const int64_t bytes = static_cast<int64_t>(reinterpret_cast<intptr_t>(b.base) - reinterpret_cast<intptr_t>(a.base));
+    return bytes % 2 != 0 || !moved_disjoint(a, b, 0, bytes / 2);
+}
+
+Layout heads_layout(const gemm_heads &h, int64_t tokens, int64_t head_dim)
+{
+    return Layout{h.data, head_dim, 2, {tokens, h.heads, 1}, {h.token_stride, h.head_stride, 0}};
+}
+
+Layout cache_layout(const gemm_kv_cache &c, const void *base)
+{
+    return Layout{base,
+                  c.head_dim,
+                  3,
+                  {c.num_pages, c.kv_heads, c.page_size},
+                  {c.page_stride, c.head_stride, c.row_stride}};
+}
+
+bool same_heads(const gemm_heads &a, const gemm_heads &b)
+{
+    return a.data == b.data && a.heads == b.heads && a.token_stride == b.token_stride && a.head_stride == b.head_stride;
+}
+
+bool on_ctx(const gemm_ctx *ctx, const void *p) { return on_device(p, ctx->device); }
+
+bool aligned_to(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// Sizes, strides and alignment of one operand (not what memory it is); `out`: its vectors must
+// be disjoint.
+int check_heads(const gemm_heads *h, int64_t tokens, int64_t head_dim, bool out)
+{
+    if (!h || h->heads < 0 || h->heads > kMaxHeads)
+        return GEMM_ERR_ARG;
+    if (h->heads == 0 || tokens == 0)
+        return GEMM_OK;
+    if (!h->data || h->token_stride < 0 || h->head_stride < 0 || h->token_stride > kMaxStride ||
+        h->head_stride > kMaxStride)
+        return GEMM_ERR_ARG;
+    if (static_cast<i128>(tokens) * h->token_stride + static_cast<i128>(h->heads) * h->head_stride > (i128(1) << 60))
+        return GEMM_ERR_ARG;
+    if (!aligned16(h->data) || h->token_stride % 8 != 0 || h->head_stride % 8 != 0)
+        return GEMM_ERR_ALIGN;
+    if (out && !self_disjoint(sorted(heads_layout(*h, tokens, head_dim))))
+        return GEMM_ERR_ARG;
+    return GEMM_OK;
+}
+
+int check_dtype_dim(int dtype, int64_t head_dim)
+{
+    return (dtype == GEMM_F16 || dtype == GEMM_BF16) && (head_dim == 64 || head_dim == 128) ? GEMM_OK : GEMM_ERR_ARG;
+}
+
+int check_rope(const gemm_ctx *ctx, const gemm_rope *r, int64_t head_dim)
+{
+    if (!r || r->rotary_dim < 0 || r->rotary_dim > head_dim || r->rotary_dim % 16 != 0 ||
+        (r->interleaved != 0 && r->interleaved != 1) || !std::isfinite(r->scale) || !(r->eps >= 0.0f) ||
+        !std::isfinite(r->eps) || (r->rotary_dim > 0 && !r->table))
+        return GEMM_ERR_ARG;
+    if ((r->rotary_dim > 0 && !aligned_to(r->table, 8)) || (r->q_norm && !aligned16(r->q_norm)) ||
+        (r->k_norm && !aligned16(r->k_norm)))
+        return GEMM_ERR_ALIGN;
+    if ((r->rotary_dim > 0 && !on_ctx(ctx, r->table)) || (r->q_norm && !on_ctx(ctx, r->q_norm)) ||
+        (r->k_norm && !on_ctx(ctx, r->k_norm)))
+        return GEMM_ERR_DEVICE;
+    return GEMM_OK;
+}
+
+int check_cache(const gemm_ctx *ctx, const gemm_kv_cache *c)
+{
+    if (!c || check_dtype_dim(c->dtype, c->head_dim) != GEMM_OK)
+        return GEMM_ERR_ARG;
+    if (c->page_size < 16 || c->page_size > 1024 || (c->page_size & (c->page_size - 1)) != 0 || c->kv_heads < 1 ||
+        c->kv_heads > kMaxHeads || c->num_pages < 1 || c->num_pages > INT32_MAX - 1)
+        return GEMM_ERR_ARG;
+    if (!c->k || !c->v || c->page_stride <= 0 || c->head_stride <= 0 || c->row_stride <= 0 ||
+        c->page_stride > kMaxStride || c->head_stride > kMaxStride || c->row_stride > kMaxStride)
+        return GEMM_ERR_ARG;
+    if (static_cast<i128>(c->num_pages) * c->page_stride > (i128(1) << 59))
+        return GEMM_ERR_ARG;
+    if (!aligned16(c->k) || !aligned16(c->v) || c->page_stride % 8 != 0 || c->head_stride % 8 != 0 ||
+        c->row_stride % 8 != 0)
+        return GEMM_ERR_ALIGN;
+    const Layout k = cache_layout(*c, c->k), v = cache_layout(*c, c->v);
+    if (!self_disjoint(sorted(k)) || may_overlap(k, v))
+        return GEMM_ERR_ARG;
+    if (!on_ctx(ctx, c->k) || !on_ctx(ctx, c->v))
+        return GEMM_ERR_DEVICE;
+    return GEMM_OK;
+}
+
+// `pointers`: the device arrays are checked too. `prefix`: prefix_pages is read.
+int check_batch(const gemm_ctx *ctx, const gemm_kv_cache *c, const gemm_kv_batch *b, bool pointers, bool prefix)
+{
+    if (!b || b->num_seqs < 0 || b->num_seqs > INT32_MAX - 1 || b->num_tokens < 0 || b->num_tokens > INT32_MAX ||
+        b->max_q < 0 || b->table_width < 0 || b->table_stride < 0 || b->table_stride > kMaxStride ||
+        b->num_prefix_pages < 0)
+        return GEMM_ERR_ARG;
+    if (b->table_width > INT32_MAX || b->num_prefix_pages > INT32_MAX ||
+        (b->table_width + b->num_prefix_pages) * c->page_size > INT32_MAX)
+        return GEMM_ERR_ARG;
+    if (!pointers || b->num_seqs == 0 || b->num_tokens == 0)
+        return GEMM_OK;
+    const bool table = b->table_width > 0, pre = prefix && b->num_prefix_pages > 0;
+    if (!b->q_start || !b->kv_lens || (table && !b->page_table) || (pre && !b->prefix_pages))
+        return GEMM_ERR_ARG;
+    if (!aligned_to(b->q_start, 4) || !aligned_to(b->kv_lens, 4) || (table && !aligned_to(b->page_table, 4)) ||
+        (pre && !aligned_to(b->prefix_pages, 4)))
+        return GEMM_ERR_ALIGN;
+    if (!on_ctx(ctx, b->q_start) || !on_ctx(ctx, b->kv_lens) || (table && !on_ctx(ctx, b->page_table)) ||
+        (pre && !on_ctx(ctx, b->prefix_pages)))
+        return GEMM_ERR_DEVICE;
+    return GEMM_OK;
+}
+
+gb300::BatchView batch_view(const gemm_kv_cache &c, const gemm_kv_batch &b)
+{
+    gb300::BatchView v;
+    v.q_start = b.q_start;
+    v.kv_lens = b.kv_lens;
+    v.table = b.page_table;
+    v.table_stride = b.table_stride;
+    v.num_seqs = static_cast<int>(b.num_seqs);
+    v.num_tokens = static_cast<int>(b.num_tokens);
+    v.table_width = static_cast<int>(b.table_width);
+    v.num_pages = static_cast<int>(c.num_pages);
+    v.page_shift = 0;
+    while ((int64_t(1) << v.page_shift) < c.page_size)
+        ++v.page_shift;
+    v.prefix_len = static_cast<int>(b.num_prefix_pages * c.page_size);
+    return v;
+}
+
+// Launch with programmatic stream serialisation (see gemm_api.cu): every kernel here starts with
+// grid_dependency_wait.
+template <typename... P, typename... A>
+cudaError_t launch_serving(void (*kernel)(P...), int64_t grid, int threads, int smem, cudaStream_t stream, A &&...args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+}
+
+// ---- rotation ---------------------------------------------------------------------------------
+
+gb300::HeadsView heads_view(const gemm_heads &in, const gemm_heads &out)
+{
+    return gb300::HeadsView{in.data, in.token_stride, in.head_stride, out.data, out.token_stride, out.head_stride,
+                            static_cast<int>(in.heads)};
+}
+
+template <bool PAGED>
+int launch_rope(gemm_ctx *ctx, int dtype, int64_t head_dim, gb300::RopeParams &p, const gemm_rope &r, cudaStream_t stream)
+{
+    p.table = r.table;
+    p.q_norm = r.q_norm;
+    p.k_norm = r.k_norm;
+    p.rotary_dim = static_cast<int>(r.rotary_dim);
+    p.interleaved = r.interleaved;
+    p.eps = r.eps;
+    p.scale = r.scale;
+    p.err = ctx->d_err;
+    const int all = p.q.heads + p.k.heads + p.v.heads;
+    // As many heads per group of lanes as leave the GPU's 2048 threads per SM busy: the cosines
+    // are computed once per group.
+    const int64_t lanes = head_dim / 8;
+    int per = 16;
+    while (per > 1 && p.tokens * int64_t((all + per - 1) / per) * lanes < int64_t(ctx->num_sms) * 2048)
+        per /= 2;
+    p.heads_per_item = per;
+    p.chunks = (all + per - 1) / per;
+    const int64_t per_block = gb300::kRopeThreads / lanes;
+    const int64_t grid = (static_cast<int64_t>(p.tokens) * p.chunks + per_block - 1) / per_block;
+    if (grid > INT32_MAX)
+        return GEMM_ERR_ARG;
+    DeviceGuard guard(ctx->device);
+    auto run = [&](auto kernel) { return launch_serving(kernel, grid, gb300::kRopeThreads, 0, stream, p); };
+    cudaError_t e;
+    if (dtype == GEMM_F16)
+        e = head_dim == 64 ? run(gb300::rope_kernel<__half, 64, PAGED>) : run(gb300::rope_kernel<__half, 128, PAGED>);
+    else
+        e = head_dim == 64 ? run(gb300::rope_kernel<__nv_bfloat16, 64, PAGED>)
+                           : run(gb300::rope_kernel<__nv_bfloat16, 128, PAGED>);
+    return e == cudaSuccess ? GEMM_OK : cuda_fail(ctx, e, GEMM_ERR_LAUNCH);
+}
+
+// ---- paged attention ----------------------------------------------------------------------------
+
+// The launches of one call and where their parts of the workspace are.
+struct AttnLaunch {
+    int tiles = 1;            // query tiles per item (the kernel's NT)
+    int keys = 0, seqs = 0;   // KEYS_*, SEQS_*
+    int64_t grid = 0;
+    int64_t o_off = 0, ml_off = 0;   // PartsView
+};
+
+struct AttnPlan {
+    bool empty = true, joint = false;
+    int count = 0;
+    AttnLaunch launch[3];
+    int tile_tokens = 0;
+    int64_t rows = 0;   // kept per tile
+    int64_t own_off = 0, prefix_off = 0;               // PartInfo tables
+    int64_t row_o_off[2] = {}, row_ml_off[2] = {};     // whole items (joint): own, prefix
+    int64_t bytes = 0;
+};
+
+AttnPlan attention_plan(const gemm_ctx *ctx, const gemm_kv_cache &c, const gemm_kv_batch &b, int64_t q_heads)
+{
+    AttnPlan pl;
+    const int64_t T = b.num_tokens, group = q_heads / c.kv_heads;
+    if (T == 0 || b.num_seqs == 0 || q_heads == 0)
+        return pl;
+    pl.empty = false;
+    pl.tile_tokens = static_cast<int>(128 / group);
+    const int64_t tq = pl.tile_tokens;
+    pl.rows = std::min<int64_t>(tq, T) * group;
+    const int64_t prefix = b.num_prefix_pages * c.page_size, own = b.table_width * c.page_size;
+    const int64_t flat_tiles = (T + tq - 1) / tq;
+    // The prefix by itself, for the tokens of all sequences together, when that takes fewer tiles
+    // of rows than there are sequences (each of which would read the prefix again).
+    pl.joint = prefix > 0 && flat_tiles < b.num_seqs;
+    auto add = [&](int tiles, int keys, int seqs, int64_t max_tiles, int64_t key_count) {
+        AttnLaunch &l = pl.launch[pl.count++];
+        l.tiles = tiles;
+        l.keys = keys;
+        l.seqs = seqs;
+        const int64_t bkv = tiles == 1 ? 64 : 128;
+        const int64_t units = c.kv_heads * max_tiles * std::max<int64_t>(1, (key_count + bkv - 1) / bkv);
+        l.grid = std::min<int64_t>(static_cast<int64_t>(ctx->num_sms) * (tiles == 1 ? 2 : 1), units);
+    };
+    if (pl.joint)
+        add(flat_tiles > 1 ? 2 : 1, gb300::KEYS_PREFIX, gb300::SEQS_ALL, flat_tiles, prefix);
+    const int keys = pl.joint ? gb300::KEYS_OWN : gb300::KEYS_ALL;
+    const int64_t seen = own + (pl.joint ? 0 : prefix);
+    // Sequences with more new tokens than a tile takes go to the two-tile kernel, the others to
+    // the one-tile kernel; a kernel that no sequence can need is left out, and if max_q says that
+    // all are short the one-tile kernel takes whatever there is.
+    const bool may_long = (b.max_q == 0 || b.max_q > tq) && T > tq;
+    const bool may_short = !may_long || b.num_seqs > 1;
+    if (may_long)
+        add(2, keys, may_short ? gb300::SEQS_LONG : gb300::SEQS_ALL, std::min(T, T / (2 * tq) + b.num_seqs), seen);
+    if (may_short)
+        add(1, keys, may_long ? gb300::SEQS_SHORT : gb300::SEQS_ALL, std::min(T, T / tq + b.num_seqs), seen);
+    int64_t at = 0;
+    auto take = [&](int64_t bytes) {
+        const int64_t off = at;
+        at += (bytes + 255) / 256 * 256;
+        return off;
+    };
+    const int64_t info = T * c.kv_heads * static_cast<int64_t>(sizeof(gb300::PartInfo));
+    pl.own_off = take(info);
+    if (pl.joint) {
+        pl.prefix_off = take(info);
+        for (int i = 0; i < 2; ++i) {
+            pl.row_o_off[i] = take(T * q_heads * c.head_dim * 4);
+            pl.row_ml_off[i] = take(T * q_heads * 8);
+        }
+    }
+    for (int i = 0; i < pl.count; ++i) {
+        const int64_t rows = 2 * pl.launch[i].grid * pl.launch[i].tiles * pl.rows;
+        pl.launch[i].o_off = take(rows * c.head_dim * 4);
+        pl.launch[i].ml_off = take(rows * 8);
+    }
+    pl.bytes = at;
+    return pl;
+}
+
+// Sizes and counts; `pointers`: the batch's device arrays too.
+int check_attention(const gemm_ctx *ctx, const gemm_kv_cache *cache, const gemm_kv_batch *batch, int64_t q_heads, bool pointers)
+{
+    if (!ctx)
+        return GEMM_ERR_ARG;
+    int rc = check_cache(ctx, cache);
+    if (rc == GEMM_OK)
+        rc = check_batch(ctx, cache, batch, pointers, true);
+    if (rc != GEMM_OK)
+        return rc;
+    if (q_heads < 0 || q_heads > kMaxHeads || q_heads % cache->kv_heads != 0 || q_heads / cache->kv_heads > 128)
+        return GEMM_ERR_ARG;
+    if (batch->num_tokens * q_heads > (int64_t(1) << 33) || batch->num_seqs > (1 << 24))
+        return GEMM_ERR_ARG;
+    return GEMM_OK;
+}
+
+bool encode_4d(const gemm_ctx *ctx, CUtensorMap *map, const void *ptr, int dtype, const int64_t (&dims)[4],
+               const int64_t (&strides)[3] /* elements */, const uint32_t (&box)[4])
+{
+    cuuint64_t d[4], s[3];
+    cuuint32_t bx[4], es[4];
+    for (int i = 0; i < 4; ++i) {
+        d[i] = static_cast<cuuint64_t>(dims[i]);
+        bx[i] = box[i];
+        es[i] = 1;
+    }
+    for (int i = 0; i < 3; ++i)   // (that of a dimension of one element does not matter)
+        s[i] = static_cast<cuuint64_t>(dims[i + 1] > 1 ? strides[i] : dims[0]) * 2;
+    return ctx->encode(map, dtype == GEMM_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                       const_cast<void *>(ptr), d, s, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <class Cfg>
+cudaError_t launch_paged(int64_t grid, cudaStream_t stream, const CUtensorMap &tq, const CUtensorMap &tk,
+                         const CUtensorMap &tv, const gb300::PagedParams &p)
+{
+    return launch_serving(gb300::paged_attention_kernel<Cfg>, grid, Cfg::NUM_THREADS, Cfg::SMEM_BYTES, stream, tq, tk, tv, p);
+}
+
+// fn(config) with the PagedConfig of these run-time choices.
+template <class Fn>
+auto with_config(int dtype, int64_t head_dim, int tiles, Fn &&fn)
+{
+    using H = __half;
+    using B = __nv_bfloat16;
+    if (dtype == GEMM_F16) {
+        if (head_dim == 64)
+            return tiles == 1 ? fn(gb300::PagedConfig<H, 64, 1>{}) : fn(gb300::PagedConfig<H, 64, 2>{});
+        return tiles == 1 ? fn(gb300::PagedConfig<H, 128, 1>{}) : fn(gb300::PagedConfig<H, 128, 2>{});
+    }
+    if (head_dim == 64)
+        return tiles == 1 ? fn(gb300::PagedConfig<B, 64, 1>{}) : fn(gb300::PagedConfig<B, 64, 2>{});
+    return tiles == 1 ? fn(gb300::PagedConfig<B, 128, 1>{}) : fn(gb300::PagedConfig<B, 128, 2>{});
+}
+
+}  // namespace
+
+namespace gb300_host {
+
+cudaError_t serving_init(gemm_ctx *)
+{
+    for (int dtype : {GEMM_F16, GEMM_BF16})
+        for (int d : {64, 128})
+            for (int tiles : {1, 2}) {
+                const cudaError_t e = with_config(dtype, d, tiles, [](auto cfg) {
+                    using Cfg = decltype(cfg);
+                    return cudaFuncSetAttribute(gb300::paged_attention_kernel<Cfg>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                Cfg::SMEM_BYTES);
+                });
+                if (e != cudaSuccess)
+                    return e;
+            }
+    return cudaSuccess;
+}
+
+}  // namespace gb300_host
+
+extern "C" {
+
+int gemm_rope_table(int64_t rotary_dim, double base, int scaling, double factor, double original, uint64_t *table,
+                    float *scale)
+{
+    if (!table || rotary_dim < 16 || rotary_dim > 128 || rotary_dim % 16 != 0 || !(base > 1.0) || !std::isfinite(base) ||
+        scaling < GEMM_ROPE_PLAIN || scaling > GEMM_ROPE_YARN || !(factor >= 1.0) || !std::isfinite(factor))
+        return GEMM_ERR_ARG;
+    if (scaling == GEMM_ROPE_YARN && (!(original > 0.0) || !std::isfinite(original)))
+        return GEMM_ERR_ARG;
+    const double two_pi = 6.283185307179586476925;
+    const int64_t half = rotary_dim / 2;
+    if (scaling == GEMM_ROPE_NTK)
+        base *= std::pow(factor, static_cast<double>(rotary_dim) / static_cast<double>(rotary_dim - 2));
+    for (int64_t i = 0; i < half; ++i) {
+        double f = std::pow(base, -static_cast<double>(i) / static_cast<double>(half));
+        if (scaling == GEMM_ROPE_LINEAR)
+            f /= factor;
+        if (scaling == GEMM_ROPE_YARN) {
+            // turns within the original length: below 1 interpolated, above 32 kept
+            const double turns = original * f / two_pi;
+            const double keep = std::min(1.0, std::max(0.0, (turns - 1.0) / 31.0));
+            f = keep * f + (1.0 - keep) * f / factor;
+        }
+        // f <= 1 rad, so under 2^62 units: fits
+        table[i] = static_cast<uint64_t>(std::nearbyint(f / two_pi * 18446744073709551616.0));
+    }
+    if (scale)
+        *scale = scaling == GEMM_ROPE_YARN ? static_cast<float>(0.1 * std::log(factor) + 1.0) : 1.0f;
+    return GEMM_OK;
+}
+
+int gemm_qk_rope(gemm_ctx *ctx, int dtype, int64_t tokens, int64_t head_dim, const gemm_heads *q, const gemm_heads *k,
+                 const int32_t *positions, const gemm_rope *rope, const gemm_heads *q_out, const gemm_heads *k_out,
+                 void *stream)
+{
+    if (!ctx || tokens < 0 || tokens > INT32_MAX)
+        return GEMM_ERR_ARG;
+    int rc = check_dtype_dim(dtype, head_dim);
+    if (rc == GEMM_OK)
+        rc = check_heads(q, tokens, head_dim, false);
+    if (rc == GEMM_OK)
+        rc = check_heads(k, tokens, head_dim, false);
+    if (rc == GEMM_OK)
+        rc = check_heads(q_out, tokens, head_dim, true);
+    if (rc == GEMM_OK)
+        rc = check_heads(k_out, tokens, head_dim, true);
+    if (rc == GEMM_OK)
+        rc = check_rope(ctx, rope, head_dim);
+    if (rc != GEMM_OK)
+        return rc;
+    if (q_out->heads != q->heads || k_out->heads != k->heads)
+        return GEMM_ERR_ARG;
+    if (tokens == 0 || q->heads + k->heads == 0)
+        return GEMM_OK;
+    if (!positions)
+        return GEMM_ERR_ARG;
+    if (!aligned_to(positions, 4))
+        return GEMM_ERR_ALIGN;
+    const gemm_heads *in[2] = {q, k}, *out[2] = {q_out, k_out};
+    for (int i = 0; i < 2; ++i) {
+        if (out[i]->heads == 0)
+            continue;
+        const Layout o = heads_layout(*out[i], tokens, head_dim);
+        for (int j = 0; j < 2; ++j) {
+            if (in[j]->heads > 0 && !(i == j && same_heads(*out[i], *in[i])) &&
+                may_overlap(o, heads_layout(*in[j], tokens, head_dim)))
+                return GEMM_ERR_ARG;
+            if (i != j && out[j]->heads > 0 && may_overlap(o, heads_layout(*out[j], tokens, head_dim)))
+                return GEMM_ERR_ARG;
+        }
+        if (overlaps(o.base, static_cast<size_t>(span(o)) * 2, positions, static_cast<size_t>(tokens) * 4))
+            return GEMM_ERR_ARG;
+    }
+    if (!on_ctx(ctx, positions))
+        return GEMM_ERR_DEVICE;
+    for (int i = 0; i < 2; ++i)
+        if (in[i]->heads > 0 && (!on_ctx(ctx, in[i]->data) || !on_ctx(ctx, out[i]->data)))
+            return GEMM_ERR_DEVICE;
+    gb300::RopeParams p = {};
+    p.q = heads_view(*q, *q_out);
+    p.k = heads_view(*k, *k_out);
+    p.tokens = static_cast<int>(tokens);
+    p.positions = positions;
+    return launch_rope<false>(ctx, dtype, head_dim, p, *rope, static_cast<cudaStream_t>(stream));
+}
+
+int gemm_kv_append(gemm_ctx *ctx, const gemm_kv_cache *cache, const gemm_kv_batch *batch, const gemm_heads *q,
+                   const gemm_heads *k, const gemm_heads *v, const gemm_rope *rope, const gemm_heads *q_out, void *stream)
+{
+    if (!ctx)
+        return GEMM_ERR_ARG;
+    int rc = check_cache(ctx, cache);
+    if (rc == GEMM_OK)
+        rc = check_batch(ctx, cache, batch, true, false);
+    if (rc != GEMM_OK)
+        return rc;
+    const int64_t tokens = batch->num_tokens, d = cache->head_dim;
+    rc = check_heads(q, tokens, d, false);
+    if (rc == GEMM_OK)
+        rc = check_heads(k, tokens, d, false);
+    if (rc == GEMM_OK)
+        rc = check_heads(v, tokens, d, false);
+    if (rc == GEMM_OK)
+        rc = check_heads(q_out, tokens, d, true);
+    if (rc == GEMM_OK)
+        rc = check_rope(ctx, rope, d);
+    if (rc != GEMM_OK)
+        return rc;
+    if (q_out->heads != q->heads || k->heads != cache->kv_heads || v->heads != cache->kv_heads)
+        return GEMM_ERR_ARG;
+    if (tokens == 0 || batch->num_seqs == 0)
+        return GEMM_OK;
+    const Layout kc = cache_layout(*cache, cache->k), vc = cache_layout(*cache, cache->v);
+    const gemm_heads *used[4] = {q, k, v, q_out};
+    for (const gemm_heads *h : used) {
+        if (h->heads == 0)
+            continue;
+        const Layout l = heads_layout(*h, tokens, d);
+        if (may_overlap(l, kc) || may_overlap(l, vc))
+            return GEMM_ERR_ARG;
+        if (q_out->heads > 0 && h != q_out && !(h == q && same_heads(*q, *q_out)) &&
+            may_overlap(heads_layout(*q_out, tokens, d), l))
+            return GEMM_ERR_ARG;
+    }
+    for (const gemm_heads *h : used)
+        if (h->heads > 0 && !on_ctx(ctx, h->data))
+            return GEMM_ERR_DEVICE;
+    gb300::RopeParams p = {};
+    p.q = heads_view(*q, *q_out);
+    p.k = heads_view(*k, gemm_heads{cache->k, k->heads, cache->page_stride, cache->head_stride});
+    p.v = heads_view(*v, gemm_heads{cache->v, v->heads, cache->page_stride, cache->head_stride});
+    p.tokens = static_cast<int>(tokens);
+    p.batch = batch_view(*cache, *batch);
+    p.row_stride = cache->row_stride;
+    return launch_rope<true>(ctx, cache->dtype, d, p, *rope, static_cast<cudaStream_t>(stream));
+}
+
+int64_t gemm_paged_attention_workspace(gemm_ctx *ctx, const gemm_kv_cache *cache, const gemm_kv_batch *batch, int64_t q_heads)
+{
+    const int rc = check_attention(ctx, cache, batch, q_heads, false);
+    return rc == GEMM_OK ? attention_plan(ctx, *cache, *batch, q_heads).bytes : rc;
+}
+
+int gemm_paged_attention(gemm_ctx *ctx, const gemm_kv_cache *cache, const gemm_kv_batch *batch, const gemm_heads *q,
+                         float scale, const gemm_heads *out, float *lse, int64_t lse_stride, void *workspace,
+                         int64_t workspace_bytes, void *stream)
+{
+    if (!q || !out || !std::isfinite(scale))
+        return GEMM_ERR_ARG;
+    int rc = check_attention(ctx, cache, batch, q->heads, true);
+    if (rc != GEMM_OK)
+        return rc;
+    const int64_t tokens = batch->num_tokens, d = cache->head_dim;
+    rc = check_heads(q, tokens, d, true);   // (no broadcast queries: a tensor map has no zero strides)
+    if (rc == GEMM_OK)
+        rc = check_heads(out, tokens, d, true);
+    if (rc != GEMM_OK)
+        return rc;
+    if (out->heads != q->heads || lse_stride < 0 || lse_stride > kMaxStride)
+        return GEMM_ERR_ARG;
+    const AttnPlan pl = attention_plan(ctx, *cache, *batch, q->heads);
+    if (pl.empty)
+        return GEMM_OK;
+    if (!workspace || workspace_bytes < pl.bytes || (lse && tokens > 1 && lse_stride < q->heads))
+        return GEMM_ERR_ARG;
+    if (!aligned_to(workspace, 256) || (lse && !aligned_to(lse, 4)))
+        return GEMM_ERR_ALIGN;
+    const Layout lq = heads_layout(*q, tokens, d), lo = heads_layout(*out, tokens, d);
+    const Layout kc = cache_layout(*cache, cache->k), vc = cache_layout(*cache, cache->v);
+    if (may_overlap(lo, lq) || may_overlap(lo, kc) || may_overlap(lo, vc))
+        return GEMM_ERR_ARG;
+    const size_t lse_bytes = lse ? static_cast<size_t>((tokens - 1) * lse_stride + q->heads) * 4 : 0;
+    for (const Layout *l : {&lq, &lo, &kc, &vc}) {
+        const size_t n = static_cast<size_t>(span(*l)) * 2;
+        if (overlaps(workspace, static_cast<size_t>(pl.bytes), l->base, n) || overlaps(lse, lse_bytes, l->base, n))
+            return GEMM_ERR_ARG;
+    }
+    if (overlaps(workspace, static_cast<size_t>(pl.bytes), lse, lse_bytes))
+        return GEMM_ERR_ARG;
+    if (!on_ctx(ctx, q->data) || !on_ctx(ctx, out->data) || !on_ctx(ctx, workspace) || (lse && !on_ctx(ctx, lse)))
+        return GEMM_ERR_DEVICE;
+
+    const int64_t group = q->heads / cache->kv_heads;
+    gb300::PagedParams p = {};
+    p.batch = batch_view(*cache, *batch);
+    p.prefix_pages = batch->prefix_pages;
+    p.n_prefix_pages = static_cast<int>(batch->num_prefix_pages);
+    p.kv_heads = static_cast<int>(cache->kv_heads);
+    p.group = static_cast<int>(group);
+    p.tile_tokens = pl.tile_tokens;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.out = out->data;
+    p.out_token = out->token_stride;
+    p.out_head = out->head_stride;
+    p.lse = lse;
+    p.lse_token = lse_stride;
+    p.err = ctx->d_err;
+    p.timeout_ns = ctx->timeout_ns;
+    p.debug = ctx->debug & GEMM_DEBUG_WITHHOLD_FIRST_LOAD;
+    char *ws = static_cast<char *>(workspace);
+    CUtensorMap tq, tk, tv;
+    if (!encode_4d(ctx, &tq, q->data, cache->dtype, {d, group, cache->kv_heads, tokens},
+                   {q->head_stride, group * q->head_stride, q->token_stride},
+                   {64, static_cast<uint32_t>(group), 1, static_cast<uint32_t>(pl.tile_tokens)}))
+        return GEMM_ERR_LAUNCH;
+    gb300::CombineParams cp = {};
+    cp.num_tokens = static_cast<int>(tokens);
+    cp.kv_heads = p.kv_heads;
+    cp.group = p.group;
+    cp.num_seqs = p.batch.num_seqs;
+    cp.q_start = batch->q_start;
+    cp.tile_tokens = pl.tile_tokens;
+    cp.own = reinterpret_cast<gb300::PartInfo *>(ws + pl.own_off);
+    cp.prefix = pl.joint ? reinterpret_cast<gb300::PartInfo *>(ws + pl.prefix_off) : nullptr;
+    for (int i = 0; i < 2; ++i) {
+        cp.row_o[i] = reinterpret_cast<float *>(ws + pl.row_o_off[i]);
+        cp.row_ml[i] = reinterpret_cast<float2 *>(ws + pl.row_ml_off[i]);
+    }
+    cp.out = p.out;
+    cp.out_token = p.out_token;
+    cp.out_head = p.out_head;
+    cp.lse = lse;
+    cp.lse_token = lse_stride;
+
+    DeviceGuard guard(ctx->device);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    for (int i = 0; i < pl.count; ++i) {
+        const AttnLaunch &l = pl.launch[i];
+        const bool prefix = l.keys == gb300::KEYS_PREFIX;
+        p.keys = l.keys;
+        p.seqs = l.seqs;
+        p.launch = i;
+        p.parts.o = reinterpret_cast<float *>(ws + l.o_off);
+        p.parts.ml = reinterpret_cast<float2 *>(ws + l.ml_off);
+        p.parts.rows = static_cast<int>(pl.rows);
+        p.parts.tiles = l.tiles;
+        p.info = reinterpret_cast<gb300::PartInfo *>(ws + (prefix ? pl.prefix_off : pl.own_off));
+        p.row_o = reinterpret_cast<float *>(ws + pl.row_o_off[prefix]);
+        p.row_ml = reinterpret_cast<float2 *>(ws + pl.row_ml_off[prefix]);
+        cp.parts[i] = p.parts;
+        cp.ctas[i] = static_cast<int>(l.grid);
+        const uint32_t rows = static_cast<uint32_t>(std::min<int64_t>(cache->page_size, l.tiles == 1 ? 64 : 128));
+        const int64_t dims[4] = {d, cache->page_size, cache->kv_heads, cache->num_pages};
+        const int64_t strides[3] = {cache->row_stride, cache->head_stride, cache->page_stride};
+        if (!encode_4d(ctx, &tk, cache->k, cache->dtype, dims, strides, {64, rows, 1, 1}) ||
+            !encode_4d(ctx, &tv, cache->v, cache->dtype, dims, strides, {64, rows, 1, 1}))
+            return GEMM_ERR_LAUNCH;
+        const cudaError_t e = with_config(cache->dtype, d, l.tiles, [&](auto cfg) {
+            return launch_paged<decltype(cfg)>(l.grid, st, tq, tk, tv, p);
+        });
+        if (e != cudaSuccess)
+            return cuda_fail(ctx, e, GEMM_ERR_LAUNCH);
+    }
+    const int64_t combine_grid = (tokens * q->heads + 7) / 8;
+    auto combine = [&](auto kernel) { return launch_serving(kernel, combine_grid, 256, 0, st, cp); };
+    cudaError_t e;
+    if (cache->dtype == GEMM_F16)
+        e = d == 64 ? combine(gb300::paged_combine_kernel<__half, 64>) : combine(gb300::paged_combine_kernel<__half, 128>);
+    else
+        e = d == 64 ? combine(gb300::paged_combine_kernel<__nv_bfloat16, 64>)
+                    : combine(gb300::paged_combine_kernel<__nv_bfloat16, 128>);
+    return e == cudaSuccess ? GEMM_OK : cuda_fail(ctx, e, GEMM_ERR_LAUNCH);
+}
+
+}  // extern "C"
