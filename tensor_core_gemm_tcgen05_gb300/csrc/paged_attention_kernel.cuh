@@ -53,8 +53,10 @@ struct PartsView {
     int tiles;
 };
 
-// Where a token's result is, per key head: CTA of the first part, number of parts, the item's
-// first token, the launch (index of its PartsView).
+// Where the parts of an item are. For each CTA, of the item that goes on past its range (its part
+// 1): {first token, tokens, key head, parts}, parts = 0 if there is none. For each token and key
+// head, when the prefix is a launch of its own: {CTA of the first part, parts (1: whole, in the
+// row tables), the item's first token, launch}.
 using PartInfo = int4;
 
 struct PagedParams {
@@ -63,15 +65,16 @@ struct PagedParams {
     int n_prefix_pages;
     int kv_heads, group, tile_tokens;   // G and 128 / G
     int keys, seqs;                     // KEYS_*, SEQS_*
-    int launch;                         // index for PartInfo
+    int launch;                         // index for the tokens' PartInfo
     float scale_log2;                   // scale * log2(e)
     void *out;
     int64_t out_token, out_head;
     float *lse;
     int64_t lse_token;
     PartsView parts;
-    PartInfo *info;                     // [num_tokens][kv_heads]
-    float *row_o;                       // KEYS_OWN / KEYS_PREFIX: whole items, [num_tokens][heads][D]
+    PartInfo *cuts;                     // [CTAs]; KEYS_ALL only
+    PartInfo *info;                     // [num_tokens][kv_heads]; not KEYS_ALL
+    float *row_o;                       // whole items, [num_tokens][heads][D]; not KEYS_ALL
     float2 *row_ml;
     uint32_t *err;
     uint64_t timeout_ns;
@@ -90,9 +93,11 @@ struct PagedConfig {
     static constexpr int KV_ATOM = BKV * 128, KV_TILE = ATOMS * KV_ATOM;
     // ring of K and V tiles (K0 V0 K1 V1 ...): what fits beside Q in half of (NT = 1) or all of
     // an SM's shared memory
-    static constexpr int STAGES = NT == 1 ? (D == 128 ? 4 : 8) : (D == 128 ? 5 : 8);
+    static constexpr int STAGES = D == 128 ? 4 : 8;
     static constexpr int Q_OFF = 0, RING_OFF = NT * Q_TILE;
-    static constexpr int BAR_OFF = RING_OFF + STAGES * KV_TILE;
+    // NT = 2: 32 rows x 128 bytes for each softmax warp, through which results are written
+    static constexpr int STAGE_WARP = 32 * 128, STAGE_OFF = RING_OFF + STAGES * KV_TILE;
+    static constexpr int BAR_OFF = STAGE_OFF + (NT == 2 ? 8 * STAGE_WARP : 0);
     // q_full, q_empty, drain, full[], empty[], s_full and pv_done (NT = 2: of the first tile),
     // then NT = 1: p_full[block mod 2]; NT = 2: p_half[tile], p_full[tile]
     static constexpr int NUM_BARS = 3 + 2 * STAGES + 2 + 2 * NT;
@@ -112,6 +117,10 @@ struct PagedConfig {
     static constexpr uint32_t ID_PV = (1u << 4) | TYPE_BITS | (1u << 16) | (static_cast<uint32_t>(D >> 3) << 17) | (128u >> 4 << 24);
 };
 
+// NT = 2: with fewer than kPagedCoarse blocks per CTA, items are cut at multiples of kPagedQuantum
+// blocks only: a part costs about as much (128 KB of FP32 written and read again) as the blocks.
+constexpr int kPagedCoarse = 8, kPagedQuantum = 4;
+
 // A row's running maximum is raised (and its row of O rescaled) only when a block's maximum
 // exceeds it by more than this many base-2 units: probabilities stay below 2^8.
 constexpr float kPagedRescale = 8.0f;
@@ -120,9 +129,10 @@ constexpr float kPagedRescale = 8.0f;
 
 // sum over i < n of floor((a i + b) / m), a, b >= 0, m > 0 (by reducing a and b modulo m and
 // counting lattice points the other way round, as in the Euclidean algorithm).
-__device__ inline int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b)
+template <typename I>
+__device__ inline I floor_sum(I n, I m, I a, I b)
 {
-    int64_t sum = 0;
+    I sum = 0;
     while (n > 0) {
         if (a >= m) {
             sum += n * (n - 1) / 2 * (a / m);
@@ -132,12 +142,12 @@ __device__ inline int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b)
             sum += n * (b / m);
             b %= m;
         }
-        const int64_t top = a * n + b;
+        const I top = a * n + b;
         if (top < m)
             break;
         n = top / m;
         b = top % m;
-        const int64_t t = m;
+        const I t = m;
         m = a;
         a = t;
     }
@@ -192,23 +202,34 @@ __device__ __forceinline__ int blocks_upto(const SeqItems &q, int last)
     return max(1, (q.edge + last + Cfg::BKV) / Cfg::BKV);
 }
 
-// Blocks of the first `tiles` tiles together.
+// Units (`quantum` blocks, the last of a tile maybe fewer) of the tile whose last token is `last`.
 template <class Cfg>
-__device__ inline int64_t blocks_of_tiles(const SeqItems &q, int step, int tiles)
+__device__ __forceinline__ int units_upto(const SeqItems &q, int quantum, int last)
 {
-    if (q.fixed >= 0)
-        return static_cast<int64_t>(tiles) * q.fixed;
-    int64_t sum = 0;
-    int whole = tiles;                            // tiles whose last token is not cut by the sequence's end
-    if (tiles > 0 && tiles * static_cast<int64_t>(step) > q.n) {
-        sum += blocks_upto<Cfg>(q, q.n - 1);
-        --whole;
+    return (blocks_upto<Cfg>(q, last) + quantum - 1) / quantum;
+}
+
+// Units of all tiles of one key head.
+template <class Cfg>
+__device__ inline int64_t units_of_head(const SeqItems &q, int quantum, int step)
+{
+    if (q.tiles == 0)
+        return 0;
+    const int last = units_upto<Cfg>(q, quantum, q.n - 1);
+    if (q.fixed >= 0 || q.tiles == 1)
+        return static_cast<int64_t>(q.tiles) * last;
+    // the tiles before the last: tile t sees the edge + (t + 1) step first keys; one unit up to
+    // `keys`, then the ceiling of their quotient
+    const int whole = q.tiles - 1, keys = Cfg::BKV * quantum;
+    const int ones = min(whole, max(0, (keys - q.edge) / step));
+    int64_t sum = last + ones;
+    if (whole > ones) {
+        const int64_t b = static_cast<int64_t>(q.edge) + static_cast<int64_t>(ones + 1) * step + keys - 1;
+        if (static_cast<int64_t>(whole) * (last + 1) < (1 << 22))   // (then nothing leaves 32 bits: last * keys < 2^31)
+            sum += floor_sum<uint32_t>(whole - ones, keys, step, static_cast<uint32_t>(b));
+        else
+            sum += floor_sum<int64_t>(whole - ones, keys, step, b);
     }
-    // tile t < whole: last token (t + 1) step - 1; one block while edge + (t + 1) step <= BKV
-    const int ones = min(whole, max(0, (Cfg::BKV - q.edge) / step));
-    sum += ones;
-    if (whole > ones)
-        sum += floor_sum(whole - ones, Cfg::BKV, step, static_cast<int64_t>(q.edge) + static_cast<int64_t>(ones + 1) * step + Cfg::BKV - 1);
     return sum;
 }
 
@@ -216,7 +237,7 @@ __device__ inline int64_t blocks_of_tiles(const SeqItems &q, int step, int tiles
 struct Walk {
     int s;            // sequence (KEYS_PREFIX: 0)
     SeqItems q;
-    int head, tile, block;
+    int head, tile, unit, quantum;
     int64_t left;     // units left in the range
 };
 
@@ -225,6 +246,7 @@ struct Segment {
     int s, head, tok0, toks;   // tokens [tok0, tok0 + toks) of the flat dimension
     int q0, n, kv, edge;       // of the sequence
     int b0, b1, blocks;
+    int units;                 // of the item
     int64_t left;              // units left in the range, this stretch included
 };
 
@@ -255,15 +277,17 @@ __device__ __forceinline__ bool next_segment(const PagedParams &p, Walk &w, Segm
     g.kv = w.q.kv;
     g.edge = w.q.edge;
     g.blocks = blocks_upto<Cfg>(w.q, first + toks - 1);
-    g.b0 = w.block;
-    g.b1 = static_cast<int>(min(static_cast<int64_t>(g.blocks), w.block + w.left));
+    g.units = (g.blocks + w.quantum - 1) / w.quantum;
+    const int u1 = static_cast<int>(min(static_cast<int64_t>(g.units), w.unit + w.left));
+    g.b0 = w.unit * w.quantum;
+    g.b1 = min(g.blocks, u1 * w.quantum);
     g.left = w.left;
-    w.left -= g.b1 - g.b0;
-    if (g.b1 == g.blocks) {
+    w.left -= u1 - w.unit;
+    if (u1 == g.units) {
         ++w.tile;
-        w.block = 0;
+        w.unit = 0;
     } else {
-        w.block = g.b1;   // the range ends here
+        w.unit = u1;   // the range ends here
     }
     return true;
 }
@@ -310,13 +334,34 @@ __device__ __forceinline__ void tmem_chunks(uint32_t addr, uint32_t (&va)[32], u
     }
 }
 
+// Every lane of the warp has 128 bytes (8 pieces) for its address `row` (16-byte aligned; nullptr:
+// none): they go through the warp's 4 KB at `stage`, so that 8 lanes write one row's 128 bytes
+// (piece k of row r at k ^ (r mod 8): no bank conflicts either way). Stored a row per lane, each
+// store instruction touches 32 lines, 16 bytes in each.
+__device__ __forceinline__ void store_rows(uint32_t stage, int lane, const uint4 (&piece)[8], char *row)
+{
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        st_shared_v4(stage + static_cast<uint32_t>(lane) * 128u + static_cast<uint32_t>(k ^ (lane & 7)) * 16u, piece[k]);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = 4 * i + lane / 8, k = lane & 7;
+        const float4 v = ld_shared_f4(stage + static_cast<uint32_t>(r) * 128u + static_cast<uint32_t>(k ^ (r & 7)) * 16u);
+        char *dst = reinterpret_cast<char *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row), r));
+        if (dst)
+            *reinterpret_cast<float4 *>(dst + 16 * k) = v;
+    }
+    __syncwarp();
+}
+
 struct PagedBars {
     uint32_t q_full, q_empty, drain, full0, empty0, s_full, pv_done, p_half0, p_full0;
 };
 
 template <class Cfg>
 __device__ __forceinline__ void paged_softmax_warp(const PagedParams &p, const PagedBars &bar, const WaitCtl &wc, uint32_t tmem,
-                                                   uint32_t ring, Walk walk, const Shares &shares, int tile, int warp, int lane)
+                                                   uint32_t ring, uint32_t stage, Walk walk, const Shares &shares, int tile, int warp, int lane)
 {
     using T = typename Cfg::Type;
     constexpr int D = Cfg::D, BKV = Cfg::BKV, CH = BKV / 32;
@@ -505,12 +550,18 @@ __device__ __forceinline__ void paged_softmax_warp(const PagedParams &p, const P
         // ---- the stretch's result
         const bool starts = g.b0 == 0, ends = g.b1 == g.blocks;
         const bool whole = starts && ends;
-        if (starts && tile == 0 && quarter == 0) {
-            const int64_t u0 = shares.begin(blockIdx.x + 1) - g.left;
-            const int parts = shares.owner(u0 + g.blocks - 1) - static_cast<int>(blockIdx.x) + 1;
-            for (int t = lane; t < g.toks; t += 32)
-                p.info[static_cast<int64_t>(g.tok0 + t) * p.kv_heads + g.head] =
-                    make_int4(static_cast<int>(blockIdx.x), parts, g.tok0, p.launch);
+        if (starts && tile == 0 && quarter == 0 && (!ends || p.keys != KEYS_ALL)) {
+            int parts = 1;
+            if (!ends)   // (its last range holds its last unit)
+                parts = shares.owner(shares.begin(blockIdx.x + 1) - g.left + g.units - 1) - static_cast<int>(blockIdx.x) + 1;
+            if (p.keys == KEYS_ALL) {
+                if (lane == 0)
+                    p.cuts[blockIdx.x] = make_int4(g.tok0, g.toks, g.head, parts);
+            } else {
+                for (int t = lane; t < g.toks; t += 32)
+                    p.info[static_cast<int64_t>(g.tok0 + t) * p.kv_heads + g.head] =
+                        make_int4(static_cast<int>(blockIdx.x), parts, g.tok0, p.launch);
+            }
         }
         if (!active)
             continue;
@@ -524,19 +575,22 @@ __device__ __forceinline__ void paged_softmax_warp(const PagedParams &p, const P
         if (whole && p.keys == KEYS_ALL) {
             const float inv = 1.0f / l;
             T *dst = static_cast<T *>(p.out) + token * p.out_token + head * p.out_head;
+            uint4 piece[8];   // 64 columns
             tmem_chunks<D / 32>(o_addr, va, vb, [&](const uint32_t(&x)[32], int c) {
-                if (row_ok) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t w[4];
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t w[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float a = __uint_as_float(x[8 * i + 2 * e]), bb = __uint_as_float(x[8 * i + 2 * e + 1]);
-                            w[e] = l == 0.0f ? 0u : pack2<T>(a * inv, bb * inv);
-                        }
-                        *reinterpret_cast<uint4 *>(dst + 32 * c + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+                    for (int e = 0; e < 4; ++e) {
+                        const float a = __uint_as_float(x[8 * i + 2 * e]), bb = __uint_as_float(x[8 * i + 2 * e + 1]);
+                        w[e] = l == 0.0f ? 0u : pack2<T>(a * inv, bb * inv);
                     }
+                    piece[4 * (c & 1) + i] = make_uint4(w[0], w[1], w[2], w[3]);
+                    if (Cfg::NT == 1 && row_ok)
+                        *reinterpret_cast<uint4 *>(dst + 32 * c + 8 * i) = piece[4 * (c & 1) + i];
                 }
+                if (Cfg::NT == 2 && (c & 1))
+                    store_rows(stage, lane, piece, row_ok ? reinterpret_cast<char *>(dst + 32 * (c - 1)) : nullptr);
             });
             if (row_ok && p.lse)
                 p.lse[token * p.lse_token + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
@@ -555,11 +609,15 @@ __device__ __forceinline__ void paged_softmax_warp(const PagedParams &p, const P
         }
         if (any_block) {
             tmem_chunks<D / 32>(o_addr, va, vb, [&](const uint32_t(&x)[32], int c) {
-                if (row_ok) {
+                uint4 piece[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        *reinterpret_cast<uint4 *>(dst + 32 * c + 4 * i) = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                for (int i = 0; i < 8; ++i) {
+                    piece[i] = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                    if (Cfg::NT == 1 && row_ok)
+                        *reinterpret_cast<uint4 *>(dst + 32 * c + 4 * i) = piece[i];
                 }
+                if (Cfg::NT == 2)
+                    store_rows(stage, lane, piece, row_ok ? reinterpret_cast<char *>(dst + 32 * c) : nullptr);
             });
         }
         if (row_ok)
@@ -627,78 +685,106 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, Cfg::CTAS_PER_SM)
     // ---- this CTA's share of the units
     const int step = NT * p.tile_tokens;
     const int seqs = p.keys == KEYS_PREFIX ? 1 : p.batch.num_seqs;
-    auto units_of = [&](int s) -> int64_t {
+    // sum over the CTA's threads (block_sum, too), and over the threads before this one
+    int64_t block_sum = 0;
+    auto block_scan = [&](int64_t value, int64_t &ahead) -> int64_t {
+        int64_t scan = value;
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+            const int64_t v = __shfl_up_sync(0xffffffffu, scan, o);
+            scan += lane >= o ? v : 0;
+        }
+        if (lane == 31)
+            warp_sum[warp] = scan;
+        __syncthreads();
+        block_sum = 0;
+        ahead = scan - value;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) {
+            ahead += w < warp ? warp_sum[w] : 0;
+            block_sum += warp_sum[w];
+        }
+        __syncthreads();   // warp_sum may be written again
+        return block_sum;
+    };
+    auto units_of = [&](int s, int quantum) -> int64_t {
         if (s >= seqs)
             return 0;
         const SeqItems q = seq_items<Cfg>(p, s);
         if (q.bad)
             atomicCAS(p.err, 0u, static_cast<uint32_t>(ERR_BATCH_INDEX));
-        return p.kv_heads * blocks_of_tiles<Cfg>(q, step, q.tiles);
+        return p.kv_heads * units_of_head<Cfg>(q, quantum, step);
     };
-    int64_t mine = 0;
-    for (int s = threadIdx.x; s < seqs; s += Cfg::NUM_THREADS)
-        mine += units_of(s);
-#pragma unroll
-    for (int o = 16; o > 0; o /= 2)
-        mine += __shfl_xor_sync(0xffffffffu, mine, o);
-    if (lane == 0)
-        warp_sum[warp] = mine;
+    // units of the first chunk's sequence of this thread, those before it, and the sum over all
+    int64_t own = 0, from = 0;
+    auto add_up = [&](int quantum) -> int64_t {
+        own = units_of(threadIdx.x, quantum);
+        const int64_t first = block_scan(own, from);
+        if (seqs <= Cfg::NUM_THREADS)
+            return first;
+        int64_t mine = 0, ahead;
+        for (int s = threadIdx.x + Cfg::NUM_THREADS; s < seqs; s += Cfg::NUM_THREADS)
+            mine += units_of(s, quantum);
+        const int64_t total = first + block_scan(mine, ahead);
+        block_sum = first;
+        return total;
+    };
     tc_fence_before_sync();
-    __syncthreads();
+    Shares shares;
+    int quantum = 1;
+    shares.total = add_up(1);
+    if (NT == 2 && shares.total < static_cast<int64_t>(kPagedCoarse) * gridDim.x) {
+        quantum = kPagedQuantum;
+        shares.total = add_up(quantum);
+    }
     tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
     grid_dependents_launch();
-    Shares shares;
-    shares.total = 0;
-    for (int w = 0; w < WARPS; ++w)
-        shares.total += warp_sum[w];
     shares.ctas = static_cast<int>(min(static_cast<int64_t>(gridDim.x), shares.total));
     const bool works = static_cast<int>(blockIdx.x) < shares.ctas;
+    if (threadIdx.x == 0 && p.keys == KEYS_ALL)
+        p.cuts[blockIdx.x] = make_int4(0, 0, 0, 0);   // written again (after a barrier) if an item goes on
     if (works) {   // (the same answer in every thread)
-        const int64_t u0 = shares.begin(blockIdx.x), u1 = shares.begin(blockIdx.x + 1);
+        const int64_t u0 = shares.begin(blockIdx.x);
         int64_t before = 0;   // units of the sequences before this chunk
-        for (int s0 = 0; s0 < seqs && before <= u0; s0 += Cfg::NUM_THREADS) {
+        for (int s0 = 0;; s0 += Cfg::NUM_THREADS) {
             const int s = s0 + static_cast<int>(threadIdx.x);
-            const int64_t own = units_of(s);
-            int64_t scan = own;
-#pragma unroll
-            for (int o = 1; o < 32; o *= 2) {
-                const int64_t v = __shfl_up_sync(0xffffffffu, scan, o);
-                scan += lane >= o ? v : 0;
-            }
-            __syncthreads();   // warp_sum was read
-            if (lane == 31)
-                warp_sum[warp] = scan;
-            __syncthreads();
-            int64_t ahead = before;
-            for (int w = 0; w < WARPS; ++w) {
-                if (w < warp)
-                    ahead += warp_sum[w];
-                before += warp_sum[w];
-            }
-            const int64_t from = ahead + scan - own;
-            if (own > 0 && from <= u0 && u0 < from + own) {   // one thread: unit u0 is in its sequence
-                Walk w;
-                w.s = s;
-                w.q = seq_items<Cfg>(p, s);
+            if (own > 0 && before + from <= u0 && u0 < before + from + own) {   // one thread: unit u0 is in its sequence
+                const int64_t at = u0 - before - from;
+                start.s = s;
+                start.q = seq_items<Cfg>(p, s);
                 const int64_t per_head = own / p.kv_heads;
-                w.head = static_cast<int>((u0 - from) / per_head);
-                const int64_t at = (u0 - from) - w.head * per_head;
-                int lo = 0, hi = w.q.tiles;   // blocks of the first lo tiles <= at
-                while (hi - lo > 1) {
-                    const int mid = (lo + hi) / 2;
-                    if (blocks_of_tiles<Cfg>(w.q, step, mid) <= at)
-                        lo = mid;
-                    else
-                        hi = mid;
-                }
-                w.tile = lo;
-                w.block = static_cast<int>(at - blocks_of_tiles<Cfg>(w.q, step, lo));
-                w.left = u1 - u0;
-                start = w;
+                start.head = static_cast<int>(at / per_head);
+                start.tile = 0;
+                start.unit = static_cast<int>(at - start.head * per_head);   // of the head, for now
+                start.quantum = quantum;
+                start.left = shares.begin(blockIdx.x + 1) - u0;
             }
+            before += block_sum;
+            if (s0 + Cfg::NUM_THREADS >= seqs || before > u0)
+                break;
+            own = units_of(s + Cfg::NUM_THREADS, quantum);
+            block_scan(own, from);
         }
         __syncthreads();
+        // the tile that holds it: the units of the tiles, added up by all threads
+        Walk w = start;
+        if (w.q.tiles > 1) {
+            int64_t done = 0;
+            const int64_t at = w.unit;
+            for (int t0 = 0; t0 < w.q.tiles && done <= at; t0 += Cfg::NUM_THREADS) {
+                const int t = t0 + static_cast<int>(threadIdx.x);
+                const int units = t < w.q.tiles ? units_upto<Cfg>(w.q, quantum, min((t + 1) * step, w.q.n) - 1) : 0;
+                int64_t first;
+                const int64_t all = block_scan(units, first);
+                if (units > 0 && done + first <= at && at < done + first + units) {
+                    start.tile = t;
+                    start.unit = static_cast<int>(at - done - first);
+                }
+                done += all;
+            }
+            __syncthreads();
+        }
     }
     Walk walk = {};
     if (works)
@@ -974,7 +1060,8 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, Cfg::CTAS_PER_SM)
         __syncwarp();
     } else {
         // ---------------------------------------------------------------- softmax
-        paged_softmax_warp<Cfg>(p, bar, wc, tmem, ring, walk, shares, (warp - 2) >> 2, warp, lane);
+        paged_softmax_warp<Cfg>(p, bar, wc, tmem, ring, base + Cfg::STAGE_OFF + static_cast<uint32_t>(warp - 2) * Cfg::STAGE_WARP, walk,
+                                shares, (warp - 2) >> 2, warp, lane);
     }
 
     tc_fence_before_sync();
@@ -990,11 +1077,14 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, Cfg::CTAS_PER_SM)
 struct CombineParams {
     int num_tokens, kv_heads, group, num_seqs;
     const int *q_start;
+    int launches;
     PartsView parts[3];
-    int ctas[3];                 // grid sizes of the launches
-    int tile_tokens;
-    const PartInfo *own, *prefix;   // prefix: nullptr when all keys were one launch's
-    const float *row_o[2];       // whole items of the own (0) and prefix (1) keys
+    int ctas[3];                    // grid sizes of the launches
+    int tile_tokens[3];
+    const PartInfo *cuts[3];        // of the CTAs, or (joint) of the tokens:
+    int64_t blocks[3];              // combine blocks of each launch: CTAs x blocks per item
+    const PartInfo *own, *prefix;   // [num_tokens][kv_heads]
+    const float *row_o[2];          // whole items of the own (0) and prefix (1) keys
     const float2 *row_ml[2];
     void *out;
     int64_t out_token, out_head;
@@ -1002,97 +1092,212 @@ struct CombineParams {
     int64_t lse_token;
 };
 
-// One warp per token and head: out = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i over its parts,
-// in the order of the keys (the same bits whichever CTA was first). Lane i of a step of 32 holds
-// part i's (m, l); every lane then adds up its D / 32 dimensions.
-template <typename T, int D>
-__global__ void __launch_bounds__(256) paged_combine_kernel(const CombineParams p)
-{
-    constexpr int V = D / 32;
-    grid_dependency_wait();
-    grid_dependents_launch();
-    const int lane = threadIdx.x & 31;
-    const int heads = p.kv_heads * p.group;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    if (row >= static_cast<int64_t>(p.num_tokens) * heads)
-        return;
-    const int token = static_cast<int>(row / heads), head = static_cast<int>(row - static_cast<int64_t>(token) * heads);
-    if (token < __ldg(p.q_start) || token >= __ldg(p.q_start + p.num_seqs))
-        return;   // of no sequence: nothing was written for it
-    const int kv_head = head / p.group, g = head - kv_head * p.group;
-    const bool joint = p.prefix != nullptr;
+constexpr int kCombineWarps = 8;    // per block
+constexpr int kCombineRows = 32;    // rows of an item per block
+constexpr int kCombineFew = 4;      // parts up to which a warp joins four rows at once
+
+// A row's running sum over parts: lane's D / 32 dimensions.
+template <int V>
+struct RowSum {
     float m = -INFINITY, l = 0.0f;
     float acc[V] = {};
-    for (int side = joint ? 1 : 0; side >= 0; --side) {
-        const PartInfo info = (side == 1 ? p.prefix : p.own)[static_cast<int64_t>(token) * p.kv_heads + kv_head];
-        // (a token of an unsorted q_start may have no entry: what is not a possible one is left out)
-        if (info.w < 0 || info.w > 2 || info.y < 1 || info.x < 0 || info.y > p.ctas[info.w] - info.x)
-            continue;
-        if (!joint && info.y == 1)
-            return;   // finished by its CTA
-        const PartsView &parts = p.parts[info.w];
-        const int at = token - info.z;
-        if (at < 0 || at >= parts.tiles * p.tile_tokens)
-            continue;
-        const int tile = at / p.tile_tokens, r = (at - tile * p.tile_tokens) * p.group + g;
-        auto part_row = [&](int i) -> int64_t {   // the first part is its CTA's last stretch, the others their CTAs' first
-            return (static_cast<int64_t>(2 * (info.x + i) + (i == 0 ? 1 : 0)) * parts.tiles + tile) * parts.rows + r;
-        };
-        for (int i0 = 0; i0 < info.y; i0 += 32) {
-            const int n = min(32, info.y - i0);
-            float2 ml = make_float2(-INFINITY, 0.0f);
-            if (lane < n)
-                ml = info.y == 1 ? p.row_ml[side][row] : parts.ml[part_row(i0 + lane)];
+
+    // Adds n parts, in order: lane i of a step of 32 fetches (m, l) of part i, then all lanes add up
+    // their dimensions, eight parts' loads at a time. part(i): the row of part i in `ml` and `o`.
+    template <class Row>
+    __device__ __forceinline__ void add(const float *__restrict__ o, const float2 *__restrict__ ml_of, int n, int lane, Row &&part)
+    {
+        for (int i0 = 0; i0 < n; i0 += 32) {
+            const int k = min(32, n - i0);
+            const float2 ml = lane < k ? ml_of[part(i0 + lane)] : make_float2(-INFINITY, 0.0f);
             float top = ml.x;
 #pragma unroll
-            for (int o = 16; o > 0; o /= 2)
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            for (int s = 16; s > 0; s /= 2)
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
             const float m_new = fmaxf(m, top);
             const float keep = m == -INFINITY ? 0.0f : exp2f(m - m_new);
-            float w = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - m_new);
-            if (ml.y != ml.y)
-                w = ml.y;   // NaN stays NaN
-            float sum = ml.y == 0.0f ? 0.0f : w * ml.y;
+            const bool none = ml.y == 0.0f;   // a part without a key: its O may not be written
+            const float w = none ? 0.0f : ml.y != ml.y ? ml.y : exp2f(ml.x - m_new);   // (NaN stays NaN)
+            float sum = none ? 0.0f : w * ml.y;
 #pragma unroll
-            for (int o = 16; o > 0; o /= 2)
-                sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            for (int s = 16; s > 0; s /= 2)
+                sum += __shfl_xor_sync(0xffffffffu, sum, s);
             l = l * keep + sum;
             m = m_new;
 #pragma unroll
             for (int e = 0; e < V; ++e)
                 acc[e] *= keep;
-            const bool none = ml.y == 0.0f;   // a part without a key: its O may not be written
-            for (int i = 0; i < n; ++i) {
-                const float wi = __shfl_sync(0xffffffffu, w, i);
-                if (__shfl_sync(0xffffffffu, none, i))
-                    continue;
-                const float *o = (info.y == 1 ? p.row_o[side] + row * D : parts.o + part_row(i0 + i) * D) + lane * V;
-                if constexpr (V == 4) {
-                    const float4 x = *reinterpret_cast<const float4 *>(o);
-                    acc[0] = fmaf(wi, x.x, acc[0]);
-                    acc[1] = fmaf(wi, x.y, acc[1]);
-                    acc[2] = fmaf(wi, x.z, acc[2]);
-                    acc[3] = fmaf(wi, x.w, acc[3]);
-                } else {
-                    const float2 x = *reinterpret_cast<const float2 *>(o);
-                    acc[0] = fmaf(wi, x.x, acc[0]);
-                    acc[1] = fmaf(wi, x.y, acc[1]);
+            const uint32_t some = __ballot_sync(0xffffffffu, !none);
+            for (int j0 = 0; j0 < k; j0 += 8) {
+                float x[8][V];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {   // (past the end: the last part again, with weight 0)
+                    const float *src = o + part(i0 + min(j0 + j, k - 1)) * (32 * V) + lane * V;
+                    if constexpr (V == 4)
+                        *reinterpret_cast<float4 *>(x[j]) = *reinterpret_cast<const float4 *>(src);
+                    else
+                        *reinterpret_cast<float2 *>(x[j]) = *reinterpret_cast<const float2 *>(src);
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const bool on = j0 + j < k && (some >> (j0 + j) & 1u);
+                    const float wj = __shfl_sync(0xffffffffu, w, (j0 + j) & 31);
+#pragma unroll
+                    for (int e = 0; e < V; ++e)
+                        acc[e] = on ? fmaf(wj, x[j][e], acc[e]) : acc[e];
                 }
             }
         }
     }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    T *dst = static_cast<T *>(p.out) + token * p.out_token + head * p.out_head + lane * V;
-    uint32_t w[V / 2];
+
+    template <typename T>
+    __device__ __forceinline__ void write(const CombineParams &p, int64_t token, int head, int lane) const
+    {
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        T *dst = static_cast<T *>(p.out) + token * p.out_token + head * p.out_head + lane * V;
+        uint32_t w[V / 2];
 #pragma unroll
-    for (int e = 0; e < V / 2; ++e)
-        w[e] = pack2<T>(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-    if constexpr (V == 4)
-        *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
-    else
-        *reinterpret_cast<uint32_t *>(dst) = w[0];
-    if (p.lse && lane == 0)
+        for (int e = 0; e < V / 2; ++e)
+            w[e] = pack2<T>(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+        if constexpr (V == 4)
+            *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
+        else
+            *reinterpret_cast<uint32_t *>(dst) = w[0];
+        if (p.lse && lane == 0)
+            p.lse[token * p.lse_token + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+    }
+};
+
+// Joins n <= kCombineFew parts of four rows, eight lanes each (`sub`: lane of the eight), all loads
+// at once: item rows cut in two or three, of which there are many, are bound by latency otherwise.
+template <typename T, int D, class Row>
+__device__ __forceinline__ void combine_few(const CombineParams &p, const PartsView &v, int n, int lane, bool on, int64_t token,
+                                            int head, Row &&part)
+{
+    constexpr int V = D / 32;   // 16-byte vectors of a lane: sub, sub + 8, ...
+    const int sub = lane & 7;
+    float4 x[kCombineFew][V];
+    float2 ml[kCombineFew];
+#pragma unroll
+    for (int i = 0; i < kCombineFew; ++i) {
+        ml[i] = make_float2(-INFINITY, 0.0f);
+        if (on && i < n) {
+            const int64_t row = part(i);
+            ml[i] = v.ml[row];
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                x[i][e] = *reinterpret_cast<const float4 *>(v.o + row * D + 4 * (sub + 8 * e));
+        }
+    }
+    if (!on)
+        return;
+    float m = ml[0].x, l = 0.0f;
+#pragma unroll
+    for (int i = 1; i < kCombineFew; ++i)
+        m = fmaxf(m, ml[i].x);
+    float4 acc[V] = {};
+#pragma unroll
+    for (int i = 0; i < kCombineFew; ++i) {
+        if (ml[i].y == 0.0f)
+            continue;   // a part without a key: its O may not be written
+        const float w = ml[i].y != ml[i].y ? ml[i].y : exp2f(ml[i].x - m);   // (NaN stays NaN)
+        l += w * ml[i].y;
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            acc[e].x = fmaf(w, x[i][e].x, acc[e].x);
+            acc[e].y = fmaf(w, x[i][e].y, acc[e].y);
+            acc[e].z = fmaf(w, x[i][e].z, acc[e].z);
+            acc[e].w = fmaf(w, x[i][e].w, acc[e].w);
+        }
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    T *dst = static_cast<T *>(p.out) + token * p.out_token + head * p.out_head;
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+        *reinterpret_cast<uint2 *>(dst + 4 * (sub + 8 * e)) =
+            make_uint2(pack2<T>(acc[e].x * inv, acc[e].y * inv), pack2<T>(acc[e].z * inv, acc[e].w * inv));
+    if (p.lse && sub == 0)
         p.lse[token * p.lse_token + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+}
+
+// out = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i over an item's parts, in the order of the keys
+// (the same bits whichever CTA was first). JOINT = false: the items that CTAs left open (everything
+// else is written already), kCombineRows rows per block. JOINT = true: every token and head, its
+// prefix parts before its own, a warp each.
+template <typename T, int D, bool JOINT>
+__global__ void __launch_bounds__(32 * kCombineWarps) paged_combine_kernel(const CombineParams p)
+{
+    constexpr int V = D / 32;
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    // row of the first part (its CTA's part 1) and of the others (their CTAs' part 0)
+    auto part_row = [&](const PartsView &v, int cta, int i, int tile, int r) -> int64_t {
+        return (static_cast<int64_t>(2 * (cta + i) + (i == 0 ? 1 : 0)) * v.tiles + tile) * v.rows + r;
+    };
+    if constexpr (!JOINT) {
+        int64_t at = blockIdx.x;
+        int i = 0;
+        while (i + 1 < p.launches && at >= p.blocks[i])
+            at -= p.blocks[i++];
+        const PartsView &v = p.parts[i];
+        const int cta = static_cast<int>(at % p.ctas[i]), chunk = static_cast<int>(at / p.ctas[i]);
+        const int4 cut = p.cuts[i][cta];
+        if (cut.w < 1 || cut.w > p.ctas[i] - cta)
+            return;
+        const int tt = p.tile_tokens[i];
+        // where an item's row is, and whether it has a token
+        auto place = [&](int row, int &tile, int &r, int &tok, int &g) -> bool {
+            tile = row / v.rows;
+            r = row - tile * v.rows;
+            tok = r / p.group;
+            g = r - tok * p.group;
+            const bool ok = tile < v.tiles && tok < tt && tile * tt + tok < cut.y;
+            tok += tile * tt;
+            return ok;
+        };
+        int tile, r, tok, g;
+        if (cut.w <= kCombineFew) {
+            const bool on = place(chunk * kCombineRows + 4 * warp + lane / 8, tile, r, tok, g);
+            combine_few<T, D>(p, v, cut.w, lane, on, cut.x + tok, cut.z * p.group + g,
+                              [&](int k) { return part_row(v, cta, k, tile, r); });
+            return;
+        }
+        for (int row = chunk * kCombineRows + warp; row < (chunk + 1) * kCombineRows; row += kCombineWarps) {
+            if (!place(row, tile, r, tok, g))
+                continue;
+            RowSum<V> sum;
+            sum.add(v.o, v.ml, cut.w, lane, [&](int k) { return part_row(v, cta, k, tile, r); });
+            sum.template write<T>(p, cut.x + tok, cut.z * p.group + g, lane);
+        }
+    } else {
+        RowSum<V> sum;
+        const int heads = p.kv_heads * p.group;
+        const int64_t row = static_cast<int64_t>(blockIdx.x) * kCombineWarps + warp;
+        const int64_t token = row / heads;
+        const int head = static_cast<int>(row - token * heads);
+        if (token >= p.num_tokens || token < __ldg(p.q_start) || token >= __ldg(p.q_start + p.num_seqs))
+            return;   // of no sequence: nothing was written for it
+        const int kv_head = head / p.group, g = head - kv_head * p.group;
+#pragma unroll
+        for (int side = 1; side >= 0; --side) {
+            const int4 info = (side == 1 ? p.prefix : p.own)[token * p.kv_heads + kv_head];
+            // (a token of an unsorted q_start may have no entry: what is not a possible one is left out)
+            if (info.w < 0 || info.w >= p.launches || info.y < 1 || info.x < 0 || info.y > p.ctas[info.w] - info.x)
+                continue;
+            if (info.y == 1) {
+                sum.add(p.row_o[side], p.row_ml[side], 1, lane, [&](int) { return row; });
+                continue;
+            }
+            const PartsView &v = p.parts[info.w];
+            const int tt = p.tile_tokens[info.w], at = static_cast<int>(token - info.z);
+            if (at < 0 || at >= v.tiles * tt)
+                continue;
+            const int tile = at / tt, r = (at - tile * tt) * p.group + g;
+            sum.add(v.o, v.ml, info.y, lane, [&](int k) { return part_row(v, info.x, k, tile, r); });
+        }
+        sum.template write<T>(p, token, head, lane);
+    }
 }
 
 }  // namespace gb300

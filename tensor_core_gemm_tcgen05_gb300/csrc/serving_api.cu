@@ -327,6 +327,7 @@ struct AttnLaunch {
     int keys = 0, seqs = 0;   // KEYS_*, SEQS_*
     int64_t grid = 0;
     int64_t o_off = 0, ml_off = 0;   // PartsView
+    int64_t cuts_off = 0;
 };
 
 struct AttnPlan {
@@ -383,9 +384,9 @@ AttnPlan attention_plan(const gemm_ctx *ctx, const gemm_kv_cache &c, const gemm_
         at += (bytes + 255) / 256 * 256;
         return off;
     };
-    const int64_t info = T * c.kv_heads * static_cast<int64_t>(sizeof(gb300::PartInfo));
-    pl.own_off = take(info);
     if (pl.joint) {
+        const int64_t info = T * c.kv_heads * static_cast<int64_t>(sizeof(gb300::PartInfo));
+        pl.own_off = take(info);
         pl.prefix_off = take(info);
         for (int i = 0; i < 2; ++i) {
             pl.row_o_off[i] = take(T * q_heads * c.head_dim * 4);
@@ -396,6 +397,7 @@ AttnPlan attention_plan(const gemm_ctx *ctx, const gemm_kv_cache &c, const gemm_
         const int64_t rows = 2 * pl.launch[i].grid * pl.launch[i].tiles * pl.rows;
         pl.launch[i].o_off = take(rows * c.head_dim * 4);
         pl.launch[i].ml_off = take(rows * 8);
+        pl.launch[i].cuts_off = take(pl.launch[i].grid * static_cast<int64_t>(sizeof(gb300::PartInfo)));
     }
     pl.bytes = at;
     return pl;
@@ -692,9 +694,9 @@ int gemm_paged_attention(gemm_ctx *ctx, const gemm_kv_cache *cache, const gemm_k
     cp.group = p.group;
     cp.num_seqs = p.batch.num_seqs;
     cp.q_start = batch->q_start;
-    cp.tile_tokens = pl.tile_tokens;
+    cp.launches = pl.count;
     cp.own = reinterpret_cast<gb300::PartInfo *>(ws + pl.own_off);
-    cp.prefix = pl.joint ? reinterpret_cast<gb300::PartInfo *>(ws + pl.prefix_off) : nullptr;
+    cp.prefix = reinterpret_cast<gb300::PartInfo *>(ws + pl.prefix_off);
     for (int i = 0; i < 2; ++i) {
         cp.row_o[i] = reinterpret_cast<float *>(ws + pl.row_o_off[i]);
         cp.row_ml[i] = reinterpret_cast<float2 *>(ws + pl.row_ml_off[i]);
@@ -707,6 +709,7 @@ int gemm_paged_attention(gemm_ctx *ctx, const gemm_kv_cache *cache, const gemm_k
 
     DeviceGuard guard(ctx->device);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    int64_t combine_grid = 0;
     for (int i = 0; i < pl.count; ++i) {
         const AttnLaunch &l = pl.launch[i];
         const bool prefix = l.keys == gb300::KEYS_PREFIX;
@@ -720,8 +723,13 @@ int gemm_paged_attention(gemm_ctx *ctx, const gemm_kv_cache *cache, const gemm_k
         p.info = reinterpret_cast<gb300::PartInfo *>(ws + (prefix ? pl.prefix_off : pl.own_off));
         p.row_o = reinterpret_cast<float *>(ws + pl.row_o_off[prefix]);
         p.row_ml = reinterpret_cast<float2 *>(ws + pl.row_ml_off[prefix]);
+        p.cuts = reinterpret_cast<gb300::PartInfo *>(ws + l.cuts_off);
         cp.parts[i] = p.parts;
         cp.ctas[i] = static_cast<int>(l.grid);
+        cp.tile_tokens[i] = p.tile_tokens;
+        cp.cuts[i] = p.cuts;
+        cp.blocks[i] = l.grid * ((l.tiles * pl.rows + gb300::kCombineRows - 1) / gb300::kCombineRows);
+        combine_grid += cp.blocks[i];
         const uint32_t rows = static_cast<uint32_t>(std::min<int64_t>(cache->page_size, l.tiles == 1 ? 64 : 128));
         const int64_t dims[4] = {d, cache->page_size, cache->kv_heads, cache->num_pages};
         const int64_t strides[3] = {cache->row_stride, cache->head_stride, cache->page_stride};
@@ -734,14 +742,16 @@ int gemm_paged_attention(gemm_ctx *ctx, const gemm_kv_cache *cache, const gemm_k
         if (e != cudaSuccess)
             return cuda_fail(ctx, e, GEMM_ERR_LAUNCH);
     }
-    const int64_t combine_grid = (tokens * q->heads + 7) / 8;
-    auto combine = [&](auto kernel) { return launch_serving(kernel, combine_grid, 256, 0, st, cp); };
-    cudaError_t e;
-    if (cache->dtype == GEMM_F16)
-        e = d == 64 ? combine(gb300::paged_combine_kernel<__half, 64>) : combine(gb300::paged_combine_kernel<__half, 128>);
-    else
-        e = d == 64 ? combine(gb300::paged_combine_kernel<__nv_bfloat16, 64>)
-                    : combine(gb300::paged_combine_kernel<__nv_bfloat16, 128>);
+    if (pl.joint)
+        combine_grid = (tokens * q->heads + gb300::kCombineWarps - 1) / gb300::kCombineWarps;
+    auto combine = [&](auto kernel) { return launch_serving(kernel, combine_grid, 32 * gb300::kCombineWarps, 0, st, cp); };
+    auto by_dim = [&](auto type) {
+        using T = decltype(type);
+        if (pl.joint)
+            return d == 64 ? combine(gb300::paged_combine_kernel<T, 64, true>) : combine(gb300::paged_combine_kernel<T, 128, true>);
+        return d == 64 ? combine(gb300::paged_combine_kernel<T, 64, false>) : combine(gb300::paged_combine_kernel<T, 128, false>);
+    };
+    const cudaError_t e = cache->dtype == GEMM_F16 ? by_dim(__half{}) : by_dim(__nv_bfloat16{});
     return e == cudaSuccess ? GEMM_OK : cuda_fail(ctx, e, GEMM_ERR_LAUNCH);
 }
 
