@@ -63,7 +63,9 @@ struct PagedParams {
     BatchView batch;
     const int *prefix_pages;
     int n_prefix_pages;
-    int kv_heads, group, tile_tokens;   // G and 128 / G
+    int kv_heads, group;                // G: query heads per key head
+    int tile_tokens, long_tokens;       // tokens per tile of this launch; what a full tile takes, 128 / G
+    int q_rows, q_bufs;                 // NT = 1: rows of a query buffer (whole groups of 8), buffers
     int keys, seqs;                     // KEYS_*, SEQS_*
     int launch;                         // index for the tokens' PartInfo
     float scale_log2;                   // scale * log2(e)
@@ -98,9 +100,12 @@ struct PagedConfig {
     // NT = 2: 32 rows x 128 bytes for each softmax warp, through which results are written
     static constexpr int STAGE_WARP = 32 * 128, STAGE_OFF = RING_OFF + STAGES * KV_TILE;
     static constexpr int BAR_OFF = STAGE_OFF + (NT == 2 ? 8 * STAGE_WARP : 0);
-    // q_full, q_empty, drain, full[], empty[], s_full and pv_done (NT = 2: of the first tile),
+    // q_full[], q_empty[], drain, full[], empty[], s_full and pv_done (NT = 2: of the first tile),
     // then NT = 1: p_full[block mod 2]; NT = 2: p_half[tile], p_full[tile]
-    static constexpr int NUM_BARS = 3 + 2 * STAGES + 2 + 2 * NT;
+    static constexpr int Q_BUFS = NT == 1 ? 4 : 1;   // at most
+    static constexpr int NUM_BARS = 2 * Q_BUFS + 1 + 2 * STAGES + 2 + 2 * NT;
+    // what beginning and ending an item costs, in blocks
+    static constexpr int ITEM_COST = NT == 1 ? 2 : 2;
     static constexpr int SMEM_BYTES = 1024 + BAR_OFF + NUM_BARS * 8 + 16;
     static constexpr int NUM_THREADS = 64 + NT * 128;
     static constexpr int CTAS_PER_SM = NT == 1 ? 2 : 1;
@@ -188,7 +193,7 @@ __device__ __forceinline__ SeqItems seq_items(const PagedParams &p, int s)
     q.fixed = -1;
     q.edge = (p.keys == KEYS_ALL ? p.batch.prefix_len : 0) + v.kv - v.n;
     q.bad = v.bad;
-    const bool mine = p.seqs == SEQS_ALL || (v.n > p.tile_tokens) == (p.seqs == SEQS_LONG);
+    const bool mine = p.seqs == SEQS_ALL || (v.n > p.long_tokens) == (p.seqs == SEQS_LONG);
     q.tiles = mine ? (v.n + step - 1) / step : 0;
     return q;
 }
@@ -202,11 +207,20 @@ __device__ __forceinline__ int blocks_upto(const SeqItems &q, int last)
     return max(1, (q.edge + last + Cfg::BKV) / Cfg::BKV);
 }
 
-// Units (`quantum` blocks, the last of a tile maybe fewer) of the tile whose last token is `last`.
+// Units of the tile whose last token is `last`: its blocks and, ahead of them, what beginning an
+// item costs (ITEM_COST blocks' time), in steps of `quantum` (the last maybe fewer). A range that
+// ends within the cost leaves the whole item to the next.
 template <class Cfg>
 __device__ __forceinline__ int units_upto(const SeqItems &q, int quantum, int last)
 {
-    return (blocks_upto<Cfg>(q, last) + quantum - 1) / quantum;
+    return (blocks_upto<Cfg>(q, last) + Cfg::ITEM_COST + quantum - 1) / quantum;
+}
+
+// First block of an item's unit `u`.
+template <class Cfg>
+__device__ __forceinline__ int block_of(int u, int quantum, int blocks)
+{
+    return min(blocks, max(0, u * quantum - Cfg::ITEM_COST));
 }
 
 // Units of all tiles of one key head.
@@ -218,13 +232,12 @@ __device__ inline int64_t units_of_head(const SeqItems &q, int quantum, int step
     const int last = units_upto<Cfg>(q, quantum, q.n - 1);
     if (q.fixed >= 0 || q.tiles == 1)
         return static_cast<int64_t>(q.tiles) * last;
-    // the tiles before the last: tile t sees the edge + (t + 1) step first keys; one unit up to
-    // `keys`, then the ceiling of their quotient
+    // the tiles before the last: tile t sees the edge + (t + 1) step first keys, at least one block's
     const int whole = q.tiles - 1, keys = Cfg::BKV * quantum;
-    const int ones = min(whole, max(0, (keys - q.edge) / step));
-    int64_t sum = last + ones;
+    const int ones = min(whole, max(0, (Cfg::BKV - q.edge) / step));
+    int64_t sum = last + static_cast<int64_t>(ones) * ((1 + Cfg::ITEM_COST + quantum - 1) / quantum);
     if (whole > ones) {
-        const int64_t b = static_cast<int64_t>(q.edge) + static_cast<int64_t>(ones + 1) * step + keys - 1;
+        const int64_t b = static_cast<int64_t>(q.edge) + static_cast<int64_t>(ones + 1) * step + Cfg::ITEM_COST * Cfg::BKV + keys - 1;
         if (static_cast<int64_t>(whole) * (last + 1) < (1 << 22))   // (then nothing leaves 32 bits: last * keys < 2^31)
             sum += floor_sum<uint32_t>(whole - ones, keys, step, static_cast<uint32_t>(b));
         else
@@ -247,48 +260,50 @@ struct Segment {
     int q0, n, kv, edge;       // of the sequence
     int b0, b1, blocks;
     int units;                 // of the item
-    int64_t left;              // units left in the range, this stretch included
+    int64_t ahead;             // from the item's first unit to the end of the CTA's range
 };
 
 template <class Cfg>
 __device__ __forceinline__ bool next_segment(const PagedParams &p, Walk &w, Segment &g)
 {
-    if (w.left <= 0)
-        return false;
     const int step = Cfg::NT * p.tile_tokens;
-    while (w.tile >= w.q.tiles) {   // on to the next head or the next sequence with items (units are left)
-        if (w.q.tiles > 0 && w.head + 1 < p.kv_heads) {
-            ++w.head;
-        } else {
-            w.head = 0;
-            if (++w.s >= p.batch.num_seqs)
-                return false;
-            w.q = seq_items<Cfg>(p, w.s);
+    do {
+        if (w.left <= 0)
+            return false;
+        while (w.tile >= w.q.tiles) {   // on to the next head or the next sequence with items (units are left)
+            if (w.q.tiles > 0 && w.head + 1 < p.kv_heads) {
+                ++w.head;
+            } else {
+                w.head = 0;
+                if (++w.s >= p.batch.num_seqs)
+                    return false;
+                w.q = seq_items<Cfg>(p, w.s);
+            }
+            w.tile = 0;
         }
-        w.tile = 0;
-    }
-    const int first = w.tile * step, toks = min(step, w.q.n - first);
-    g.s = w.s;
-    g.head = w.head;
-    g.tok0 = w.q.q0 + first;
-    g.toks = toks;
-    g.q0 = w.q.q0;
-    g.n = w.q.n;
-    g.kv = w.q.kv;
-    g.edge = w.q.edge;
-    g.blocks = blocks_upto<Cfg>(w.q, first + toks - 1);
-    g.units = (g.blocks + w.quantum - 1) / w.quantum;
-    const int u1 = static_cast<int>(min(static_cast<int64_t>(g.units), w.unit + w.left));
-    g.b0 = w.unit * w.quantum;
-    g.b1 = min(g.blocks, u1 * w.quantum);
-    g.left = w.left;
-    w.left -= u1 - w.unit;
-    if (u1 == g.units) {
-        ++w.tile;
-        w.unit = 0;
-    } else {
-        w.unit = u1;   // the range ends here
-    }
+        const int first = w.tile * step, toks = min(step, w.q.n - first);
+        g.s = w.s;
+        g.head = w.head;
+        g.tok0 = w.q.q0 + first;
+        g.toks = toks;
+        g.q0 = w.q.q0;
+        g.n = w.q.n;
+        g.kv = w.q.kv;
+        g.edge = w.q.edge;
+        g.blocks = blocks_upto<Cfg>(w.q, first + toks - 1);
+        g.units = (g.blocks + Cfg::ITEM_COST + w.quantum - 1) / w.quantum;
+        const int u1 = static_cast<int>(min(static_cast<int64_t>(g.units), w.unit + w.left));
+        g.b0 = block_of<Cfg>(w.unit, w.quantum, g.blocks);
+        g.b1 = block_of<Cfg>(u1, w.quantum, g.blocks);
+        g.ahead = w.left + w.unit;
+        w.left -= u1 - w.unit;
+        if (u1 == g.units) {
+            ++w.tile;
+            w.unit = 0;
+        } else {
+            w.unit = u1;   // the range ends here
+        }
+    } while (g.b0 == g.b1);   // (units of the item's cost only)
     return true;
 }
 
@@ -299,6 +314,20 @@ struct Shares {
     __device__ int64_t begin(int c) const { return total * c / ctas; }
     // the range that holds unit u
     __device__ int owner(int64_t u) const { return static_cast<int>(((u + 1) * ctas + total - 1) / total) - 1; }
+};
+
+// Position in the ring of query buffers (their number is the launch's).
+struct QueryPos {
+    int bufs, buf = 0;
+    uint32_t parity = 0;
+    __device__ explicit QueryPos(int n) : bufs(n) {}
+    __device__ void step()
+    {
+        if (++buf == bufs) {
+            buf = 0;
+            parity ^= 1u;
+        }
+    }
 };
 
 // Ring position of the K/V tiles.
@@ -356,7 +385,7 @@ __device__ __forceinline__ void store_rows(uint32_t stage, int lane, const uint4
 }
 
 struct PagedBars {
-    uint32_t q_full, q_empty, drain, full0, empty0, s_full, pv_done, p_half0, p_full0;
+    uint32_t q_full0, q_empty0, drain, full0, empty0, s_full, pv_done, p_half0, p_full0;
 };
 
 template <class Cfg>
@@ -438,14 +467,17 @@ __device__ __forceinline__ void paged_softmax_warp(const PagedParams &p, const P
                 tmem + lane_base + static_cast<uint32_t>(Cfg::S_COL + (Cfg::NT == 1 ? static_cast<int>(count & 1u) : tile) * BKV);
             if (active) {
                 const bool all_seen = __all_sync(0xffffffffu, k0 + BKV <= seen);
+                // Two bodies, chosen per warp and block: no key masked for any row of the warp, or
+                // chunks of 32 keys one after the other, those that no row sees left out (on the
+                // diagonal a warp sees part of one chunk, all of those before, none after).
                 auto block = [&](auto full_tag) -> bool {
                     constexpr bool full = decltype(full_tag)::value;
-                    // Block maximum of scale * s: on unmasked blocks the extreme of the raw scores in
-                    // four independent chains, scaled once.
+                    const int lim = seen - k0;   // masked: keys of the block that this row sees
                     float mb = -INFINITY;
-                    float r0 = sl2 >= 0.0f ? -INFINITY : INFINITY, r1 = r0, r2 = r0, r3 = r0;
-                    tmem_chunks<CH>(s_addr, va, vb, [&](const uint32_t(&x)[32], int c) {
-                        if constexpr (full) {
+                    if constexpr (full) {
+                        // the extreme of the raw scores in four independent chains, scaled once
+                        float r0 = sl2 >= 0.0f ? -INFINITY : INFINITY, r1 = r0, r2 = r0, r3 = r0;
+                        tmem_chunks<CH>(s_addr, va, vb, [&](const uint32_t(&x)[32], int) {
                             if (sl2 >= 0.0f) {
 #pragma unroll
                                 for (int e = 0; e < 32; e += 8) {
@@ -463,15 +495,20 @@ __device__ __forceinline__ void paged_softmax_warp(const PagedParams &p, const P
                                     r3 = fmin3(r3, __uint_as_float(x[e + 6]), __uint_as_float(x[e + 7]));
                                 }
                             }
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (k0 + 32 * c + e < seen)
-                                    mb = fmaxf(mb, __uint_as_float(x[e]) * sl2);
-                        }
-                    });
-                    if constexpr (full)
+                        });
                         mb = (sl2 >= 0.0f ? fmax3(fmaxf(r0, r1), r2, r3) : fmin3(fminf(r0, r1), r2, r3)) * sl2;
+                    } else {
+#pragma unroll 1
+                        for (int c = 0; c < CH && __any_sync(0xffffffffu, row_ok && 32 * c < lim); ++c) {
+                            tmem_ld_32x32b_x32(s_addr + 32u * c, va);
+                            tmem_ld_wait_regs(va);
+                            const int lim_c = lim - 32 * c;
+#pragma unroll
+                            for (int e = 0; e < 32; e += 2)
+                                mb = fmax3(mb, e < lim_c ? __uint_as_float(va[e]) * sl2 : -INFINITY,
+                                           e + 1 < lim_c ? __uint_as_float(va[e + 1]) * sl2 : -INFINITY);
+                        }
+                    }
                     const bool raise = mb > m + kPagedRescale || m == -INFINITY;
                     const float m_new = raise ? mb : m;
                     const float m_use = m_new == -INFINITY ? 0.0f : m_new;
@@ -496,7 +533,8 @@ __device__ __forceinline__ void paged_softmax_warp(const PagedParams &p, const P
                     uint64_t sum2[4] = {f32x2_pack(0.0f, 0.0f), f32x2_pack(0.0f, 0.0f), f32x2_pack(0.0f, 0.0f),
                                         f32x2_pack(0.0f, 0.0f)};
                     const uint64_t scale2 = f32x2_pack(sl2, sl2), neg_m2 = f32x2_pack(-m_use, -m_use);
-                    tmem_chunks<CH>(s_addr, va, vb, [&](const uint32_t(&x)[32], int c) {
+                    // P of 32 keys, over scores already read; keys from lim_c on are masked
+                    auto p_chunk = [&](const uint32_t(&x)[32], int c, int lim_c) {
                         uint32_t pk[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
@@ -506,14 +544,13 @@ __device__ __forceinline__ void paged_softmax_warp(const PagedParams &p, const P
                                          t0, t1);
                             float p0 = ex2_approx(t0), p1 = ex2_approx(t1);
                             if constexpr (!full) {
-                                const int k = k0 + 32 * c + 2 * i;
-                                p0 = k < seen ? p0 : 0.0f;
-                                p1 = k + 1 < seen ? p1 : 0.0f;
+                                p0 = 2 * i < lim_c ? p0 : 0.0f;
+                                p1 = 2 * i + 1 < lim_c ? p1 : 0.0f;
                             }
                             sum2[i & 3] = f32x2_add(sum2[i & 3], f32x2_pack(p0, p1));
                             pk[i] = pack2<T>(p0, p1);
                         }
-                        tmem_st_32x32b_x16(s_addr + 16u * static_cast<uint32_t>(c), pk);   // over scores already read
+                        tmem_st_32x32b_x16(s_addr + 16u * static_cast<uint32_t>(c), pk);
                         if (Cfg::NT == 2 && c == CH / 2 - 1) {
                             // the first half of the keys: their product can start
                             tmem_st_wait();
@@ -522,7 +559,23 @@ __device__ __forceinline__ void paged_softmax_warp(const PagedParams &p, const P
                             if (lane == 0)
                                 mbar_arrive(p_half);
                         }
-                    });
+                    };
+                    if constexpr (full) {
+                        tmem_chunks<CH>(s_addr, va, vb, [&](const uint32_t(&x)[32], int c) { p_chunk(x, c, 32); });
+                    } else {
+#pragma unroll 1
+                        for (int c = 0; c < CH; ++c) {
+                            if (__any_sync(0xffffffffu, row_ok && 32 * c < lim)) {
+                                tmem_ld_32x32b_x32(s_addr + 32u * c, va);
+                                tmem_ld_wait_regs(va);
+                            } else {
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    va[e] = 0;   // (P comes out as 0 for every row that counts)
+                            }
+                            p_chunk(va, c, lim - 32 * c);
+                        }
+                    }
                     float s0, s1;
                     f32x2_unpack(f32x2_add(f32x2_add(sum2[0], sum2[1]), f32x2_add(sum2[2], sum2[3])), s0, s1);
                     l = l * alpha + (s0 + s1);
@@ -553,7 +606,7 @@ __device__ __forceinline__ void paged_softmax_warp(const PagedParams &p, const P
         if (starts && tile == 0 && quarter == 0 && (!ends || p.keys != KEYS_ALL)) {
             int parts = 1;
             if (!ends)   // (its last range holds its last unit)
-                parts = shares.owner(shares.begin(blockIdx.x + 1) - g.left + g.units - 1) - static_cast<int>(blockIdx.x) + 1;
+                parts = shares.owner(shares.begin(blockIdx.x + 1) - g.ahead + g.units - 1) - static_cast<int>(blockIdx.x) + 1;
             if (p.keys == KEYS_ALL) {
                 if (lane == 0)
                     p.cuts[blockIdx.x] = make_int4(g.tok0, g.toks, g.head, parts);
@@ -642,10 +695,10 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, Cfg::CTAS_PER_SM)
     uint8_t *sp = smem_raw + (base - raw);
     const uint32_t sQ = base + Cfg::Q_OFF, ring = base + Cfg::RING_OFF;
     PagedBars bar;
-    bar.q_full = base + Cfg::BAR_OFF;
-    bar.q_empty = bar.q_full + 8u;
-    bar.drain = bar.q_full + 16u;
-    bar.full0 = bar.q_full + 24u;
+    bar.q_full0 = base + Cfg::BAR_OFF;
+    bar.q_empty0 = bar.q_full0 + 8u * Cfg::Q_BUFS;
+    bar.drain = bar.q_empty0 + 8u * Cfg::Q_BUFS;
+    bar.full0 = bar.drain + 8u;
     bar.empty0 = bar.full0 + 8u * STAGES;
     bar.s_full = bar.empty0 + 8u * STAGES;
     bar.pv_done = bar.s_full + 8u;
@@ -656,8 +709,8 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, Cfg::CTAS_PER_SM)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        mbar_init(bar.q_full, 1);
-        mbar_init(bar.q_empty, 1);
+        for (int i = 0; i < 2 * Cfg::Q_BUFS; ++i)
+            mbar_init(bar.q_full0 + 8u * i, 1);
         mbar_init(bar.drain, 1);
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(bar.full0 + 8u * s, 1);
@@ -801,23 +854,26 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, Cfg::CTAS_PER_SM)
         const int box_rows = min(page_rows, BKV), boxes = BKV / box_rows;   // boxes per atom of a tile
         const int key_base = p.keys == KEYS_OWN ? p.batch.prefix_len : 0;
         RingPos<STAGES> pos;
-        uint32_t issued = 0, issued_parity = 0, q_loads = 0;
+        uint32_t issued = 0, issued_parity = 0, q_issued = 0, q_issued_parity = 0;
+        QueryPos qp(NT == 1 ? p.q_bufs : 1);
         bool ok = true;
         Segment g;
         while (ok && next_segment<Cfg>(p, walk, g)) {
-            if (q_loads > 0)   // the previous item's scores are complete
-                ok = wait_warp(bar.q_empty, (q_loads - 1u) & 1u, wc, ERR_PRODUCER_SLOT, lane);
-            if (!ok)
+            // the scores that read this buffer before are complete
+            if (!(ok = wait_warp(bar.q_empty0 + 8u * qp.buf, qp.parity ^ 1u, wc, ERR_PRODUCER_SLOT, lane)))
                 break;
+            const uint32_t q_full = bar.q_full0 + 8u * qp.buf;
             if (lane == 0)
-                mbar_arrive_expect_tx(bar.q_full, static_cast<uint32_t>(NT * ATOMS * p.tile_tokens * p.group * 128));
+                mbar_arrive_expect_tx(q_full, static_cast<uint32_t>(NT * ATOMS * p.tile_tokens * p.group * 128));
             __syncwarp();
             if (lane < NT * ATOMS) {
                 const int t = lane / ATOMS, a = lane % ATOMS;
-                tma_load_4d(sQ + static_cast<uint32_t>(t * Cfg::Q_TILE + a * Cfg::Q_ATOM), &tmap_q, bar.q_full, 64 * a, 0, g.head,
-                            g.tok0 + t * p.tile_tokens);
+                const int at = NT == 1 ? (qp.buf * ATOMS + a) * p.q_rows * 128 : t * Cfg::Q_TILE + a * Cfg::Q_ATOM;
+                tma_load_4d(sQ + static_cast<uint32_t>(at), &tmap_q, q_full, 64 * a, 0, g.head, g.tok0 + t * p.tile_tokens);
             }
-            ++q_loads;
+            q_issued |= 1u << qp.buf;
+            q_issued_parity = (q_issued_parity & ~(1u << qp.buf)) | (qp.parity << qp.buf);
+            qp.step();
             // pages of this stretch: numbers past the last key's page (and bad ones) become
             // num_pages, which TMA reads as zeros
             const int own_pages = (g.kv + page_rows - 1) >> p.batch.page_shift;
@@ -869,8 +925,9 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, Cfg::CTAS_PER_SM)
             }
         }
         if (!ok && lane == 0) {   // let every copy this warp started land before the CTA exits
-            if (q_loads > 0)
-                wait_until(bar.q_full, (q_loads - 1u) & 1u, p.timeout_ns, p.err);
+            for (int i = 0; i < Cfg::Q_BUFS; ++i)
+                if (q_issued & (1u << i))
+                    wait_until(bar.q_full0 + 8u * i, (q_issued_parity >> i) & 1u, p.timeout_ns, p.err);
             for (int s = 0; s < STAGES; ++s)
                 if (issued & (1u << s))
                     wait_until(bar.full0 + 8u * s, (issued_parity >> s) & 1u, p.timeout_ns, p.err);
@@ -883,12 +940,15 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, Cfg::CTAS_PER_SM)
             // 64 dims apart by KV_ATOM, 16 keys per 2048 bytes)
             const uint64_t q_desc = sw128_desc(sQ, 16, 1024), k_desc = sw128_desc(ring, 16, 1024);
             const uint64_t v_desc = sw128_desc(ring, Cfg::KV_ATOM, 1024);
-            auto issue_s = [&](int t, int slot, uint32_t d) {   // S = Q_t K^T
-                const uint64_t qd = q_desc + static_cast<uint64_t>((t * Cfg::Q_TILE) >> 4);
+            // (NT = 1: a query buffer holds q_rows rows per atom; the tile's other rows read on into
+            // whatever follows, within the ring at most, and their scores are not used)
+            const int q_atom = NT == 1 ? p.q_rows * 128 : Cfg::Q_ATOM;
+            auto issue_s = [&](int t, int slot, uint32_t d) {   // S = Q_t K^T (t: tile, or query buffer)
+                const uint64_t qd = q_desc + static_cast<uint64_t>((t * ATOMS * q_atom) >> 4);
                 const uint64_t kd = k_desc + static_cast<uint64_t>((slot * Cfg::KV_TILE) >> 4);
 #pragma unroll
                 for (int kk = 0; kk < Cfg::D / 16; ++kk) {
-                    const uint64_t qo = static_cast<uint64_t>(((kk >> 2) * Cfg::Q_ATOM + (kk & 3) * 32) >> 4);
+                    const uint64_t qo = static_cast<uint64_t>(((kk >> 2) * q_atom + (kk & 3) * 32) >> 4);
                     const uint64_t ko = static_cast<uint64_t>(((kk >> 2) * Cfg::KV_ATOM + (kk & 3) * 32) >> 4);
                     umma_f16<1>(d, qd + qo, kd + ko, Cfg::ID_S, kk != 0 ? 1u : 0u);
                 }
@@ -901,11 +961,10 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, Cfg::CTAS_PER_SM)
                                     add || kk > 0 ? 1u : 0u);
             };
             bool ok = true;
-            uint32_t q_uses = 0;
+            QueryPos qp(NT == 1 ? p.q_bufs : 1);   // of the next item (or, within one, behind this one's)
             if constexpr (NT == 1) {
                 // One tile, score buffers taken in turn: the scores of the next block are issued
-                // ahead of this block's product, except that a new item's scores, which wait for
-                // its queries, come after it.
+                // ahead of this block's product, those of a new item only if its queries are here.
                 Walk ahead = walk;
                 Segment gs, gp;
                 RingPos<STAGES> ks, kp;          // K tile of the next scores, of the next product
@@ -914,11 +973,13 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, Cfg::CTAS_PER_SM)
                 bool more_s = next_segment<Cfg>(p, ahead, gs), more_p = next_segment<Cfg>(p, walk, gp);
                 int bs = gs.b0, bp = gp.b0;
                 freed.step();
+                int q_buf = 0;                   // of the item whose scores are being issued
                 auto scores = [&]() -> bool {
                     if (bs == gs.b0) {
-                        if (!wait_bounded(bar.q_full, q_uses & 1u, wc, ERR_MMA_OPERANDS))
+                        if (!wait_bounded(bar.q_full0 + 8u * qp.buf, qp.parity, wc, ERR_MMA_OPERANDS))
                             return false;
-                        ++q_uses;
+                        q_buf = qp.buf;
+                        qp.step();
                     }
                     if (!wait_bounded(bar.full0 + 8u * ks.slot, ks.parity, wc, ERR_MMA_OPERANDS))
                         return false;
@@ -929,10 +990,10 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, Cfg::CTAS_PER_SM)
                         freed.step();
                     }
                     tc_fence_after_sync();
-                    issue_s(0, ks.slot, tmem + static_cast<uint32_t>(Cfg::S_COL + static_cast<int>(ns & 1u) * BKV));
+                    issue_s(q_buf, ks.slot, tmem + static_cast<uint32_t>(Cfg::S_COL + static_cast<int>(ns & 1u) * BKV));
                     umma_commit(bar.empty0 + 8u * ks.slot);   // K read, scores complete
                     if (bs + 1 == gs.b1)
-                        umma_commit(bar.q_empty);
+                        umma_commit(bar.q_empty0 + 8u * q_buf);
                     ks.step();
                     ks.step();
                     ++ns;
@@ -965,11 +1026,11 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, Cfg::CTAS_PER_SM)
                 };
                 ok = more_s && scores();
                 while (ok && more_p) {
-                    const bool same_item = more_s && bs != gs.b0;
-                    if (same_item)
+                    const bool ahead_now = more_s && (bs != gs.b0 || mbar_test_wait(bar.q_full0 + 8u * qp.buf, qp.parity));
+                    if (ahead_now)
                         ok = scores();
                     ok = ok && product();
-                    if (ok && !same_item && more_s)
+                    if (ok && !ahead_now && more_s)
                         ok = scores();
                 }
             } else {
@@ -985,8 +1046,8 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, Cfg::CTAS_PER_SM)
                     int mine = g.blocks;   // the first tile's blocks
                     if (p.keys != KEYS_PREFIX && g.toks > p.tile_tokens)
                         mine = max(1, (g.edge + (g.tok0 + p.tile_tokens - 1 - g.q0) + BKV) / BKV);
-                    ok = wait_bounded(bar.q_full, q_uses & 1u, wc, ERR_MMA_OPERANDS);
-                    ++q_uses;
+                    ok = wait_bounded(bar.q_full0, qp.parity, wc, ERR_MMA_OPERANDS);
+                    qp.step();
                     auto product = [&](int t, int slot, bool add) -> bool {
                         const uint32_t n = t == 0 ? na : nb, s = t == 0 ? sA : sB, o = t == 0 ? oA : oB;
 #pragma unroll
@@ -1006,7 +1067,7 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, Cfg::CTAS_PER_SM)
                         issue_s(t, at.slot, t == 0 ? sA : sB);
                         umma_commit(t == 0 ? bar.s_full : bar.empty0 + 8u * at.slot);
                         if (t == 1 && last)
-                            umma_commit(bar.q_empty);
+                            umma_commit(bar.q_empty0);
                     };
                     if (ok && (ok = wait_bounded(bar.full0 + 8u * pos.slot, pos.parity, wc, ERR_MMA_OPERANDS))) {
                         tc_fence_after_sync();

@@ -324,6 +324,7 @@ int launch_rope(gemm_ctx *ctx, int dtype, int64_t head_dim, gb300::RopeParams &p
 // The launches of one call and where their parts of the workspace are.
 struct AttnLaunch {
     int tiles = 1;            // query tiles per item (the kernel's NT)
+    int64_t tile_tokens = 0, rows = 0;   // of a tile: tokens, rows kept in the workspace
     int keys = 0, seqs = 0;   // KEYS_*, SEQS_*
     int64_t grid = 0;
     int64_t o_off = 0, ml_off = 0;   // PartsView
@@ -334,8 +335,6 @@ struct AttnPlan {
     bool empty = true, joint = false;
     int count = 0;
     AttnLaunch launch[3];
-    int tile_tokens = 0;
-    int64_t rows = 0;   // kept per tile
     int64_t own_off = 0, prefix_off = 0;               // PartInfo tables
     int64_t row_o_off[2] = {}, row_ml_off[2] = {};     // whole items (joint): own, prefix
     int64_t bytes = 0;
@@ -348,17 +347,17 @@ AttnPlan attention_plan(const gemm_ctx *ctx, const gemm_kv_cache &c, const gemm_
     if (T == 0 || b.num_seqs == 0 || q_heads == 0)
         return pl;
     pl.empty = false;
-    pl.tile_tokens = static_cast<int>(128 / group);
-    const int64_t tq = pl.tile_tokens;
-    pl.rows = std::min<int64_t>(tq, T) * group;
+    const int64_t tq = 128 / group;   // tokens of a full tile
     const int64_t prefix = b.num_prefix_pages * c.page_size, own = b.table_width * c.page_size;
     const int64_t flat_tiles = (T + tq - 1) / tq;
     // The prefix by itself, for the tokens of all sequences together, when that takes fewer tiles
     // of rows than there are sequences (each of which would read the prefix again).
     pl.joint = prefix > 0 && flat_tiles < b.num_seqs;
-    auto add = [&](int tiles, int keys, int seqs, int64_t max_tiles, int64_t key_count) {
+    auto add = [&](int tiles, int64_t tile_tokens, int keys, int seqs, int64_t max_tiles, int64_t key_count) {
         AttnLaunch &l = pl.launch[pl.count++];
         l.tiles = tiles;
+        l.tile_tokens = tile_tokens;
+        l.rows = std::min(tile_tokens, T) * group;
         l.keys = keys;
         l.seqs = seqs;
         const int64_t bkv = tiles == 1 ? 64 : 128;
@@ -366,7 +365,7 @@ AttnPlan attention_plan(const gemm_ctx *ctx, const gemm_kv_cache &c, const gemm_
         l.grid = std::min<int64_t>(static_cast<int64_t>(ctx->num_sms) * (tiles == 1 ? 2 : 1), units);
     };
     if (pl.joint)
-        add(flat_tiles > 1 ? 2 : 1, gb300::KEYS_PREFIX, gb300::SEQS_ALL, flat_tiles, prefix);
+        add(flat_tiles > 1 ? 2 : 1, tq, gb300::KEYS_PREFIX, gb300::SEQS_ALL, flat_tiles, prefix);
     const int keys = pl.joint ? gb300::KEYS_OWN : gb300::KEYS_ALL;
     const int64_t seen = own + (pl.joint ? 0 : prefix);
     // Sequences with more new tokens than a tile takes go to the two-tile kernel, the others to
@@ -375,9 +374,13 @@ AttnPlan attention_plan(const gemm_ctx *ctx, const gemm_kv_cache &c, const gemm_
     const bool may_long = (b.max_q == 0 || b.max_q > tq) && T > tq;
     const bool may_short = !may_long || b.num_seqs > 1;
     if (may_long)
-        add(2, keys, may_short ? gb300::SEQS_LONG : gb300::SEQS_ALL, std::min(T, T / (2 * tq) + b.num_seqs), seen);
-    if (may_short)
-        add(1, keys, may_long ? gb300::SEQS_SHORT : gb300::SEQS_ALL, std::min(T, T / tq + b.num_seqs), seen);
+        add(2, tq, keys, may_short ? gb300::SEQS_LONG : gb300::SEQS_ALL, std::min(T, T / (2 * tq) + b.num_seqs), seen);
+    if (may_short) {
+        // tiles no larger than the sequences need, as far as that is known: less to load per item,
+        // and several query buffers in the space of one full tile
+        const int64_t tt = b.max_q > 0 ? std::min(tq, b.max_q) : tq;
+        add(1, tt, keys, may_long ? gb300::SEQS_SHORT : gb300::SEQS_ALL, std::min(T, T / tt + b.num_seqs), seen);
+    }
     int64_t at = 0;
     auto take = [&](int64_t bytes) {
         const int64_t off = at;
@@ -394,7 +397,7 @@ AttnPlan attention_plan(const gemm_ctx *ctx, const gemm_kv_cache &c, const gemm_
         }
     }
     for (int i = 0; i < pl.count; ++i) {
-        const int64_t rows = 2 * pl.launch[i].grid * pl.launch[i].tiles * pl.rows;
+        const int64_t rows = 2 * pl.launch[i].grid * pl.launch[i].tiles * pl.launch[i].rows;
         pl.launch[i].o_off = take(rows * c.head_dim * 4);
         pl.launch[i].ml_off = take(rows * 8);
         pl.launch[i].cuts_off = take(pl.launch[i].grid * static_cast<int64_t>(sizeof(gb300::PartInfo)));
@@ -672,7 +675,7 @@ int gemm_paged_attention(gemm_ctx *ctx, const gemm_kv_cache *cache, const gemm_k
     p.n_prefix_pages = static_cast<int>(batch->num_prefix_pages);
     p.kv_heads = static_cast<int>(cache->kv_heads);
     p.group = static_cast<int>(group);
-    p.tile_tokens = pl.tile_tokens;
+    p.long_tokens = static_cast<int>(128 / group);
     p.scale_log2 = scale * 1.4426950408889634f;
     p.out = out->data;
     p.out_token = out->token_stride;
@@ -684,10 +687,6 @@ int gemm_paged_attention(gemm_ctx *ctx, const gemm_kv_cache *cache, const gemm_k
     p.debug = ctx->debug & GEMM_DEBUG_WITHHOLD_FIRST_LOAD;
     char *ws = static_cast<char *>(workspace);
     CUtensorMap tq, tk, tv;
-    if (!encode_4d(ctx, &tq, q->data, cache->dtype, {d, group, cache->kv_heads, tokens},
-                   {q->head_stride, group * q->head_stride, q->token_stride},
-                   {64, static_cast<uint32_t>(group), 1, static_cast<uint32_t>(pl.tile_tokens)}))
-        return GEMM_ERR_LAUNCH;
     gb300::CombineParams cp = {};
     cp.num_tokens = static_cast<int>(tokens);
     cp.kv_heads = p.kv_heads;
@@ -716,9 +715,12 @@ int gemm_paged_attention(gemm_ctx *ctx, const gemm_kv_cache *cache, const gemm_k
         p.keys = l.keys;
         p.seqs = l.seqs;
         p.launch = i;
+        p.tile_tokens = static_cast<int>(l.tile_tokens);
+        p.q_rows = static_cast<int>((l.tile_tokens * group + 7) / 8 * 8);
+        p.q_bufs = std::min(128 / p.q_rows, gb300::PagedConfig<__half, 128, 1>::Q_BUFS);
         p.parts.o = reinterpret_cast<float *>(ws + l.o_off);
         p.parts.ml = reinterpret_cast<float2 *>(ws + l.ml_off);
-        p.parts.rows = static_cast<int>(pl.rows);
+        p.parts.rows = static_cast<int>(l.rows);
         p.parts.tiles = l.tiles;
         p.info = reinterpret_cast<gb300::PartInfo *>(ws + (prefix ? pl.prefix_off : pl.own_off));
         p.row_o = reinterpret_cast<float *>(ws + pl.row_o_off[prefix]);
@@ -728,9 +730,13 @@ int gemm_paged_attention(gemm_ctx *ctx, const gemm_kv_cache *cache, const gemm_k
         cp.ctas[i] = static_cast<int>(l.grid);
         cp.tile_tokens[i] = p.tile_tokens;
         cp.cuts[i] = p.cuts;
-        cp.blocks[i] = l.grid * ((l.tiles * pl.rows + gb300::kCombineRows - 1) / gb300::kCombineRows);
+        cp.blocks[i] = l.grid * ((l.tiles * l.rows + gb300::kCombineRows - 1) / gb300::kCombineRows);
         combine_grid += cp.blocks[i];
         const uint32_t rows = static_cast<uint32_t>(std::min<int64_t>(cache->page_size, l.tiles == 1 ? 64 : 128));
+        if (!encode_4d(ctx, &tq, q->data, cache->dtype, {d, group, cache->kv_heads, tokens},
+                       {q->head_stride, group * q->head_stride, q->token_stride},
+                       {64, static_cast<uint32_t>(group), 1, static_cast<uint32_t>(l.tile_tokens)}))
+            return GEMM_ERR_LAUNCH;
         const int64_t dims[4] = {d, cache->page_size, cache->kv_heads, cache->num_pages};
         const int64_t strides[3] = {cache->row_stride, cache->head_stride, cache->page_stride};
         if (!encode_4d(ctx, &tk, cache->k, cache->dtype, dims, strides, {64, rows, 1, 1}) ||
