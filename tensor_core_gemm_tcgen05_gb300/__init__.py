@@ -17,6 +17,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sys
 import threading
 
 from . import serving as _serving
@@ -24,6 +25,8 @@ from .inputs import EPI_GELU, EPI_NONE, EPI_RELU, EPI_SOFTMAX  # noqa: F401  (C 
 from .serving import (  # noqa: F401  (include/gemm_serving.h)
     GEMM_BF16, GEMM_F16, GEMM_ROPE_LINEAR, GEMM_ROPE_NTK, GEMM_ROPE_PLAIN, GEMM_ROPE_YARN, SERVING_EXPORTS, kv_append,
     paged_attention, paged_attention_workspace, qk_rope, rope_table)
+
+_serving._g = sys.modules[__name__]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libgb300gemm.so")

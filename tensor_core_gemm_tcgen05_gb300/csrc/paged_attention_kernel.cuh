@@ -1155,7 +1155,9 @@ struct CombineParams {
 
 constexpr int kCombineWarps = 8;    // per block
 constexpr int kCombineRows = 32;    // rows of an item per block
-constexpr int kCombineFew = 4;      // parts up to which a warp joins four rows at once
+// Parts up to which a warp joins four rows at once, and how many parts' loads it has in flight
+// (prompts 175.4 us with 8 and 2, 178.2 with 8 and 4, 177.5 with 4 and 4).
+constexpr int kCombineFew = 8, kCombineStep = 2;
 
 // A row's running sum over parts: lane's D / 32 dimensions.
 template <int V>
@@ -1229,46 +1231,52 @@ struct RowSum {
     }
 };
 
-// Joins n <= kCombineFew parts of four rows, eight lanes each (`sub`: lane of the eight), all loads
-// at once: item rows cut in two or three, of which there are many, are bound by latency otherwise.
+// Joins n parts of four rows, eight lanes each (`sub`: lane of the eight), kCombineStep parts' loads
+// at a time: for rows cut in few parts, of which there are many, which latency would bound otherwise.
 template <typename T, int D, class Row>
 __device__ __forceinline__ void combine_few(const CombineParams &p, const PartsView &v, int n, int lane, bool on, int64_t token,
                                             int head, Row &&part)
 {
     constexpr int V = D / 32;   // 16-byte vectors of a lane: sub, sub + 8, ...
     const int sub = lane & 7;
-    float4 x[kCombineFew][V];
-    float2 ml[kCombineFew];
+    if (!on)
+        return;
+    float m = -INFINITY, l = 0.0f;
+    float4 acc[V] = {};
+    for (int i0 = 0; i0 < n; i0 += kCombineStep) {
+        float4 x[kCombineStep][V];
+        float2 ml[kCombineStep];
 #pragma unroll
-    for (int i = 0; i < kCombineFew; ++i) {
-        ml[i] = make_float2(-INFINITY, 0.0f);
-        if (on && i < n) {
-            const int64_t row = part(i);
+        for (int i = 0; i < kCombineStep; ++i) {   // (past the end: the last part again, not counted)
+            const int64_t row = part(min(i0 + i, n - 1));
             ml[i] = v.ml[row];
 #pragma unroll
             for (int e = 0; e < V; ++e)
                 x[i][e] = *reinterpret_cast<const float4 *>(v.o + row * D + 4 * (sub + 8 * e));
         }
-    }
-    if (!on)
-        return;
-    float m = ml[0].x, l = 0.0f;
+        float top = m;
 #pragma unroll
-    for (int i = 1; i < kCombineFew; ++i)
-        m = fmaxf(m, ml[i].x);
-    float4 acc[V] = {};
+        for (int i = 0; i < kCombineStep; ++i)
+            top = fmaxf(top, ml[i].x);
+        const float keep = m == -INFINITY ? 0.0f : exp2f(m - top);
+        m = top;
+        l *= keep;
 #pragma unroll
-    for (int i = 0; i < kCombineFew; ++i) {
-        if (ml[i].y == 0.0f)
-            continue;   // a part without a key: its O may not be written
-        const float w = ml[i].y != ml[i].y ? ml[i].y : exp2f(ml[i].x - m);   // (NaN stays NaN)
-        l += w * ml[i].y;
+        for (int e = 0; e < V; ++e)
+            acc[e] = make_float4(acc[e].x * keep, acc[e].y * keep, acc[e].z * keep, acc[e].w * keep);
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-            acc[e].x = fmaf(w, x[i][e].x, acc[e].x);
-            acc[e].y = fmaf(w, x[i][e].y, acc[e].y);
-            acc[e].z = fmaf(w, x[i][e].z, acc[e].z);
-            acc[e].w = fmaf(w, x[i][e].w, acc[e].w);
+        for (int i = 0; i < kCombineStep; ++i) {
+            if (i0 + i >= n || ml[i].y == 0.0f)
+                continue;   // a part without a key: its O may not be written
+            const float w = ml[i].y != ml[i].y ? ml[i].y : exp2f(ml[i].x - m);   // (NaN stays NaN)
+            l += w * ml[i].y;
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                acc[e].x = fmaf(w, x[i][e].x, acc[e].x);
+                acc[e].y = fmaf(w, x[i][e].y, acc[e].y);
+                acc[e].z = fmaf(w, x[i][e].z, acc[e].z);
+                acc[e].w = fmaf(w, x[i][e].w, acc[e].w);
+            }
         }
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;

@@ -16,6 +16,11 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
+
+import torch
+
+_g = None   # the package (set by it: this module is part of its import)
 
 _i64, _i32, _vp, _f32 = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_float
 
@@ -48,20 +53,24 @@ class Rope(ctypes.Structure):
                 ("interleaved", _i32)]
 
 
+# The same structs as the calls below pack them (a bytes object costs a third of a Structure to make).
+_HEADS, _CACHE = struct.Struct("@Pqqq"), struct.Struct("@PPqqqqqqqi4x")
+_BATCH, _ROPE = struct.Struct("@qqqPPPqqPq"), struct.Struct("@PqPPffi4x")
+_NO_HEADS = _HEADS.pack(0, 0, 0, 0)
+
 # Every symbol include/gemm_serving.h declares (the CPU tests check the library exports them).
 SERVING_EXPORTS = ("gemm_rope_table", "gemm_qk_rope", "gemm_kv_append", "gemm_paged_attention",
                    "gemm_paged_attention_workspace")
 
 
 def _declare(L):
-    """Argument types of the serving calls (from ``lib()``)."""
-    ph, pc, pb, pr = (ctypes.POINTER(t) for t in (Heads, KvCache, KvBatch, Rope))
+    """Argument types of the serving calls (from ``lib()``); structs go by address or as bytes."""
     L.gemm_rope_table.argtypes = [_i64, ctypes.c_double, ctypes.c_int, ctypes.c_double, ctypes.c_double, _vp,
                                   ctypes.POINTER(_f32)]
-    L.gemm_qk_rope.argtypes = [_vp, ctypes.c_int, _i64, _i64, ph, ph, _vp, pr, ph, ph, _vp]
-    L.gemm_kv_append.argtypes = [_vp, pc, pb, ph, ph, ph, pr, ph, _vp]
-    L.gemm_paged_attention.argtypes = [_vp, pc, pb, ph, _f32, ph, _vp, _i64, _vp, _i64, _vp]
-    L.gemm_paged_attention_workspace.argtypes = [_vp, pc, pb, _i64]
+    L.gemm_qk_rope.argtypes = [_vp, ctypes.c_int, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp]
+    L.gemm_kv_append.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]
+    L.gemm_paged_attention.argtypes = [_vp, _vp, _vp, _vp, _f32, _vp, _vp, _i64, _vp, _i64, _vp]
+    L.gemm_paged_attention_workspace.argtypes = [_vp, _vp, _vp, _i64]
     for name in SERVING_EXPORTS:
         getattr(L, name).restype = ctypes.c_int
     L.gemm_paged_attention_workspace.restype = _i64
@@ -69,99 +78,107 @@ def _declare(L):
 
 # ---------------------------------------------------------------------- from tensors to structs
 
-def _pkg():
-    import sys
-    return sys.modules[__package__]
+def _lib():
+    return _g._lib or _g.lib()
 
 
-def _stride(t, dim, other):
-    """The stride of ``dim``; that of a dimension of one element does not matter and may be odd."""
-    return t.stride(dim) if t.shape[dim] > 1 else other
+_CODES = {torch.float16: GEMM_F16, torch.bfloat16: GEMM_BF16}
 
 
-def _dtype_code(t):
-    import torch
-    if t.dtype == torch.float16:
-        return GEMM_F16
-    if t.dtype == torch.bfloat16:
-        return GEMM_BF16
-    raise ValueError(f"float16 or bfloat16 expected, got {t.dtype}")
+def _dtype_code(dtype):
+    code = _CODES.get(dtype)
+    if code is None:
+        raise ValueError(f"float16 or bfloat16 expected, got {dtype}")
+    return code
 
 
-def _heads(t, what, like):
-    """``gemm_heads`` of ``t`` [tokens, heads, head_dim], of the dtype and device of ``like``."""
-    if t is None:
-        return Heads(None, 0, 0, 0)
-    if t.dim() != 3 or t.dtype != like.dtype or t.device != like.device:
-        raise ValueError(f"{what}: a [tokens, heads, head_dim] tensor of {like.dtype} on {like.device} expected")
-    if t.shape[2] > 1 and t.stride(2) != 1:
+def _heads(t, what, dtype, device, shape=None):
+    """``gemm_heads`` of ``t`` [tokens, heads, head_dim] (the stride of a dimension of one element
+    does not matter and may be odd: a plain one stands in for it)."""
+    s = t.shape
+    if len(s) != 3 or t.dtype != dtype or t.device != device:
+        raise ValueError(f"{what}: a [tokens, heads, head_dim] tensor of {dtype} on {device} expected")
+    if shape is not None and s != shape:
+        raise ValueError(f"{what}: shape {tuple(shape)} expected, got {tuple(s)}")
+    st, sh, sd = t.stride()
+    n, h, d = s
+    if sd != 1 and d > 1:
         raise ValueError(f"{what}: head_dim must be contiguous")
-    d = t.shape[2]
-    return Heads(t.data_ptr(), t.shape[1], _stride(t, 0, t.shape[1] * d), _stride(t, 1, d))
-
-
-def _same(a, b, what):
-    if a.shape != b.shape:
-        raise ValueError(f"{what}: shape {tuple(a.shape)} expected, got {tuple(b.shape)}")
+    return _HEADS.pack(t.data_ptr(), h, st if n > 1 else h * d, sh if h > 1 else d)
 
 
 def _ints(t, what, shape, device):
     """The address of an int32 tensor of ``shape`` (entries None: any), its last dimension contiguous."""
-    import torch
-    if t.dtype != torch.int32 or t.device != device or t.dim() != len(shape) or any(
-            s is not None and s != n for s, n in zip(shape, t.shape)):
+    s = t.shape
+    if t.dtype != torch.int32 or t.device != device or len(s) != len(shape) or s[0] != shape[0] and shape[0] is not None:
         raise ValueError(f"{what}: an int32 tensor of shape {shape} on {device} expected")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    if s[-1] > 1 and t.stride(-1) != 1:
         raise ValueError(f"{what}: the last dimension must be contiguous")
     return t.data_ptr()
 
 
 def _cache(k_cache, v_cache):
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype or (
-            k_cache.device != v_cache.device):
+    """``gemm_kv_cache``, page size, heads and head_dim."""
+    s = k_cache.shape
+    if len(s) != 4 or s != v_cache.shape or k_cache.dtype != v_cache.dtype or k_cache.device != v_cache.device:
         raise ValueError("k_cache and v_cache: [pages, kv_heads, page_size, head_dim] of one shape, type and device expected")
-    n, h, p, d = k_cache.shape
-    if any(k_cache.shape[i] > 1 and k_cache.stride(i) != v_cache.stride(i) for i in range(4)):
+    n, h, p, d = s
+    strides = k_cache.stride()
+    if strides != v_cache.stride() and any(m > 1 and a != b for m, a, b in zip(s, strides, v_cache.stride())):
         raise ValueError("k_cache and v_cache must have the same strides")
-    if d > 1 and k_cache.stride(3) != 1:
+    sn, sh, sp, sd = strides
+    if sd != 1 and d > 1:
         raise ValueError("k_cache and v_cache: head_dim must be contiguous")
-    return KvCache(k_cache.data_ptr(), v_cache.data_ptr(), n, p, h, d, _stride(k_cache, 0, d), _stride(k_cache, 1, d),
-                   _stride(k_cache, 2, d), _dtype_code(k_cache))
+    return _CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), n, p, h, d, sn if n > 1 else d, sh if h > 1 else d,
+                       sp if p > 1 else d, _dtype_code(k_cache.dtype)), p, h, d
 
 
 def _batch(tokens, q_start, kv_lens, page_table, device, max_q=None, prefix_pages=None, num_prefix_pages=0):
-    n = kv_lens.shape[0]
+    n = kv_lens.shape[0] if kv_lens.dim() else -1
     ps = _ints(q_start, "q_start", (n + 1,), device)
     pk = _ints(kv_lens, "kv_lens", (n,), device)
     pt = _ints(page_table, "page_table", (n, None), device)
-    pre = None
+    pre = 0
     if prefix_pages is not None:
         pre = _ints(prefix_pages, "prefix_pages", (None,), device)
         num_prefix_pages = prefix_pages.shape[0]
     width = page_table.shape[1]
-    return KvBatch(n, tokens, 0 if max_q is None else int(max_q), ps, pk, pt, width, _stride(page_table, 0, width), pre,
-                   num_prefix_pages)
+    return _BATCH.pack(n, tokens, 0 if max_q is None else int(max_q), ps, pk, pt, width,
+                       page_table.stride(0) if n > 1 else width, pre, num_prefix_pages)
 
 
-def _rope(q_norm, k_norm, eps, table, interleaved, scale, like):
-    import torch
-    for name, w in (("q_norm", q_norm), ("k_norm", k_norm)):
-        if w is not None and (w.dtype != like.dtype or w.device != like.device or w.shape != (like.shape[2],)
-                              or not w.is_contiguous()):
-            raise ValueError(f"{name}: {like.shape[2]} contiguous weights of {like.dtype} on {like.device} expected")
-    if table is not None and (table.dtype not in (torch.int64, torch.uint64) or table.device != like.device
-                              or table.dim() != 1 or not table.is_contiguous()):
-        raise ValueError(f"table: a contiguous int64 vector on {like.device} expected")
-    return Rope(None if table is None else table.data_ptr(), 0 if table is None else 2 * table.shape[0],
-                None if q_norm is None else q_norm.data_ptr(), None if k_norm is None else k_norm.data_ptr(),
-                float(eps), float(scale), int(bool(interleaved)))
+def _weights(w, what, d, dtype, device):
+    if w is None:
+        return 0
+    if w.dtype != dtype or w.device != device or w.shape != (d,) or not w.is_contiguous():
+        raise ValueError(f"{what}: {d} contiguous weights of {dtype} on {device} expected")
+    return w.data_ptr()
 
 
-def _on(stream, t):
-    """The handle of ``stream``; None is the current stream of ``t``'s device."""
-    import torch
-    s = torch.cuda.current_stream(t.device) if stream is None else stream
-    return int(s.cuda_stream) if hasattr(s, "cuda_stream") else int(s)
+def _rope(q_norm, k_norm, eps, table, interleaved, scale, d, dtype, device):
+    words, half = 0, 0
+    if table is not None:
+        if table.dtype != torch.int64 and table.dtype != torch.uint64 or table.device != device or table.dim() != 1 or (
+                not table.is_contiguous()):
+            raise ValueError(f"table: a contiguous int64 vector on {device} expected")
+        words, half = table.data_ptr(), table.shape[0]
+    return _ROPE.pack(words, 2 * half, _weights(q_norm, "q_norm", d, dtype, device), _weights(k_norm, "k_norm", d, dtype, device),
+                      eps, scale, 1 if interleaved else 0)
+
+
+def _current(device):
+    """The handle of torch's current stream of ``device``."""
+    try:   # a fifth of current_stream()'s cost
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if device.index is None else device.index)
+    except AttributeError:
+        return torch.cuda.current_stream(device).cuda_stream
+
+
+def _on(stream, device):
+    """The handle of ``stream``; None is the current stream of ``device``."""
+    if stream is None:
+        return _current(device)
+    return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
 # --------------------------------------------------------------------------------- the calls
@@ -171,15 +188,13 @@ def rope_table(rotary_dim, base=10000.0, scaling=None, factor=1.0, original=None
     ``rotary_dim / 2`` words (turns a position in units of 2^-64) and the factor for
     ``rope_scale``. ``scaling``: None, "linear", "ntk" or "yarn" (with ``original``, the trained
     length), for contexts ``factor`` times as long."""
-    import torch
-    g = _pkg()
     if scaling not in _SCALINGS:
         raise ValueError(f"scaling: one of {sorted(k for k in _SCALINGS if k)} or None expected, got {scaling!r}")
     if not 16 <= int(rotary_dim) <= 128:
-        raise g.GemmError(g.GEMM_ERR_ARG, "gemm_rope_table")
+        raise _g.GemmError(_g.GEMM_ERR_ARG, "gemm_rope_table")
     table = torch.empty(int(rotary_dim) // 2, dtype=torch.int64)
     scale = _f32(1.0)
-    g._check(g.lib().gemm_rope_table(int(rotary_dim), float(base), _SCALINGS[scaling], float(factor),
+    _g._check(_lib().gemm_rope_table(int(rotary_dim), float(base), _SCALINGS[scaling], float(factor),
                                      0.0 if original is None else float(original), table.data_ptr(), ctypes.byref(scale)),
              "gemm_rope_table")
     return table, float(scale.value)
@@ -190,25 +205,23 @@ def qk_rope(ctx, q, k, positions, table=None, interleaved=False, rope_scale=1.0,
     """Norm (if there are weights) and rotation (if there is a table) of ``q`` and ``k`` at
     ``positions`` (int32, one per token) through ``gemm_qk_rope``. Returns ``(q_out, k_out)``,
     allocated contiguous when not given; an output may be its own input. ``k`` may be None."""
-    import torch
-    g = _pkg()
+    shape, dtype, device = q.shape, q.dtype, q.device
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    if k_out is None and k is not None:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    if (k is None) != (k_out is None):
-        raise ValueError("k_out without k")
-    hq, hqo = _heads(q, "q", q), _heads(q_out, "q_out", q)
-    hk, hko = _heads(k, "k", q), _heads(k_out, "k_out", q)
-    _same(q, q_out, "q_out")
+        q_out = torch.empty(shape, dtype=dtype, device=device)
+    hq, hqo = _heads(q, "q", dtype, device), _heads(q_out, "q_out", dtype, device, shape)
+    hk = hko = _NO_HEADS
     if k is not None:
-        _same(k, k_out, "k_out")
-        if k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2]:
-            raise ValueError(f"k: {q.shape[0]} tokens of head_dim {q.shape[2]} expected, got {tuple(k.shape)}")
-    pos = _ints(positions, "positions", (q.shape[0],), q.device)
-    r = _rope(q_norm, k_norm, eps, table, interleaved, rope_scale, q)
-    rc = g.lib().gemm_qk_rope(g._h(ctx), _dtype_code(q), q.shape[0], q.shape[2], hq, hk, pos, r, hqo, hko, _on(stream, q))
-    g._check(rc, "gemm_qk_rope")
+        if k_out is None:
+            k_out = torch.empty(k.shape, dtype=dtype, device=device)
+        hk, hko = _heads(k, "k", dtype, device), _heads(k_out, "k_out", dtype, device, k.shape)
+        if k.shape[0] != shape[0] or k.shape[2] != shape[2]:
+            raise ValueError(f"k: {shape[0]} tokens of head_dim {shape[2]} expected, got {tuple(k.shape)}")
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    pos = _ints(positions, "positions", (shape[0],), device)
+    r = _rope(q_norm, k_norm, eps, table, interleaved, rope_scale, shape[2], dtype, device)
+    _g._check(_lib().gemm_qk_rope(_g._h(ctx), _dtype_code(dtype), shape[0], shape[2], hq, hk, pos, r, hqo, hko,
+                                  _on(stream, device)), "gemm_qk_rope")
     return q_out, k_out
 
 
@@ -218,28 +231,26 @@ def kv_append(ctx, q, k, v, k_cache, v_cache, q_start, kv_lens, page_table, tabl
     their rows of the cache, through ``gemm_kv_append``. ``kv_lens`` counts each sequence's own
     keys with the new ones; ``prefix_len`` (whole pages) the keys of a shared prefix before them.
     Returns ``q_out`` (allocated when not given; may be ``q``; None if ``q`` is None)."""
-    import torch
-    g = _pkg()
-    c = _cache(k_cache, v_cache)
-    if prefix_len < 0 or c.page_size == 0 or prefix_len % c.page_size:
-        raise ValueError(f"prefix_len: whole pages of {c.page_size} expected, got {prefix_len}")
-    if q_out is None and q is not None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    if (q is None) != (q_out is None):
-        raise ValueError("q_out without q")
-    hk, hv = _heads(k, "k", k_cache), _heads(v, "v", k_cache)
-    hq, hqo = _heads(q, "q", k_cache), _heads(q_out, "q_out", k_cache)
-    _same(k, v, "v")
-    if k.shape[1:] != (c.kv_heads, c.head_dim):
-        raise ValueError(f"k: [tokens, {c.kv_heads}, {c.head_dim}] expected, got {tuple(k.shape)}")
+    dtype, device = k_cache.dtype, k_cache.device
+    c, page, kv_heads, d = _cache(k_cache, v_cache)
+    if prefix_len < 0 or page == 0 or prefix_len % page:
+        raise ValueError(f"prefix_len: whole pages of {page} expected, got {prefix_len}")
+    hk, hv = _heads(k, "k", dtype, device), _heads(v, "v", dtype, device, k.shape)
+    tokens = k.shape[0]
+    if k.shape[1] != kv_heads or k.shape[2] != d:
+        raise ValueError(f"k: [tokens, {kv_heads}, {d}] expected, got {tuple(k.shape)}")
+    hq = hqo = _NO_HEADS
     if q is not None:
-        _same(q, q_out, "q_out")
-        if q.shape[0] != k.shape[0] or q.shape[2] != c.head_dim:
-            raise ValueError(f"q: {k.shape[0]} tokens of head_dim {c.head_dim} expected, got {tuple(q.shape)}")
-    b = _batch(k.shape[0], q_start, kv_lens, page_table, k_cache.device, num_prefix_pages=prefix_len // c.page_size)
-    r = _rope(q_norm, k_norm, eps, table, interleaved, rope_scale, k)
-    rc = g.lib().gemm_kv_append(g._h(ctx), c, b, hq, hk, hv, r, hqo, _on(stream, k_cache))
-    g._check(rc, "gemm_kv_append")
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=dtype, device=device)
+        hq, hqo = _heads(q, "q", dtype, device), _heads(q_out, "q_out", dtype, device, q.shape)
+        if q.shape[0] != tokens or q.shape[2] != d:
+            raise ValueError(f"q: {tokens} tokens of head_dim {d} expected, got {tuple(q.shape)}")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    b = _batch(tokens, q_start, kv_lens, page_table, device, num_prefix_pages=prefix_len // page)
+    r = _rope(q_norm, k_norm, eps, table, interleaved, rope_scale, d, dtype, device)
+    _g._check(_lib().gemm_kv_append(_g._h(ctx), c, b, hq, hk, hv, r, hqo, _on(stream, device)), "gemm_kv_append")
     return q_out
 
 
@@ -252,48 +263,43 @@ def paged_attention(ctx, q, k_cache, v_cache, q_start, kv_lens, page_table, max_
     tensor to fill with the log of each row's sum of exponentials. ``workspace``: a uint8 tensor
     of at least ``paged_attention_workspace`` bytes, allocated for the call when not given.
     Returns ``out`` (allocated when not given)."""
-    import torch
-    g = _pkg()
-    c = _cache(k_cache, v_cache)
+    L, h = _lib(), _g._h(ctx)
+    shape, dtype, device = q.shape, k_cache.dtype, k_cache.device
+    c, _, _, d = _cache(k_cache, v_cache)
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    hq, ho = _heads(q, "q", k_cache), _heads(out, "out", k_cache)
-    _same(q, out, "out")
-    if q.shape[2] != c.head_dim:
-        raise ValueError(f"q: head_dim {c.head_dim} expected, got {q.shape[2]}")
-    b = _batch(q.shape[0], q_start, kv_lens, page_table, q.device, max_q, prefix_pages)
+        out = torch.empty(shape, dtype=dtype, device=device)
+    hq, ho = _heads(q, "q", dtype, device), _heads(out, "out", dtype, device, shape)
+    tokens, heads, q_dim = shape
+    if q_dim != d:
+        raise ValueError(f"q: head_dim {d} expected, got {q_dim}")
+    b = _batch(tokens, q_start, kv_lens, page_table, device, max_q, prefix_pages)
     lse_ptr, lse_stride = None, 0
     if lse is not None:
-        if lse.dtype != torch.float32 or lse.device != q.device or lse.shape != q.shape[:2] or (
-                lse.shape[1] > 1 and lse.stride(1) != 1):
-            raise ValueError(f"lse: a float32 tensor of shape {tuple(q.shape[:2])} on {q.device}, heads contiguous, expected")
-        lse_ptr, lse_stride = lse.data_ptr(), _stride(lse, 0, lse.shape[1])
-    if workspace is not None and (workspace.dtype != torch.uint8 or not workspace.is_contiguous()
-                                  or workspace.device != q.device):
-        raise ValueError(f"workspace: a contiguous uint8 tensor on {q.device} expected")
-    handle = _on(stream, q)
+        if lse.dtype != torch.float32 or lse.device != device or lse.shape != shape[:2] or heads > 1 and lse.stride(1) != 1:
+            raise ValueError(f"lse: a float32 tensor of shape {tuple(shape[:2])} on {device}, heads contiguous, expected")
+        lse_ptr, lse_stride = lse.data_ptr(), lse.stride(0) if tokens > 1 else heads
+    if workspace is not None and (workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != device):
+        raise ValueError(f"workspace: a contiguous uint8 tensor on {device} expected")
+    handle = _on(stream, device)
     if workspace is None:
-        need = g.lib().gemm_paged_attention_workspace(g._h(ctx), c, b, q.shape[1])
+        need = L.gemm_paged_attention_workspace(h, c, b, heads)
         if need < 0:
-            raise g.GemmError(int(need), "gemm_paged_attention_workspace")
-        if handle == torch.cuda.current_stream(q.device).cuda_stream:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            raise _g.GemmError(int(need), "gemm_paged_attention_workspace")
+        if stream is None or handle == _current(device):
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
         else:   # the allocator must know the stream that uses the memory
-            with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=q.device)):
-                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    s = 1.0 / math.sqrt(c.head_dim) if scale is None else float(scale)
-    rc = g.lib().gemm_paged_attention(g._h(ctx), c, b, hq, s, ho, lse_ptr, lse_stride, workspace.data_ptr(),
-                                      workspace.numel(), handle)
-    g._check(rc, "gemm_paged_attention")
+            with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=device)):
+                workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    _g._check(L.gemm_paged_attention(h, c, b, hq, 1.0 / math.sqrt(d) if scale is None else scale, ho, lse_ptr, lse_stride,
+                                    workspace.data_ptr(), workspace.numel(), handle), "gemm_paged_attention")
     return out
 
 
 def paged_attention_workspace(ctx, q, k_cache, v_cache, q_start, kv_lens, page_table, max_q=None, prefix_pages=None):
     """Workspace bytes of ``paged_attention`` for these arguments (shapes are read, contents are not)."""
-    g = _pkg()
-    c = _cache(k_cache, v_cache)
-    b = _batch(q.shape[0], q_start, kv_lens, page_table, q.device, max_q, prefix_pages)
-    need = g.lib().gemm_paged_attention_workspace(g._h(ctx), c, b, q.shape[1])
+    c, _, _, _ = _cache(k_cache, v_cache)
+    b = _batch(q.shape[0], q_start, kv_lens, page_table, k_cache.device, max_q, prefix_pages)
+    need = _lib().gemm_paged_attention_workspace(_g._h(ctx), c, b, q.shape[1])
     if need < 0:
-        raise g.GemmError(int(need), "gemm_paged_attention_workspace")
+        raise _g.GemmError(int(need), "gemm_paged_attention_workspace")
     return int(need)

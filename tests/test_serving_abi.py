@@ -57,6 +57,13 @@ def test_structs_match_header(tmp_path):
     for s in structs.values():
         want += [ctypes.sizeof(s)] + [getattr(s, f[0]).offset for f in s._fields_]
     assert got == want
+    packed = (serving._HEADS, serving._CACHE, serving._BATCH, serving._ROPE)
+    assert [p.size for p in packed] == [ctypes.sizeof(s) for s in structs.values()]
+    # and field by field: the packed bytes read back through the structs
+    for p, s in zip(packed, structs.values()):
+        values = [i + 1 for i in range(len(s._fields_))]
+        x = s.from_buffer_copy(p.pack(*values))
+        assert [getattr(x, f[0]) for f in s._fields_] == values
 
 
 def turns(table):
@@ -98,7 +105,7 @@ def test_rope_table_refusals(lib):
 
 
 def test_null_arguments_are_rejected(lib):
-    h, c, b, r = serving.Heads(), serving.KvCache(), serving.KvBatch(), serving.Rope()
+    h, c, b, r = (ctypes.byref(s()) for s in (serving.Heads, serving.KvCache, serving.KvBatch, serving.Rope))
     assert lib.gemm_qk_rope(None, 0, 1, 128, h, h, None, r, h, h, None) == g.GEMM_ERR_ARG
     assert lib.gemm_kv_append(None, c, b, h, h, h, r, h, None) == g.GEMM_ERR_ARG
     assert lib.gemm_paged_attention(None, c, b, h, 1.0, h, None, 0, None, 0, None) == g.GEMM_ERR_ARG

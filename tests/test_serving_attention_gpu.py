@@ -1,5 +1,6 @@
 """Attention over the paged cache against 64 bits: ragged batches, masks, pages, shared prefixes,
 layouts, stale rows, captured graphs, streams, refusals, and a whole serving step."""
+import ctypes
 import math
 
 import pytest
@@ -315,16 +316,20 @@ def test_refusals(ctx):
     def rp(**kw):
         return Rope(**{**dict(table=table.data_ptr(), rotary_dim=d, q_norm=None, k_norm=None, eps=1e-6, scale=1.0, interleaved=0), **kw})
 
+    def at(x):
+        return ctypes.byref(x)
+
     def attend(c=None, b=None, hq_=None, ho=None, scale=0.1, lse=None, stride=0, w=ws.data_ptr(), n=ws.numel()):
-        return L.gemm_paged_attention(h, c or cache(), b or bt(), hq_ or heads(q), scale, ho or heads(out), lse, stride, w, n, stream)
+        return L.gemm_paged_attention(h, at(c or cache()), at(b or bt()), at(hq_ or heads(q)), scale, at(ho or heads(out)), lse,
+                                      stride, w, n, stream)
 
     def append(c=None, b=None, **kw):
         a = {**dict(q=heads(q), k=heads(k), v=heads(v), r=rp(), o=heads(out)), **kw}
-        return L.gemm_kv_append(h, c or cache(), b or bt(), a["q"], a["k"], a["v"], a["r"], a["o"], stream)
+        return L.gemm_kv_append(h, at(c or cache()), at(b or bt()), at(a["q"]), at(a["k"]), at(a["v"]), at(a["r"]), at(a["o"]), stream)
 
     def rope_(**kw):
         a = {**dict(dtype=0, T=T, d=d, q=heads(q), k=heads(k), p=pos.data_ptr(), r=rp(), qo=heads(out), ko=heads(v)), **kw}
-        return L.gemm_qk_rope(h, a["dtype"], a["T"], a["d"], a["q"], a["k"], a["p"], a["r"], a["qo"], a["ko"], stream)
+        return L.gemm_qk_rope(h, a["dtype"], a["T"], a["d"], at(a["q"]), at(a["k"]), a["p"], at(a["r"]), at(a["qo"]), at(a["ko"]), stream)
 
     ARG, ALIGN, DEVICE, OK = g.GEMM_ERR_ARG, g.GEMM_ERR_ALIGN, g.GEMM_ERR_DEVICE, g.GEMM_OK
     assert attend() == OK and append() == OK and rope_() == OK
@@ -373,9 +378,9 @@ def test_refusals(ctx):
     assert rope_(T=0, p=None) == OK and rope_(qo=heads(q)) == OK
     # nothing to do
     assert attend(b=bt(num_tokens=0)) == OK and append(b=bt(num_seqs=0)) == OK
-    assert L.gemm_paged_attention_workspace(h, cache(), bt(num_tokens=0), 4) == 0
-    assert L.gemm_paged_attention_workspace(h, cache(), bt(), 5) == ARG
-    assert 0 < L.gemm_paged_attention_workspace(h, cache(), bt(q_start=None), 4) <= ws.numel()
+    assert L.gemm_paged_attention_workspace(h, at(cache()), at(bt(num_tokens=0)), 4) == 0
+    assert L.gemm_paged_attention_workspace(h, at(cache()), at(bt()), 5) == ARG
+    assert 0 < L.gemm_paged_attention_workspace(h, at(cache()), at(bt(q_start=None)), 4) <= ws.numel()
     done(ctx)
 
 
