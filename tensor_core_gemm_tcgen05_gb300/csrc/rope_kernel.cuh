@@ -11,10 +11,12 @@
 // operations per clock and SM).
 //
 // Bound by memory: every value is read once and written once. A group of head_dim / 8 lanes
-// takes one token and `heads_per_item` of its heads, 16 bytes per lane and head, four heads in
-// flight; a lane's dimensions are the same for all of them, so cosines and sines are computed
-// once per group, the pair partner (half layout) and the sum of squares go through shuffles, and
-// nothing needs shared memory or a barrier.
+// takes one token and up to `heads_per_item` of its query, its key or its value heads, 16 bytes
+// per lane and head, kRopeInFlight heads in flight. A lane's dimensions are the same for all of
+// them, so its cosines and sines, times the norm's weights, are computed once per group (in the
+// half layout the two lanes of a pair compute half of them each); the pair's other value and the
+// sum of squares go through shuffles, and nothing needs shared memory or a barrier. The first
+// heads are loaded before the token's sequence is looked up.
 #pragma once
 
 #include "serving_common.cuh"
@@ -30,11 +32,12 @@ struct HeadsView {
 };
 
 struct RopeParams {
-    HeadsView q, k, v;            // in the order of a token's heads; v is copied
-    int tokens, chunks, heads_per_item;
-    const int *positions;         // not paged
-    BatchView batch;              // paged
-    int64_t row_stride;           // paged: of the cache
+    HeadsView q, k, v;                // v is copied
+    int tokens, heads_per_item;
+    int q_chunks, k_chunks, chunks;   // items of a token: its query heads', key heads', all
+    const int *positions;             // not paged
+    BatchView batch;                  // paged
+    int64_t row_stride;               // paged: of the cache
     const uint64_t *table;
     const void *q_norm, *k_norm;
     int rotary_dim, interleaved;
@@ -42,24 +45,58 @@ struct RopeParams {
     uint32_t *err;
 };
 
-constexpr int kRopeThreads = 256;
+// 64 registers a thread: 1024 threads per SM, 64 KB of heads in flight (8200 tokens, 32 + 32 heads of
+// 128: 42.8 us, 6.28 TB/s; 256-thread blocks 43.6; five of those per SM, spilling, 81; three 46.5;
+// two heads in flight 76, eight 46.9). Streaming stores or loads: 3 % slower.
+constexpr int kRopeThreads = 128;
 constexpr int kRopeInFlight = 4;   // heads loaded before the first is worked on
 
+template <typename T>
+__device__ __forceinline__ void unpack8(const uint4 &x, float (&f)[8])
+{
+    const uint32_t raw[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float2 v = unpack2<T>(raw[e]);
+        f[2 * e] = v.x;
+        f[2 * e + 1] = v.y;
+    }
+}
+
 template <typename T, int D, bool PAGED>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p)
+__global__ void __launch_bounds__(kRopeThreads, 8) rope_kernel(const __grid_constant__ RopeParams p)
 {
     constexpr int L = D / 8;   // lanes per token
     grid_dependency_wait();
     grid_dependents_launch();
-    const int lane = threadIdx.x & 31, sub = lane % L;
+    const int lane = threadIdx.x & 31, sub = lane % L, d0 = sub * 8;
     const int64_t item = static_cast<int64_t>(blockIdx.x) * (kRopeThreads / L) + threadIdx.x / L;
     const int64_t token64 = item / p.chunks;
-    const int chunk = static_cast<int>(item - token64 * p.chunks);
-    bool live = token64 < p.tokens;
-    const int token = live ? static_cast<int>(token64) : p.tokens - 1;
+    int chunk = static_cast<int>(item - token64 * p.chunks);
+    const bool in_range = token64 < p.tokens;
+    const int token = in_range ? static_cast<int>(token64) : p.tokens - 1;
+    const int kind = chunk < p.q_chunks ? 0 : chunk < p.q_chunks + p.k_chunks ? 1 : 2;   // query, key, value
+    chunk -= kind == 0 ? 0 : kind == 1 ? p.q_chunks : p.q_chunks + p.k_chunks;
+    const HeadsView &g = kind == 0 ? p.q : kind == 1 ? p.k : p.v;
+    const int h0 = chunk * p.heads_per_item, h1 = min(g.heads, h0 + p.heads_per_item);
 
-    // the token's position, and its row of the cache
-    int64_t pos, cache_row = -1;
+    uint4 x[kRopeInFlight];
+    const T *src = static_cast<const T *>(g.in) + token * g.in_token + h0 * g.in_head + d0;
+    const int64_t in_head = g.in_head;
+    auto load = [&](int i0) {
+#pragma unroll
+        for (int u = 0; u < kRopeInFlight; ++u) {
+            x[u] = make_uint4(0, 0, 0, 0);
+            if (in_range && h0 + i0 + u < h1)
+                x[u] = *reinterpret_cast<const uint4 *>(src + (i0 + u) * in_head);
+        }
+    };
+    load(0);
+
+    // the token's position, and where its heads go
+    int64_t pos;
+    bool live = in_range;
+    T *dst = static_cast<T *>(g.out) + token * g.out_token;
     if constexpr (PAGED) {
         const int s = find_seq<L>(p.batch.q_start, p.batch.num_seqs, token, lane);
         const SeqView seq = load_seq(p.batch, s);
@@ -67,89 +104,82 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p)
         const int64_t place = static_cast<int64_t>(seq.kv) - seq.n + (token - seq.q0);
         pos = p.batch.prefix_len + place;
         bool bad = seq.bad;
-        if (live && place >= 0) {   // place < kv <= the keys of table_width pages
-            const int page = __ldg(p.batch.table + s * p.batch.table_stride + (place >> p.batch.page_shift));
-            if (page >= 0 && page < p.batch.num_pages)
-                cache_row = (static_cast<int64_t>(page) << p.batch.page_shift) + (place & ((1 << p.batch.page_shift) - 1));
+        if (kind != 0 && live) {
+            int page = -1;
+            if (place >= 0)   // place < kv <= the keys of table_width pages
+                page = __ldg(p.batch.table + s * p.batch.table_stride + (place >> p.batch.page_shift));
+            live = page >= 0 && page < p.batch.num_pages;
+            bad = bad || !live;
+            dst = static_cast<T *>(g.out) + page * g.out_token + (place & ((1 << p.batch.page_shift) - 1)) * p.row_stride;
         }
-        bad = bad || (live && cache_row < 0);
         if (bad && sub == 0)
             atomicCAS(p.err, 0u, static_cast<uint32_t>(ERR_BATCH_INDEX));
     } else {
         pos = __ldg(p.positions + token);
     }
+    dst += h0 * g.out_head + d0;
+    const int64_t out_head = g.out_head;
 
-    // cosine and signed sine of this lane's eight values: y[e] = x[e] * cs[e] + partner[e] * sn[e]
-    const int d0 = sub * 8, half = p.rotary_dim / 2;
-    const bool rotates = d0 < p.rotary_dim;
-    const bool second = !p.interleaved && d0 >= half;
-    float cs[8] = {}, sn[8] = {};
-    auto angle = [&](int pair, float &c, float &s) {
-        const uint64_t turns = static_cast<uint64_t>(pos) * __ldg(p.table + pair);
-        // the top 32 bits as a signed part of a turn, in half turns (2^-31 each)
-        const float x = static_cast<float>(static_cast<int32_t>(turns >> 32)) * 4.656612873077393e-10f;
-        sincospif(x, &s, &c);
-        c *= p.scale;
-        s *= p.scale;
-    };
-    if (rotates && p.interleaved) {
+    // y[e] = x[e] * cs[e] + partner[e] * sn[e], with the norm's weights in the factors
+    const int half = p.rotary_dim / 2;
+    const bool rotates = d0 < p.rotary_dim && kind != 2, pairs = d0 < p.rotary_dim && !p.interleaved;
+    const bool second = pairs && d0 >= half;
+    const int partner = pairs ? lane + (second ? -half / 8 : half / 8) : lane;
+    float cs[8], sn[8];
+    {
+        float c4[4], s4[4];   // of four pairs
+        const int pair0 = p.interleaved ? d0 / 2 : d0 - (second ? half - 4 : 0);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            angle(d0 / 2 + e, cs[2 * e], sn[2 * e + 1]);
-            cs[2 * e + 1] = cs[2 * e];
-            sn[2 * e] = -sn[2 * e + 1];
-        }
-    } else if (rotates) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            angle(d0 - (second ? half : 0) + e, cs[e], sn[e]);
-            sn[e] = second ? sn[e] : -sn[e];
-        }
-    }
-    const int partner = rotates && !p.interleaved ? lane + (second ? -half / 8 : half / 8) : lane;
-
-    uint4 wq = make_uint4(0, 0, 0, 0), wk = wq;
-    if (p.q_norm)
-        wq = __ldg(static_cast<const uint4 *>(p.q_norm) + sub);
-    if (p.k_norm)
-        wk = __ldg(static_cast<const uint4 *>(p.k_norm) + sub);
-
-    const int all = p.q.heads + p.k.heads + p.v.heads;
-    const int h_end = min(all, (chunk + 1) * p.heads_per_item);
-    // (every lane runs the same number of steps: the shuffles below are warp-wide)
-    for (int i0 = 0; i0 < p.heads_per_item; i0 += kRopeInFlight) {
-        uint4 x[kRopeInFlight];
-        T *dst[kRopeInFlight];
-        int kind[kRopeInFlight];   // 0 query, 1 key, 2 value
-#pragma unroll
-        for (int u = 0; u < kRopeInFlight; ++u) {
-            const int h = chunk * p.heads_per_item + i0 + u;
-            const bool on = live && i0 + u < p.heads_per_item && h < h_end;
-            kind[u] = h < p.q.heads ? 0 : h < p.q.heads + p.k.heads ? 1 : 2;
-            const HeadsView &g = kind[u] == 0 ? p.q : kind[u] == 1 ? p.k : p.v;
-            const int hh = kind[u] == 0 ? h : kind[u] == 1 ? h - p.q.heads : h - p.q.heads - p.k.heads;
-            dst[u] = nullptr;
-            x[u] = make_uint4(0, 0, 0, 0);
-            if (on) {
-                x[u] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(g.in) + token * g.in_token + hh * g.in_head + d0);
-                if (!PAGED || kind[u] == 0)
-                    dst[u] = static_cast<T *>(g.out) + token * g.out_token + hh * g.out_head + d0;
-                else if (cache_row >= 0)
-                    dst[u] = static_cast<T *>(g.out) + (cache_row >> p.batch.page_shift) * g.out_token + hh * g.out_head +
-                             (cache_row & ((1 << p.batch.page_shift) - 1)) * p.row_stride + d0;
+            c4[e] = 1.0f;
+            s4[e] = 0.0f;
+            if (d0 < p.rotary_dim) {
+                const uint64_t turns = static_cast<uint64_t>(pos) * __ldg(p.table + pair0 + e);
+                // the top 32 bits as a signed part of a turn, in half turns (2^-31 each)
+                sincospif(static_cast<float>(static_cast<int32_t>(turns >> 32)) * 4.656612873077393e-10f, &s4[e], &c4[e]);
+                c4[e] *= p.scale;
+                s4[e] *= p.scale;
             }
         }
-#pragma unroll
-        for (int u = 0; u < kRopeInFlight; ++u) {
-            float f[8];
-            const uint32_t raw[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+        if (p.interleaved) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float2 v = unpack2<T>(raw[e]);
-                f[2 * e] = v.x;
-                f[2 * e + 1] = v.y;
+                cs[2 * e] = cs[2 * e + 1] = c4[e];
+                sn[2 * e] = -s4[e];
+                sn[2 * e + 1] = s4[e];
             }
-            if (p.q_norm || p.k_norm) {
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float co = __shfl_sync(0xffffffffu, c4[e], partner), so = __shfl_sync(0xffffffffu, s4[e], partner);
+                cs[e] = second ? co : c4[e];
+                cs[e + 4] = second ? c4[e] : co;
+                sn[e] = second ? so : -s4[e];
+                sn[e + 4] = second ? s4[e] : -so;
+            }
+        }
+    }
+    const void *norm = kind == 0 ? p.q_norm : kind == 1 ? p.k_norm : nullptr;
+    if (norm) {
+        float w[8], wp[8];
+        unpack8<T>(__ldg(static_cast<const uint4 *>(norm) + sub), w);
+        unpack8<T>(__ldg(static_cast<const uint4 *>(norm) + partner % L), wp);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            cs[e] *= w[e];
+            sn[e] *= p.interleaved ? w[e ^ 1] : wp[e];
+        }
+    }
+
+    // (every lane runs the same number of steps: the shuffles are warp-wide)
+    const bool any_norm = p.q_norm || p.k_norm;
+    for (int i0 = 0;;) {
+#pragma unroll
+        for (int u = 0; u < kRopeInFlight; ++u) {
+            float f[8], y[8];
+            unpack8<T>(x[u], f);
+            float r = 1.0f;
+            if (any_norm) {
                 float ss = 0.0f;
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
@@ -157,38 +187,41 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p)
 #pragma unroll
                 for (int o = L / 2; o > 0; o /= 2)
                     ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                const uint4 w = kind[u] == 0 ? wq : wk;
-                if (kind[u] == 0 ? p.q_norm != nullptr : kind[u] == 1 && p.k_norm) {
-                    const float r = rsqrtf(ss * (1.0f / D) + p.eps);
-                    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float2 v = unpack2<T>(ww[e]);
-                        f[2 * e] = f[2 * e] * r * v.x;
-                        f[2 * e + 1] = f[2 * e + 1] * r * v.y;
-                    }
-                }
+                r = norm ? rsqrtf(ss * (1.0f / D) + p.eps) : 1.0f;
             }
-            float y[8];
             if (p.interleaved) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    y[e] = fmaf(f[e], cs[e], f[e ^ 1] * sn[e]);
+                for (int e = 0; e < 8; ++e) {
+                    y[e] = f[e] * cs[e];
+                    if (rotates)
+                        y[e] = fmaf(f[e ^ 1], sn[e], y[e]);
+                }
             } else {
+                uint4 xp;
+                xp.x = __shfl_sync(0xffffffffu, x[u].x, partner);
+                xp.y = __shfl_sync(0xffffffffu, x[u].y, partner);
+                xp.z = __shfl_sync(0xffffffffu, x[u].z, partner);
+                xp.w = __shfl_sync(0xffffffffu, x[u].w, partner);
+                float fp[8];
+                unpack8<T>(xp, fp);
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    y[e] = fmaf(f[e], cs[e], __shfl_sync(0xffffffffu, f[e], partner) * sn[e]);
+                for (int e = 0; e < 8; ++e) {
+                    y[e] = f[e] * cs[e];
+                    if (rotates)
+                        y[e] = fmaf(fp[e], sn[e], y[e]);
+                }
             }
-            uint4 r;
-            r.x = rotates ? pack2<T>(y[0], y[1]) : pack2<T>(f[0], f[1]);
-            r.y = rotates ? pack2<T>(y[2], y[3]) : pack2<T>(f[2], f[3]);
-            r.z = rotates ? pack2<T>(y[4], y[5]) : pack2<T>(f[4], f[5]);
-            r.w = rotates ? pack2<T>(y[6], y[7]) : pack2<T>(f[6], f[7]);
-            if (kind[u] == 2)
-                r = x[u];   // bit for bit, NaN payloads too
-            if (dst[u])
-                *reinterpret_cast<uint4 *>(dst[u]) = r;
+            uint4 out = x[u];   // values: bit for bit, NaN payloads too
+            if (kind != 2)
+                out = make_uint4(pack2<T>(y[0] * r, y[1] * r), pack2<T>(y[2] * r, y[3] * r), pack2<T>(y[4] * r, y[5] * r),
+                                 pack2<T>(y[6] * r, y[7] * r));
+            if (live && h0 + i0 + u < h1)
+                *reinterpret_cast<uint4 *>(dst + (i0 + u) * out_head) = out;
         }
+        i0 += kRopeInFlight;
+        if (i0 >= p.heads_per_item)
+            break;
+        load(i0);
     }
 }
 
