@@ -402,13 +402,16 @@ __device__ __forceinline__ void paged_softmax_warp(const PagedParams &p, const P
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t o_addr = tmem + lane_base + static_cast<uint32_t>(Cfg::O_COL + tile * D);
     const int row_tok = r / p.group, row_head = r - row_tok * p.group;
-    const float sl2 = p.scale_log2;
+    const float sl2 = p.scale_log2;   // not 0 (the host sees to it): a masked score times it is -inf
+    const uint32_t hidden = __float_as_uint(sl2 >= 0.0f ? -INFINITY : INFINITY);
     const uint32_t p_half = bar.p_half0 + 8u * tile;
     RingPos<Cfg::STAGES> ring_k;   // this block's K tile (its V tile is the next position)
     uint32_t count = 0;            // blocks this tile has worked on
     uint32_t va[32], vb[32];
-    Segment g;
-    while (next_segment<Cfg>(p, walk, g)) {
+    Segment g, next;
+    bool more = next_segment<Cfg>(p, walk, next);
+    while (more) {
+        g = next;
         // ---- rows and masks of the stretch
         const int first = tile * p.tile_tokens;              // of the item's tokens
         const int toks = min(p.tile_tokens, g.toks - first); // of this tile (<= 0: none)
@@ -466,125 +469,99 @@ __device__ __forceinline__ void paged_softmax_warp(const PagedParams &p, const P
             const uint32_t s_addr =
                 tmem + lane_base + static_cast<uint32_t>(Cfg::S_COL + (Cfg::NT == 1 ? static_cast<int>(count & 1u) : tile) * BKV);
             if (active) {
-                const bool all_seen = __all_sync(0xffffffffu, k0 + BKV <= seen);
-                // Two bodies, chosen per warp and block: no key masked for any row of the warp, or
-                // chunks of 32 keys one after the other, those that no row sees left out (on the
-                // diagonal a warp sees part of one chunk, all of those before, none after).
-                auto block = [&](auto full_tag) -> bool {
-                    constexpr bool full = decltype(full_tag)::value;
-                    const int lim = seen - k0;   // masked: keys of the block that this row sees
-                    float mb = -INFINITY;
-                    if constexpr (full) {
-                        // the extreme of the raw scores in four independent chains, scaled once
-                        float r0 = sl2 >= 0.0f ? -INFINITY : INFINITY, r1 = r0, r2 = r0, r3 = r0;
-                        tmem_chunks<CH>(s_addr, va, vb, [&](const uint32_t(&x)[32], int) {
-                            if (sl2 >= 0.0f) {
-#pragma unroll
-                                for (int e = 0; e < 32; e += 8) {
-                                    r0 = fmax3(r0, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
-                                    r1 = fmax3(r1, __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
-                                    r2 = fmax3(r2, __uint_as_float(x[e + 4]), __uint_as_float(x[e + 5]));
-                                    r3 = fmax3(r3, __uint_as_float(x[e + 6]), __uint_as_float(x[e + 7]));
-                                }
-                            } else {
-#pragma unroll
-                                for (int e = 0; e < 32; e += 8) {
-                                    r0 = fmin3(r0, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
-                                    r1 = fmin3(r1, __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
-                                    r2 = fmin3(r2, __uint_as_float(x[e + 4]), __uint_as_float(x[e + 5]));
-                                    r3 = fmin3(r3, __uint_as_float(x[e + 6]), __uint_as_float(x[e + 7]));
-                                }
-                            }
-                        });
-                        mb = (sl2 >= 0.0f ? fmax3(fmaxf(r0, r1), r2, r3) : fmin3(fminf(r0, r1), r2, r3)) * sl2;
-                    } else {
+                // Masked scores are overwritten in TMEM first, 32 keys at a time, only where a key is
+                // masked for some row of the warp: the code below, which every block runs, stays the
+                // only copy (a second, masked one was fetched anew at every item's end: 2.8 us a block
+                // against 0.95).
+                if (!__all_sync(0xffffffffu, k0 + BKV <= seen)) {
 #pragma unroll 1
-                        for (int c = 0; c < CH && __any_sync(0xffffffffu, row_ok && 32 * c < lim); ++c) {
+                    for (int c = 0; c < CH; ++c) {
+                        const int lim = seen - k0 - 32 * c;   // keys of these 32 that the row sees
+                        if (__all_sync(0xffffffffu, lim >= 32))
+                            continue;
+                        if (__any_sync(0xffffffffu, row_ok && lim > 0)) {
                             tmem_ld_32x32b_x32(s_addr + 32u * c, va);
                             tmem_ld_wait_regs(va);
-                            const int lim_c = lim - 32 * c;
-#pragma unroll
-                            for (int e = 0; e < 32; e += 2)
-                                mb = fmax3(mb, e < lim_c ? __uint_as_float(va[e]) * sl2 : -INFINITY,
-                                           e + 1 < lim_c ? __uint_as_float(va[e + 1]) * sl2 : -INFINITY);
                         }
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            va[e] = e < lim ? va[e] : hidden;
+                        tmem_st_32x32b_x32(s_addr + 32u * c, va);
                     }
-                    const bool raise = mb > m + kPagedRescale || m == -INFINITY;
-                    const float m_new = raise ? mb : m;
-                    const float m_use = m_new == -INFINITY ? 0.0f : m_new;
-                    const float alpha = raise && row_ok ? ex2_approx(m - m_use) : 1.0f;   // 0 on the first block
-                    if (any_block && __any_sync(0xffffffffu, alpha != 1.0f)) {
-                        // O holds the blocks before: once their product is complete, rescale the rows
-                        if (!(last_tile ? wait_warp(bar.empty0 + 8u * prev_v.slot, prev_v.parity, wc, ERR_EPILOGUE_ACCUMULATOR, lane)
-                                        : wait_warp(bar.pv_done, (count - 1u) & 1u, wc, ERR_EPILOGUE_ACCUMULATOR, lane)))
-                            return false;
-                        tc_fence_after_sync();
-#pragma unroll 1
-                        for (int c = 0; c < D / 32; ++c) {
-                            tmem_ld_32x32b_x32(o_addr + 32u * c, va);
-                            tmem_ld_wait_regs(va);
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                va[e] = __float_as_uint(__uint_as_float(va[e]) * alpha);
-                            tmem_st_32x32b_x32(o_addr + 32u * c, va);
-                        }
-                        tmem_st_wait();
-                    }
-                    uint64_t sum2[4] = {f32x2_pack(0.0f, 0.0f), f32x2_pack(0.0f, 0.0f), f32x2_pack(0.0f, 0.0f),
-                                        f32x2_pack(0.0f, 0.0f)};
-                    const uint64_t scale2 = f32x2_pack(sl2, sl2), neg_m2 = f32x2_pack(-m_use, -m_use);
-                    // P of 32 keys, over scores already read; keys from lim_c on are masked
-                    auto p_chunk = [&](const uint32_t(&x)[32], int c, int lim_c) {
-                        uint32_t pk[16];
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            float t0, t1;
-                            f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), scale2,
-                                                   neg_m2),
-                                         t0, t1);
-                            float p0 = ex2_approx(t0), p1 = ex2_approx(t1);
-                            if constexpr (!full) {
-                                p0 = 2 * i < lim_c ? p0 : 0.0f;
-                                p1 = 2 * i + 1 < lim_c ? p1 : 0.0f;
-                            }
-                            sum2[i & 3] = f32x2_add(sum2[i & 3], f32x2_pack(p0, p1));
-                            pk[i] = pack2<T>(p0, p1);
-                        }
-                        tmem_st_32x32b_x16(s_addr + 16u * static_cast<uint32_t>(c), pk);
-                        if (Cfg::NT == 2 && c == CH / 2 - 1) {
-                            // the first half of the keys: their product can start
-                            tmem_st_wait();
-                            tc_fence_before_sync();
-                            __syncwarp();
-                            if (lane == 0)
-                                mbar_arrive(p_half);
-                        }
-                    };
-                    if constexpr (full) {
-                        tmem_chunks<CH>(s_addr, va, vb, [&](const uint32_t(&x)[32], int c) { p_chunk(x, c, 32); });
-                    } else {
-#pragma unroll 1
-                        for (int c = 0; c < CH; ++c) {
-                            if (__any_sync(0xffffffffu, row_ok && 32 * c < lim)) {
-                                tmem_ld_32x32b_x32(s_addr + 32u * c, va);
-                                tmem_ld_wait_regs(va);
-                            } else {
-#pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    va[e] = 0;   // (P comes out as 0 for every row that counts)
-                            }
-                            p_chunk(va, c, lim - 32 * c);
-                        }
-                    }
-                    float s0, s1;
-                    f32x2_unpack(f32x2_add(f32x2_add(sum2[0], sum2[1]), f32x2_add(sum2[2], sum2[3])), s0, s1);
-                    l = l * alpha + (s0 + s1);
-                    m = m_new;
                     tmem_st_wait();
-                    return true;
-                };
-                if (!(all_seen ? block(std::true_type{}) : block(std::false_type{})))
-                    return;
+                }
+                // the extreme of the raw scores in four independent chains, scaled once
+                float r0 = sl2 >= 0.0f ? -INFINITY : INFINITY, r1 = r0, r2 = r0, r3 = r0;
+                tmem_chunks<CH>(s_addr, va, vb, [&](const uint32_t(&x)[32], int) {
+                    if (sl2 >= 0.0f) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) {
+                            r0 = fmax3(r0, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+                            r1 = fmax3(r1, __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
+                            r2 = fmax3(r2, __uint_as_float(x[e + 4]), __uint_as_float(x[e + 5]));
+                            r3 = fmax3(r3, __uint_as_float(x[e + 6]), __uint_as_float(x[e + 7]));
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) {
+                            r0 = fmin3(r0, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+                            r1 = fmin3(r1, __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
+                            r2 = fmin3(r2, __uint_as_float(x[e + 4]), __uint_as_float(x[e + 5]));
+                            r3 = fmin3(r3, __uint_as_float(x[e + 6]), __uint_as_float(x[e + 7]));
+                        }
+                    }
+                });
+                const float mb = (sl2 >= 0.0f ? fmax3(fmaxf(r0, r1), r2, r3) : fmin3(fminf(r0, r1), r2, r3)) * sl2;
+                const bool raise = mb > m + kPagedRescale || m == -INFINITY;
+                const float m_new = raise ? mb : m;
+                const float m_use = m_new == -INFINITY ? 0.0f : m_new;
+                const float alpha = raise && row_ok ? ex2_approx(m - m_use) : 1.0f;   // 0 on the first block
+                if (any_block && __any_sync(0xffffffffu, alpha != 1.0f)) {
+                    // O holds the blocks before: once their product is complete, rescale the rows
+                    if (!(last_tile ? wait_warp(bar.empty0 + 8u * prev_v.slot, prev_v.parity, wc, ERR_EPILOGUE_ACCUMULATOR, lane)
+                                    : wait_warp(bar.pv_done, (count - 1u) & 1u, wc, ERR_EPILOGUE_ACCUMULATOR, lane)))
+                        return;
+                    tc_fence_after_sync();
+#pragma unroll 1
+                    for (int c = 0; c < D / 32; ++c) {
+                        tmem_ld_32x32b_x32(o_addr + 32u * c, va);
+                        tmem_ld_wait_regs(va);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            va[e] = __float_as_uint(__uint_as_float(va[e]) * alpha);
+                        tmem_st_32x32b_x32(o_addr + 32u * c, va);
+                    }
+                    tmem_st_wait();
+                }
+                uint64_t sum2[4] = {f32x2_pack(0.0f, 0.0f), f32x2_pack(0.0f, 0.0f), f32x2_pack(0.0f, 0.0f),
+                                    f32x2_pack(0.0f, 0.0f)};
+                const uint64_t scale2 = f32x2_pack(sl2, sl2), neg_m2 = f32x2_pack(-m_use, -m_use);
+                tmem_chunks<CH>(s_addr, va, vb, [&](const uint32_t(&x)[32], int c) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        float t0, t1;
+                        f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), scale2, neg_m2),
+                                     t0, t1);
+                        const float p0 = ex2_approx(t0), p1 = ex2_approx(t1);
+                        sum2[i & 3] = f32x2_add(sum2[i & 3], f32x2_pack(p0, p1));
+                        pk[i] = pack2<T>(p0, p1);
+                    }
+                    tmem_st_32x32b_x16(s_addr + 16u * static_cast<uint32_t>(c), pk);   // over scores already read
+                    if (Cfg::NT == 2 && c == CH / 2 - 1) {
+                        // the first half of the keys: their product can start
+                        tmem_st_wait();
+                        tc_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(p_half);
+                    }
+                });
+                float s0, s1;
+                f32x2_unpack(f32x2_add(f32x2_add(sum2[0], sum2[1]), f32x2_add(sum2[2], sum2[3])), s0, s1);
+                l = l * alpha + (s0 + s1);
+                m = m_new;
+                tmem_st_wait();
             } else if (Cfg::NT == 2) {
                 __syncwarp();
                 if (lane == 0)
@@ -600,6 +577,7 @@ __device__ __forceinline__ void paged_softmax_warp(const PagedParams &p, const P
             ring_k = ring_v;
             ring_k.step();
         }
+        more = next_segment<Cfg>(p, walk, next);   // (while the last product runs)
         // ---- the stretch's result
         const bool starts = g.b0 == 0, ends = g.b1 == g.blocks;
         const bool whole = starts && ends;
@@ -628,23 +606,32 @@ __device__ __forceinline__ void paged_softmax_warp(const PagedParams &p, const P
         if (whole && p.keys == KEYS_ALL) {
             const float inv = 1.0f / l;
             T *dst = static_cast<T *>(p.out) + token * p.out_token + head * p.out_head;
-            uint4 piece[8];   // 64 columns
-            tmem_chunks<D / 32>(o_addr, va, vb, [&](const uint32_t(&x)[32], int c) {
+#pragma unroll 1
+            for (int c = 0; c < D; c += 64) {
+                tmem_ld_32x32b_x32(o_addr + static_cast<uint32_t>(c), va);
+                tmem_ld_32x32b_x32(o_addr + static_cast<uint32_t>(c) + 32u, vb);
+                tmem_ld_wait_regs(va);
+                tmem_ld_wait_regs(vb);
+                uint4 piece[8];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < 8; ++i) {
                     uint32_t w[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float a = __uint_as_float(x[8 * i + 2 * e]), bb = __uint_as_float(x[8 * i + 2 * e + 1]);
+                        const int k = 8 * (i & 3) + 2 * e;
+                        const float a = __uint_as_float(i < 4 ? va[k] : vb[k]), bb = __uint_as_float(i < 4 ? va[k + 1] : vb[k + 1]);
                         w[e] = l == 0.0f ? 0u : pack2<T>(a * inv, bb * inv);
                     }
-                    piece[4 * (c & 1) + i] = make_uint4(w[0], w[1], w[2], w[3]);
-                    if (Cfg::NT == 1 && row_ok)
-                        *reinterpret_cast<uint4 *>(dst + 32 * c + 8 * i) = piece[4 * (c & 1) + i];
+                    piece[i] = make_uint4(w[0], w[1], w[2], w[3]);
                 }
-                if (Cfg::NT == 2 && (c & 1))
-                    store_rows(stage, lane, piece, row_ok ? reinterpret_cast<char *>(dst + 32 * (c - 1)) : nullptr);
-            });
+                if (Cfg::NT == 2) {
+                    store_rows(stage, lane, piece, row_ok ? reinterpret_cast<char *>(dst + c) : nullptr);
+                } else if (row_ok) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        *reinterpret_cast<uint4 *>(dst + c + 8 * i) = piece[i];
+                }
+            }
             if (row_ok && p.lse)
                 p.lse[token * p.lse_token + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
             continue;
@@ -661,17 +648,22 @@ __device__ __forceinline__ void paged_softmax_warp(const PagedParams &p, const P
             ml = p.parts.ml + row;
         }
         if (any_block) {
-            tmem_chunks<D / 32>(o_addr, va, vb, [&](const uint32_t(&x)[32], int c) {
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+                tmem_ld_32x32b_x32(o_addr + static_cast<uint32_t>(c), va);
+                tmem_ld_wait_regs(va);
                 uint4 piece[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    piece[i] = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-                    if (Cfg::NT == 1 && row_ok)
-                        *reinterpret_cast<uint4 *>(dst + 32 * c + 4 * i) = piece[i];
+                for (int i = 0; i < 8; ++i)
+                    piece[i] = make_uint4(va[4 * i], va[4 * i + 1], va[4 * i + 2], va[4 * i + 3]);
+                if (Cfg::NT == 2) {
+                    store_rows(stage, lane, piece, row_ok ? reinterpret_cast<char *>(dst + c) : nullptr);
+                } else if (row_ok) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        *reinterpret_cast<uint4 *>(dst + c + 4 * i) = piece[i];
                 }
-                if (Cfg::NT == 2)
-                    store_rows(stage, lane, piece, row_ok ? reinterpret_cast<char *>(dst + 32 * c) : nullptr);
-            });
+            }
         }
         if (row_ok)
             *ml = make_float2(m, l);
@@ -1039,10 +1031,12 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, Cfg::CTAS_PER_SM)
                 // the barriers that free their K and V tiles.
                 RingPos<STAGES> pos;       // K tile of the current block
                 uint32_t na = 0, nb = 0;   // blocks of the first and of the second tile so far
-                Segment g;
+                Segment g, next;
                 const uint32_t sA = tmem + static_cast<uint32_t>(Cfg::S_COL), sB = sA + BKV;
                 const uint32_t oA = tmem + static_cast<uint32_t>(Cfg::O_COL), oB = oA + Cfg::D;
-                while (ok && next_segment<Cfg>(p, walk, g)) {
+                bool more = next_segment<Cfg>(p, walk, next);
+                while (ok && more) {
+                    g = next;
                     int mine = g.blocks;   // the first tile's blocks
                     if (p.keys != KEYS_PREFIX && g.toks > p.tile_tokens)
                         mine = max(1, (g.edge + (g.tok0 + p.tile_tokens - 1 - g.q0) + BKV) / BKV);
@@ -1075,6 +1069,7 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, Cfg::CTAS_PER_SM)
                             scores(0, pos, false);
                         scores(1, pos, g.b0 + 1 == g.b1);
                     }
+                    more = next_segment<Cfg>(p, walk, next);   // (while the softmax works)
                     for (int b = g.b0; ok && b < g.b1; ++b) {
                         RingPos<STAGES> v = pos, k_next;
                         v.step();

@@ -680,7 +680,10 @@ int gemm_paged_attention(gemm_ctx *ctx, const gemm_kv_cache *cache, const gemm_k
     p.kv_heads = static_cast<int>(cache->kv_heads);
     p.group = static_cast<int>(group);
     p.long_tokens = static_cast<int>(128 / group);
+    // (a scale of 0 becomes one that no finite score shows, so that -inf times it stays -inf)
     p.scale_log2 = scale * 1.4426950408889634f;
+    if (std::fabs(p.scale_log2) < 1.2e-38f)
+        p.scale_log2 = 1.2e-38f;
     p.out = out->data;
     p.out_token = out->token_stride;
     p.out_head = out->head_stride;
