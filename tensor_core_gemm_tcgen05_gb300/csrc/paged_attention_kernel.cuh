@@ -41,6 +41,7 @@ enum : int {
     KEYS_ALL = 0,     // the prefix (if any), then the sequence's own
     KEYS_OWN = 1,     // the sequence's own (the prefix is another launch's)
     KEYS_PREFIX = 2,  // the prefix, for the tokens of all sequences together
+    KEYS_BOTH = 3,    // the items of KEYS_PREFIX, then those of KEYS_OWN
 };
 // Which sequences a launch takes, by their new tokens against a tile's.
 enum : int { SEQS_ALL = 0, SEQS_SHORT = 1, SEQS_LONG = 2 };
@@ -64,7 +65,8 @@ struct PagedParams {
     const int *prefix_pages;
     int n_prefix_pages;
     int kv_heads, group;                // G: query heads per key head
-    int tile_tokens, long_tokens;       // tokens per tile of this launch; what a full tile takes, 128 / G
+    int tile_tokens, long_tokens;       // tokens per tile of this launch; what a full tile takes, 128 / G:
+                                        // the tile of prefix items
     int q_rows, q_bufs;                 // NT = 1: rows of a query buffer (whole groups of 8), buffers
     int keys, seqs;                     // KEYS_*, SEQS_*
     int launch;                         // index for the tokens' PartInfo
@@ -75,9 +77,10 @@ struct PagedParams {
     int64_t lse_token;
     PartsView parts;
     PartInfo *cuts;                     // [CTAs]; KEYS_ALL only
-    PartInfo *info;                     // [num_tokens][kv_heads]; not KEYS_ALL
-    float *row_o;                       // whole items, [num_tokens][heads][D]; not KEYS_ALL
-    float2 *row_ml;
+    // not KEYS_ALL, of own [0] and of prefix keys [1]:
+    PartInfo *info[2];                  // [num_tokens][kv_heads]
+    float *row_o[2];                    // whole items, [num_tokens][heads][D]
+    float2 *row_ml[2];
     uint32_t *err;
     uint64_t timeout_ns;
     int debug;                          // DEBUG_WITHHOLD_FIRST_LOAD
@@ -159,22 +162,28 @@ __device__ inline I floor_sum(I n, I m, I a, I b)
     return sum;
 }
 
-// The items of one sequence (or, KEYS_PREFIX, of all tokens together): tiles of NT * tile_tokens
-// tokens for each key head. `edge`: keys that the token before the first would see, counted from
-// the launch's first key (token i sees the edge + i + 1 first of them); fixed >= 0: every tile
-// has `fixed` blocks instead.
+// The items of one sequence (or the prefix items, of all tokens together): tiles of `step` tokens
+// for each key head. `edge`: keys that the token before the first would see, counted from the
+// items' first key (token i sees the edge + i + 1 first of them); fixed >= 0: every tile has
+// `fixed` blocks instead.
 struct SeqItems {
     int q0, n, kv, tiles, fixed;
-    int edge;
+    int edge, step;
     bool bad;
+    __device__ bool prefix() const { return fixed >= 0; }
 };
+
+// Sequences of a launch, the prefix counted as one; number s of them.
+__device__ __forceinline__ int seq_count(const PagedParams &p)
+{
+    return p.keys == KEYS_PREFIX ? 1 : p.keys == KEYS_BOTH ? p.batch.num_seqs + 1 : p.batch.num_seqs;
+}
 
 template <class Cfg>
 __device__ __forceinline__ SeqItems seq_items(const PagedParams &p, int s)
 {
     SeqItems q;
-    const int step = Cfg::NT * p.tile_tokens;
-    if (p.keys == KEYS_PREFIX) {
+    if (p.keys == KEYS_PREFIX || (p.keys == KEYS_BOTH && s == 0)) {
         const int a = min(max(__ldg(p.batch.q_start), 0), p.batch.num_tokens);
         const int b = min(max(__ldg(p.batch.q_start + p.batch.num_seqs), a), p.batch.num_tokens);
         q.q0 = a;
@@ -182,19 +191,21 @@ __device__ __forceinline__ SeqItems seq_items(const PagedParams &p, int s)
         q.kv = 0;
         q.fixed = (p.batch.prefix_len + Cfg::BKV - 1) / Cfg::BKV;
         q.edge = 0;
+        q.step = Cfg::NT * p.long_tokens;
         q.bad = false;
-        q.tiles = (q.n + step - 1) / step;
+        q.tiles = (q.n + q.step - 1) / q.step;
         return q;
     }
-    const SeqView v = load_seq(p.batch, s);
+    const SeqView v = load_seq(p.batch, p.keys == KEYS_BOTH ? s - 1 : s);
     q.q0 = v.q0;
     q.n = v.n;
     q.kv = v.kv;
     q.fixed = -1;
     q.edge = (p.keys == KEYS_ALL ? p.batch.prefix_len : 0) + v.kv - v.n;
+    q.step = Cfg::NT * p.tile_tokens;
     q.bad = v.bad;
     const bool mine = p.seqs == SEQS_ALL || (v.n > p.long_tokens) == (p.seqs == SEQS_LONG);
-    q.tiles = mine ? (v.n + step - 1) / step : 0;
+    q.tiles = mine ? (v.n + q.step - 1) / q.step : 0;
     return q;
 }
 
@@ -225,8 +236,9 @@ __device__ __forceinline__ int block_of(int u, int quantum, int blocks)
 
 // Units of all tiles of one key head.
 template <class Cfg>
-__device__ inline int64_t units_of_head(const SeqItems &q, int quantum, int step)
+__device__ inline int64_t units_of_head(const SeqItems &q, int quantum)
 {
+    const int step = q.step;
     if (q.tiles == 0)
         return 0;
     const int last = units_upto<Cfg>(q, quantum, q.n - 1);
@@ -248,7 +260,7 @@ __device__ inline int64_t units_of_head(const SeqItems &q, int quantum, int step
 
 // A CTA's walk over the units of its range.
 struct Walk {
-    int s;            // sequence (KEYS_PREFIX: 0)
+    int s;            // see seq_items()
     SeqItems q;
     int head, tile, unit, quantum;
     int64_t left;     // units left in the range
@@ -256,17 +268,38 @@ struct Walk {
 
 // One stretch of an item: key blocks [b0, b1) of `blocks`.
 struct Segment {
-    int s, head, tok0, toks;   // tokens [tok0, tok0 + toks) of the flat dimension
-    int q0, n, kv, edge;       // of the sequence
+    bool prefix;               // keys of the prefix
+    int s, head, tok0, toks;   // sequence; tokens [tok0, tok0 + toks) of the flat dimension
+    int tile_tokens;           // per tile
+    int q0, kv, edge;          // see SeqItems
     int b0, b1, blocks;
     int units;                 // of the item
     int64_t ahead;             // from the item's first unit to the end of the CTA's range
+
+    // Tokens of a tile: the first (of the item's) and how many. The only tile of an item is the
+    // last one, so that the barriers it completes are always the same.
+    template <int NT>
+    __device__ int tile_first(int tile) const { return NT == 1 || toks <= tile_tokens ? 0 : tile * tile_tokens; }
+    template <int NT>
+    __device__ int tile_toks(int tile) const
+    {
+        return NT == 2 && tile == 0 && toks <= tile_tokens ? 0 : min(tile_tokens, toks - tile_first<NT>(tile));
+    }
+    // Its blocks: the first tile of two may see fewer keys than the second.
+    template <int NT, int BKV>
+    __device__ int tile_blocks(int tile) const
+    {
+        if (NT == 1 || tile == 1)
+            return blocks;
+        if (toks <= tile_tokens)
+            return 0;
+        return prefix ? blocks : max(1, (edge + (tok0 + tile_tokens - 1 - q0) + BKV) / BKV);
+    }
 };
 
 template <class Cfg>
 __device__ __forceinline__ bool next_segment(const PagedParams &p, Walk &w, Segment &g)
 {
-    const int step = Cfg::NT * p.tile_tokens;
     do {
         if (w.left <= 0)
             return false;
@@ -275,19 +308,20 @@ __device__ __forceinline__ bool next_segment(const PagedParams &p, Walk &w, Segm
                 ++w.head;
             } else {
                 w.head = 0;
-                if (++w.s >= p.batch.num_seqs)
+                if (++w.s >= seq_count(p))
                     return false;
                 w.q = seq_items<Cfg>(p, w.s);
             }
             w.tile = 0;
         }
-        const int first = w.tile * step, toks = min(step, w.q.n - first);
-        g.s = w.s;
+        const int first = w.tile * w.q.step, toks = min(w.q.step, w.q.n - first);
+        g.prefix = w.q.prefix();
+        g.s = p.keys == KEYS_BOTH ? w.s - 1 : w.s;
+        g.tile_tokens = w.q.step / Cfg::NT;
         g.head = w.head;
         g.tok0 = w.q.q0 + first;
         g.toks = toks;
         g.q0 = w.q.q0;
-        g.n = w.q.n;
         g.kv = w.q.kv;
         g.edge = w.q.edge;
         g.blocks = blocks_upto<Cfg>(w.q, first + toks - 1);
@@ -401,7 +435,7 @@ __device__ __forceinline__ void paged_softmax_warp(const PagedParams &p, const P
     const int r = quarter * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t o_addr = tmem + lane_base + static_cast<uint32_t>(Cfg::O_COL + tile * D);
-    const int row_tok = r / p.group, row_head = r - row_tok * p.group;
+    const int row_tok = r / p.group, row_head = r - row_tok * p.group;   // token of the tile, head of the group
     const float sl2 = p.scale_log2;   // not 0 (the host sees to it): a masked score times it is -inf
     const uint32_t hidden = __float_as_uint(sl2 >= 0.0f ? -INFINITY : INFINITY);
     const uint32_t p_half = bar.p_half0 + 8u * tile;
@@ -413,12 +447,11 @@ __device__ __forceinline__ void paged_softmax_warp(const PagedParams &p, const P
     while (more) {
         g = next;
         // ---- rows and masks of the stretch
-        const int first = tile * p.tile_tokens;              // of the item's tokens
-        const int toks = min(p.tile_tokens, g.toks - first); // of this tile (<= 0: none)
+        const int first = g.tile_first<Cfg::NT>(tile), toks = g.tile_toks<Cfg::NT>(tile);
         const bool row_ok = row_tok < toks;
         const int token = g.tok0 + first + row_tok;
-        int seen = INT32_MAX;   // keys of this launch that the row sees (idle rows: as if all)
-        if (p.keys == KEYS_PREFIX) {
+        int seen = INT32_MAX;   // keys, from the item's first, that the row sees (idle rows: as if all)
+        if (g.prefix) {
             // normally all of the prefix; a token that stands inside it sees less
             int s = find_seq<32>(p.batch.q_start, p.batch.num_seqs, __shfl_sync(0xffffffffu, token, 0), lane);
             if (row_ok) {
@@ -432,11 +465,8 @@ __device__ __forceinline__ void paged_softmax_warp(const PagedParams &p, const P
         }
         const bool active = __any_sync(0xffffffffu, row_ok);
         // keys that any row of the item sees: rows of V past them are zeroed
-        const int alive = p.keys == KEYS_PREFIX ? p.batch.prefix_len : max(0, g.edge + (g.tok0 + g.toks - g.q0));
-        // this tile's last block (the first tile of a pair may see fewer keys than the second)
-        int mine = g.blocks;
-        if (!last_tile && p.keys != KEYS_PREFIX && g.toks > p.tile_tokens)
-            mine = max(1, (g.edge + (g.tok0 + p.tile_tokens - 1 - g.q0) + BKV) / BKV);
+        const int alive = g.prefix ? p.batch.prefix_len : max(0, g.edge + (g.tok0 + g.toks - g.q0));
+        const int mine = g.tile_blocks<Cfg::NT, BKV>(tile);
         float m = -INFINITY, l = 0.0f;
         bool any_block = false;
         RingPos<Cfg::STAGES> prev_v = ring_k;
@@ -590,7 +620,7 @@ __device__ __forceinline__ void paged_softmax_warp(const PagedParams &p, const P
                     p.cuts[blockIdx.x] = make_int4(g.tok0, g.toks, g.head, parts);
             } else {
                 for (int t = lane; t < g.toks; t += 32)
-                    p.info[static_cast<int64_t>(g.tok0 + t) * p.kv_heads + g.head] =
+                    p.info[g.prefix][static_cast<int64_t>(g.tok0 + t) * p.kv_heads + g.head] =
                         make_int4(static_cast<int>(blockIdx.x), parts, g.tok0, p.launch);
             }
         }
@@ -640,10 +670,11 @@ __device__ __forceinline__ void paged_softmax_warp(const PagedParams &p, const P
         float2 *ml;
         if (whole) {
             const int64_t row = static_cast<int64_t>(token) * (p.kv_heads * p.group) + head;
-            dst = p.row_o + row * D;
-            ml = p.row_ml + row;
+            dst = p.row_o[g.prefix] + row * D;
+            ml = p.row_ml[g.prefix] + row;
         } else {
-            const int64_t row = (static_cast<int64_t>(2 * blockIdx.x + (starts ? 1 : 0)) * p.parts.tiles + tile) * p.parts.rows + r;
+            const int64_t row =
+                (static_cast<int64_t>(2 * blockIdx.x + (starts ? 1 : 0)) * p.parts.tiles + (first > 0 ? 1 : 0)) * p.parts.rows + r;
             dst = p.parts.o + row * D;
             ml = p.parts.ml + row;
         }
@@ -674,8 +705,9 @@ __device__ __forceinline__ void paged_softmax_warp(const PagedParams &p, const P
 
 template <class Cfg>
 __global__ void __launch_bounds__(Cfg::NUM_THREADS, Cfg::CTAS_PER_SM)
-    paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
-                           const __grid_constant__ CUtensorMap tmap_v, const PagedParams p)
+    paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_qp,
+                           const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
+                           const __grid_constant__ PagedParams p)
 {
     constexpr int NT = Cfg::NT, ATOMS = Cfg::ATOMS, BKV = Cfg::BKV, STAGES = Cfg::STAGES;
     constexpr int WARPS = Cfg::NUM_THREADS / 32;
@@ -728,8 +760,7 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, Cfg::CTAS_PER_SM)
     grid_dependency_wait();   // nothing above touched global memory
 
     // ---- this CTA's share of the units
-    const int step = NT * p.tile_tokens;
-    const int seqs = p.keys == KEYS_PREFIX ? 1 : p.batch.num_seqs;
+    const int seqs = seq_count(p);
     // sum over the CTA's threads (block_sum, too), and over the threads before this one
     int64_t block_sum = 0;
     auto block_scan = [&](int64_t value, int64_t &ahead) -> int64_t {
@@ -758,7 +789,7 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, Cfg::CTAS_PER_SM)
         const SeqItems q = seq_items<Cfg>(p, s);
         if (q.bad)
             atomicCAS(p.err, 0u, static_cast<uint32_t>(ERR_BATCH_INDEX));
-        return p.kv_heads * units_of_head<Cfg>(q, quantum, step);
+        return p.kv_heads * units_of_head<Cfg>(q, quantum);
     };
     // units of the first chunk's sequence of this thread, those before it, and the sum over all
     int64_t own = 0, from = 0;
@@ -819,7 +850,7 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, Cfg::CTAS_PER_SM)
             const int64_t at = w.unit;
             for (int t0 = 0; t0 < w.q.tiles && done <= at; t0 += Cfg::NUM_THREADS) {
                 const int t = t0 + static_cast<int>(threadIdx.x);
-                const int units = t < w.q.tiles ? units_upto<Cfg>(w.q, quantum, min((t + 1) * step, w.q.n) - 1) : 0;
+                const int units = t < w.q.tiles ? units_upto<Cfg>(w.q, quantum, min((t + 1) * w.q.step, w.q.n) - 1) : 0;
                 int64_t first;
                 const int64_t all = block_scan(units, first);
                 if (units > 0 && done + first <= at && at < done + first + units) {
@@ -844,7 +875,6 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, Cfg::CTAS_PER_SM)
         // boxes of its K and V tiles.
         const int page_rows = 1 << p.batch.page_shift;
         const int box_rows = min(page_rows, BKV), boxes = BKV / box_rows;   // boxes per atom of a tile
-        const int key_base = p.keys == KEYS_OWN ? p.batch.prefix_len : 0;
         RingPos<STAGES> pos;
         uint32_t issued = 0, issued_parity = 0, q_issued = 0, q_issued_parity = 0;
         QueryPos qp(NT == 1 ? p.q_bufs : 1);
@@ -856,18 +886,20 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, Cfg::CTAS_PER_SM)
                 break;
             const uint32_t q_full = bar.q_full0 + 8u * qp.buf;
             if (lane == 0)
-                mbar_arrive_expect_tx(q_full, static_cast<uint32_t>(NT * ATOMS * p.tile_tokens * p.group * 128));
+                mbar_arrive_expect_tx(q_full, static_cast<uint32_t>(NT * ATOMS * g.tile_tokens * p.group * 128));
             __syncwarp();
             if (lane < NT * ATOMS) {
                 const int t = lane / ATOMS, a = lane % ATOMS;
                 const int at = NT == 1 ? (qp.buf * ATOMS + a) * p.q_rows * 128 : t * Cfg::Q_TILE + a * Cfg::Q_ATOM;
-                tma_load_4d(sQ + static_cast<uint32_t>(at), &tmap_q, q_full, 64 * a, 0, g.head, g.tok0 + t * p.tile_tokens);
+                tma_load_4d(sQ + static_cast<uint32_t>(at), g.prefix ? &tmap_qp : &tmap_q, q_full, 64 * a, 0, g.head,
+                            g.tok0 + g.tile_first<NT>(t));
             }
             q_issued |= 1u << qp.buf;
             q_issued_parity = (q_issued_parity & ~(1u << qp.buf)) | (qp.parity << qp.buf);
             qp.step();
             // pages of this stretch: numbers past the last key's page (and bad ones) become
             // num_pages, which TMA reads as zeros
+            const int key_base = g.prefix || p.keys == KEYS_ALL ? 0 : p.batch.prefix_len;
             const int own_pages = (g.kv + page_rows - 1) >> p.batch.page_shift;
             auto page_of = [&](int b) -> int {
                 if (lane >= boxes || b >= g.b1)
@@ -876,7 +908,7 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, Cfg::CTAS_PER_SM)
                 int id;
                 if (lp < p.n_prefix_pages)
                     id = __ldg(p.prefix_pages + lp);
-                else if (p.keys != KEYS_PREFIX && lp - p.n_prefix_pages < own_pages)
+                else if (!g.prefix && lp - p.n_prefix_pages < own_pages)
                     id = __ldg(p.batch.table + g.s * p.batch.table_stride + (lp - p.n_prefix_pages));
                 else
                     return p.batch.num_pages;
@@ -1037,9 +1069,7 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, Cfg::CTAS_PER_SM)
                 bool more = next_segment<Cfg>(p, walk, next);
                 while (ok && more) {
                     g = next;
-                    int mine = g.blocks;   // the first tile's blocks
-                    if (p.keys != KEYS_PREFIX && g.toks > p.tile_tokens)
-                        mine = max(1, (g.edge + (g.tok0 + p.tile_tokens - 1 - g.q0) + BKV) / BKV);
+                    const int mine = g.tile_blocks<NT, BKV>(0);   // the first tile's blocks
                     ok = wait_bounded(bar.q_full0, qp.parity, wc, ERR_MMA_OPERANDS);
                     qp.step();
                     auto product = [&](int t, int slot, bool add) -> bool {
@@ -1137,6 +1167,7 @@ struct CombineParams {
     PartsView parts[3];
     int ctas[3];                    // grid sizes of the launches
     int tile_tokens[3];
+    int prefix_tokens;              // tokens per tile of prefix items
     const PartInfo *cuts[3];        // of the CTAs, or (joint) of the tokens:
     int64_t blocks[3];              // combine blocks of each launch: CTAs x blocks per item
     const PartInfo *own, *prefix;   // [num_tokens][kv_heads]
@@ -1154,6 +1185,11 @@ constexpr int kCombineRows = 32;    // rows of an item per block
 // (prompts 175.4 us with 8 and 2, 178.2 with 8 and 4, 177.5 with 4 and 4).
 constexpr int kCombineFew = 8, kCombineStep = 2;
 
+struct PartAt {
+    const float *o;
+    const float2 *ml;
+};
+
 // A row's running sum over parts: lane's D / 32 dimensions.
 template <int V>
 struct RowSum {
@@ -1161,13 +1197,13 @@ struct RowSum {
     float acc[V] = {};
 
     // Adds n parts, in order: lane i of a step of 32 fetches (m, l) of part i, then all lanes add up
-    // their dimensions, eight parts' loads at a time. part(i): the row of part i in `ml` and `o`.
-    template <class Row>
-    __device__ __forceinline__ void add(const float *__restrict__ o, const float2 *__restrict__ ml_of, int n, int lane, Row &&part)
+    // their dimensions, eight parts' loads at a time. part(i): where part i's O and (m, l) are.
+    template <class Part>
+    __device__ __forceinline__ void add(int n, int lane, Part &&part)
     {
         for (int i0 = 0; i0 < n; i0 += 32) {
             const int k = min(32, n - i0);
-            const float2 ml = lane < k ? ml_of[part(i0 + lane)] : make_float2(-INFINITY, 0.0f);
+            const float2 ml = lane < k ? *part(i0 + lane).ml : make_float2(-INFINITY, 0.0f);
             float top = ml.x;
 #pragma unroll
             for (int s = 16; s > 0; s /= 2)
@@ -1190,7 +1226,7 @@ struct RowSum {
                 float x[8][V];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {   // (past the end: the last part again, with weight 0)
-                    const float *src = o + part(i0 + min(j0 + j, k - 1)) * (32 * V) + lane * V;
+                    const float *src = part(i0 + min(j0 + j, k - 1)).o + lane * V;
                     if constexpr (V == 4)
                         *reinterpret_cast<float4 *>(x[j]) = *reinterpret_cast<const float4 *>(src);
                     else
@@ -1331,7 +1367,10 @@ __global__ void __launch_bounds__(32 * kCombineWarps) paged_combine_kernel(const
             if (!place(row, tile, r, tok, g))
                 continue;
             RowSum<V> sum;
-            sum.add(v.o, v.ml, cut.w, lane, [&](int k) { return part_row(v, cta, k, tile, r); });
+            sum.add(cut.w, lane, [&](int k) {
+                const int64_t at_row = part_row(v, cta, k, tile, r);
+                return PartAt{v.o + at_row * D, v.ml + at_row};
+            });
             sum.template write<T>(p, cut.x + tok, cut.z * p.group + g, lane);
         }
     } else {
@@ -1340,26 +1379,34 @@ __global__ void __launch_bounds__(32 * kCombineWarps) paged_combine_kernel(const
         const int64_t row = static_cast<int64_t>(blockIdx.x) * kCombineWarps + warp;
         const int64_t token = row / heads;
         const int head = static_cast<int>(row - token * heads);
-        if (token >= p.num_tokens || token < __ldg(p.q_start) || token >= __ldg(p.q_start + p.num_seqs))
-            return;   // of no sequence: nothing was written for it
+        if (token >= p.num_tokens)
+            return;
         const int kv_head = head / p.group, g = head - kv_head * p.group;
+        const int4 info[2] = {p.own[token * p.kv_heads + kv_head], p.prefix[token * p.kv_heads + kv_head]};
+        if (token < __ldg(p.q_start) || token >= __ldg(p.q_start + p.num_seqs))
+            return;   // of no sequence: nothing was written for it
+        int n[2], tile[2], r[2];
 #pragma unroll
-        for (int side = 1; side >= 0; --side) {
-            const int4 info = (side == 1 ? p.prefix : p.own)[token * p.kv_heads + kv_head];
+        for (int side = 0; side < 2; ++side) {
+            const int4 &f = info[side];
+            const int i = min(max(f.w, 0), p.launches - 1);
+            const int tt = side == 1 ? p.prefix_tokens : p.tile_tokens[i], at = static_cast<int>(token - f.z);
             // (a token of an unsorted q_start may have no entry: what is not a possible one is left out)
-            if (info.w < 0 || info.w >= p.launches || info.y < 1 || info.x < 0 || info.y > p.ctas[info.w] - info.x)
-                continue;
-            if (info.y == 1) {
-                sum.add(p.row_o[side], p.row_ml[side], 1, lane, [&](int) { return row; });
-                continue;
-            }
-            const PartsView &v = p.parts[info.w];
-            const int tt = p.tile_tokens[info.w], at = static_cast<int>(token - info.z);
-            if (at < 0 || at >= v.tiles * tt)
-                continue;
-            const int tile = at / tt, r = (at - tile * tt) * p.group + g;
-            sum.add(v.o, v.ml, info.y, lane, [&](int k) { return part_row(v, info.x, k, tile, r); });
+            const bool ok = f.w == i && f.y >= 1 && f.x >= 0 && f.y <= p.ctas[i] - f.x &&
+                            (f.y == 1 || (at >= 0 && at < p.parts[i].tiles * tt));
+            n[side] = ok ? f.y : 0;
+            tile[side] = at / tt;
+            r[side] = (at - tile[side] * tt) * p.group + g;
         }
+        sum.add(n[1] + n[0], lane, [&](int k) {
+            const int side = k < n[1] ? 1 : 0;
+            const int4 &f = info[side];
+            if (f.y == 1)
+                return PartAt{p.row_o[side] + row * D, p.row_ml[side] + row};
+            const PartsView &v = p.parts[f.w];
+            const int64_t at_row = part_row(v, f.x, side == 1 ? k : k - n[1], tile[side], r[side]);
+            return PartAt{v.o + at_row * D, v.ml + at_row};
+        });
         sum.template write<T>(p, token, head, lane);
     }
 }

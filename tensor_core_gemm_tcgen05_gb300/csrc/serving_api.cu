@@ -21,6 +21,7 @@ namespace {
 using i128 = __int128;
 constexpr int64_t kMaxStride = (int64_t(1) << 39) - 8;   // elements: tensor maps hold strides below 2^40 bytes
 constexpr int64_t kMaxHeads = 1 << 16;
+constexpr int64_t kJointTiles = 4;   // tiles of rows up to which prefix and own keys share a launch
 
 // ---- strided operands ------------------------------------------------------------------------
 
@@ -368,22 +369,29 @@ AttnPlan attention_plan(const gemm_ctx *ctx, const gemm_kv_cache &c, const gemm_
         const int64_t units = c.kv_heads * max_tiles * std::max<int64_t>(1, (key_count + bkv - 1) / bkv);
         l.grid = std::min<int64_t>(static_cast<int64_t>(ctx->num_sms) * (tiles == 1 ? 2 : 1), units);
     };
-    if (pl.joint)
+    // Few tiles of short sequences: prefix and own keys are the items of one launch.
+    const bool may_long = (b.max_q == 0 || b.max_q > tq) && T > tq;
+    const bool one_launch = pl.joint && flat_tiles <= kJointTiles && !may_long;
+    if (pl.joint && !one_launch)
         add(flat_tiles > 1 ? 2 : 1, tq, gb300::KEYS_PREFIX, gb300::SEQS_ALL, flat_tiles, prefix);
     const int keys = pl.joint ? gb300::KEYS_OWN : gb300::KEYS_ALL;
     const int64_t seen = own + (pl.joint ? 0 : prefix);
     // Sequences with more new tokens than a tile takes go to the two-tile kernel, the others to
-    // the one-tile kernel; a kernel that no sequence can need is left out, and if max_q says that
-    // all are short the one-tile kernel takes whatever there is.
-    const bool may_long = (b.max_q == 0 || b.max_q > tq) && T > tq;
-    const bool may_short = !may_long || b.num_seqs > 1;
+    // the one-tile kernel. If max_q says that all are short the one-tile kernel takes whatever there
+    // is; if they have more than a tile's on average the two-tile kernel does (a second launch for
+    // a few short ones costs more than their idle rows: nine sequences of 1 to 512 tokens 145 ->
+    // 115 us).
+    const bool may_short = !may_long || (b.num_seqs > 1 && T < b.num_seqs * tq);
     if (may_long)
         add(2, tq, keys, may_short ? gb300::SEQS_LONG : gb300::SEQS_ALL, std::min(T, T / (2 * tq) + b.num_seqs), seen);
     if (may_short) {
         // tiles no larger than the sequences need, as far as that is known: less to load per item,
         // and several query buffers in the space of one full tile
         const int64_t tt = b.max_q > 0 ? std::min(tq, b.max_q) : tq;
-        add(1, tt, keys, may_long ? gb300::SEQS_SHORT : gb300::SEQS_ALL, std::min(T, T / tt + b.num_seqs), seen);
+        add(1, tt, one_launch ? gb300::KEYS_BOTH : keys, may_long ? gb300::SEQS_SHORT : gb300::SEQS_ALL,
+            std::min(T, T / tt + b.num_seqs) + (one_launch ? flat_tiles : 0), std::max(seen, prefix));
+        if (one_launch)
+            pl.launch[pl.count - 1].rows = std::min(tq, T) * group;
     }
     int64_t at = 0;
     auto take = [&](int64_t bytes) {
@@ -445,10 +453,10 @@ bool encode_4d(const gemm_ctx *ctx, CUtensorMap *map, const void *ptr, int dtype
 }
 
 template <class Cfg>
-cudaError_t launch_paged(int64_t grid, cudaStream_t stream, const CUtensorMap &tq, const CUtensorMap &tk,
-                         const CUtensorMap &tv, const gb300::PagedParams &p)
+cudaError_t launch_paged(int64_t grid, cudaStream_t stream, const CUtensorMap &tq, const CUtensorMap &tqp,
+                         const CUtensorMap &tk, const CUtensorMap &tv, const gb300::PagedParams &p)
 {
-    return launch_serving(gb300::paged_attention_kernel<Cfg>, grid, Cfg::NUM_THREADS, Cfg::SMEM_BYTES, stream, tq, tk, tv, p);
+    return launch_serving(gb300::paged_attention_kernel<Cfg>, grid, Cfg::NUM_THREADS, Cfg::SMEM_BYTES, stream, tq, tqp, tk, tv, p);
 }
 
 // fn(config) with the PagedConfig of these run-time choices.
@@ -693,7 +701,7 @@ int gemm_paged_attention(gemm_ctx *ctx, const gemm_kv_cache *cache, const gemm_k
     p.timeout_ns = ctx->timeout_ns;
     p.debug = ctx->debug & GEMM_DEBUG_WITHHOLD_FIRST_LOAD;
     char *ws = static_cast<char *>(workspace);
-    CUtensorMap tq, tk, tv;
+    CUtensorMap tq, tqp, tk, tv;   // tqp: queries of prefix items, a full tile
     gb300::CombineParams cp = {};
     cp.num_tokens = static_cast<int>(tokens);
     cp.kv_heads = p.kv_heads;
@@ -701,6 +709,7 @@ int gemm_paged_attention(gemm_ctx *ctx, const gemm_kv_cache *cache, const gemm_k
     cp.num_seqs = p.batch.num_seqs;
     cp.q_start = batch->q_start;
     cp.launches = pl.count;
+    cp.prefix_tokens = p.long_tokens;
     cp.own = reinterpret_cast<gb300::PartInfo *>(ws + pl.own_off);
     cp.prefix = reinterpret_cast<gb300::PartInfo *>(ws + pl.prefix_off);
     for (int i = 0; i < 2; ++i) {
@@ -718,20 +727,22 @@ int gemm_paged_attention(gemm_ctx *ctx, const gemm_kv_cache *cache, const gemm_k
     int64_t combine_grid = 0;
     for (int i = 0; i < pl.count; ++i) {
         const AttnLaunch &l = pl.launch[i];
-        const bool prefix = l.keys == gb300::KEYS_PREFIX;
         p.keys = l.keys;
         p.seqs = l.seqs;
         p.launch = i;
         p.tile_tokens = static_cast<int>(l.tile_tokens);
-        p.q_rows = static_cast<int>((l.tile_tokens * group + 7) / 8 * 8);
+        p.q_rows = l.keys == gb300::KEYS_BOTH ? 128 : static_cast<int>((l.tile_tokens * group + 7) / 8 * 8);
         p.q_bufs = std::min(128 / p.q_rows, gb300::PagedConfig<__half, 128, 1>::Q_BUFS);
         p.parts.o = reinterpret_cast<float *>(ws + l.o_off);
         p.parts.ml = reinterpret_cast<float2 *>(ws + l.ml_off);
         p.parts.rows = static_cast<int>(l.rows);
         p.parts.tiles = l.tiles;
-        p.info = reinterpret_cast<gb300::PartInfo *>(ws + (prefix ? pl.prefix_off : pl.own_off));
-        p.row_o = reinterpret_cast<float *>(ws + pl.row_o_off[prefix]);
-        p.row_ml = reinterpret_cast<float2 *>(ws + pl.row_ml_off[prefix]);
+        p.info[0] = reinterpret_cast<gb300::PartInfo *>(ws + pl.own_off);
+        p.info[1] = reinterpret_cast<gb300::PartInfo *>(ws + pl.prefix_off);
+        for (int side = 0; side < 2; ++side) {
+            p.row_o[side] = reinterpret_cast<float *>(ws + pl.row_o_off[side]);
+            p.row_ml[side] = reinterpret_cast<float2 *>(ws + pl.row_ml_off[side]);
+        }
         p.cuts = reinterpret_cast<gb300::PartInfo *>(ws + l.cuts_off);
         cp.parts[i] = p.parts;
         cp.ctas[i] = static_cast<int>(l.grid);
@@ -740,9 +751,12 @@ int gemm_paged_attention(gemm_ctx *ctx, const gemm_kv_cache *cache, const gemm_k
         cp.blocks[i] = l.grid * ((l.tiles * l.rows + gb300::kCombineRows - 1) / gb300::kCombineRows);
         combine_grid += cp.blocks[i];
         const uint32_t rows = static_cast<uint32_t>(std::min<int64_t>(cache->page_size, l.tiles == 1 ? 64 : 128));
-        if (!encode_4d(ctx, &tq, q->data, cache->dtype, {d, group, cache->kv_heads, tokens},
-                       {q->head_stride, group * q->head_stride, q->token_stride},
-                       {64, static_cast<uint32_t>(group), 1, static_cast<uint32_t>(l.tile_tokens)}))
+        auto encode_q = [&](CUtensorMap *map, int64_t tile_tokens) {
+            return encode_4d(ctx, map, q->data, cache->dtype, {d, group, cache->kv_heads, tokens},
+                             {q->head_stride, group * q->head_stride, q->token_stride},
+                             {64, static_cast<uint32_t>(group), 1, static_cast<uint32_t>(tile_tokens)});
+        };
+        if (!encode_q(&tq, l.tile_tokens) || !encode_q(&tqp, 128 / group))
             return GEMM_ERR_LAUNCH;
         const int64_t dims[4] = {d, cache->page_size, cache->kv_heads, cache->num_pages};
         const int64_t strides[3] = {cache->row_stride, cache->head_stride, cache->page_stride};
@@ -750,7 +764,7 @@ int gemm_paged_attention(gemm_ctx *ctx, const gemm_kv_cache *cache, const gemm_k
             !encode_4d(ctx, &tv, cache->v, cache->dtype, dims, strides, {64, rows, 1, 1}))
             return GEMM_ERR_LAUNCH;
         const cudaError_t e = with_config(cache->dtype, d, l.tiles, [&](auto cfg) {
-            return launch_paged<decltype(cfg)>(l.grid, st, tq, tk, tv, p);
+            return launch_paged<decltype(cfg)>(l.grid, st, tq, tqp, tk, tv, p);
         });
         if (e != cudaSuccess)
             return cuda_fail(ctx, e, GEMM_ERR_LAUNCH);

@@ -126,10 +126,14 @@ def test_results_do_not_depend_on_max_q(ctx, max_q):
     ([40, 1, 3], [10, 1, 2], 4, 1, 64, 16, 2),                          # ... and some before it
     ([300, 2], [300, 2], 8, 2, 128, 64, 3),                             # not joint: the prefix is read with the own keys
     ([1], [5], 8, 2, 128, 16, 30),
-    ([0, 0, 1], [0, 3, 4], 2, 2, 64, 128, 1)], ids=str)
+    ([0, 0, 1], [0, 3, 4], 2, 2, 64, 128, 1),
+    ([1] * 130, [200] * 130, 5, 1, 128, 32, 12),                        # more tiles than share a launch
+    ([2] * 30 + [90, 1], [500] * 30 + [90, 7], 4, 2, 64, 16, 33)], ids=lambda v: str(v)[:40])
 @pytest.mark.parametrize("dtype", list(TYPES))
 def test_shared_prefix(ctx, n_q, kv, hq, hk, d, page, prefix, dtype):
-    check(ctx, problem(n_q, kv, dtype, hq, hk, d, page, prefix=prefix, spare=1, seed=7), (n_q, prefix), max_q=max(n_q))
+    p = problem(n_q, kv, dtype, hq, hk, d, page, prefix=prefix, spare=1, seed=7)
+    check(ctx, p, (n_q, prefix), max_q=max(n_q))   # (what is known decides whether one launch takes all keys)
+    check(ctx, p, (n_q, prefix))
 
 
 def test_many_sequences(ctx):
