@@ -26,8 +26,8 @@
 //    few rows: bound by HBM; one CTA's latencies overlap the other's). NT = 2: two tiles share
 //    each block of 128 keys, one CTA per SM (for many rows: bound by the tensor cores; one
 //    tile's softmax runs during the other's products).
-//  * Warps: 0 producer (TMA), 1 MMA issuer, then four softmax warps per tile, a row per thread,
-//    as in attention_fwd_kernel. Every wait is bounded.
+//  * Warps: four softmax warps per tile, a row per thread, an MMA issuer and a producer (TMA), as
+//    in attention_fwd_kernel. Every wait is bounded.
 #pragma once
 
 #include <type_traits>
@@ -68,6 +68,7 @@ struct PagedParams {
     int tile_tokens, long_tokens;       // tokens per tile of this launch; what a full tile takes, 128 / G:
                                         // the tile of prefix items
     int q_rows, q_bufs;                 // NT = 1: rows of a query buffer (whole groups of 8), buffers
+    int busy_warps;                     // softmax warps of a tile that can have rows (the others leave at once)
     int keys, seqs;                     // KEYS_*, SEQS_*
     int launch;                         // index for the tokens' PartInfo
     float scale_log2;                   // scale * log2(e)
@@ -111,6 +112,9 @@ struct PagedConfig {
     static constexpr int ITEM_COST = NT == 1 ? 2 : 2;
     static constexpr int SMEM_BYTES = 1024 + BAR_OFF + NUM_BARS * 8 + 16;
     static constexpr int NUM_THREADS = 64 + NT * 128;
+    // Warps: the softmax warps of the tiles (warp w reads the Tensor Memory lanes of quarter w mod 4),
+    // then the MMA issuer and the producer
+    static constexpr int MMA_WARP = 4 * NT, PRODUCER_WARP = 4 * NT + 1;
     static constexpr int CTAS_PER_SM = NT == 1 ? 2 : 1;
     // TMEM: NT = 1: two score buffers of 64 columns, O; NT = 2: S_A S_B O_A O_B. P (16-bit pairs)
     // over the first half of its scores.
@@ -432,6 +436,8 @@ __device__ __forceinline__ void paged_softmax_warp(const PagedParams &p, const P
     // then, too); the first of two tiles has barriers of its own.
     const bool last_tile = tile == Cfg::NT - 1;
     const int quarter = warp & 3;
+    if (quarter >= p.busy_warps)
+        return;
     const int r = quarter * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t o_addr = tmem + lane_base + static_cast<uint32_t>(Cfg::O_COL + tile * D);
@@ -489,7 +495,7 @@ __device__ __forceinline__ void paged_softmax_warp(const PagedParams &p, const P
                     return;
                 const uint32_t v_tile = ring + static_cast<uint32_t>(ring_v.slot) * Cfg::KV_TILE;
                 const int from = max(0, alive - k0);
-                for (int i = from * 8 + r; i < BKV * 8; i += 128)
+                for (int i = from * 8 + r; i < BKV * 8; i += 32 * p.busy_warps)
 #pragma unroll
                     for (int a = 0; a < Cfg::ATOMS; ++a)
                         st_shared_v4(v_tile + static_cast<uint32_t>(a) * Cfg::KV_ATOM + static_cast<uint32_t>(i) * 16u,
@@ -743,8 +749,8 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, Cfg::CTAS_PER_SM)
         mbar_init(bar.s_full, 1);
         mbar_init(bar.pv_done, 1);
         for (int t = 0; t < NT; ++t) {
-            mbar_init(bar.p_half0 + 8u * t, 4);   // the four softmax warps
-            mbar_init(bar.p_full0 + 8u * t, 4);
+            mbar_init(bar.p_half0 + 8u * t, static_cast<uint32_t>(p.busy_warps));   // the tile's softmax warps
+            mbar_init(bar.p_full0 + 8u * t, static_cast<uint32_t>(p.busy_warps));
         }
         *abort_flag = 0;
         start.left = 0;
@@ -753,7 +759,7 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, Cfg::CTAS_PER_SM)
         tma_prefetch_desc(&tmap_k);
         tma_prefetch_desc(&tmap_v);
     }
-    if (warp == 1) {
+    if (warp == Cfg::MMA_WARP) {
         tmem_alloc<1>(smem_u32(tmem_slot), Cfg::TMEM_COLS);
         tmem_relinquish<1>();
     }
@@ -869,7 +875,7 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, Cfg::CTAS_PER_SM)
 
     if (!works) {
         // fewer units than CTAs
-    } else if (warp == 0) {
+    } else if (warp == Cfg::PRODUCER_WARP) {
         // ---------------------------------------------------------------- TMA producer
         // Lane i fetches the page number of page i of a block and, with the others, issues the
         // boxes of its K and V tiles.
@@ -957,7 +963,7 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, Cfg::CTAS_PER_SM)
                     wait_until(bar.full0 + 8u * s, (issued_parity >> s) & 1u, p.timeout_ns, p.err);
         }
         __syncwarp();
-    } else if (warp == 1) {
+    } else if (warp == Cfg::MMA_WARP) {
         // ---------------------------------------------------------------- MMA issuer
         if (lane == 0) {
             // descriptors: Q and K K-major (atoms of 64 dims, 32 bytes per 16), V MN-major (atoms of
@@ -1146,13 +1152,13 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, Cfg::CTAS_PER_SM)
         __syncwarp();
     } else {
         // ---------------------------------------------------------------- softmax
-        paged_softmax_warp<Cfg>(p, bar, wc, tmem, ring, base + Cfg::STAGE_OFF + static_cast<uint32_t>(warp - 2) * Cfg::STAGE_WARP, walk,
-                                shares, (warp - 2) >> 2, warp, lane);
+        paged_softmax_warp<Cfg>(p, bar, wc, tmem, ring, base + Cfg::STAGE_OFF + static_cast<uint32_t>(warp) * Cfg::STAGE_WARP, walk,
+                                shares, warp >> 2, warp, lane);
     }
 
     tc_fence_before_sync();
     __syncthreads();
-    if (warp == 1) {
+    if (warp == Cfg::MMA_WARP) {
         tc_fence_after_sync();
         tmem_dealloc<1>(tmem, Cfg::TMEM_COLS);
     }

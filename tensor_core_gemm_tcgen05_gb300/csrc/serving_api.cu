@@ -732,6 +732,7 @@ int gemm_paged_attention(gemm_ctx *ctx, const gemm_kv_cache *cache, const gemm_k
         p.launch = i;
         p.tile_tokens = static_cast<int>(l.tile_tokens);
         p.q_rows = l.keys == gb300::KEYS_BOTH ? 128 : static_cast<int>((l.tile_tokens * group + 7) / 8 * 8);
+        p.busy_warps = l.keys == gb300::KEYS_BOTH ? 4 : static_cast<int>((l.tile_tokens * group + 31) / 32);
         p.q_bufs = std::min(128 / p.q_rows, gb300::PagedConfig<__half, 128, 1>::Q_BUFS);
         p.parts.o = reinterpret_cast<float *>(ws + l.o_off);
         p.parts.ml = reinterpret_cast<float2 *>(ws + l.ml_off);
