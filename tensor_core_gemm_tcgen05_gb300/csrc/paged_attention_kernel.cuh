@@ -184,7 +184,7 @@ __device__ __forceinline__ int seq_count(const PagedParams &p)
 }
 
 template <class Cfg>
-__device__ __forceinline__ SeqItems seq_items(const PagedParams &p, int s)
+__device__ __noinline__ SeqItems seq_items(const PagedParams &p, int s)
 {
     SeqItems q;
     if (p.keys == KEYS_PREFIX || (p.keys == KEYS_BOTH && s == 0)) {
@@ -385,19 +385,17 @@ struct RingPos {
 // ---- softmax warp ------------------------------------------------------------------------------
 
 // Reads the columns addr .. addr + 32 N - 1 of this warp's TMEM lanes in chunks of 32 and hands
-// each to fn(registers, chunk); the next chunk's load is in flight meanwhile. Warp-collective.
+// each to fn(registers, chunk). Warp-collective. A loop, one load at a time: unrolled, with the
+// next load in flight, the softmax waits for instructions instead (prompts 151.2 against 160.5 us,
+// drafts 80.6 against 83.2).
 template <int N, class Fn>
-__device__ __forceinline__ void tmem_chunks(uint32_t addr, uint32_t (&va)[32], uint32_t (&vb)[32], Fn &&fn)
+__device__ __forceinline__ void tmem_chunks(uint32_t addr, uint32_t (&v)[32], Fn &&fn)
 {
-    tmem_ld_32x32b_x32(addr, va);
-#pragma unroll
+#pragma unroll 1
     for (int c = 0; c < N; ++c) {
-        uint32_t(&cur)[32] = (c & 1) ? vb : va;
-        uint32_t(&nxt)[32] = (c & 1) ? va : vb;
-        tmem_ld_wait_regs(cur);
-        if (c + 1 < N)
-            tmem_ld_32x32b_x32(addr + 32u * (c + 1), nxt);
-        fn(cur, c);
+        tmem_ld_32x32b_x32(addr + 32u * c, v);
+        tmem_ld_wait_regs(v);
+        fn(v, c);
     }
 }
 
@@ -425,6 +423,20 @@ __device__ __forceinline__ void store_rows(uint32_t stage, int lane, const uint4
 struct PagedBars {
     uint32_t q_full0, q_empty0, drain, full0, empty0, s_full, pv_done, p_half0, p_full0;
 };
+
+// Keys of the prefix that a token sees: normally all; one that stands inside it sees less. Of a
+// warp whose tokens do not decrease (not inlined: the items of a batch's own keys never call it,
+// and the instruction cache is what short items wait for). All lanes call it.
+__device__ __noinline__ int prefix_seen(const BatchView &b, int token, bool on)
+{
+    int s = find_seq<32>(b.q_start, b.num_seqs, __shfl_sync(0xffffffffu, token, 0), threadIdx.x & 31);
+    if (!on)
+        return 0;
+    while (s + 1 < b.num_seqs && __ldg(b.q_start + s + 1) <= token)
+        ++s;
+    const SeqView v = load_seq(b, s);
+    return min(b.prefix_len, max(0, b.prefix_len + v.kv - v.n + (token - v.q0) + 1));
+}
 
 template <class Cfg>
 __device__ __forceinline__ void paged_softmax_warp(const PagedParams &p, const PagedBars &bar, const WaitCtl &wc, uint32_t tmem,
@@ -458,14 +470,8 @@ __device__ __forceinline__ void paged_softmax_warp(const PagedParams &p, const P
         const int token = g.tok0 + first + row_tok;
         int seen = INT32_MAX;   // keys, from the item's first, that the row sees (idle rows: as if all)
         if (g.prefix) {
-            // normally all of the prefix; a token that stands inside it sees less
-            int s = find_seq<32>(p.batch.q_start, p.batch.num_seqs, __shfl_sync(0xffffffffu, token, 0), lane);
-            if (row_ok) {
-                while (s + 1 < p.batch.num_seqs && __ldg(p.batch.q_start + s + 1) <= token)
-                    ++s;
-                const SeqView v = load_seq(p.batch, s);
-                seen = min(p.batch.prefix_len, max(0, p.batch.prefix_len + v.kv - v.n + (token - v.q0) + 1));
-            }
+            const int n = prefix_seen(p.batch, token, row_ok);
+            seen = row_ok ? n : seen;
         } else if (row_ok) {
             seen = max(0, g.edge + (token - g.q0) + 1);
         }
@@ -528,7 +534,7 @@ __device__ __forceinline__ void paged_softmax_warp(const PagedParams &p, const P
                 }
                 // the extreme of the raw scores in four independent chains, scaled once
                 float r0 = sl2 >= 0.0f ? -INFINITY : INFINITY, r1 = r0, r2 = r0, r3 = r0;
-                tmem_chunks<CH>(s_addr, va, vb, [&](const uint32_t(&x)[32], int) {
+                tmem_chunks<CH>(s_addr, va, [&](const uint32_t(&x)[32], int) {
                     if (sl2 >= 0.0f) {
 #pragma unroll
                         for (int e = 0; e < 32; e += 8) {
@@ -572,7 +578,7 @@ __device__ __forceinline__ void paged_softmax_warp(const PagedParams &p, const P
                 uint64_t sum2[4] = {f32x2_pack(0.0f, 0.0f), f32x2_pack(0.0f, 0.0f), f32x2_pack(0.0f, 0.0f),
                                     f32x2_pack(0.0f, 0.0f)};
                 const uint64_t scale2 = f32x2_pack(sl2, sl2), neg_m2 = f32x2_pack(-m_use, -m_use);
-                tmem_chunks<CH>(s_addr, va, vb, [&](const uint32_t(&x)[32], int c) {
+                tmem_chunks<CH>(s_addr, va, [&](const uint32_t(&x)[32], int c) {
                     uint32_t pk[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
