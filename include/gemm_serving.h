@@ -63,7 +63,7 @@ typedef struct gemm_kv_cache {
  * prefix_pages[num_prefix_pages] (NULL without a prefix). num_tokens: the size of the flat token
  * dimension. max_q: the largest number of new tokens of a sequence, as far as the caller knows
  * (0: unknown); results do not depend on it, the choice of kernels does.
- * (table_width + num_prefix_pages) * page_size must stay below 2^31. */
+ * num_seqs is at most 2^24, (table_width + num_prefix_pages) * page_size at most 2^31 - 1024. */
 typedef struct gemm_kv_batch {
     int64_t num_seqs, num_tokens, max_q;
     const int32_t *q_start, *kv_lens, *page_table;
@@ -129,8 +129,9 @@ int gemm_kv_append(gemm_ctx *ctx, const gemm_kv_cache *cache, const gemm_kv_batc
 
 /* out[t][h][:] = sum_j softmax_j(scale * q[t][h][:] . K[j][h'][:]) V[j][h'][:] over the keys j
  * that token t sees, h' = h / (q->heads / kv_heads); q->heads is a multiple of kv_heads, at most
- * 128 times it. lse (may be NULL): FP32, lse[t * lse_stride + h] = ln sum_j exp(scale * q . K_j).
- * A token that sees no key gets out = 0 and lse = -inf.
+ * 128 times it, and num_tokens * q->heads at most 2^33. lse (may be NULL): FP32,
+ * lse[t * lse_stride + h] = ln sum_j exp(scale * q . K_j). A token that sees no key gets out = 0 and
+ * lse = -inf.
  * FP32 scores, statistics and sums; probabilities are rounded to the element type for the
  * product with V. Values in rows of the cache past a sequence's last key are ignored whatever
  * they are (NaN too). A non-finite value in a V row that some token of a sequence sees may also

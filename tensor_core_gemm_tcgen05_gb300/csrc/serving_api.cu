@@ -21,6 +21,8 @@ namespace {
 using i128 = __int128;
 constexpr int64_t kMaxStride = (int64_t(1) << 39) - 8;   // elements: tensor maps hold strides below 2^40 bytes
 constexpr int64_t kMaxHeads = 1 << 16;
+constexpr int64_t kMaxSeqs = 1 << 24;   // (the search of a token's sequence steps past the last one in 32 bits)
+constexpr int64_t kMaxKeys = (int64_t(1) << 31) - 1024;   // a block of keys may begin at the last one
 constexpr int64_t kJointTiles = 4;   // tiles of rows up to which prefix and own keys share a launch
 
 // ---- strided operands ------------------------------------------------------------------------
@@ -220,12 +222,12 @@ int check_cache(const gemm_ctx *ctx, const gemm_kv_cache *c)
 // `pointers`: the device arrays are checked too. `prefix`: prefix_pages is read.
 int check_batch(const gemm_ctx *ctx, const gemm_kv_cache *c, const gemm_kv_batch *b, bool pointers, bool prefix)
 {
-    if (!b || b->num_seqs < 0 || b->num_seqs > INT32_MAX - 1 || b->num_tokens < 0 || b->num_tokens > INT32_MAX ||
+    if (!b || b->num_seqs < 0 || b->num_seqs > kMaxSeqs || b->num_tokens < 0 || b->num_tokens > INT32_MAX ||
         b->max_q < 0 || b->table_width < 0 || b->table_stride < 0 || b->table_stride > kMaxStride ||
         b->num_prefix_pages < 0)
         return GEMM_ERR_ARG;
     if (b->table_width > INT32_MAX || b->num_prefix_pages > INT32_MAX ||
-        (b->table_width + b->num_prefix_pages) * c->page_size > INT32_MAX)
+        (b->table_width + b->num_prefix_pages) * c->page_size > kMaxKeys)
         return GEMM_ERR_ARG;
     if (!pointers || b->num_seqs == 0 || b->num_tokens == 0)
         return GEMM_OK;
@@ -430,7 +432,7 @@ int check_attention(const gemm_ctx *ctx, const gemm_kv_cache *cache, const gemm_
         return rc;
     if (q_heads < 0 || q_heads > kMaxHeads || q_heads % cache->kv_heads != 0 || q_heads / cache->kv_heads > 128)
         return GEMM_ERR_ARG;
-    if (batch->num_tokens * q_heads > (int64_t(1) << 33) || batch->num_seqs > (1 << 24))
+    if (batch->num_tokens * q_heads > (int64_t(1) << 33))
         return GEMM_ERR_ARG;
     return GEMM_OK;
 }
