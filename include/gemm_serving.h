@@ -133,9 +133,8 @@ int gemm_kv_append(gemm_ctx *ctx, const gemm_kv_cache *cache, const gemm_kv_batc
  * lse[t * lse_stride + h] = ln sum_j exp(scale * q . K_j). A token that sees no key gets out = 0 and
  * lse = -inf.
  * FP32 scores, statistics and sums; probabilities are rounded to the element type for the
- * product with V. Values in rows of the cache past a sequence's last key are ignored whatever
- * they are (NaN too). A non-finite value in a V row that some token of a sequence sees may also
- * reach that sequence's new tokens shortly before it, which do not see it.
+ * product with V. Keys and values that a token does not see are ignored whatever they are (NaN
+ * too).
  * out has q's heads and strides of its own and may not overlap q, the cache or the workspace.
  * workspace: 256-byte aligned device memory of at least gemm_paged_attention_workspace bytes,
  * used from this call until the stream has passed it and by no other call meanwhile (captured

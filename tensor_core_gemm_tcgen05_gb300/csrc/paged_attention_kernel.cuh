@@ -82,6 +82,9 @@ struct PagedParams {
     PartInfo *info[2];                  // [num_tokens][kv_heads]
     float *row_o[2];                    // whole items, [num_tokens][heads][D]
     float2 *row_ml[2];
+    // what repair_stretches reads: the operands as the tensor maps have them, strides in elements
+    const void *q, *k, *v;
+    int64_t q_token, q_head, page_stride, head_stride, row_stride;
     uint32_t *err;
     uint64_t timeout_ns;
     int debug;                          // DEBUG_WITHHOLD_FIRST_LOAD
@@ -438,9 +441,104 @@ __device__ __noinline__ int prefix_seen(const BatchView &b, int token, bool on)
     return min(b.prefix_len, max(0, b.prefix_len + v.kv - v.n + (token - v.q0) + 1));
 }
 
+// A key that some rows of an item see and others do not gets P = 0 for those, and 0 times a value
+// that is infinite or NaN is NaN. So a warp that finds such an O in a row that does not see all keys of
+// its stretch goes through the CTA's stretches once more when it is done, and computes those rows
+// anew, one after the other, over the keys that they see and no others. Hardly ever anything, slow,
+// and not inlined; what it costs otherwise is the look at O, instructions to fetch at the end of each
+// such item (drafts 71.7 -> 76.6 us, shared step 52.4 -> 53.0, prompts the same).
+template <class Cfg>
+__device__ __noinline__ void repair_stretches(const PagedParams &p, const Walk &start, int tile, int quarter, int lane)
+{
+    using T = typename Cfg::Type;
+    constexpr int D = Cfg::D, BKV = Cfg::BKV, V = D / 32;   // a lane's dims: lane * V ..
+    auto load = [&](const void *base, int64_t at, float(&f)[V]) {
+        const uint32_t *src = reinterpret_cast<const uint32_t *>(static_cast<const T *>(base) + at + lane * V);
+#pragma unroll
+        for (int e = 0; e < V; e += 2) {
+            const float2 x = unpack2<T>(src[e / 2]);
+            f[e] = x.x;
+            f[e + 1] = x.y;
+        }
+    };
+    Walk walk = start;
+    Segment g;
+    while (next_segment<Cfg>(p, walk, g)) {
+        const int first = g.tile_first<Cfg::NT>(tile), toks = g.tile_toks<Cfg::NT>(tile);
+        const int alive = g.prefix ? p.batch.prefix_len : max(0, g.edge + (g.tok0 + g.toks - g.q0));
+        const int begin = g.b0 * BKV, end = min(min(g.b1, g.tile_blocks<Cfg::NT, BKV>(tile)) * BKV, alive);
+        const int key_base = g.prefix || p.keys == KEYS_ALL ? 0 : p.batch.prefix_len;
+        const bool starts = g.b0 == 0, whole = starts && g.b1 == g.blocks;
+        for (int r = quarter * 32; r < quarter * 32 + 32 && r / p.group < toks; ++r) {
+            const int token = g.tok0 + first + r / p.group, head = g.head * p.group + r % p.group;
+            const int seen = g.prefix ? prefix_seen(p.batch, token, true) : max(0, g.edge + (token - g.q0) + 1);
+            if (seen >= end || seen <= begin)
+                continue;   // (all of them, or none: nothing of it is used)
+            T *out = static_cast<T *>(p.out) + token * p.out_token + head * p.out_head;
+            const int64_t row =
+                whole ? static_cast<int64_t>(token) * (p.kv_heads * p.group) + head
+                      : (static_cast<int64_t>(2 * blockIdx.x + (starts ? 1 : 0)) * p.parts.tiles + (first > 0 ? 1 : 0)) * p.parts.rows + r;
+            float *part = (whole ? p.row_o[g.prefix] : p.parts.o) + row * D + lane * V;
+            const bool final_row = whole && p.keys == KEYS_ALL;
+            float x[V];
+            bool finite = true;
+            if (final_row)
+                load(out, 0, x);
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                finite = finite && fabsf(final_row ? x[e] : part[e]) < INFINITY;
+            if (__all_sync(0xffffffffu, finite))
+                continue;
+            float q[V], acc[V] = {}, m = -INFINITY, l = 0.0f;
+            load(p.q, token * p.q_token + head * p.q_head, q);
+            for (int j = begin; j < seen; ++j) {
+                const int key = key_base + j, lp = key >> p.batch.page_shift;
+                const int page = lp < p.n_prefix_pages ? __ldg(p.prefix_pages + lp)
+                                                       : __ldg(p.batch.table + g.s * p.batch.table_stride + (lp - p.n_prefix_pages));
+                float k[V] = {}, v[V] = {};
+                if (page >= 0 && page < p.batch.num_pages) {   // (zeros otherwise)
+                    const int64_t at = page * p.page_stride + g.head * p.head_stride +
+                                       (key & ((1 << p.batch.page_shift) - 1)) * p.row_stride;
+                    load(p.k, at, k);
+                    load(p.v, at, v);
+                }
+                float score = 0.0f;
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                    score = fmaf(q[e], k[e], score);
+#pragma unroll
+                for (int o = 16; o > 0; o /= 2)
+                    score += __shfl_xor_sync(0xffffffffu, score, o);
+                score *= p.scale_log2;
+                if (score == -INFINITY)
+                    continue;
+                const float top = fmaxf(m, score), keep = m == -INFINITY ? 0.0f : exp2f(m - top), w = exp2f(score - top);
+                l = m == -INFINITY ? w : fmaf(l, keep, w);
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                    acc[e] = m == -INFINITY ? w * v[e] : fmaf(w, v[e], acc[e] * keep);
+                m = top;
+            }
+            if (final_row) {
+                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+                for (int e = 0; e < V; e += 2)
+                    *reinterpret_cast<uint32_t *>(out + lane * V + e) = pack2<T>(acc[e] * inv, acc[e + 1] * inv);
+            } else {
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                    part[e] = acc[e];
+                if (lane == 0)
+                    (whole ? p.row_ml[g.prefix] : p.parts.ml)[row] = make_float2(m, l);
+            }
+        }
+    }
+}
+
 template <class Cfg>
 __device__ __forceinline__ void paged_softmax_warp(const PagedParams &p, const PagedBars &bar, const WaitCtl &wc, uint32_t tmem,
-                                                   uint32_t ring, uint32_t stage, Walk walk, const Shares &shares, int tile, int warp, int lane)
+                                                   uint32_t ring, uint32_t stage, volatile int *spoilt, const Walk &start, const Shares &shares,
+                                                   int tile, int warp, int lane)
 {
     using T = typename Cfg::Type;
     constexpr int D = Cfg::D, BKV = Cfg::BKV, CH = BKV / 32;
@@ -460,6 +558,7 @@ __device__ __forceinline__ void paged_softmax_warp(const PagedParams &p, const P
     RingPos<Cfg::STAGES> ring_k;   // this block's K tile (its V tile is the next position)
     uint32_t count = 0;            // blocks this tile has worked on
     uint32_t va[32], vb[32];
+    Walk walk = start;
     Segment g, next;
     bool more = next_segment<Cfg>(p, walk, next);
     while (more) {
@@ -645,6 +744,23 @@ __device__ __forceinline__ void paged_softmax_warp(const PagedParams &p, const P
             tc_fence_after_sync();
         }
         const int head = g.head * p.group + row_head;
+        // rows that do not see all keys of the stretch: is their O finite
+        const bool part_seen = row_ok && l != 0.0f && seen < min(min(g.b1, mine) * BKV, alive);
+        if (__builtin_expect(__any_sync(0xffffffffu, part_seen), 0)) {
+            float top0 = 0.0f, top1 = 0.0f;   // largest magnitudes, NaN if there is one
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+                tmem_ld_32x32b_x32(o_addr + static_cast<uint32_t>(c), va);
+                tmem_ld_wait_regs(va);
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                    top0 = fmax3_abs_nan(top0, __uint_as_float(va[e]), __uint_as_float(va[e + 1]));
+                    top1 = fmax3_abs_nan(top1, __uint_as_float(va[e + 2]), __uint_as_float(va[e + 3]));
+                }
+            }
+            if (__builtin_expect(part_seen && !(top0 < INFINITY && top1 < INFINITY), 0))
+                spoilt[warp] = 1;
+        }
         if (whole && p.keys == KEYS_ALL) {
             const float inv = 1.0f / l;
             T *dst = static_cast<T *>(p.out) + token * p.out_token + head * p.out_head;
@@ -711,6 +827,9 @@ __device__ __forceinline__ void paged_softmax_warp(const PagedParams &p, const P
         if (row_ok)
             *ml = make_float2(m, l);
     }
+    __syncwarp();
+    if (__builtin_expect(spoilt[warp], 0))
+        repair_stretches<Cfg>(p, start, tile, quarter, lane);
 }
 
 // ---- kernel ------------------------------------------------------------------------------------
@@ -726,6 +845,7 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, Cfg::CTAS_PER_SM)
     extern __shared__ uint8_t smem_raw[];
     __shared__ int64_t warp_sum[WARPS];
     __shared__ Walk start;
+    __shared__ int spoilt[4 * NT];   // of each softmax warp, see repair_stretches
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t *sp = smem_raw + (base - raw);
@@ -760,6 +880,8 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, Cfg::CTAS_PER_SM)
         }
         *abort_flag = 0;
         start.left = 0;
+        for (int w = 0; w < 4 * NT; ++w)
+            spoilt[w] = 0;
         fence_mbar_init();
         tma_prefetch_desc(&tmap_q);
         tma_prefetch_desc(&tmap_k);
@@ -1158,7 +1280,7 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, Cfg::CTAS_PER_SM)
         __syncwarp();
     } else {
         // ---------------------------------------------------------------- softmax
-        paged_softmax_warp<Cfg>(p, bar, wc, tmem, ring, base + Cfg::STAGE_OFF + static_cast<uint32_t>(warp) * Cfg::STAGE_WARP, walk,
+        paged_softmax_warp<Cfg>(p, bar, wc, tmem, ring, base + Cfg::STAGE_OFF + static_cast<uint32_t>(warp) * Cfg::STAGE_WARP, spoilt, start,
                                 shares, warp >> 2, warp, lane);
     }
 

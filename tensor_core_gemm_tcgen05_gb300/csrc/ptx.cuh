@@ -520,6 +520,14 @@ __device__ __forceinline__ uint64_t f32x2_sub(uint64_t a, uint64_t b)
     return d;
 }
 
+// The largest magnitude of three; NaN if one is.
+__device__ __forceinline__ float fmax3_abs_nan(float a, float b, float c)
+{
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 // max(a, b, c) and min(a, b, c) in one instruction each.
 __device__ __forceinline__ float fmax3(float a, float b, float c)
 {

@@ -703,6 +703,14 @@ int gemm_paged_attention(gemm_ctx *ctx, const gemm_kv_cache *cache, const gemm_k
     p.out_head = out->head_stride;
     p.lse = lse;
     p.lse_token = lse_stride;
+    p.q = q->data;
+    p.q_token = q->token_stride;
+    p.q_head = q->head_stride;
+    p.k = cache->k;
+    p.v = cache->v;
+    p.page_stride = cache->page_stride;
+    p.head_stride = cache->head_stride;
+    p.row_stride = cache->row_stride;
     p.err = ctx->d_err;
     p.timeout_ns = ctx->timeout_ns;
     p.debug = ctx->debug & GEMM_DEBUG_WITHHOLD_FIRST_LOAD;

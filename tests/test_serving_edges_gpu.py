@@ -221,6 +221,53 @@ def test_captured_step_of_both_operators(ctx):
         check_attention(out.cpu(), lse.cpu(), ref, rl, spread, i)
 
 
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan], ids=str)
+@pytest.mark.parametrize("n_q,kv,hq,hk,d,page,prefix,max_q", [
+    ([3, 1, 2], [70, 1, 64], 8, 2, 64, 16, 0, 3), ([300], [300], 8, 2, 128, 16, 0, None), ([5, 40, 1], [2, 20, 9], 8, 8, 128, 32, 0, 40),
+    ([200, 3, 64], [1000, 67, 64], 6, 2, 64, 64, 0, None), ([4] * 9, [30] * 9, 4, 1, 128, 16, 5, 4), ([150], [150], 2, 2, 64, 16, 3, None),
+    ([20] * 6, [3, 9, 20, 21, 1, 50], 4, 2, 128, 16, 4, 20), ([300] * 3, [100, 300, 250], 8, 2, 64, 16, 20, 300)], ids=str)
+def test_values_that_are_not_finite_reach_those_that_see_them_only(ctx, n_q, kv, hq, hk, d, page, prefix, max_q, bad):
+    """In a sequence's new keys, which its earlier new tokens do not see (and in an old one, which all
+    do), and in the last keys of a prefix, which tokens inside it do not see."""
+    b = batch(n_q, kv, page, prefix_pages=prefix, seed=8)
+    tokens = sum(n_q)
+    q = normal((tokens, hq, d), 1)
+    k, v = normal((b["pages"], hk, page, d), 2), normal((b["pages"], hk, page, d), 3)
+    gen = torch.Generator().manual_seed(5)
+    marks = []   # (sequence, own key, head, dim)
+    for s, n in enumerate(kv):
+        for _ in range(min(n, 3)):
+            j = n - 1 - int(torch.randint(0, min(n, n_q[s] + 1), (1,), generator=gen))
+            marks.append((s, j, int(torch.randint(0, hk, (1,), generator=gen)), int(torch.randint(0, d, (1,), generator=gen))))
+    zeroed = v.clone()
+    for s, j, h, e in marks:
+        v[int(b["page_table"][s, j // page]), h, j % page, e] = bad
+        zeroed[int(b["page_table"][s, j // page]), h, j % page, e] = 0
+    for j in range(prefix * page - 1, max(0, prefix * page - 60), -13):
+        i = int(b["prefix_pages"][j // page])
+        v[i, j % hk, j % page, j % d], zeroed[i, j % hk, j % page, j % d] = bad, 0
+    ref, rl, spread = attention(q, k, zeroed, b, d ** -0.5)
+    hit = torch.zeros(tokens, hq, d, dtype=torch.bool)
+    for s, j, h, e in marks:
+        for i in range(n_q[s]):
+            if j <= kv[s] - n_q[s] + i:
+                hit[int(b["q_start"][s]) + i, h * (hq // hk) : (h + 1) * (hq // hk), e] = True
+    for j in range(prefix * page - 1, max(0, prefix * page - 60), -13):
+        for s, n in enumerate(n_q):
+            for i in range(n):
+                if j <= prefix * page + kv[s] - n + i:
+                    h = j % hk
+                    hit[int(b["q_start"][s]) + i, h * (hq // hk) : (h + 1) * (hq // hk), j % d] = True
+    lse = torch.empty(tokens, hq, device=DEV)
+    out = g.paged_attention(ctx, q.to(DEV), k.to(DEV), v.to(DEV), *on_device(b), max_q=max_q, lse=lse,
+                            prefix_pages=b["prefix_pages"].to(DEV) if prefix else None).cpu()
+    done(ctx)
+    assert hit.any() and not torch.isfinite(out[hit]).any()
+    if not math.isnan(bad):
+        assert torch.all((out[hit] == bad) | torch.isnan(out[hit]))   # (a weight that rounds to 0 makes NaN)
+    check_attention(torch.where(hit, 0, out), lse.cpu(), torch.where(hit, 0, ref), rl, spread, "others")
+
+
 def test_more_sequences_than_the_limit_are_refused(ctx):
     """By both calls, before anything is read (no array of that size exists here)."""
     cache = torch.zeros(2, 1, 16, 64, dtype=torch.float16, device=DEV)
