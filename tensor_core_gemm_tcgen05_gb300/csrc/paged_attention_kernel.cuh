@@ -112,7 +112,7 @@ struct PagedConfig {
     static constexpr int Q_BUFS = NT == 1 ? 4 : 1;   // at most
     static constexpr int NUM_BARS = 2 * Q_BUFS + 1 + 2 * STAGES + 2 + 2 * NT;
     // what beginning and ending an item costs, in blocks
-    static constexpr int ITEM_COST = NT == 1 ? 2 : 2;
+    static constexpr int ITEM_COST = 2;
     static constexpr int SMEM_BYTES = 1024 + BAR_OFF + NUM_BARS * 8 + 16;
     static constexpr int NUM_THREADS = 64 + NT * 128;
     // Warps: the softmax warps of the tiles (warp w reads the Tensor Memory lanes of quarter w mod 4),
@@ -744,8 +744,8 @@ __device__ __forceinline__ void paged_softmax_warp(const PagedParams &p, const P
             tc_fence_after_sync();
         }
         const int head = g.head * p.group + row_head;
-        // rows that do not see all keys of the stretch: is their O finite
-        const bool part_seen = row_ok && l != 0.0f && seen < min(min(g.b1, mine) * BKV, alive);
+        // rows that do not see all keys of the stretch: is their O finite (that of NaN scores is not meant to be)
+        const bool part_seen = row_ok && l > 0.0f && seen < min(min(g.b1, mine) * BKV, alive);
         if (__builtin_expect(__any_sync(0xffffffffu, part_seen), 0)) {
             float top0 = 0.0f, top1 = 0.0f;   // largest magnitudes, NaN if there is one
 #pragma unroll 1
