@@ -443,8 +443,8 @@ __device__ __noinline__ int prefix_seen(const BatchView &b, int token, bool on)
 
 // A key that some rows of an item see and others do not gets P = 0 for those, and 0 times a value
 // that is infinite or NaN is NaN. So a warp that finds such an O in a row that does not see all keys of
-// its stretch goes through the CTA's stretches once more when it is done, and computes those rows
-// anew, one after the other, over the keys that they see and no others. Hardly ever anything, slow,
+// its stretch goes through the CTA's stretches once more when it is done, and computes the rows that such
+// a value has spoilt anew, one after the other, over the keys that they see and no others. Hardly ever anything, slow,
 // and not inlined; what it costs otherwise is the look at O, instructions to fetch at the end of each
 // such item (drafts 71.7 -> 76.6 us, shared step 52.4 -> 53.0, prompts the same).
 template <class Cfg>
@@ -469,6 +469,30 @@ __device__ __noinline__ void repair_stretches(const PagedParams &p, const Walk &
         const int begin = g.b0 * BKV, end = min(min(g.b1, g.tile_blocks<Cfg::NT, BKV>(tile)) * BKV, alive);
         const int key_base = g.prefix || p.keys == KEYS_ALL ? 0 : p.batch.prefix_len;
         const bool starts = g.b0 == 0, whole = starts && g.b1 == g.blocks;
+        // element of the cache where the vector of key j is; -1: of a bad page, which counts as zeros
+        auto place = [&](int j) -> int64_t {
+            const int key = key_base + j, lp = key >> p.batch.page_shift;
+            const int page = lp < p.n_prefix_pages ? __ldg(p.prefix_pages + lp)
+                                                   : __ldg(p.batch.table + g.s * p.batch.table_stride + (lp - p.n_prefix_pages));
+            return page < 0 || page >= p.batch.num_pages
+                       ? -1
+                       : page * p.page_stride + g.head * p.head_stride + (key & ((1 << p.batch.page_shift) - 1)) * p.row_stride;
+        };
+        // the last key of the stretch whose value is not finite in each dim, among those that not all rows see:
+        // a row that sees it is as it should be
+        int bad[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            bad[e] = -1;
+        for (int j = g.prefix ? begin : max(begin, g.edge + (g.tok0 + first - g.q0) + 1); j < end; ++j) {
+            const int64_t at = place(j);
+            float v[V] = {};
+            if (at >= 0)
+                load(p.v, at, v);
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                bad[e] = fabsf(v[e]) < INFINITY ? bad[e] : j;
+        }
         for (int r = quarter * 32; r < quarter * 32 + 32 && r / p.group < toks; ++r) {
             const int token = g.tok0 + first + r / p.group, head = g.head * p.group + r % p.group;
             const int seen = g.prefix ? prefix_seen(p.batch, token, true) : max(0, g.edge + (token - g.q0) + 1);
@@ -481,24 +505,20 @@ __device__ __noinline__ void repair_stretches(const PagedParams &p, const Walk &
             float *part = (whole ? p.row_o[g.prefix] : p.parts.o) + row * D + lane * V;
             const bool final_row = whole && p.keys == KEYS_ALL;
             float x[V];
-            bool finite = true;
+            bool spoilt = false;
             if (final_row)
                 load(out, 0, x);
 #pragma unroll
             for (int e = 0; e < V; ++e)
-                finite = finite && fabsf(final_row ? x[e] : part[e]) < INFINITY;
-            if (__all_sync(0xffffffffu, finite))
+                spoilt = spoilt || (bad[e] >= seen && !(fabsf(final_row ? x[e] : part[e]) < INFINITY));
+            if (!__any_sync(0xffffffffu, spoilt))
                 continue;
             float q[V], acc[V] = {}, m = -INFINITY, l = 0.0f;
             load(p.q, token * p.q_token + head * p.q_head, q);
             for (int j = begin; j < seen; ++j) {
-                const int key = key_base + j, lp = key >> p.batch.page_shift;
-                const int page = lp < p.n_prefix_pages ? __ldg(p.prefix_pages + lp)
-                                                       : __ldg(p.batch.table + g.s * p.batch.table_stride + (lp - p.n_prefix_pages));
+                const int64_t at = place(j);
                 float k[V] = {}, v[V] = {};
-                if (page >= 0 && page < p.batch.num_pages) {   // (zeros otherwise)
-                    const int64_t at = page * p.page_stride + g.head * p.head_stride +
-                                       (key & ((1 << p.batch.page_shift) - 1)) * p.row_stride;
+                if (at >= 0) {
                     load(p.k, at, k);
                     load(p.v, at, v);
                 }
