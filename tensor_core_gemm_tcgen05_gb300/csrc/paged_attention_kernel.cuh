@@ -141,11 +141,13 @@ constexpr int kPagedCoarse = 8, kPagedQuantum = 4;
 constexpr float kPagedRescale = 8.0f;
 
 // ---- work units --------------------------------------------------------------------------------
+//
+// (compiled for the host too, so that the ranges can be checked without a GPU)
 
 // sum over i < n of floor((a i + b) / m), a, b >= 0, m > 0 (by reducing a and b modulo m and
 // counting lattice points the other way round, as in the Euclidean algorithm).
 template <typename I>
-__device__ inline I floor_sum(I n, I m, I a, I b)
+__host__ __device__ inline I floor_sum(I n, I m, I a, I b)
 {
     I sum = 0;
     while (n > 0) {
@@ -177,22 +179,22 @@ struct SeqItems {
     int q0, n, kv, tiles, fixed;
     int edge, step;
     bool bad;
-    __device__ bool prefix() const { return fixed >= 0; }
+    __host__ __device__ bool prefix() const { return fixed >= 0; }
 };
 
 // Sequences of a launch, the prefix counted as one; number s of them.
-__device__ __forceinline__ int seq_count(const PagedParams &p)
+__host__ __device__ __forceinline__ int seq_count(const PagedParams &p)
 {
     return p.keys == KEYS_PREFIX ? 1 : p.keys == KEYS_BOTH ? p.batch.num_seqs + 1 : p.batch.num_seqs;
 }
 
 template <class Cfg>
-__device__ __noinline__ SeqItems seq_items(const PagedParams &p, int s)
+__host__ __device__ __noinline__ SeqItems seq_items(const PagedParams &p, int s)
 {
     SeqItems q;
     if (p.keys == KEYS_PREFIX || (p.keys == KEYS_BOTH && s == 0)) {
-        const int a = min(max(__ldg(p.batch.q_start), 0), p.batch.num_tokens);
-        const int b = min(max(__ldg(p.batch.q_start + p.batch.num_seqs), a), p.batch.num_tokens);
+        const int a = min(max(load_int(p.batch.q_start), 0), p.batch.num_tokens);
+        const int b = min(max(load_int(p.batch.q_start + p.batch.num_seqs), a), p.batch.num_tokens);
         q.q0 = a;
         q.n = b - a;
         q.kv = 0;
@@ -218,7 +220,7 @@ __device__ __noinline__ SeqItems seq_items(const PagedParams &p, int s)
 
 // Key blocks of the tokens [.., last] (at least one, so that rows that see nothing are written).
 template <class Cfg>
-__device__ __forceinline__ int blocks_upto(const SeqItems &q, int last)
+__host__ __device__ __forceinline__ int blocks_upto(const SeqItems &q, int last)
 {
     if (q.fixed >= 0)
         return q.fixed;
@@ -229,21 +231,21 @@ __device__ __forceinline__ int blocks_upto(const SeqItems &q, int last)
 // item costs (ITEM_COST blocks' time), in steps of `quantum` (the last maybe fewer). A range that
 // ends within the cost leaves the whole item to the next.
 template <class Cfg>
-__device__ __forceinline__ int units_upto(const SeqItems &q, int quantum, int last)
+__host__ __device__ __forceinline__ int units_upto(const SeqItems &q, int quantum, int last)
 {
     return (blocks_upto<Cfg>(q, last) + Cfg::ITEM_COST + quantum - 1) / quantum;
 }
 
 // First block of an item's unit `u`.
 template <class Cfg>
-__device__ __forceinline__ int block_of(int u, int quantum, int blocks)
+__host__ __device__ __forceinline__ int block_of(int u, int quantum, int blocks)
 {
     return min(blocks, max(0, u * quantum - Cfg::ITEM_COST));
 }
 
 // Units of all tiles of one key head.
 template <class Cfg>
-__device__ inline int64_t units_of_head(const SeqItems &q, int quantum)
+__host__ __device__ inline int64_t units_of_head(const SeqItems &q, int quantum)
 {
     const int step = q.step;
     if (q.tiles == 0)
@@ -286,15 +288,15 @@ struct Segment {
     // Tokens of a tile: the first (of the item's) and how many. The only tile of an item is the
     // last one, so that the barriers it completes are always the same.
     template <int NT>
-    __device__ int tile_first(int tile) const { return NT == 1 || toks <= tile_tokens ? 0 : tile * tile_tokens; }
+    __host__ __device__ int tile_first(int tile) const { return NT == 1 || toks <= tile_tokens ? 0 : tile * tile_tokens; }
     template <int NT>
-    __device__ int tile_toks(int tile) const
+    __host__ __device__ int tile_toks(int tile) const
     {
         return NT == 2 && tile == 0 && toks <= tile_tokens ? 0 : min(tile_tokens, toks - tile_first<NT>(tile));
     }
     // Its blocks: the first tile of two may see fewer keys than the second.
     template <int NT, int BKV>
-    __device__ int tile_blocks(int tile) const
+    __host__ __device__ int tile_blocks(int tile) const
     {
         if (NT == 1 || tile == 1)
             return blocks;
@@ -305,7 +307,7 @@ struct Segment {
 };
 
 template <class Cfg>
-__device__ __forceinline__ bool next_segment(const PagedParams &p, Walk &w, Segment &g)
+__host__ __device__ __forceinline__ bool next_segment(const PagedParams &p, Walk &w, Segment &g)
 {
     do {
         if (w.left <= 0)
@@ -348,13 +350,33 @@ __device__ __forceinline__ bool next_segment(const PagedParams &p, Walk &w, Segm
     return true;
 }
 
+// The tile of `q` that holds unit `at` of a key head, found by `threads` threads together, `thread` of
+// them this one: scan(value, ahead) returns the sum of value over all and sets ahead to that over the
+// threads before this one. One thread calls found(tile, unit of the tile). A head's units pass 32 bits (2^31 of
+// them: a prompt of 1.04 million tokens, 128 query heads to a key head), those of a tile do not.
+template <class Cfg, class Scan, class Found>
+__host__ __device__ __forceinline__ void locate_tile(const SeqItems &q, int quantum, int64_t at, int thread, int threads, Scan &&scan,
+                                                     Found &&found)
+{
+    int64_t done = 0;
+    for (int t0 = 0; t0 < q.tiles && done <= at; t0 += threads) {
+        const int t = t0 + thread;
+        const int units = t < q.tiles ? units_upto<Cfg>(q, quantum, min((t + 1) * q.step, q.n) - 1) : 0;
+        int64_t first;
+        const int64_t all = scan(static_cast<int64_t>(units), first);
+        if (units > 0 && done + first <= at && at < done + first + units)
+            found(t, static_cast<int>(at - done - first));
+        done += all;
+    }
+}
+
 // What the CTAs agree on: `total` units over `ctas` non-empty ranges.
 struct Shares {
     int64_t total;
     int ctas;
-    __device__ int64_t begin(int c) const { return total * c / ctas; }
+    __host__ __device__ int64_t begin(int c) const { return total * c / ctas; }
     // the range that holds unit u
-    __device__ int owner(int64_t u) const { return static_cast<int>(((u + 1) * ctas + total - 1) / total) - 1; }
+    __host__ __device__ int owner(int64_t u) const { return static_cast<int>(((u + 1) * ctas + total - 1) / total) - 1; }
 };
 
 // Position in the ring of query buffers (their number is the launch's).
@@ -865,6 +887,7 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, Cfg::CTAS_PER_SM)
     extern __shared__ uint8_t smem_raw[];
     __shared__ int64_t warp_sum[WARPS];
     __shared__ Walk start;
+    __shared__ int64_t start_at;   // unit of the key head with which the range begins
     __shared__ int spoilt[4 * NT];   // of each softmax warp, see repair_stretches
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -985,8 +1008,9 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, Cfg::CTAS_PER_SM)
                 start.q = seq_items<Cfg>(p, s);
                 const int64_t per_head = own / p.kv_heads;
                 start.head = static_cast<int>(at / per_head);
+                start_at = at - start.head * per_head;
                 start.tile = 0;
-                start.unit = static_cast<int>(at - start.head * per_head);   // of the head, for now
+                start.unit = start.q.tiles > 1 ? 0 : static_cast<int>(start_at);
                 start.quantum = quantum;
                 start.left = shares.begin(blockIdx.x + 1) - u0;
             }
@@ -997,22 +1021,13 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, Cfg::CTAS_PER_SM)
             block_scan(own, from);
         }
         __syncthreads();
-        // the tile that holds it: the units of the tiles, added up by all threads
-        Walk w = start;
+        // the tile that holds it
+        const Walk w = start;
         if (w.q.tiles > 1) {
-            int64_t done = 0;
-            const int64_t at = w.unit;
-            for (int t0 = 0; t0 < w.q.tiles && done <= at; t0 += Cfg::NUM_THREADS) {
-                const int t = t0 + static_cast<int>(threadIdx.x);
-                const int units = t < w.q.tiles ? units_upto<Cfg>(w.q, quantum, min((t + 1) * w.q.step, w.q.n) - 1) : 0;
-                int64_t first;
-                const int64_t all = block_scan(units, first);
-                if (units > 0 && done + first <= at && at < done + first + units) {
-                    start.tile = t;
-                    start.unit = static_cast<int>(at - done - first);
-                }
-                done += all;
-            }
+            locate_tile<Cfg>(w.q, quantum, start_at, static_cast<int>(threadIdx.x), Cfg::NUM_THREADS, block_scan, [&](int t, int unit) {
+                start.tile = t;
+                start.unit = unit;
+            });
             __syncthreads();
         }
     }

@@ -57,9 +57,18 @@ struct SeqView {
     bool bad;
 };
 
-__device__ __forceinline__ SeqView load_seq(const BatchView &b, int s)
+__host__ __device__ __forceinline__ int load_int(const int *at)
 {
-    const int q0 = __ldg(b.q_start + s), q1 = __ldg(b.q_start + s + 1), kv = __ldg(b.kv_lens + s);
+#ifdef __CUDA_ARCH__
+    return __ldg(at);
+#else
+    return *at;
+#endif
+}
+
+__host__ __device__ __forceinline__ SeqView load_seq(const BatchView &b, int s)
+{
+    const int q0 = load_int(b.q_start + s), q1 = load_int(b.q_start + s + 1), kv = load_int(b.kv_lens + s);
     const int cap = b.table_width << b.page_shift;
     SeqView v;
     v.q0 = min(max(q0, 0), b.num_tokens);
