@@ -552,13 +552,13 @@ __device__ __noinline__ void repair_stretches(const PagedParams &p, const Walk &
                 for (int o = 16; o > 0; o /= 2)
                     score += __shfl_xor_sync(0xffffffffu, score, o);
                 score *= p.scale_log2;
-                if (score == -INFINITY)
-                    continue;
-                const float top = fmaxf(m, score), keep = m == -INFINITY ? 0.0f : exp2f(m - top), w = exp2f(score - top);
-                l = m == -INFINITY ? w : fmaf(l, keep, w);
+                // (as in the softmax: a NaN score leaves the maximum alone and makes the sums NaN for good)
+                const float top = fmaxf(m, score), from = top == -INFINITY ? 0.0f : top;
+                const float keep = exp2f(m - from), w = exp2f(score - from);
+                l = fmaf(l, keep, w);
 #pragma unroll
                 for (int e = 0; e < V; ++e)
-                    acc[e] = m == -INFINITY ? w * v[e] : fmaf(w, v[e], acc[e] * keep);
+                    acc[e] = fmaf(w, v[e], acc[e] * keep);
                 m = top;
             }
             if (final_row) {

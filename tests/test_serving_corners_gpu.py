@@ -1,0 +1,121 @@
+"""The serving operators where numbers or calls are out of the ordinary: keys and values that are not
+finite, scores of minus infinity only, a key far ahead of a long context, scales near zero, outputs
+on another stream, bad lengths of sequences without tokens."""
+import math
+
+import pytest
+import torch
+
+import tensor_core_gemm_tcgen05_gb300 as g
+from serving_ref import TYPES, attention, batch, check_attention, half_step, keys_of, tiny
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda:0")
+
+
+@pytest.fixture(scope="module")
+def ctx():
+    from tensor_core_gemm_tcgen05_gb300 import _build
+    _build.build()
+    c = g.Context(0)
+    yield c
+    c.close()
+
+
+def normal(shape, seed, t=torch.float16):
+    return torch.randn(*shape, generator=torch.Generator().manual_seed(seed)).to(t)
+
+
+def done(ctx):
+    torch.cuda.synchronize()
+    assert g.gemm_last_device_error(ctx) == (g.GEMM_OK, 0)
+
+
+def run(ctx, b, q, k, v, max_q=None, scale=None):
+    lse = torch.full(q.shape[:2], 7.0, device=DEV)
+    pages = None if b["prefix_pages"] is None else b["prefix_pages"].to(DEV)
+    out = g.paged_attention(ctx, q.to(DEV), k.to(DEV), v.to(DEV), b["q_start"].to(DEV), b["kv_lens"].to(DEV), b["page_table"].to(DEV),
+                            max_q=max_q, prefix_pages=pages, scale=scale, lse=lse)
+    done(ctx)
+    return out.cpu(), lse.cpu()
+
+
+def by_rows(q, k, v, b, scale):
+    """(out, lse, spread) in 64 bits, each row over the keys that it sees and no others, with what
+    infinities and NaN among them make of it: 0/0 where no weight is left, 0 x inf, inf - inf."""
+    tokens, hq, d = q.shape
+    grp = hq // k.shape[1]
+    out, spread = (torch.zeros(tokens, hq, d, dtype=torch.float64) for _ in range(2))
+    lse = torch.full((tokens, hq), -math.inf, dtype=torch.float64)
+    for s, n in enumerate(b["n_q"]):
+        ks, vs = (keys_of(x, b, s).double() for x in (k, v))
+        for i in range(n):
+            t, seen = int(b["q_start"][s]) + i, len(ks) - n + i + 1
+            if seen <= 0:
+                continue
+            for h in range(hq):
+                # the product of each pair, so that a matrix product's order plays no part
+                score = (ks[:seen, h // grp] * q[t, h].double()).sum(-1) * scale
+                p = torch.softmax(score, 0)[:, None]
+                out[t, h], spread[t, h] = (p * vs[:seen, h // grp]).sum(0), (p * vs[:seen, h // grp].abs()).sum(0)
+                lse[t, h] = torch.logsumexp(score, 0)
+    return out, lse, spread
+
+
+def check_any(out, lse, ref, ref_lse, spread, what):
+    """Finite results within check_attention's bounds, NaN where the definition has it, infinities the
+    same or NaN (a weight that rounds to 0 times one)."""
+    fine = torch.isfinite(ref)
+    got = out.double()
+    wrong = torch.where(fine, ~torch.isfinite(got), torch.where(torch.isnan(ref), ~torch.isnan(got), (got != ref) & ~torch.isnan(got)))
+    assert not wrong.any(), (what, int(wrong.sum()), wrong.nonzero()[:4].tolist(), ref[wrong][:4], got[wrong][:4])
+    # (rows whose lse is finite or that see no key; the log of a sum with an infinite or NaN score is not a number either way)
+    num = torch.isfinite(ref_lse) | (ref_lse == -math.inf)
+    assert not torch.isfinite(lse[~num]).any(), what
+    assert torch.equal(lse[ref_lse == -math.inf].double(), ref_lse[ref_lse == -math.inf]), what
+    err = (lse.double() - ref_lse)[torch.isfinite(ref_lse)].abs() / (2.0 ** -16 + 2.0 ** -22 * ref_lse[torch.isfinite(ref_lse)].abs())
+    assert err.numel() == 0 or float(err.max()) <= 1.0, what
+    bound = half_step(out.dtype) * ref.abs() * (1 + 2.0 ** -7) + (half_step(out.dtype) + 2.0 ** -16) * spread + tiny(out.dtype)
+    err = ((got - ref).abs() / bound)[fine]
+    assert err.numel() == 0 or float(err.max()) <= 1.0, (what, float(err.max()))
+
+
+def spots(b, hk, d, count, seed, late):
+    """Random (sequence, own key, head, dim); `late`: among the new keys."""
+    gen = torch.Generator().manual_seed(seed)
+    pick = lambda n: int(torch.randint(0, n, (1,), generator=gen))
+    at = []
+    for s, n in enumerate(b["kv"]):
+        for _ in range(count if n else 0):
+            j = n - 1 - pick(min(n, max(1, b["n_q"][s]))) if late else pick(n)
+            at.append((s, j, pick(hk), pick(d)))
+    return at
+
+
+def put(x, b, at, value):
+    for s, j, h, e in at:
+        x[int(b["page_table"][s, j // b["page_size"]]), h, j % b["page_size"], e] = value
+
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf], ids=str)
+@pytest.mark.parametrize("n_q,kv,hq,hk,d,page,prefix,max_q", [
+    ([4] * 160, [30 + i % 9 for i in range(160)], 8, 4, 64, 16, 0, 4),       # several items to a CTA
+    ([4] * 160, [30 + i % 9 for i in range(160)], 4, 4, 128, 32, 0, None),
+    ([70, 3, 130], [300, 67, 131], 4, 2, 64, 64, 0, None),
+    ([3, 5], [700, 5], 4, 2, 128, 16, 0, 5),
+    ([6] * 20, [20] * 20, 4, 1, 64, 16, 9, 6),
+    ([150], [150], 2, 1, 128, 16, 3, None)], ids=lambda x: str(x)[:20])
+def test_keys_and_values_that_are_not_finite(ctx, n_q, kv, hq, hk, d, page, prefix, max_q, bad):
+    """In keys (the first of a sequence, which all rows see, and others), in late values that earlier new
+    tokens do not see, and both at once."""
+    b = batch(n_q, kv, page, prefix_pages=prefix, seed=8)
+    q = normal((sum(n_q), hq, d), 1)
+    first = [(s, 0, s % hk, s % d) for s in range(0, len(kv), 2) if kv[s]]
+    late = spots(b, hk, d, 2, 3, late=True)
+    for what, in_k, in_v in (("keys", first + spots(b, hk, d, 1, 4, late=False)[::3], []), ("late keys", spots(b, hk, d, 1, 5, late=True), []),
+                             ("values", [], late), ("both", first, late), ("late both", late[::2], late[1::2])):
+        k, v = normal((b["pages"], hk, page, d), 2), normal((b["pages"], hk, page, d), 3)
+        put(k, b, in_k, bad)
+        put(v, b, in_v, bad)
+        check_any(*run(ctx, b, q, k, v, max_q=max_q), *by_rows(q, k, v, b, d ** -0.5), what)
