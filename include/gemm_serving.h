@@ -131,7 +131,7 @@ int gemm_kv_append(gemm_ctx *ctx, const gemm_kv_cache *cache, const gemm_kv_batc
  * that token t sees, h' = h / (q->heads / kv_heads); q->heads is a multiple of kv_heads, at most
  * 128 times it, and num_tokens * q->heads at most 2^33. lse (may be NULL): FP32,
  * lse[t * lse_stride + h] = ln sum_j exp(scale * q . K_j). A token that sees no key gets out = 0 and
- * lse = -inf.
+ * lse = -inf; one that sees keys, all of scores -inf, lse = -inf and out = NaN (0/0).
  * FP32 scores, statistics and sums; probabilities are rounded to the element type for the
  * product with V. Keys and values that a token does not see are ignored whatever they are (NaN
  * too).

@@ -463,6 +463,15 @@ __device__ __noinline__ int prefix_seen(const BatchView &b, int token, bool on)
     return min(b.prefix_len, max(0, b.prefix_len + v.kv - v.n + (token - v.q0) + 1));
 }
 
+// (m, l) of a part as it is kept. One of no weight has l = 0, and its O may not be written; m is NaN then if its row
+// sees a key of it all the same (scores of -inf only): 0/0 if all parts are such, where a row that sees none is 0.
+__device__ __forceinline__ float2 part_ml(float m, float l, bool sees)
+{
+    return make_float2(l == 0.0f && sees ? NAN : m, l);
+}
+
+__device__ __forceinline__ bool no_weight(float2 ml) { return ml.y == 0.0f && ml.x != ml.x; }
+
 // A key that some rows of an item see and others do not gets P = 0 for those, and 0 times a value
 // that is infinite or NaN is NaN. So a warp that finds such an O in a row that does not see all keys of
 // its stretch goes through the CTA's stretches once more when it is done, and computes the rows that such
@@ -562,7 +571,7 @@ __device__ __noinline__ void repair_stretches(const PagedParams &p, const Walk &
                 m = top;
             }
             if (final_row) {
-                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                const float inv = 1.0f / l;
 #pragma unroll
                 for (int e = 0; e < V; e += 2)
                     *reinterpret_cast<uint32_t *>(out + lane * V + e) = pack2<T>(acc[e] * inv, acc[e + 1] * inv);
@@ -571,7 +580,7 @@ __device__ __noinline__ void repair_stretches(const PagedParams &p, const Walk &
                 for (int e = 0; e < V; ++e)
                     part[e] = acc[e];
                 if (lane == 0)
-                    (whole ? p.row_ml[g.prefix] : p.parts.ml)[row] = make_float2(m, l);
+                    (whole ? p.row_ml[g.prefix] : p.parts.ml)[row] = part_ml(m, l, true);
             }
         }
     }
@@ -820,7 +829,7 @@ __device__ __forceinline__ void paged_softmax_warp(const PagedParams &p, const P
                     for (int e = 0; e < 4; ++e) {
                         const int k = 8 * (i & 3) + 2 * e;
                         const float a = __uint_as_float(i < 4 ? va[k] : vb[k]), bb = __uint_as_float(i < 4 ? va[k + 1] : vb[k + 1]);
-                        w[e] = l == 0.0f ? 0u : pack2<T>(a * inv, bb * inv);
+                        w[e] = seen == 0 ? 0u : pack2<T>(a * inv, bb * inv);
                     }
                     piece[i] = make_uint4(w[0], w[1], w[2], w[3]);
                 }
@@ -867,7 +876,7 @@ __device__ __forceinline__ void paged_softmax_warp(const PagedParams &p, const P
             }
         }
         if (row_ok)
-            *ml = make_float2(m, l);
+            *ml = part_ml(m, l, seen > g.b0 * BKV);
     }
     __syncwarp();
     if (__builtin_expect(spoilt[warp], 0))
@@ -1364,6 +1373,7 @@ template <int V>
 struct RowSum {
     float m = -INFINITY, l = 0.0f;
     float acc[V] = {};
+    bool zero = false;   // a part has keys of no weight
 
     // Adds n parts, in order: lane i of a step of 32 fetches (m, l) of part i, then all lanes add up
     // their dimensions, eight parts' loads at a time. part(i): where part i's O and (m, l) are.
@@ -1379,7 +1389,7 @@ struct RowSum {
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
             const float m_new = fmaxf(m, top);
             const float keep = m == -INFINITY ? 0.0f : exp2f(m - m_new);
-            const bool none = ml.y == 0.0f;   // a part without a key: its O may not be written
+            const bool none = ml.y == 0.0f;   // a part of no weight: its O may not be written
             const float w = none ? 0.0f : ml.y != ml.y ? ml.y : exp2f(ml.x - m_new);   // (NaN stays NaN)
             float sum = none ? 0.0f : w * ml.y;
 #pragma unroll
@@ -1391,6 +1401,8 @@ struct RowSum {
             for (int e = 0; e < V; ++e)
                 acc[e] *= keep;
             const uint32_t some = __ballot_sync(0xffffffffu, !none);
+            if (some == 0)   // (matters only if no part has any weight)
+                zero = zero || __any_sync(0xffffffffu, no_weight(ml));
             for (int j0 = 0; j0 < k; j0 += 8) {
                 float x[8][V];
 #pragma unroll
@@ -1416,7 +1428,7 @@ struct RowSum {
     template <typename T>
     __device__ __forceinline__ void write(const CombineParams &p, int64_t token, int head, int lane) const
     {
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        const float inv = l == 0.0f ? (zero ? NAN : 0.0f) : 1.0f / l;
         T *dst = static_cast<T *>(p.out) + token * p.out_token + head * p.out_head + lane * V;
         uint32_t w[V / 2];
 #pragma unroll
@@ -1443,6 +1455,7 @@ __device__ __forceinline__ void combine_few(const CombineParams &p, const PartsV
         return;
     float m = -INFINITY, l = 0.0f;
     float4 acc[V] = {};
+    bool zero = false;   // a part has keys of no weight
     for (int i0 = 0; i0 < n; i0 += kCombineStep) {
         float4 x[kCombineStep][V];
         float2 ml[kCombineStep];
@@ -1466,8 +1479,9 @@ __device__ __forceinline__ void combine_few(const CombineParams &p, const PartsV
             acc[e] = make_float4(acc[e].x * keep, acc[e].y * keep, acc[e].z * keep, acc[e].w * keep);
 #pragma unroll
         for (int i = 0; i < kCombineStep; ++i) {
+            zero = zero || no_weight(ml[i]);   // (the last part again: the same answer)
             if (i0 + i >= n || ml[i].y == 0.0f)
-                continue;   // a part without a key: its O may not be written
+                continue;   // a part of no weight: its O may not be written
             const float w = ml[i].y != ml[i].y ? ml[i].y : exp2f(ml[i].x - m);   // (NaN stays NaN)
             l += w * ml[i].y;
 #pragma unroll
@@ -1479,7 +1493,7 @@ __device__ __forceinline__ void combine_few(const CombineParams &p, const PartsV
             }
         }
     }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const float inv = l == 0.0f ? (zero ? NAN : 0.0f) : 1.0f / l;
     T *dst = static_cast<T *>(p.out) + token * p.out_token + head * p.out_head;
 #pragma unroll
     for (int e = 0; e < V; ++e)

@@ -119,3 +119,25 @@ def test_keys_and_values_that_are_not_finite(ctx, n_q, kv, hq, hk, d, page, pref
         put(k, b, in_k, bad)
         put(v, b, in_v, bad)
         check_any(*run(ctx, b, q, k, v, max_q=max_q), *by_rows(q, k, v, b, d ** -0.5), what)
+
+
+@pytest.mark.parametrize("n_q,kv,hq,hk,d,page,prefix,max_q", [
+    ([1, 3, 1], [70, 5, 1], 4, 2, 64, 16, 0, 3), ([1, 1], [3000, 90], 4, 2, 128, 16, 0, 1), ([200, 40], [200, 60], 4, 2, 64, 16, 0, None),
+    ([1] * 12, [30] * 12, 4, 2, 64, 16, 8, 1), ([150, 2, 1], [150, 5, 9], 4, 2, 128, 16, 2, None), ([5, 40], [2, 20], 4, 1, 64, 16, 0, 40)],
+    ids=lambda x: str(x)[:20])
+def test_rows_whose_scores_are_all_minus_infinity(ctx, n_q, kv, hq, hk, d, page, prefix, max_q):
+    """No weight is left and a key is seen: 0/0, not the zeros of a row that sees none. One such key among
+    others only loses its weight; a whole such prefix leaves the own keys theirs."""
+    b = batch(n_q, kv, page, prefix_pages=prefix, seed=8)
+    q = normal((sum(n_q), hq, d), 1)
+    q[..., 3] = q[..., 3].abs() + 0.5   # (so that -inf in that dim is -inf in the score)
+    v = normal((b["pages"], hk, page, d), 3)
+    plain = normal((b["pages"], hk, page, d), 2)
+    every = [(s, j, h, 3) for s in range(len(kv)) for j in range(kv[s]) for h in range(hk)]
+    for what, own, pre in (("all", every, True), ("one head", [x for x in every if x[2] == 0], False), ("the first key", [x for x in every if x[1] == 0], False),
+                           ("all but the last", [x for x in every if x[1] < kv[x[0]] - 1], True), ("the prefix", [], True)):
+        k = plain.clone()
+        put(k, b, own, -math.inf)
+        if pre and prefix:
+            k[b["prefix_pages"].long(), ..., 3] = -math.inf
+        check_any(*run(ctx, b, q, k, v, max_q=max_q), *by_rows(q, k, v, b, d ** -0.5), what)
