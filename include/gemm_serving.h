@@ -133,7 +133,7 @@ int gemm_kv_append(gemm_ctx *ctx, const gemm_kv_cache *cache, const gemm_kv_batc
  * lse[t * lse_stride + h] = ln sum_j exp(scale * q . K_j). A token that sees no key gets out = 0 and
  * lse = -inf; one that sees keys, all of scores -inf, lse = -inf and out = NaN (0/0).
  * FP32 scores, statistics and sums; probabilities are rounded to the element type for the
- * product with V. Keys and values that a token does not see are ignored whatever they are (NaN
+ * product with V (FP16: with 11 bits down to 2^-25 of the row's largest, with fewer down to 2^-36). Keys and values that a token does not see are ignored whatever they are (NaN
  * too).
  * out has q's heads and strides of its own and may not overlap q, the cache or the workspace.
  * workspace: 256-byte aligned device memory of at least gemm_paged_attention_workspace bytes,

@@ -113,6 +113,13 @@ struct PagedConfig {
     static constexpr int NUM_BARS = 2 * Q_BUFS + 1 + 2 * STAGES + 2 + 2 * NT;
     // what beginning and ending an item costs, in blocks
     static constexpr int ITEM_COST = 2;
+    // Probabilities are kept as P = 2^(s - m), m = the running maximum - SHIFT; m is raised (and the row's O
+    // rescaled) only when a block's maximum exceeds it by more than RESCALE base-2 units, so P stays below
+    // 2^(SHIFT + RESCALE). In FP16 that uses the range up to 2^15: weights keep their 11 bits down to 2^-25 of the largest
+    // and vanish below 2^-36, so that a long context behind a key far ahead of it is not lost (with m = the maximum
+    // itself, below 2^-25: 32767 keys 17.4 natural units behind one summed to nothing). BF16 has FP32's range.
+    static constexpr float SHIFT = std::is_same<T, __half>::value ? 11.0f : 0.0f;
+    static constexpr float RESCALE = std::is_same<T, __half>::value ? 4.0f : 8.0f;
     static constexpr int SMEM_BYTES = 1024 + BAR_OFF + NUM_BARS * 8 + 16;
     static constexpr int NUM_THREADS = 64 + NT * 128;
     // Warps: the softmax warps of the tiles (warp w reads the Tensor Memory lanes of quarter w mod 4),
@@ -135,10 +142,6 @@ struct PagedConfig {
 // NT = 2: with fewer than kPagedCoarse blocks per CTA, items are cut at multiples of kPagedQuantum
 // blocks only: a part costs about as much (128 KB of FP32 written and read again) as the blocks.
 constexpr int kPagedCoarse = 8, kPagedQuantum = 4;
-
-// A row's running maximum is raised (and its row of O rescaled) only when a block's maximum
-// exceeds it by more than this many base-2 units: probabilities stay below 2^8.
-constexpr float kPagedRescale = 8.0f;
 
 // ---- work units --------------------------------------------------------------------------------
 //
@@ -703,8 +706,8 @@ __device__ __forceinline__ void paged_softmax_warp(const PagedParams &p, const P
                         }
                     }
                 });
-                const float mb = (sl2 >= 0.0f ? fmax3(fmaxf(r0, r1), r2, r3) : fmin3(fminf(r0, r1), r2, r3)) * sl2;
-                const bool raise = mb > m + kPagedRescale || m == -INFINITY;
+                const float mb = (sl2 >= 0.0f ? fmax3(fmaxf(r0, r1), r2, r3) : fmin3(fminf(r0, r1), r2, r3)) * sl2 - Cfg::SHIFT;
+                const bool raise = mb > m + Cfg::RESCALE || m == -INFINITY;
                 const float m_new = raise ? mb : m;
                 const float m_use = m_new == -INFINITY ? 0.0f : m_new;
                 const float alpha = raise && row_ok ? ex2_approx(m - m_use) : 1.0f;   // 0 on the first block

@@ -141,3 +141,39 @@ def test_rows_whose_scores_are_all_minus_infinity(ctx, n_q, kv, hq, hk, d, page,
         if pre and prefix:
             k[b["prefix_pages"].long(), ..., 3] = -math.inf
         check_any(*run(ctx, b, q, k, v, max_q=max_q), *by_rows(q, k, v, b, d ** -0.5), what)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("ahead", [0.0, 10.0, 14.0, 16.0, 17.4])
+@pytest.mark.parametrize("n_q,seqs,sink", [(1, 200, 0), (1, 200, 20000), (130, 50, 0)])
+def test_a_key_far_ahead_of_a_long_context(ctx, n_q, seqs, sink, ahead, dtype):
+    """One key whose value is zero and whose score is ahead of 32767 equal ones, in as many sequences (of the
+    same pages) as leave most items to one CTA: the output is what the many small weights leave. Each is
+    off by half a step of the type at most, or by half of FP16's smallest step 2^-24, the largest weight
+    being 2^11 or more; what check_attention counts besides is the same."""
+    t, hk, d, page, n = TYPES[dtype], 8, 64, 1024, 32768
+    b = batch([n_q], [n], page, seed=1)
+    k = torch.zeros(b["pages"], hk, page, d, dtype=t)
+    v = (torch.rand(b["pages"], 1, page, d, generator=torch.Generator().manual_seed(2)) + 0.5).to(t).repeat(1, hk, 1, 1)
+    put(k, b, [(0, sink, h, 0) for h in range(hk)], ahead)
+    v[int(b["page_table"][0, sink // page]), :, sink % page] = 0
+    q = torch.zeros(seqs * n_q, 2 * hk, d, dtype=t)
+    q[..., 0] = 1
+    x = float(k.max())   # (rounded to the type)
+    many = dict(b, q_start=torch.arange(0, seqs * n_q + 1, n_q, dtype=torch.int32), kv_lens=b["kv_lens"].repeat(seqs),
+                page_table=b["page_table"].repeat(seqs, 1))
+    out, lse = run(ctx, many, q, k, v, max_q=n_q, scale=1.0)
+    values = keys_of(v, b, 0)[:, 0].double().cumsum(0)
+    seen = torch.arange(n - n_q + 1, n + 1)
+    total = math.exp(x) + (seen - 1).double()
+    ref = (values[seen - 1] / total[:, None])[:, None]
+    step = half_step(t)
+    bound = step * ref * (1 + 2.0 ** -7) + (step + 2.0 ** -16) * ref
+    if t == torch.float16:
+        bound = bound + 2.0 ** -36 * math.exp(x) * ref
+    got = out.double().view(seqs, n_q, 2 * hk, d)
+    assert float(((got - ref).abs() / bound).max()) <= 1.0, float(((got - ref).abs() / ref).max())
+    err = (lse.double().view(seqs, n_q, 2 * hk) - total.log()[:, None]).abs()
+    # (the sum of exponentials grows block by block of 64 keys, n / 64 additions in FP32, each off by half a step
+    # of a sum that hardly changes: at most 2^-24 of it, always the same way where the blocks are equal)
+    assert float((err / (2.0 ** -16 + n / 64 * 2.0 ** -24 + 2.0 ** -22 * total.log()[:, None])).max()) <= 1.0
