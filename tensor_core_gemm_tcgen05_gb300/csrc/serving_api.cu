@@ -7,6 +7,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <limits>
 #include <utility>
 
 #include "gemm_ctx.h"
@@ -651,7 +652,12 @@ int gemm_paged_attention(gemm_ctx *ctx, const gemm_kv_cache *cache, const gemm_k
                          float scale, const gemm_heads *out, float *lse, int64_t lse_stride, void *workspace,
                          int64_t workspace_bytes, void *stream)
 {
-    if (!q || !out || !std::isfinite(scale))
+    // In base 2. 0 becomes the smallest number of its sign, so that -inf times it stays -inf: finite scores times 2^-149
+    // are below 2^-21, less than the exponential's own error.
+    float scale_log2 = scale * 1.4426950408889634f;
+    if (scale_log2 == 0.0f)
+        scale_log2 = std::copysign(std::numeric_limits<float>::denorm_min(), scale);
+    if (!q || !out || !std::isfinite(scale_log2))
         return GEMM_ERR_ARG;
     int rc = check_attention(ctx, cache, batch, q->heads, true);
     if (rc != GEMM_OK)
@@ -694,10 +700,7 @@ int gemm_paged_attention(gemm_ctx *ctx, const gemm_kv_cache *cache, const gemm_k
     p.kv_heads = static_cast<int>(cache->kv_heads);
     p.group = static_cast<int>(group);
     p.long_tokens = static_cast<int>(128 / group);
-    // (a scale of 0 becomes one that no finite score shows, so that -inf times it stays -inf)
-    p.scale_log2 = scale * 1.4426950408889634f;
-    if (std::fabs(p.scale_log2) < 1.2e-38f)
-        p.scale_log2 = 1.2e-38f;
+    p.scale_log2 = scale_log2;
     p.out = out->data;
     p.out_token = out->token_stride;
     p.out_head = out->head_stride;

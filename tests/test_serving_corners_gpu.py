@@ -177,3 +177,28 @@ def test_a_key_far_ahead_of_a_long_context(ctx, n_q, seqs, sink, ahead, dtype):
     # (the sum of exponentials grows block by block of 64 keys, n / 64 additions in FP32, each off by half a step
     # of a sum that hardly changes: at most 2^-24 of it, always the same way where the blocks are equal)
     assert float((err / (2.0 ** -16 + n / 64 * 2.0 ** -24 + 2.0 ** -22 * total.log()[:, None])).max()) <= 1.0
+
+
+@pytest.mark.parametrize("scale", [0.0, 1e-39, -1e-39, 8.4e-39, -8.4e-39, 1e-38, -3e-38, -0.0], ids=str)
+@pytest.mark.parametrize("n_q,kv", [([1, 4], [300, 70]), ([150], [150])], ids=str)
+def test_scales_near_zero(ctx, n_q, kv, scale):
+    """Scores up to 1e38, as bfloat16 queries and keys of 1e19 have them: scale 0 is the mean, and the
+    smallest scales keep their size and sign (scale log2(e) below 2^-126 has 2^-149 as its step: with scores
+    of 1e38 an error of 2^-23.8 in the exponent)."""
+    b = batch(n_q, kv, 16, seed=3)
+    q, k, v = (torch.zeros(s, dtype=torch.bfloat16) for s in ((sum(n_q), 4, 64), (b["pages"], 2, 16, 64), (b["pages"], 2, 16, 64)))
+    q[..., 5] = 1e19
+    k[..., 5] = normal(k.shape[:3], 1, torch.float32).clamp(-3, 3) * 3e18
+    v.copy_(normal(v.shape, 2, torch.float32))
+    ref = attention(q, k, v, b, scale)
+    check_attention(*run(ctx, b, q, k, v, scale=scale), *ref, scale)
+
+
+@pytest.mark.parametrize("scale", [2.4e38, -2.4e38, 3.4e38])
+def test_scales_that_leave_the_range_are_refused(ctx, scale):
+    b = batch([1], [20], 16)
+    q, k, v = normal((1, 2, 64), 1), normal((b["pages"], 1, 16, 64), 2), normal((b["pages"], 1, 16, 64), 3)
+    with pytest.raises(g.GemmError) as e:
+        run(ctx, b, q, k, v, scale=scale)
+    assert e.value.status == g.GEMM_ERR_ARG
+    done(ctx)
