@@ -9,6 +9,7 @@ Queries, keys and values are ``[tokens, heads, head_dim]``, caches ``[pages, kv_
 head_dim]`` (a token-major cache ``[pages, page_size, kv_heads, head_dim]`` is passed as
 ``cache.transpose(1, 2)``), all float16 or all bfloat16 with ``head_dim`` (64 or 128) contiguous
 and the other strides free (multiples of 8). Lengths and tables are int32 tensors on the device.
+Calls run on ``stream`` (None: torch's current one); what they allocate belongs to that stream.
 Like the rest of the package this module only marshals arguments; the header says what each call
 computes and refuses.
 """
@@ -181,6 +182,20 @@ def _on(stream, device):
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _empty(shape, dtype, device, stream):
+    """A tensor for a kernel on ``stream`` (None: the current one) to write. The memory comes from what is free
+    on that stream: a block that is free on the current one may still be in use by work queued there."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    handle = _on(stream, device)
+    if handle == _current(device):
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=device)):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))   # the caller's, that goes on with it
+    return t
+
+
 # --------------------------------------------------------------------------------- the calls
 
 def rope_table(rotary_dim, base=10000.0, scaling=None, factor=1.0, original=None):
@@ -207,12 +222,12 @@ def qk_rope(ctx, q, k, positions, table=None, interleaved=False, rope_scale=1.0,
     allocated contiguous when not given; an output may be its own input. ``k`` may be None."""
     shape, dtype, device = q.shape, q.dtype, q.device
     if q_out is None:
-        q_out = torch.empty(shape, dtype=dtype, device=device)
+        q_out = _empty(shape, dtype, device, stream)
     hq, hqo = _heads(q, "q", dtype, device), _heads(q_out, "q_out", dtype, device, shape)
     hk = hko = _NO_HEADS
     if k is not None:
         if k_out is None:
-            k_out = torch.empty(k.shape, dtype=dtype, device=device)
+            k_out = _empty(k.shape, dtype, device, stream)
         hk, hko = _heads(k, "k", dtype, device), _heads(k_out, "k_out", dtype, device, k.shape)
         if k.shape[0] != shape[0] or k.shape[2] != shape[2]:
             raise ValueError(f"k: {shape[0]} tokens of head_dim {shape[2]} expected, got {tuple(k.shape)}")
@@ -242,7 +257,7 @@ def kv_append(ctx, q, k, v, k_cache, v_cache, q_start, kv_lens, page_table, tabl
     hq = hqo = _NO_HEADS
     if q is not None:
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=dtype, device=device)
+            q_out = _empty(q.shape, dtype, device, stream)
         hq, hqo = _heads(q, "q", dtype, device), _heads(q_out, "q_out", dtype, device, q.shape)
         if q.shape[0] != tokens or q.shape[2] != d:
             raise ValueError(f"q: {tokens} tokens of head_dim {d} expected, got {tuple(q.shape)}")
@@ -267,7 +282,7 @@ def paged_attention(ctx, q, k_cache, v_cache, q_start, kv_lens, page_table, max_
     shape, dtype, device = q.shape, k_cache.dtype, k_cache.device
     c, _, _, d = _cache(k_cache, v_cache)
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=device)
+        out = _empty(shape, dtype, device, stream)
     hq, ho = _heads(q, "q", dtype, device), _heads(out, "out", dtype, device, shape)
     tokens, heads, q_dim = shape
     if q_dim != d:
@@ -280,18 +295,13 @@ def paged_attention(ctx, q, k_cache, v_cache, q_start, kv_lens, page_table, max_
         lse_ptr, lse_stride = lse.data_ptr(), lse.stride(0) if tokens > 1 else heads
     if workspace is not None and (workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != device):
         raise ValueError(f"workspace: a contiguous uint8 tensor on {device} expected")
-    handle = _on(stream, device)
     if workspace is None:
         need = L.gemm_paged_attention_workspace(h, c, b, heads)
         if need < 0:
             raise _g.GemmError(int(need), "gemm_paged_attention_workspace")
-        if stream is None or handle == _current(device):
-            workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        else:   # the allocator must know the stream that uses the memory
-            with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=device)):
-                workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        workspace = _empty((need,), torch.uint8, device, stream)
     _g._check(L.gemm_paged_attention(h, c, b, hq, 1.0 / math.sqrt(d) if scale is None else scale, ho, lse_ptr, lse_stride,
-                                    workspace.data_ptr(), workspace.numel(), handle), "gemm_paged_attention")
+                                    workspace.data_ptr(), workspace.numel(), _on(stream, device)), "gemm_paged_attention")
     return out
 
 

@@ -202,3 +202,45 @@ def test_scales_that_leave_the_range_are_refused(ctx, scale):
         run(ctx, b, q, k, v, scale=scale)
     assert e.value.status == g.GEMM_ERR_ARG
     done(ctx)
+
+
+@pytest.mark.parametrize("call", ["qk_rope", "kv_append", "paged_attention"])
+def test_outputs_for_another_stream_leave_freed_memory_alone(ctx, call):
+    """A block that was freed on the current stream while queued work there still reads it must not become the
+    output of a call on another stream."""
+    n, hq, d = 4099, 8, 128
+    b = batch([n], [n], 64, seed=1)
+    q, k = normal((n, hq, d), 1).to(DEV), normal((n, hq, d), 2).to(DEV)
+    kd, vd = (normal((b["pages"], hq, 64, d), 3 + i).to(DEV) for i in range(2))
+    args = tuple(b[x].to(DEV) for x in ("q_start", "kv_lens", "page_table"))
+    table, pos = g.rope_table(d)[0].to(DEV), torch.arange(n, dtype=torch.int32, device=DEV)
+    lse, copy = torch.empty(n, hq, device=DEV), torch.zeros(n, hq, d, dtype=torch.float16, device=DEV)
+    ws = torch.empty(g.paged_attention_workspace(ctx, q, kd, vd, *args), dtype=torch.uint8, device=DEV)
+    side = torch.cuda.Stream()
+
+    def calls(stream):
+        if call == "qk_rope":
+            return g.qk_rope(ctx, q, k, pos, table, stream=stream)
+        if call == "kv_append":
+            return (g.kv_append(ctx, q, k, k, kd, vd, *args, table, stream=stream),)
+        return (g.paged_attention(ctx, q, kd, vd, *args, lse=lse, workspace=ws, stream=stream),)
+
+    want = [x.clone() for x in calls(None)]
+    torch.cuda.synchronize()
+    main = torch.cuda.default_stream()
+    for current, stream in ((main, side), (main, side.cuda_stream), (side, main), (side, 0)):
+        with torch.cuda.stream(current):
+            old = [torch.full((n, hq, d), 3.0, dtype=torch.float16, device=DEV) for _ in want]
+            torch.cuda.synchronize()
+            torch.cuda._sleep(200_000_000)   # (about 0.1 s)
+            for x in old:
+                copy.add_(x)
+            del old, x
+            outs = calls(stream)
+            torch.cuda.synchronize()
+            assert torch.all(copy == 3.0 * len(want)), "a block still in use became the output"
+            copy.zero_()
+            for x, y in zip(outs, want):
+                assert torch.equal(x, y)
+            del outs, x, y
+    done(ctx)
