@@ -112,7 +112,11 @@ __global__ void __launch_bounds__(kRopeThreads, 8) rope_kernel(const __grid_cons
             bad = bad || !live;
             dst = static_cast<T *>(g.out) + page * g.out_token + (place & ((1 << p.batch.page_shift) - 1)) * p.row_stride;
         }
-        if (bad && sub == 0)
+        // the threads of the grid look at all sequences, those without tokens here too
+        for (int64_t i = static_cast<int64_t>(blockIdx.x) * kRopeThreads + threadIdx.x; i < p.batch.num_seqs;
+             i += static_cast<int64_t>(gridDim.x) * kRopeThreads)
+            bad = bad || load_seq(p.batch, static_cast<int>(i)).bad;
+        if (bad)
             atomicCAS(p.err, 0u, static_cast<uint32_t>(ERR_BATCH_INDEX));
     } else {
         pos = __ldg(p.positions + token);

@@ -244,3 +244,33 @@ def test_outputs_for_another_stream_leave_freed_memory_alone(ctx, call):
                 assert torch.equal(x, y)
             del outs, x, y
     done(ctx)
+
+
+@pytest.mark.parametrize("what", ["kv_negative", "kv_long", "q_start_steps_back", "q_start_negative", "q_start_far"])
+def test_bad_lengths_of_sequences_without_tokens_are_reported(ctx, what):
+    """By gemm_kv_append as by attention, whether a token's search comes past them or not."""
+    hk, d, page, n = 2, 64, 16, 300
+    n_q = [i % 2 for i in range(n)]
+    b = batch(n_q, [20] * n, page, seed=2)
+    starts, lens = b["q_start"].clone(), b["kv_lens"].clone()
+    if what == "kv_negative":
+        lens[100] = -1
+    elif what == "kv_long":
+        lens[298] = b["page_table"].shape[1] * page + 1
+    elif what == "q_start_steps_back":
+        starts[101] -= 1   # (sequence 100, which has none; 101 then has one token more)
+    elif what == "q_start_negative":
+        starts[0] = -4
+    else:
+        starts[300] = 2 ** 31 - 1
+    tokens = sum(n_q)
+    q, k, v = (normal((tokens, h, d), i).to(DEV) for i, h in enumerate((4, hk, hk)))
+    kd, vd = (torch.zeros(b["pages"], hk, page, d, dtype=torch.float16, device=DEV) for _ in range(2))
+    args = (starts.to(DEV), lens.to(DEV), b["page_table"].to(DEV))
+    g.kv_append(ctx, q, k, v, kd, vd, *args)
+    torch.cuda.synchronize()
+    assert g.gemm_last_device_error(ctx) == (g.GEMM_ERR_INDEX, 8)
+    for s in range(1, 99, 2):   # sequences that nothing is wrong with
+        assert torch.equal(vd[int(b["page_table"][s, 1]), :, 3], v[int(b["q_start"][s])])
+    g.kv_append(ctx, q, k, v, kd, vd, *(b[x].to(DEV) for x in ("q_start", "kv_lens", "page_table")))
+    done(ctx)
