@@ -478,21 +478,58 @@ __device__ __forceinline__ bool no_weight(float2 ml) { return ml.y == 0.0f && ml
 // A key that some rows of an item see and others do not gets P = 0 for those, and 0 times a value
 // that is infinite or NaN is NaN. So a warp that finds such an O in a row that does not see all keys of
 // its stretch goes through the CTA's stretches once more when it is done, and computes the rows that such
-// a value has spoilt anew, one after the other, over the keys that they see and no others. Hardly ever anything, slow,
-// and not inlined; what it costs otherwise is the look at O, instructions to fetch at the end of each
-// such item (drafts 71.7 -> 76.6 us, shared step 52.4 -> 53.0, prompts the same).
+// a value has spoilt anew, over the keys that they see and no others: kRepairRows rows at a time, a lane
+// holding D / 32 dimensions of all of them, so that a key and its value are fetched once for all;
+// kRepairKeys keys at a time, those after them in flight. A NaN in the last key of a prompt of 4096 tokens behind 32
+// heads (128 rows each over all keys): 6.9 ms, 71 with a row at a time (0.15 without the NaN); in every last key of a
+// mixed step 9.7, 101. Bound by latency, 193 instructions a key and group of rows at 4 clocks each, one warp to a
+// scheduler. Hardly ever anything, and not inlined; what it costs
+// otherwise is the look at O, instructions to fetch at the end of each such item (drafts 71.7 -> 76.6 us, shared
+// step 52.4 -> 53.0, prompts the same).
+constexpr int kRepairRows = 8, kRepairKeys = 4;
+
+// Sums of x[0 .. 7] over the warp: lane i gets that of x[i / 4].
+__device__ __forceinline__ float sum_rows(float (&x)[8], int lane)
+{
+#pragma unroll
+    for (int n = 4; n > 0; n /= 2) {
+        const bool upper = lane & (4 * n);
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            const float send = upper ? x[i] : x[i + n];
+            x[i] = (upper ? x[i + n] : x[i]) + __shfl_xor_sync(0xffffffffu, send, 4 * n);
+        }
+    }
+    x[0] += __shfl_xor_sync(0xffffffffu, x[0], 2);
+    return x[0] + __shfl_xor_sync(0xffffffffu, x[0], 1);
+}
+
 template <class Cfg>
 __device__ __noinline__ void repair_stretches(const PagedParams &p, const Walk &start, int tile, int quarter, int lane)
 {
     using T = typename Cfg::Type;
     constexpr int D = Cfg::D, BKV = Cfg::BKV, V = D / 32;   // a lane's dims: lane * V ..
-    auto load = [&](const void *base, int64_t at, float(&f)[V]) {
-        const uint32_t *src = reinterpret_cast<const uint32_t *>(static_cast<const T *>(base) + at + lane * V);
+    constexpr int R = kRepairRows, KEYS = kRepairKeys;
+    constexpr uint32_t ALL = 0xffffffffu;
+    struct Vec {
+        uint32_t w[V / 2];
+    };
+    auto fetch = [&](const void *base, int64_t at) -> Vec {   // this lane's dims of the vector there; at < 0: zeros
+        Vec x = {};
+        if (at >= 0) {
+            const uint32_t *src = reinterpret_cast<const uint32_t *>(static_cast<const T *>(base) + at + lane * V);
+#pragma unroll
+            for (int e = 0; e < V / 2; ++e)
+                x.w[e] = src[e];
+        }
+        return x;
+    };
+    auto unpack = [](const Vec &x, float(&f)[V]) {
 #pragma unroll
         for (int e = 0; e < V; e += 2) {
-            const float2 x = unpack2<T>(src[e / 2]);
-            f[e] = x.x;
-            f[e + 1] = x.y;
+            const float2 y = unpack2<T>(x.w[e / 2]);
+            f[e] = y.x;
+            f[e + 1] = y.y;
         }
     };
     Walk walk = start;
@@ -503,8 +540,11 @@ __device__ __noinline__ void repair_stretches(const PagedParams &p, const Walk &
         const int begin = g.b0 * BKV, end = min(min(g.b1, g.tile_blocks<Cfg::NT, BKV>(tile)) * BKV, alive);
         const int key_base = g.prefix || p.keys == KEYS_ALL ? 0 : p.batch.prefix_len;
         const bool starts = g.b0 == 0, whole = starts && g.b1 == g.blocks;
-        // element of the cache where the vector of key j is; -1: of a bad page, which counts as zeros
-        auto place = [&](int j) -> int64_t {
+        const bool final_row = whole && p.keys == KEYS_ALL;
+        // element of the cache where the vector of key j is; -1: of a bad page (which counts as zeros), or past `last`
+        auto place = [&](int j, int last) -> int64_t {
+            if (j >= last)
+                return -1;
             const int key = key_base + j, lp = key >> p.batch.page_shift;
             const int page = lp < p.n_prefix_pages ? __ldg(p.prefix_pages + lp)
                                                    : __ldg(p.batch.table + g.s * p.batch.table_stride + (lp - p.n_prefix_pages));
@@ -512,78 +552,166 @@ __device__ __noinline__ void repair_stretches(const PagedParams &p, const Walk &
                        ? -1
                        : page * p.page_stride + g.head * p.head_stride + (key & ((1 << p.batch.page_shift) - 1)) * p.row_stride;
         };
+        // this lane's row, and where its O and (m, l) are
+        const int r = quarter * 32 + lane, token = g.tok0 + first + r / p.group, head = g.head * p.group + r % p.group;
+        const bool on = r / p.group < toks;
+        int seen;
+        if (g.prefix)
+            seen = prefix_seen(p.batch, token, on);
+        else
+            seen = on ? max(0, g.edge + (token - g.q0) + 1) : 0;
+        const uint32_t some = __ballot_sync(ALL, on && seen > begin && seen < end);   // not all of the stretch, and not none
+        if (some == 0)
+            continue;
+        const int64_t row =
+            whole ? static_cast<int64_t>(token) * (p.kv_heads * p.group) + head
+                  : (static_cast<int64_t>(2 * blockIdx.x + (starts ? 1 : 0)) * p.parts.tiles + (first > 0 ? 1 : 0)) * p.parts.rows + r;
+        const int64_t at_o = final_row ? token * p.out_token + head * p.out_head : row * D;   // elements
+        float *const part_o = whole ? p.row_o[g.prefix] : p.parts.o;
         // the last key of the stretch whose value is not finite in each dim, among those that not all rows see:
         // a row that sees it is as it should be
         int bad[V];
 #pragma unroll
         for (int e = 0; e < V; ++e)
             bad[e] = -1;
-        for (int j = g.prefix ? begin : max(begin, g.edge + (g.tok0 + first - g.q0) + 1); j < end; ++j) {
-            const int64_t at = place(j);
-            float v[V] = {};
-            if (at >= 0)
-                load(p.v, at, v);
-#pragma unroll
-            for (int e = 0; e < V; ++e)
-                bad[e] = fabsf(v[e]) < INFINITY ? bad[e] : j;
-        }
-        for (int r = quarter * 32; r < quarter * 32 + 32 && r / p.group < toks; ++r) {
-            const int token = g.tok0 + first + r / p.group, head = g.head * p.group + r % p.group;
-            const int seen = g.prefix ? prefix_seen(p.batch, token, true) : max(0, g.edge + (token - g.q0) + 1);
-            if (seen >= end || seen <= begin)
-                continue;   // (all of them, or none: nothing of it is used)
-            T *out = static_cast<T *>(p.out) + token * p.out_token + head * p.out_head;
-            const int64_t row =
-                whole ? static_cast<int64_t>(token) * (p.kv_heads * p.group) + head
-                      : (static_cast<int64_t>(2 * blockIdx.x + (starts ? 1 : 0)) * p.parts.tiles + (first > 0 ? 1 : 0)) * p.parts.rows + r;
-            float *part = (whole ? p.row_o[g.prefix] : p.parts.o) + row * D + lane * V;
-            const bool final_row = whole && p.keys == KEYS_ALL;
-            float x[V];
-            bool spoilt = false;
-            if (final_row)
-                load(out, 0, x);
-#pragma unroll
-            for (int e = 0; e < V; ++e)
-                spoilt = spoilt || (bad[e] >= seen && !(fabsf(final_row ? x[e] : part[e]) < INFINITY));
-            if (!__any_sync(0xffffffffu, spoilt))
-                continue;
-            float q[V], acc[V] = {}, m = -INFINITY, l = 0.0f;
-            load(p.q, token * p.q_token + head * p.q_head, q);
-            for (int j = begin; j < seen; ++j) {
-                const int64_t at = place(j);
-                float k[V] = {}, v[V] = {};
-                if (at >= 0) {
-                    load(p.k, at, k);
-                    load(p.v, at, v);
-                }
-                float score = 0.0f;
+        const int hidden = __reduce_min_sync(ALL, some >> lane & 1u ? seen : INT32_MAX);
+        for (int j0 = hidden; j0 < end; j0 += 32) {
+            const int64_t mine = place(j0 + lane, end);
+#pragma unroll 4
+            for (int i = 0; i < 32; ++i) {
+                float v[V];
+                unpack(fetch(p.v, __shfl_sync(ALL, mine, i)), v);
 #pragma unroll
                 for (int e = 0; e < V; ++e)
-                    score = fmaf(q[e], k[e], score);
-#pragma unroll
-                for (int o = 16; o > 0; o /= 2)
-                    score += __shfl_xor_sync(0xffffffffu, score, o);
-                score *= p.scale_log2;
-                // (as in the softmax: a NaN score leaves the maximum alone and makes the sums NaN for good)
-                const float top = fmaxf(m, score), from = top == -INFINITY ? 0.0f : top;
-                const float keep = exp2f(m - from), w = exp2f(score - from);
-                l = fmaf(l, keep, w);
-#pragma unroll
-                for (int e = 0; e < V; ++e)
-                    acc[e] = fmaf(w, v[e], acc[e] * keep);
-                m = top;
+                    bad[e] = fabsf(v[e]) < INFINITY ? bad[e] : j0 + i;
             }
-            if (final_row) {
-                const float inv = 1.0f / l;
+        }
+        uint32_t rows = 0;
+#pragma unroll 4
+        for (int i = 0; i < 32; ++i) {
+            const int64_t at = __shfl_sync(ALL, at_o, i);
+            const int n = __shfl_sync(ALL, seen, i);
+            float x[V] = {};
+            if (some >> i & 1u) {
+                if (final_row) {
+                    unpack(fetch(p.out, at), x);
+                } else {
 #pragma unroll
-                for (int e = 0; e < V; e += 2)
-                    *reinterpret_cast<uint32_t *>(out + lane * V + e) = pack2<T>(acc[e] * inv, acc[e + 1] * inv);
-            } else {
+                    for (int e = 0; e < V; ++e)
+                        x[e] = part_o[at + lane * V + e];
+                }
+            }
+            bool spoilt = false;
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                spoilt = spoilt || (bad[e] >= n && !(fabsf(x[e]) < INFINITY));
+            rows |= __any_sync(ALL, spoilt) && (some >> i & 1u) ? 1u << i : 0u;
+        }
+        while (rows) {
+            // the next R rows (or what there is: then the last one again, not written)
+            int lanes[R], count = 0, mine = 0;
+            float q[R][V], acc[R][V];
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                if (rows) {
+                    lanes[i] = __ffs(static_cast<int>(rows)) - 1;
+                    rows &= rows - 1;
+                    ++count;
+                } else {
+                    lanes[i] = lanes[i > 0 ? i - 1 : 0];
+                }
+                mine = lane / 4 == i ? lanes[i] : mine;
+                const int from = quarter * 32 + lanes[i];
+                unpack(fetch(p.q, (g.tok0 + first + from / p.group) * p.q_token + (g.head * p.group + from % p.group) * p.q_head), q[i]);
 #pragma unroll
                 for (int e = 0; e < V; ++e)
-                    part[e] = acc[e];
-                if (lane == 0)
-                    (whole ? p.row_ml[g.prefix] : p.parts.ml)[row] = part_ml(m, l, true);
+                    acc[i][e] = 0.0f;
+            }
+            // of row lane / 4: keys it sees, running maximum (raised beyond 2^8, as in the softmax) and sum
+            const int sees = __shfl_sync(ALL, seen, mine), last = __reduce_max_sync(ALL, sees);
+            float m = -INFINITY, l = 0.0f;
+            for (int j0 = begin; j0 < last; j0 += 32) {
+                const int64_t at = place(j0 + lane, last);
+                Vec k[KEYS], v[KEYS];
+#pragma unroll
+                for (int u = 0; u < KEYS; ++u) {
+                    k[u] = fetch(p.k, __shfl_sync(ALL, at, u));
+                    v[u] = fetch(p.v, __shfl_sync(ALL, at, u));
+                }
+#pragma unroll 1
+                for (int i0 = 0; i0 < 32 && j0 + i0 < last; i0 += KEYS) {
+                    float score[KEYS], top = -INFINITY;
+                    Vec now[KEYS];   // the values of these keys
+#pragma unroll
+                    for (int u = 0; u < KEYS; ++u) {
+                        float kf[V], x[R];
+                        unpack(k[u], kf);
+                        now[u] = v[u];
+#pragma unroll
+                        for (int i = 0; i < R; ++i) {
+                            x[i] = q[i][0] * kf[0];
+#pragma unroll
+                            for (int e = 1; e < V; ++e)
+                                x[i] = fmaf(q[i][e], kf[e], x[i]);
+                        }
+                        score[u] = sum_rows(x, lane) * p.scale_log2;
+                        top = j0 + i0 + u < sees ? fmaxf(top, score[u]) : top;   // (a NaN score leaves it alone)
+                        // the same of the next KEYS keys (past this step's 32: fetched above, when it comes)
+                        const int64_t next = __shfl_sync(ALL, at, (i0 + KEYS + u) & 31);
+                        if (i0 + KEYS < 32) {
+                            k[u] = fetch(p.k, next);
+                            v[u] = fetch(p.v, next);
+                        }
+                    }
+                    const bool raise = top > m + 8.0f;
+                    if (__any_sync(ALL, raise)) {
+                        const float keep = raise ? exp2f(m - top) : 1.0f;
+                        m = raise ? top : m;
+                        l *= keep;
+#pragma unroll
+                        for (int i = 0; i < R; ++i) {
+                            const float x = __shfl_sync(ALL, keep, 4 * i);
+#pragma unroll
+                            for (int e = 0; e < V; ++e)
+                                acc[i][e] *= x;
+                        }
+                    }
+                    const float from = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+                    for (int u = 0; u < KEYS; ++u) {
+                        const bool on_key = j0 + i0 + u < sees;
+                        const float w = on_key ? exp2f(score[u] - from) : -1.0f;   // -1: not seen
+                        l += on_key ? w : 0.0f;
+                        float vf[V];
+                        unpack(now[u], vf);
+#pragma unroll
+                        for (int i = 0; i < R; ++i) {
+                            const float x = __shfl_sync(ALL, w, 4 * i);
+#pragma unroll
+                            for (int e = 0; e < V; ++e)
+                                acc[i][e] = x == -1.0f ? acc[i][e] : fmaf(x, vf[e], acc[i][e]);
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const int64_t at = __shfl_sync(ALL, at_o, lanes[i]), at_ml = __shfl_sync(ALL, row, lanes[i]);
+                const float mi = __shfl_sync(ALL, m, 4 * i), li = __shfl_sync(ALL, l, 4 * i), inv = 1.0f / li;
+                if (i >= count)
+                    continue;
+                if (final_row) {
+                    T *out = static_cast<T *>(p.out) + at + lane * V;
+#pragma unroll
+                    for (int e = 0; e < V; e += 2)
+                        *reinterpret_cast<uint32_t *>(out + e) = pack2<T>(acc[i][e] * inv, acc[i][e + 1] * inv);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < V; ++e)
+                        part_o[at + lane * V + e] = acc[i][e];
+                    if (lane == 0)
+                        (whole ? p.row_ml[g.prefix] : p.parts.ml)[at_ml] = part_ml(mi, li, true);
+                }
             }
         }
     }
