@@ -141,36 +141,29 @@ struct PagedConfig {
 
 // NT = 2: with fewer than kPagedCoarse blocks per CTA, items are cut at multiples of kPagedQuantum
 // blocks only: a part costs about as much (128 KB of FP32 written and read again) as the blocks.
-constexpr int kPagedCoarse = 8, kPagedQuantum = 4;
+constexpr int kPagedCoarse = 8, kPagedLog2Quantum = 2, kPagedQuantum = 1 << kPagedLog2Quantum;
 
 // ---- work units --------------------------------------------------------------------------------
 //
 // (compiled for the host too, so that the ranges can be checked without a GPU)
 
-// sum over i < n of floor((a i + b) / m), a, b >= 0, m > 0 (by reducing a and b modulo m and
-// counting lattice points the other way round, as in the Euclidean algorithm).
-template <typename I>
-__host__ __device__ inline I floor_sum(I n, I m, I a, I b)
+// sum over i < n of floor((a i + b) / 2^k), a > 0, b >= 0. Twos that a has are taken out of both sides. An odd a meets
+// each remainder mod P = 2^k once in P steps, so these sum to (a - 1)(P - 1) / 2 + b, the next P to a P more, and
+// so on; the steps after the last whole P (fewer than 2^k, with k at most 9; few or none for a power of two) are added up.
+__host__ __device__ __noinline__ int64_t sum_of_shares(int64_t n, int k, int a, int64_t b)
 {
-    I sum = 0;
-    while (n > 0) {
-        if (a >= m) {
-            sum += n * (n - 1) / 2 * (a / m);
-            a %= m;
-        }
-        if (b >= m) {
-            sum += n * (b / m);
-            b %= m;
-        }
-        const I top = a * n + b;
-        if (top < m)
-            break;
-        n = top / m;
-        b = top % m;
-        const I t = m;
-        m = a;
-        a = t;
+#pragma unroll 1
+    for (; k > 0 && a % 2 == 0; --k) {
+        a /= 2;
+        b >>= 1;
     }
+    const int64_t times = n >> k;
+    const int rest = static_cast<int>(n - (times << k)), low = static_cast<int>(b & ((1 << k) - 1));
+    const int64_t first = static_cast<int64_t>(a - 1) * ((1 << k) - 1) / 2 + b;
+    int64_t sum = times * first + times * (times - 1) / 2 * (static_cast<int64_t>(a) << k) + rest * (times * a + (b >> k));
+#pragma unroll 1
+    for (int i = 0; i < rest; ++i)
+        sum += (a * i + low) >> k;
     return sum;
 }
 
@@ -262,10 +255,7 @@ __host__ __device__ inline int64_t units_of_head(const SeqItems &q, int quantum)
     int64_t sum = last + static_cast<int64_t>(ones) * ((1 + Cfg::ITEM_COST + quantum - 1) / quantum);
     if (whole > ones) {
         const int64_t b = static_cast<int64_t>(q.edge) + static_cast<int64_t>(ones + 1) * step + Cfg::ITEM_COST * Cfg::BKV + keys - 1;
-        if (static_cast<int64_t>(whole) * (last + 1) < (1 << 22))   // (then nothing leaves 32 bits: last * keys < 2^31)
-            sum += floor_sum<uint32_t>(whole - ones, keys, step, static_cast<uint32_t>(b));
-        else
-            sum += floor_sum<int64_t>(whole - ones, keys, step, b);
+        sum += sum_of_shares(whole - ones, (Cfg::BKV == 64 ? 6 : 7) + (quantum == 1 ? 0 : kPagedLog2Quantum), step, b);
     }
     return sum;
 }
