@@ -1695,8 +1695,10 @@ __global__ void __launch_bounds__(32 * kCombineWarps) paged_combine_kernel(const
             const int4 &f = info[side];
             const int i = min(max(f.w, 0), p.launches - 1);
             const int tt = side == 1 ? p.prefix_tokens : p.tile_tokens[i], at = static_cast<int>(token - f.z);
-            // (a token of an unsorted q_start may have no entry: what is not a possible one is left out)
-            const bool ok = f.w == i && f.y >= 1 && f.x >= 0 && f.y <= p.ctas[i] - f.x &&
+            // (a token whose CTA gave up, its wait over, has no entry: what is not a possible one is left out. With
+            // first tokens from 0 on, a row is among those that the parts have, also where there are fewer tokens
+            // than a tile takes)
+            const bool ok = f.w == i && f.y >= 1 && f.x >= 0 && f.y <= p.ctas[i] - f.x && f.z >= 0 &&
                             (f.y == 1 || (at >= 0 && at < p.parts[i].tiles * tt));
             n[side] = ok ? f.y : 0;
             tile[side] = at / tt;

@@ -274,3 +274,29 @@ def test_bad_lengths_of_sequences_without_tokens_are_reported(ctx, what):
         assert torch.equal(vd[int(b["page_table"][s, 1]), :, 3], v[int(b["q_start"][s])])
     g.kv_append(ctx, q, k, v, kd, vd, *(b[x].to(DEV) for x in ("q_start", "kv_lens", "page_table")))
     done(ctx)
+
+
+def test_join_after_a_timeout_reads_the_parts_only(ctx):
+    """CTAs that give up leave the tokens' entries as the workspace had them: here such as would lead in front
+    of the first token of a part, in a batch of fewer tokens than a tile takes."""
+    n, hq, hk, d, page, prefix = 6, 8, 2, 64, 16, 30
+    b = batch([1] * n, [20] * n, page, prefix_pages=prefix, seed=1)
+    q, k, v = normal((n, hq, d), 1), normal((b["pages"], hk, page, d), 2), normal((b["pages"], hk, page, d), 3)
+    qd, kd, vd = q.to(DEV), k.to(DEV), v.to(DEV)
+    args, pages = (b["q_start"].to(DEV), b["kv_lens"].to(DEV), b["page_table"].to(DEV)), b["prefix_pages"].to(DEV)
+    ws = torch.empty(g.paged_attention_workspace(ctx, qd, kd, vd, *args, max_q=1, prefix_pages=pages), dtype=torch.uint8, device=DEV)
+    lse = torch.empty(n, hq, device=DEV)
+    g.gemm_set_timeout_ns(ctx, 20 * 10 ** 6)
+    g.gemm_set_debug(ctx, g.GEMM_DEBUG_WITHHOLD_FIRST_LOAD)
+    try:
+        for first in (-20, -31, 0, 2 ** 31 - 1):
+            ws.view(torch.int32).copy_(torch.tensor([0, 2, first, 0], dtype=torch.int32).repeat(ws.numel() // 16))
+            g.paged_attention(ctx, qd, kd, vd, *args, max_q=1, prefix_pages=pages, lse=lse, workspace=ws)
+            torch.cuda.synchronize()
+            assert g.gemm_last_device_error(ctx)[0] == g.GEMM_ERR_TIMEOUT
+    finally:
+        g.gemm_set_debug(ctx, g.GEMM_DEBUG_NONE)
+        g.gemm_set_timeout_ns(ctx, 2 * 10 ** 9)
+    out = g.paged_attention(ctx, qd, kd, vd, *args, max_q=1, prefix_pages=pages, lse=lse, workspace=ws)
+    done(ctx)
+    check_attention(out.cpu(), lse.cpu(), *attention(q, k, v, b, d ** -0.5), "after")
