@@ -63,7 +63,7 @@ typedef struct gemm_kv_cache {
  * prefix_pages[num_prefix_pages] (NULL without a prefix). num_tokens: the size of the flat token
  * dimension. max_q: the largest number of new tokens of a sequence, as far as the caller knows
  * (0: unknown); results do not depend on it, the choice of kernels does.
- * num_seqs is at most 2^24, (table_width + num_prefix_pages) * page_size at most 2^31 - 1024. */
+ * num_seqs is at most 2^24, num_tokens at most 2^31 - 1024, (table_width + num_prefix_pages) * page_size at most 2^31 - 1024. */
 typedef struct gemm_kv_batch {
     int64_t num_seqs, num_tokens, max_q;
     const int32_t *q_start, *kv_lens, *page_table;

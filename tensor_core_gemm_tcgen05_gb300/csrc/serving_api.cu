@@ -24,6 +24,7 @@ constexpr int64_t kMaxStride = (int64_t(1) << 39) - 8;   // elements: tensor map
 constexpr int64_t kMaxHeads = 1 << 16;
 constexpr int64_t kMaxSeqs = 1 << 24;   // (the search of a token's sequence steps past the last one in 32 bits)
 constexpr int64_t kMaxKeys = (int64_t(1) << 31) - 1024;   // a block of keys may begin at the last one
+constexpr int64_t kMaxTokens = (int64_t(1) << 31) - 1024;   // of a batch: a tile may end past the last one
 constexpr int64_t kJointTiles = 4;   // tiles of rows up to which prefix and own keys share a launch
 
 // ---- strided operands ------------------------------------------------------------------------
@@ -223,7 +224,7 @@ int check_cache(const gemm_ctx *ctx, const gemm_kv_cache *c)
 // `pointers`: the device arrays are checked too. `prefix`: prefix_pages is read.
 int check_batch(const gemm_ctx *ctx, const gemm_kv_cache *c, const gemm_kv_batch *b, bool pointers, bool prefix)
 {
-    if (!b || b->num_seqs < 0 || b->num_seqs > kMaxSeqs || b->num_tokens < 0 || b->num_tokens > INT32_MAX ||
+    if (!b || b->num_seqs < 0 || b->num_seqs > kMaxSeqs || b->num_tokens < 0 || b->num_tokens > kMaxTokens ||
         b->max_q < 0 || b->table_width < 0 || b->table_stride < 0 || b->table_stride > kMaxStride ||
         b->num_prefix_pages < 0)
         return GEMM_ERR_ARG;

@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import tensor_core_gemm_tcgen05_gb300 as g
+from tensor_core_gemm_tcgen05_gb300 import serving
 from serving_ref import TYPES, attention, batch, check_attention, half_step, keys_of, tiny
 
 pytestmark = pytest.mark.gpu
@@ -300,3 +301,18 @@ def test_join_after_a_timeout_reads_the_parts_only(ctx):
     out = g.paged_attention(ctx, qd, kd, vd, *args, max_q=1, prefix_pages=pages, lse=lse, workspace=ws)
     done(ctx)
     check_attention(out.cpu(), lse.cpu(), *attention(q, k, v, b, d ** -0.5), "after")
+
+
+def test_more_tokens_than_the_limit_are_refused(ctx):
+    """By both calls, before anything is read (no array of that size exists here)."""
+    cache = torch.zeros(2, 2, 1, 16, 64, dtype=torch.float16, device=DEV)
+    c = bytes(serving.KvCache(cache[0].data_ptr(), cache[1].data_ptr(), 2, 16, 1, 64, 1024, 1024, 64, serving.GEMM_F16))
+    of = lambda tokens: bytes(serving.KvBatch(0, tokens, 0, None, None, None, 1, 1, None, 0))
+    h = bytes(serving.Heads(None, 0, 64, 64))
+    k = bytes(serving.Heads(cache.data_ptr(), 1, 0, 0))
+    r = bytes(serving.Rope(None, 0, None, None, 0.0, 1.0, 0))
+    stream = torch.cuda.current_stream().cuda_stream
+    for tokens, want in ((2 ** 31 - 1024, g.GEMM_OK), (2 ** 31 - 1023, g.GEMM_ERR_ARG), (2 ** 31 - 1, g.GEMM_ERR_ARG)):
+        assert g.lib().gemm_paged_attention_workspace(ctx.handle, c, of(tokens), 1) == want
+        assert g.lib().gemm_kv_append(ctx.handle, c, of(tokens), h, k, k, r, h, stream) == want
+    done(ctx)

@@ -46,6 +46,12 @@ def test_small_tiles_over_a_long_cache(walk):
     assert walk(1, 16, 1, [(2000, 2_000_000_000), (1, 7)])[1] > 2 ** 31
 
 
+@pytest.mark.parametrize("group,kv", [(1, 100), (4, 2 ** 31 - 1024)])
+def test_as_many_tokens_as_a_batch_may_have(walk, group, kv):
+    """The last tile ends past them, the first new token stands far in front of the first key."""
+    walk(2, group, 1, [(2 ** 31 - 1024, kv)], grid=3)
+
+
 def test_random_batches(walk):
     rng = random.Random(5)
     for i in range(150):
