@@ -316,3 +316,12 @@ def test_more_tokens_than_the_limit_are_refused(ctx):
         assert g.lib().gemm_paged_attention_workspace(ctx.handle, c, of(tokens), 1) == want
         assert g.lib().gemm_kv_append(ctx.handle, c, of(tokens), h, k, k, r, h, stream) == want
     done(ctx)
+
+
+@pytest.mark.parametrize("slots,every,n,kv,prefix", [(3000, 61, 1, 40, 20), (3000, 700, 3, 9, 2), (5000, 2, 1, 5, 3), (700, 699, 2, 1, 4)], ids=str)
+def test_prefix_of_a_padded_batch(ctx, slots, every, n, kv, prefix):
+    """Tokens with many empty sequences before, between and behind them."""
+    n_q = [n if i % every == every - 1 else 0 for i in range(slots)]
+    b = batch(n_q, [kv if x else 0 for x in n_q], 16, prefix_pages=prefix, seed=4)
+    q, k, v = normal((sum(n_q), 4, 64), 1), normal((b["pages"], 1, 16, 64), 2), normal((b["pages"], 1, 16, 64), 3)
+    check_attention(*run(ctx, b, q, k, v, max_q=n), *attention(q, k, v, b, 0.125), "padded")
