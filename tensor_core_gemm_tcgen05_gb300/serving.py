@@ -185,7 +185,7 @@ def _on(stream, device):
 def _empty(shape, dtype, device, stream):
     """A tensor for a kernel on ``stream`` (None: the current one) to write. The memory comes from what is free
     on that stream: a block that is free on the current one may still be in use by work queued there."""
-    if stream is None:
+    if stream is None or device.type != "cuda":   # (the library refuses host memory)
         return torch.empty(shape, dtype=dtype, device=device)
     handle = _on(stream, device)
     if handle == _current(device):
@@ -300,7 +300,9 @@ def paged_attention(ctx, q, k_cache, v_cache, q_start, kv_lens, page_table, max_
         if need < 0:
             raise _g.GemmError(int(need), "gemm_paged_attention_workspace")
         workspace = _empty((need,), torch.uint8, device, stream)
-    _g._check(L.gemm_paged_attention(h, c, b, hq, 1.0 / math.sqrt(d) if scale is None else scale, ho, lse_ptr, lse_stride,
+    if scale is None:
+        scale = 1.0 / math.sqrt(d) if d else 1.0   # (a head_dim of 0 is the library's to refuse)
+    _g._check(L.gemm_paged_attention(h, c, b, hq, scale, ho, lse_ptr, lse_stride,
                                     workspace.data_ptr(), workspace.numel(), _on(stream, device)), "gemm_paged_attention")
     return out
 
