@@ -143,6 +143,13 @@ struct PagedConfig {
 // blocks only: a part costs about as much (128 KB of FP32 written and read again) as the blocks.
 constexpr int kPagedCoarse = 8, kPagedLog2Quantum = 2, kPagedQuantum = 1 << kPagedLog2Quantum;
 
+// 2^(s - m) is off by as much for all keys of a row as m is rounded, which the sums take out again: as long as that is
+// little. From this |m| on (half a step of 2^-12; scores of 2840) the raw scores are made relative to the one that m comes
+// from before they are scaled, so that what m rounds to plays no part (a score of 2^26 lies up to 4 off its rounded m,
+// which FP16's P does not hold). Costs ordinary scores a comparison and a vote more per block: prompts 148.3 -> 149.9 us,
+// drafts 78.5 -> 79.9.
+constexpr float kPagedLarge = 4096.0f;
+
 // ---- work units --------------------------------------------------------------------------------
 //
 // (compiled for the host too, so that the ranges can be checked without a GPU)
@@ -415,6 +422,23 @@ __device__ __forceinline__ void tmem_chunks(uint32_t addr, uint32_t (&v)[32], Fn
         tmem_ld_wait_regs(v);
         fn(v, c);
     }
+}
+
+// Subtracts x from 32 N columns of this warp's lanes.
+template <int N>
+__device__ __forceinline__ void subtract_scores(uint32_t addr, float x)
+{
+    uint32_t v[32];
+#pragma unroll 1
+    for (int c = 0; c < N; ++c) {
+        tmem_ld_32x32b_x32(addr + 32u * c, v);
+        tmem_ld_wait_regs(v);
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+            v[e] = __float_as_uint(__uint_as_float(v[e]) - x);
+        tmem_st_32x32b_x32(addr + 32u * c, v);
+    }
+    tmem_st_wait();
 }
 
 // Every lane of the warp has 128 bytes (8 pieces) for its address `row` (16-byte aligned; nullptr:
@@ -709,8 +733,8 @@ __device__ __noinline__ void repair_stretches(const PagedParams &p, const Walk &
 
 template <class Cfg>
 __device__ __forceinline__ void paged_softmax_warp(const PagedParams &p, const PagedBars &bar, const WaitCtl &wc, uint32_t tmem,
-                                                   uint32_t ring, uint32_t stage, volatile int *spoilt, const Walk &start, const Shares &shares,
-                                                   int tile, int warp, int lane)
+                                                   uint32_t ring, uint32_t stage, volatile int *spoilt, volatile float *ref, const Walk &start,
+                                                   const Shares &shares, int tile, int warp, int lane)
 {
     using T = typename Cfg::Type;
     constexpr int D = Cfg::D, BKV = Cfg::BKV, CH = BKV / 32;
@@ -824,27 +848,45 @@ __device__ __forceinline__ void paged_softmax_warp(const PagedParams &p, const P
                         }
                     }
                 });
-                const float mb = (sl2 >= 0.0f ? fmax3(fmaxf(r0, r1), r2, r3) : fmin3(fminf(r0, r1), r2, r3)) * sl2 - Cfg::SHIFT;
+                const float rb = sl2 >= 0.0f ? fmax3(fmaxf(r0, r1), r2, r3) : fmin3(fminf(r0, r1), r2, r3);
+                const float mb = rb * sl2 - Cfg::SHIFT;
                 const bool raise = mb > m + Cfg::RESCALE || m == -INFINITY;
-                const float m_new = raise ? mb : m;
-                const float m_use = m_new == -INFINITY ? 0.0f : m_new;
-                const float alpha = raise && row_ok ? ex2_approx(m - m_use) : 1.0f;   // 0 on the first block
-                if (any_block && __any_sync(0xffffffffu, alpha != 1.0f)) {
-                    // O holds the blocks before: once their product is complete, rescale the rows
-                    if (!(last_tile ? wait_warp(bar.empty0 + 8u * prev_v.slot, prev_v.parity, wc, ERR_EPILOGUE_ACCUMULATOR, lane)
-                                    : wait_warp(bar.pv_done, (count - 1u) & 1u, wc, ERR_EPILOGUE_ACCUMULATOR, lane)))
-                        return;
-                    tc_fence_after_sync();
-#pragma unroll 1
-                    for (int c = 0; c < D / 32; ++c) {
-                        tmem_ld_32x32b_x32(o_addr + 32u * c, va);
-                        tmem_ld_wait_regs(va);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            va[e] = __float_as_uint(__uint_as_float(va[e]) * alpha);
-                        tmem_st_32x32b_x32(o_addr + 32u * c, va);
+                float m_new = raise ? mb : m;
+                float m_use = m_new == -INFINITY ? 0.0f : m_new;
+                float alpha = raise && row_ok ? ex2_approx(m - m_use) : 1.0f;   // 0 on the first block
+                const bool large = row_ok && fabsf(m_use) > kPagedLarge;
+                if (__any_sync(0xffffffffu, large || (any_block && alpha != 1.0f))) {
+                    if (__builtin_expect(__any_sync(0xffffffffu, large), 0)) {
+                        if (large) {
+                            bool up = raise;
+                            if (m != -INFINITY && fabsf(m) > kPagedLarge) {   // (then *ref is what m comes from)
+                                up = (rb - *ref) * sl2 > Cfg::RESCALE;
+                                m_new = up ? mb : m;
+                                alpha = up ? ex2_approx((*ref - rb) * sl2) : 1.0f;
+                            }
+                            if (up)
+                                *ref = rb;
+                            m_use = -Cfg::SHIFT;
+                        }
+                        subtract_scores<CH>(s_addr, large ? *ref : 0.0f);
                     }
-                    tmem_st_wait();
+                    if (any_block) {
+                        // O holds the blocks before: once their product is complete, rescale the rows
+                        if (!(last_tile ? wait_warp(bar.empty0 + 8u * prev_v.slot, prev_v.parity, wc, ERR_EPILOGUE_ACCUMULATOR, lane)
+                                        : wait_warp(bar.pv_done, (count - 1u) & 1u, wc, ERR_EPILOGUE_ACCUMULATOR, lane)))
+                            return;
+                        tc_fence_after_sync();
+#pragma unroll 1
+                        for (int c = 0; c < D / 32; ++c) {
+                            tmem_ld_32x32b_x32(o_addr + 32u * c, va);
+                            tmem_ld_wait_regs(va);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                va[e] = __float_as_uint(__uint_as_float(va[e]) * alpha);
+                            tmem_st_32x32b_x32(o_addr + 32u * c, va);
+                        }
+                        tmem_st_wait();
+                    }
                 }
                 uint64_t sum2[4] = {f32x2_pack(0.0f, 0.0f), f32x2_pack(0.0f, 0.0f), f32x2_pack(0.0f, 0.0f),
                                     f32x2_pack(0.0f, 0.0f)};
@@ -1018,6 +1060,7 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, Cfg::CTAS_PER_SM)
     __shared__ int64_t warp_sum[WARPS];
     __shared__ Walk start;
     __shared__ int64_t start_at;   // unit of the key head with which the range begins
+    __shared__ float refs[128 * NT];   // of each row, the raw score that a large m comes from
     __shared__ int spoilt[4 * NT];   // of each softmax warp, see repair_stretches
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -1445,8 +1488,8 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, Cfg::CTAS_PER_SM)
         __syncwarp();
     } else {
         // ---------------------------------------------------------------- softmax
-        paged_softmax_warp<Cfg>(p, bar, wc, tmem, ring, base + Cfg::STAGE_OFF + static_cast<uint32_t>(warp) * Cfg::STAGE_WARP, spoilt, start,
-                                shares, warp >> 2, warp, lane);
+        paged_softmax_warp<Cfg>(p, bar, wc, tmem, ring, base + Cfg::STAGE_OFF + static_cast<uint32_t>(warp) * Cfg::STAGE_WARP, spoilt,
+                                refs + threadIdx.x, start, shares, warp >> 2, warp, lane);
     }
 
     tc_fence_before_sync();

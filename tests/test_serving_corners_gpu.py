@@ -325,3 +325,25 @@ def test_prefix_of_a_padded_batch(ctx, slots, every, n, kv, prefix):
     b = batch(n_q, [kv if x else 0 for x in n_q], 16, prefix_pages=prefix, seed=4)
     q, k, v = normal((sum(n_q), 4, 64), 1), normal((b["pages"], 1, 16, 64), 2), normal((b["pages"], 1, 16, 64), 3)
     check_attention(*run(ctx, b, q, k, v, max_q=n), *attention(q, k, v, b, 0.125), "padded")
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("top", [1e2, 4e3, 6e3, 1e5, 3e7, 2e8, 1e9, 3e10], ids=str)
+@pytest.mark.parametrize("n_q,kv,prefix,scale", [([1, 3], [70, 300], 0, 1.0), ([150, 40], [150, 700], 0, 1.0), ([1] * 9, [50] * 9, 6, 0.7),
+                                                 ([1], [9000], 0, -0.3), ([200], [900], 0, -0.9)], ids=lambda x: str(x)[:12])
+def test_scores_of_any_size(ctx, n_q, kv, prefix, scale, top, dtype):
+    """Scores whose FP32 steps are larger than the exponents of the type's probabilities: keys of the largest
+    score share the weight (some in each sequence, so in several blocks, tiles and parts), the others, a tenth
+    behind at least, have e^-10 of it or less. Queries of a power of two and keys of 64 equal values: FP32 holds
+    the scores exactly."""
+    t, page, d, hk = TYPES[dtype], 16, 64, 2
+    b = batch(n_q, kv, page, prefix_pages=prefix, seed=3)
+    gen = torch.Generator().manual_seed(4)
+    a = 2.0 ** math.floor(math.log2((top / abs(scale) / d) ** 0.5))
+    most = top / abs(scale) / d / a
+    x = (torch.rand(b["pages"], hk, page, 1, generator=gen) * 1.9 - 1) * most
+    x[torch.rand(x.shape, generator=gen) < 0.02] = most
+    q, k = torch.full((sum(n_q), 4, d), math.copysign(a, scale), dtype=t), x.to(t).repeat(1, 1, 1, d)
+    v = normal(k.shape, 5, torch.float32).to(t)
+    assert torch.isfinite(k).all() and torch.isfinite(q).all()
+    check_attention(*run(ctx, b, q, k, v, scale=scale), *attention(q, k, v, b, scale), top)
