@@ -78,7 +78,8 @@ typedef struct gemm_kv_batch {
  *   rotary_dim: the first rotary_dim values of a head are rotated (a multiple of 16, 0 for none,
  *     up to head_dim), in pairs (i, i + rotary_dim / 2), or (2i, 2i + 1) if interleaved. Pair i
  *     at position p turns by p * table[i] * 2^-64 of a full turn, computed modulo one turn in
- *     64-bit integers, so that the angle is as exact at far positions as at near ones:
+ *     64-bit integers, so that far positions add no error but the table's own, p times; the
+ *     sine takes the angle to 2^-26 of a turn:
  *       (a, b) -> scale * (a cos - b sin, b cos + a sin).
  *   table: rotary_dim / 2 words (device, 8-byte aligned), see gemm_rope_table. */
 typedef struct gemm_rope {
@@ -96,14 +97,17 @@ enum gemm_rope_scaling {
     GEMM_ROPE_LINEAR = 1, /* f_i / factor (positions interpolated)                        */
     GEMM_ROPE_NTK = 2,    /* base replaced by base * factor^(rotary_dim / (rotary_dim - 2)) */
     GEMM_ROPE_YARN = 3    /* "YaRN" by parts (Peng et al., 2023): f_i / factor where fewer than 1
-                             turn fits the original length, f_i where more than 32 do, a linear
-                             mix in between; *scale = 0.1 ln(factor) + 1, else 1            */
+                             turn fits the original length, f_i where more than 32 do, between
+                             them a mix linear in the number of turns, as in the paper (code
+                             that mixes linearly in the pair's index has other frequencies
+                             there: for its checkpoints fill a table of your own);
+                             *scale = 0.1 ln(factor) + 1, else 1                           */
 };
 
 /* Fills `table` (HOST memory, rotary_dim / 2 words) with the turns per position of each pair in
- * units of 2^-64, and *scale (may be NULL) with the factor for gemm_rope.scale. `original`: the
- * trained length in positions (read for GEMM_ROPE_YARN only). Computes on the host; needs no
- * context. GEMM_ERR_ARG if rotary_dim is not a positive multiple of 16 up to 128, base <= 1,
+ * units of 2^-64 (f_i / 2 pi times 2^64, rounded; computed in FP64, so within 2^-55 of a turn), and
+ * *scale (may be NULL) with the factor for gemm_rope.scale. `original`: the trained length in
+ * positions (read for GEMM_ROPE_YARN only). Computes on the host; needs no context. GEMM_ERR_ARG if rotary_dim is not a positive multiple of 16 up to 128, base <= 1,
  * factor < 1 or not finite, or original <= 0 where it is read. */
 int gemm_rope_table(int64_t rotary_dim, double base, int scaling, double factor, double original,
                     uint64_t *table, float *scale);

@@ -5,9 +5,10 @@
 //     (a, b) -> scale * (a cos t - b sin t, b cos t + a sin t)  t = 2 pi * frac(p * f)
 //
 // over pairs of the first rotary_dim values. The turns f of a pair per position are held in
-// units of 2^-64, so that p * f modulo one turn is one wrapping 64-bit product, exact at any
-// position: the angle's error is that of the table's rounding, p * 2^-65 turns, where an FP32
-// product is off by 0.06 rad at a million positions and an FP64 one costs the FP64 units (a few
+// units of 2^-64, so that p * f modulo one turn is one wrapping 64-bit product, which adds no error
+// at any position. The angle's error is p times the table's (gemm_rope_table computes in FP64: up to 2^-55 turns for
+// the fastest pairs) and 2^-26 of a turn everywhere, from the float in which the fraction's top 32 bits go to the sine.
+// An FP32 product is off by 0.06 rad at a million positions, and an FP64 one costs the FP64 units (a few
 // operations per clock and SM).
 //
 // Bound by memory: every value is read once and written once. A group of head_dim / 8 lanes

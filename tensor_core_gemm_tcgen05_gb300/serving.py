@@ -202,7 +202,8 @@ def rope_table(rotary_dim, base=10000.0, scaling=None, factor=1.0, original=None
     """``(table, scale)``: the frequencies of ``gemm_rope`` as an int64 CPU tensor of
     ``rotary_dim / 2`` words (turns a position in units of 2^-64) and the factor for
     ``rope_scale``. ``scaling``: None, "linear", "ntk" or "yarn" (with ``original``, the trained
-    length), for contexts ``factor`` times as long."""
+    length; by the paper's formula, see the header), for contexts ``factor`` times as long. Frequencies
+    ``f`` of any other rule, in radians a position, are a table as ``round(f / (2 pi) * 2**64)``."""
     if scaling not in _SCALINGS:
         raise ValueError(f"scaling: one of {sorted(k for k in _SCALINGS if k)} or None expected, got {scaling!r}")
     if not 16 <= int(rotary_dim) <= 128:
