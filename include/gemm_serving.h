@@ -74,7 +74,8 @@ typedef struct gemm_kv_batch {
 
 /* Norm and rotation of query and key heads.
  *   q_norm, k_norm: head_dim weights (device, 16-byte aligned) of an RMS norm over each head,
- *     y = x / sqrt(mean(x^2) + eps) * w, done first; NULL: no norm.
+ *     y = x / sqrt(mean(x^2) + eps) * w, done first, the mean in FP32 (magnitudes up to 1e18);
+ *     NULL: no norm.
  *   rotary_dim: the first rotary_dim values of a head are rotated (a multiple of 16, 0 for none,
  *     up to head_dim), in pairs (i, i + rotary_dim / 2), or (2i, 2i + 1) if interleaved. Pair i
  *     at position p turns by p * table[i] * 2^-64 of a full turn, computed modulo one turn in
@@ -107,8 +108,9 @@ enum gemm_rope_scaling {
 /* Fills `table` (HOST memory, rotary_dim / 2 words) with the turns per position of each pair in
  * units of 2^-64 (f_i / 2 pi times 2^64, rounded; computed in FP64, so within 2^-55 of a turn), and
  * *scale (may be NULL) with the factor for gemm_rope.scale. `original`: the trained length in
- * positions (read for GEMM_ROPE_YARN only). Computes on the host; needs no context. GEMM_ERR_ARG if rotary_dim is not a positive multiple of 16 up to 128, base <= 1,
- * factor < 1 or not finite, or original <= 0 where it is read. */
+ * positions (read for GEMM_ROPE_YARN only). Computes on the host; needs no context. GEMM_ERR_ARG if
+ * rotary_dim is not a positive multiple of 16 up to 128, base <= 1, factor < 1 or not finite, or
+ * original <= 0 where it is read. */
 int gemm_rope_table(int64_t rotary_dim, double base, int scaling, double factor, double original,
                     uint64_t *table, float *scale);
 

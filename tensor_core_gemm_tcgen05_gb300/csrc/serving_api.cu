@@ -25,7 +25,9 @@ constexpr int64_t kMaxHeads = 1 << 16;
 constexpr int64_t kMaxSeqs = 1 << 24;   // (the search of a token's sequence steps past the last one in 32 bits)
 constexpr int64_t kMaxKeys = (int64_t(1) << 31) - 1024;   // a block of keys may begin at the last one
 constexpr int64_t kMaxTokens = (int64_t(1) << 31) - 1024;   // of a batch: a tile may end past the last one
-constexpr int64_t kJointTiles = 4;   // tiles of rows up to which prefix and own keys share a launch
+// Tiles of rows up to which prefix and own keys share a launch (32 + 8 heads of 128, 300 own keys behind 16480: one launch
+// against two, 2 tiles 58 / 80 us, 4 tiles 87 / 110, 8 tiles 162 / 165, 12 tiles 236 / 221)
+constexpr int64_t kJointTiles = 4;
 
 // ---- strided operands ------------------------------------------------------------------------
 
@@ -360,7 +362,10 @@ AttnPlan attention_plan(const gemm_ctx *ctx, const gemm_kv_cache &c, const gemm_
     const int64_t prefix = b.num_prefix_pages * c.page_size, own = b.table_width * c.page_size;
     const int64_t flat_tiles = (T + tq - 1) / tq;
     // The prefix by itself, for the tokens of all sequences together, when that takes fewer tiles
-    // of rows than there are sequences (each of which would read the prefix again).
+    // of rows than there are sequences (each of which would read the prefix again): 64 sequences of 300 keys behind
+    // 2048 35.5 us against 74.3, behind 16480 58 against 449. Every row then goes through the workspace, which a short
+    // prefix does not earn: behind 256 keys 30.0 against 29.3, behind 32 35 against 26 (64 of 4000 keys: 186
+    // against 168 behind 256, equal at 1024; 8 of 300: equal at 4096).
     pl.joint = prefix > 0 && flat_tiles < b.num_seqs;
     auto add = [&](int tiles, int64_t tile_tokens, int keys, int seqs, int64_t max_tiles, int64_t key_count) {
         AttnLaunch &l = pl.launch[pl.count++];
@@ -384,7 +389,9 @@ AttnPlan attention_plan(const gemm_ctx *ctx, const gemm_kv_cache &c, const gemm_
     // the one-tile kernel. If max_q says that all are short the one-tile kernel takes whatever there
     // is; if they have more than a tile's on average the two-tile kernel does (a second launch for
     // a few short ones costs more than their idle rows: nine sequences of 1 to 512 tokens 145 ->
-    // 115 us).
+    // 115 us; 8192 tokens beside 64 single ones that see 2000 keys 553 against 558 with both, 2048 158
+    // against 160, 512 behind 8000 keys 178 against 176). An unknown max_q counts as long (64 single tokens of 2000 keys 102 us,
+    // 91 with max_q = 1).
     const bool may_short = !may_long || (b.num_seqs > 1 && T < b.num_seqs * tq);
     if (may_long)
         add(2, tq, keys, may_short ? gb300::SEQS_LONG : gb300::SEQS_ALL, std::min(T, T / (2 * tq) + b.num_seqs), seen);
