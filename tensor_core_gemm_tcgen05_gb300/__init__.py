@@ -243,7 +243,7 @@ def row_softmax(ctx, X, out=None, stream=None):
 
     rows, cols = X.shape
     if out is None:
-        out = torch.empty_like(X)
+        out = _serving._empty(X.shape, X.dtype, X.device, stream)
     for t in (X, out):
         if t.dtype != torch.float16 or not t.is_contiguous():
             raise ValueError("X and out must be contiguous float16 tensors")
@@ -269,7 +269,7 @@ def attention(ctx, Q, K, V, scale=None, causal=False, out=None, stream=None):
     H, Sq, D = Q.shape
     Sk = K.shape[1]
     if out is None:
-        out = torch.empty_like(Q)
+        out = _serving._empty(Q.shape, Q.dtype, Q.device, stream)
     for t in (Q, K, V, out):
         if t.dtype != torch.float16 or not t.is_contiguous():
             raise ValueError("Q, K, V and out must be contiguous float16 tensors")
@@ -301,7 +301,7 @@ def gemm(ctx, A, B, bias=None, epilogue=EPI_NONE, out=None, stream=None):
     if K != K2:
         raise ValueError(f"shape mismatch {tuple(A.shape)} @ {tuple(B.shape)}")
     if out is None:
-        out = torch.empty((M, N), dtype=torch.float16, device=A.device)
+        out = _serving._empty((M, N), torch.float16, A.device, stream)
     for t in (A, B, bias, out):
         if t is not None and (t.dtype != torch.float16 or not t.is_contiguous()):
             raise ValueError("A, B, bias and out must be contiguous float16 tensors")
