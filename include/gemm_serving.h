@@ -134,7 +134,8 @@ int gemm_kv_append(gemm_ctx *ctx, const gemm_kv_cache *cache, const gemm_kv_batc
                    void *stream);
 
 /* out[t][h][:] = sum_j softmax_j(scale * q[t][h][:] . K[j][h'][:]) V[j][h'][:] over the keys j
- * that token t sees (scale: any sign, 0 for the mean, |scale| up to 2.35e38), h' = h / (q->heads / kv_heads); q->heads is a multiple of kv_heads, at most
+ * that token t sees (scale: any sign, |scale| up to 2.35e38; 0 for the mean, of which
+ * scores of -inf are no part), h' = h / (q->heads / kv_heads); q->heads is a multiple of kv_heads, at most
  * 128 times it, and num_tokens * q->heads at most 2^33. lse (may be NULL): FP32,
  * lse[t * lse_stride + h] = ln sum_j exp(scale * q . K_j). A token that sees no key gets out = 0 and
  * lse = -inf; one that sees keys, all of scores -inf, lse = -inf and out = NaN (0/0).

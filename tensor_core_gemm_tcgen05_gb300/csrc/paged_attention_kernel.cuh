@@ -480,14 +480,15 @@ __device__ __noinline__ int prefix_seen(const BatchView &b, int token, bool on)
     return min(b.prefix_len, max(0, b.prefix_len + v.kv - v.n + (token - v.q0) + 1));
 }
 
-// (m, l) of a part as it is kept. One of no weight has l = 0, and its O may not be written; m is NaN then if its row
-// sees a key of it all the same (scores of -inf only): 0/0 if all parts are such, where a row that sees none is 0.
+// (m, l) of a part as it is kept. Of no weight is l = 0; m is NaN then if the row sees a key of the part all the same (scores of
+// -inf only): its O counts, 0 unless a value is not finite, and the row is 0/0 if all its parts are such. With any other
+// m the part has no key for the row: its O may not be written, and a row of such parts only is 0.
 __device__ __forceinline__ float2 part_ml(float m, float l, bool sees)
 {
     return make_float2(l == 0.0f && sees ? NAN : m, l);
 }
 
-__device__ __forceinline__ bool no_weight(float2 ml) { return ml.y == 0.0f && ml.x != ml.x; }
+__device__ __forceinline__ bool no_key(float2 ml) { return ml.y == 0.0f && ml.x == ml.x; }
 
 // A key that some rows of an item see and others do not gets P = 0 for those, and 0 times a value
 // that is infinite or NaN is NaN. So a warp that finds such an O in a row that does not see all keys of
@@ -959,7 +960,7 @@ __device__ __forceinline__ void paged_softmax_warp(const PagedParams &p, const P
         }
         const int head = g.head * p.group + row_head;
         // rows that do not see all keys of the stretch: is their O finite (that of NaN scores is not meant to be)
-        const bool part_seen = row_ok && l > 0.0f && seen < min(min(g.b1, mine) * BKV, alive);
+        const bool part_seen = row_ok && l == l && seen < min(min(g.b1, mine) * BKV, alive);
         if (__builtin_expect(__any_sync(0xffffffffu, part_seen), 0)) {
             float top0 = 0.0f, top1 = 0.0f;   // largest magnitudes, NaN if there is one
 #pragma unroll 1
@@ -1537,7 +1538,7 @@ template <int V>
 struct RowSum {
     float m = -INFINITY, l = 0.0f;
     float acc[V] = {};
-    bool zero = false;   // a part has keys of no weight
+    bool sees = false;   // a part has keys for the row
 
     // Adds n parts, in order: lane i of a step of 32 fetches (m, l) of part i, then all lanes add up
     // their dimensions, eight parts' loads at a time. part(i): where part i's O and (m, l) are.
@@ -1553,9 +1554,8 @@ struct RowSum {
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
             const float m_new = fmaxf(m, top);
             const float keep = m == -INFINITY ? 0.0f : exp2f(m - m_new);
-            const bool none = ml.y == 0.0f;   // a part of no weight: its O may not be written
-            const float w = none ? 0.0f : ml.y != ml.y ? ml.y : exp2f(ml.x - m_new);   // (NaN stays NaN)
-            float sum = none ? 0.0f : w * ml.y;
+            const float w = ml.y == 0.0f ? 0.0f : ml.y != ml.y ? ml.y : exp2f(ml.x - m_new);   // (NaN stays NaN)
+            float sum = w * ml.y;
 #pragma unroll
             for (int s = 16; s > 0; s /= 2)
                 sum += __shfl_xor_sync(0xffffffffu, sum, s);
@@ -1564,9 +1564,8 @@ struct RowSum {
 #pragma unroll
             for (int e = 0; e < V; ++e)
                 acc[e] *= keep;
-            const uint32_t some = __ballot_sync(0xffffffffu, !none);
-            if (some == 0)   // (matters only if no part has any weight)
-                zero = zero || __any_sync(0xffffffffu, no_weight(ml));
+            const uint32_t some = __ballot_sync(0xffffffffu, !no_key(ml));
+            sees = sees || some != 0;
             for (int j0 = 0; j0 < k; j0 += 8) {
                 float x[8][V];
 #pragma unroll
@@ -1592,7 +1591,7 @@ struct RowSum {
     template <typename T>
     __device__ __forceinline__ void write(const CombineParams &p, int64_t token, int head, int lane) const
     {
-        const float inv = l == 0.0f ? (zero ? NAN : 0.0f) : 1.0f / l;
+        const float inv = l == 0.0f ? (sees ? NAN : 0.0f) : 1.0f / l;
         T *dst = static_cast<T *>(p.out) + token * p.out_token + head * p.out_head + lane * V;
         uint32_t w[V / 2];
 #pragma unroll
@@ -1619,7 +1618,7 @@ __device__ __forceinline__ void combine_few(const CombineParams &p, const PartsV
         return;
     float m = -INFINITY, l = 0.0f;
     float4 acc[V] = {};
-    bool zero = false;   // a part has keys of no weight
+    bool sees = false;   // a part has keys for the row
     for (int i0 = 0; i0 < n; i0 += kCombineStep) {
         float4 x[kCombineStep][V];
         float2 ml[kCombineStep];
@@ -1643,10 +1642,10 @@ __device__ __forceinline__ void combine_few(const CombineParams &p, const PartsV
             acc[e] = make_float4(acc[e].x * keep, acc[e].y * keep, acc[e].z * keep, acc[e].w * keep);
 #pragma unroll
         for (int i = 0; i < kCombineStep; ++i) {
-            zero = zero || no_weight(ml[i]);   // (the last part again: the same answer)
-            if (i0 + i >= n || ml[i].y == 0.0f)
-                continue;   // a part of no weight: its O may not be written
-            const float w = ml[i].y != ml[i].y ? ml[i].y : exp2f(ml[i].x - m);   // (NaN stays NaN)
+            if (i0 + i >= n || no_key(ml[i]))
+                continue;
+            sees = true;
+            const float w = ml[i].y == 0.0f ? 0.0f : ml[i].y != ml[i].y ? ml[i].y : exp2f(ml[i].x - m);   // (NaN stays NaN)
             l += w * ml[i].y;
 #pragma unroll
             for (int e = 0; e < V; ++e) {
@@ -1657,7 +1656,7 @@ __device__ __forceinline__ void combine_few(const CombineParams &p, const PartsV
             }
         }
     }
-    const float inv = l == 0.0f ? (zero ? NAN : 0.0f) : 1.0f / l;
+    const float inv = l == 0.0f ? (sees ? NAN : 0.0f) : 1.0f / l;
     T *dst = static_cast<T *>(p.out) + token * p.out_token + head * p.out_head;
 #pragma unroll
     for (int e = 0; e < V; ++e)

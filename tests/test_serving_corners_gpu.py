@@ -347,3 +347,20 @@ def test_scores_of_any_size(ctx, n_q, kv, prefix, scale, top, dtype):
     v = normal(k.shape, 5, torch.float32).to(t)
     assert torch.isfinite(k).all() and torch.isfinite(q).all()
     check_attention(*run(ctx, b, q, k, v, scale=scale), *attention(q, k, v, b, scale), top)
+
+
+@pytest.mark.parametrize("n_q,kv,hq,hk,d,page,prefix,max_q", [
+    ([1] * 12, [1] * 12, 4, 2, 64, 16, 8, 1), ([1, 1], [3000, 90], 4, 2, 128, 16, 0, 1), ([3, 40], [70, 300], 4, 2, 64, 16, 0, 40),
+    ([150, 2, 1], [150, 5, 9], 4, 2, 128, 16, 2, None), ([6] * 20, [9] * 20, 4, 1, 64, 16, 9, 6)], ids=lambda x: str(x)[:20])
+def test_values_that_are_not_finite_of_keys_without_weight(ctx, n_q, kv, hq, hk, d, page, prefix, max_q):
+    """A weight of 0 times an infinite value is NaN for the rows that see the key, wherever the keys are cut into
+    parts, and nothing for the others."""
+    b = batch(n_q, kv, page, prefix_pages=prefix, seed=8)
+    q = normal((sum(n_q), hq, d), 1)
+    q[..., 3] = q[..., 3].abs() + 0.5
+    for what, at in (("last", [(s, n - 1, s % hk, 3) for s, n in enumerate(kv)]), ("new", spots(b, hk, 1, 3, 5, late=True)),
+                     ("late half", [(s, j, h, 3) for s, n in enumerate(kv) for j in range(n // 2, n) for h in range(hk)])):
+        k, v = normal((b["pages"], hk, page, d), 2), normal((b["pages"], hk, page, d), 3)
+        put(k, b, [(s, j, h, 3) for s, j, h, _ in at], -math.inf)
+        put(v, b, [(s, j, h, (5 * j + s) % d) for s, j, h, _ in at], math.inf)
+        check_any(*run(ctx, b, q, k, v, max_q=max_q), *by_rows(q, k, v, b, d ** -0.5), what)
