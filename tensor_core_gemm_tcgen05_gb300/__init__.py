@@ -20,13 +20,16 @@ import os
 import sys
 import threading
 
+from . import decode as _decode
 from . import serving as _serving
+from .decode import (  # noqa: F401  (include/gemm_decode.h)
+    DECODE_EXPORTS, GEMM_TREE_MAX_WORDS, kv_compact, kv_select, kv_weigh, tree_attention, tree_attention_workspace, tree_mask, w4_gemm)
 from .inputs import EPI_GELU, EPI_NONE, EPI_RELU, EPI_SOFTMAX  # noqa: F401  (C ABI epilogue codes)
 from .serving import (  # noqa: F401  (include/gemm_serving.h)
     GEMM_BF16, GEMM_F16, GEMM_ROPE_LINEAR, GEMM_ROPE_NTK, GEMM_ROPE_PLAIN, GEMM_ROPE_YARN, SERVING_EXPORTS, kv_append,
     paged_attention, paged_attention_workspace, qk_rope, rope_table)
 
-_serving._g = sys.modules[__name__]
+_serving._g = _decode._g = sys.modules[__name__]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libgb300gemm.so")
@@ -101,6 +104,7 @@ def lib() -> ctypes.CDLL:
                 if name != "gemm_status_string":
                     getattr(L, name).restype = i32
             _serving._declare(L)
+            _decode._declare(L)
             _lib = L
     return _lib
 

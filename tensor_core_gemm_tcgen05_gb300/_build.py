@@ -9,7 +9,7 @@ import subprocess
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libgb300gemm.so")
-SOURCES = [os.path.join(PKG, "csrc", name) for name in ("gemm_api.cu", "gemm_noalloc.cu", "serving_api.cu")]
+SOURCES = [os.path.join(PKG, "csrc", name) for name in ("gemm_api.cu", "gemm_noalloc.cu", "serving_api.cu", "decode_api.cu")]
 DEPS = (SOURCES + glob.glob(os.path.join(PKG, "csrc", "*.cuh")) + glob.glob(os.path.join(PKG, "csrc", "*.h"))
         + glob.glob(os.path.join(ROOT, "include", "*.h")))
 

@@ -1,0 +1,499 @@
+// Host side of the C ABI declared in include/gemm_decode.h (tree attention apart, which shares its
+// launches with paged attention in serving_api.cu): argument checks, launch shapes and launches.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <limits>
+
+#include "gemm_ctx.h"
+#include "gemm_decode.h"
+#include "kv_upkeep_kernel.cuh"
+#include "serving_host.h"
+#include "w4_kernel.cuh"
+
+using namespace gb300_host;
+
+namespace {
+
+constexpr int64_t kMaxW4Rows = 1 << 20, kMaxW4Size = 1 << 24;
+constexpr int kSelectHeldMax = 48 * 1024;   // keys: 192 KB of shared memory
+
+// launch_serving in clusters of `cluster` CTAs along x.
+template <typename... P, typename... A>
+cudaError_t launch_cluster(void (*kernel)(P...), dim3 grid, int threads, int smem, int cluster, cudaStream_t stream, A &&...args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+}
+
+// Bytes from the first to the last of `n` int32 (or FP32) values.
+size_t words(int64_t n) { return static_cast<size_t>(std::max<int64_t>(n, 0)) * 4; }
+
+struct Range {
+    const void *base;
+    size_t bytes;
+};
+
+Range range_of(const Layout &l) { return Range{l.base, static_cast<size_t>(span(l)) * 2}; }
+
+bool overlap(const Range &a, const Range &b) { return overlaps(a.base, a.bytes, b.base, b.bytes); }
+
+int check_seqs(const gemm_ctx *ctx, const gemm_kv_seqs *s, int64_t page_size)
+{
+    if (!s || s->num_seqs < 0 || s->num_seqs > kMaxSeqs || s->table_width < 0 || s->table_stride < 0 ||
+        s->table_stride > kMaxStride || s->table_width > INT32_MAX || s->table_width * page_size > kMaxKeys ||
+        static_cast<i128>(s->num_seqs) * s->table_stride > (i128(1) << 59))
+        return GEMM_ERR_ARG;
+    if (s->num_seqs == 0)
+        return GEMM_OK;
+    const bool table = s->table_width > 0;
+    if (!s->kv_lens || (table && !s->page_table))
+        return GEMM_ERR_ARG;
+    if (!aligned_to(s->kv_lens, 4) || (table && !aligned_to(s->page_table, 4)))
+        return GEMM_ERR_ALIGN;
+    if (!on_ctx(ctx, s->kv_lens) || (table && !on_ctx(ctx, s->page_table)))
+        return GEMM_ERR_DEVICE;
+    return GEMM_OK;
+}
+
+Range table_range(const gemm_kv_seqs &s)
+{
+    return Range{s.page_table, s.table_width > 0 ? words((s.num_seqs - 1) * s.table_stride + s.table_width) : 0};
+}
+
+bool valid_pages(int64_t num_pages, int64_t page_size, int64_t kv_heads)
+{
+    return page_size >= 16 && page_size <= 1024 && (page_size & (page_size - 1)) == 0 && kv_heads >= 1 && kv_heads <= kMaxHeads &&
+           num_pages >= 1 && num_pages <= INT32_MAX - 1;
+}
+
+int check_weights(const gemm_ctx *ctx, const gemm_kv_weights *w, int64_t num_pages, int64_t page_size, int64_t kv_heads)
+{
+    if (!w || !w->data || w->page_stride <= 0 || w->head_stride <= 0 || w->page_stride > kMaxStride || w->head_stride > kMaxStride ||
+        static_cast<i128>(num_pages) * w->page_stride > (i128(1) << 59))
+        return GEMM_ERR_ARG;
+    const Layout l = sorted(Layout{w->data, page_size, 2, {num_pages, kv_heads, 1}, {w->page_stride, w->head_stride, 0}});
+    if (!self_disjoint(l))
+        return GEMM_ERR_ARG;
+    if (!aligned_to(w->data, 4))
+        return GEMM_ERR_ALIGN;
+    return on_ctx(ctx, w->data) ? GEMM_OK : GEMM_ERR_DEVICE;
+}
+
+Range weights_range(const gemm_kv_weights &w, int64_t num_pages, int64_t page_size, int64_t kv_heads)
+{
+    return Range{w.data, words((num_pages - 1) * w.page_stride + (kv_heads - 1) * w.head_stride + page_size)};
+}
+
+// Index lists [seqs][heads][most] (head_stride 0: one for all heads).
+bool valid_lists(int64_t seqs, int64_t heads, int64_t most, int64_t seq_stride, int64_t head_stride, bool written)
+{
+    if (seq_stride < 0 || head_stride < 0 || seq_stride > kMaxStride || head_stride > kMaxStride ||
+        static_cast<i128>(seqs) * seq_stride > (i128(1) << 59))
+        return false;
+    return !written || self_disjoint(sorted(Layout{nullptr, most, 2, {seqs, heads, 1}, {seq_stride, head_stride, 0}}));
+}
+
+int page_shift(int64_t page_size)
+{
+    int shift = 0;
+    while ((int64_t(1) << shift) < page_size)
+        ++shift;
+    return shift;
+}
+
+int launched(gemm_ctx *ctx, cudaError_t e) { return e == cudaSuccess ? GEMM_OK : cuda_fail(ctx, e, GEMM_ERR_LAUNCH); }
+
+template <typename T, int TILES, class Fn>
+cudaError_t with_group(int64_t group, Fn &&fn)
+{
+    return group == 128 ? fn(gb300::w4_kernel<T, TILES, 4>) : group == 64 ? fn(gb300::w4_kernel<T, TILES, 2>) : fn(gb300::w4_kernel<T, TILES, 1>);
+}
+
+template <typename T, class Fn>
+cudaError_t with_tiles(int tiles, int64_t group, Fn &&fn)
+{
+    switch (tiles) {
+    case 1: return with_group<T, 1>(group, fn);
+    case 2: return with_group<T, 2>(group, fn);
+    case 4: return with_group<T, 4>(group, fn);
+    default: return with_group<T, 8>(group, fn);
+    }
+}
+
+template <class Fn>
+cudaError_t with_w4(int dtype, int tiles, int64_t group, Fn &&fn)
+{
+    return dtype == GEMM_F16 ? with_tiles<__half>(tiles, group, fn) : with_tiles<__nv_bfloat16>(tiles, group, fn);
+}
+
+// Shared memory of a CTA: the chunk of A, or the partial sums.
+int w4_smem(int tiles, int row_warps)
+{
+    const int k_warps = gb300::kW4Warps / row_warps;
+    return std::max(gb300::kW4Ahead * k_warps * 4 * tiles * 32 * 16, k_warps * tiles * 8 * (16 * row_warps + 4) * 4);
+}
+
+}  // namespace
+
+namespace gb300_host {
+
+cudaError_t decode_init(gemm_ctx *)
+{
+    for (int dtype : {GEMM_F16, GEMM_BF16})
+        for (int tiles : {1, 2, 4, 8})
+            for (int64_t group : {32, 64, 128}) {
+                const cudaError_t e = with_w4(dtype, tiles, group, [&](auto kernel) {
+                    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+                });
+                if (e != cudaSuccess)
+                    return e;
+            }
+    return cudaFuncSetAttribute(gb300::kv_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelectHeldMax * 4);
+}
+
+}  // namespace gb300_host
+
+extern "C" {
+
+int gemm_tree_mask(gemm_ctx *ctx, const gemm_kv_batch *batch, int64_t prefix_len, const int32_t *parents, uint32_t *mask,
+                   int64_t mask_words, int64_t mask_stride, int32_t *positions, void *stream)
+{
+    if (!ctx || !batch || batch->num_seqs < 0 || batch->num_seqs > kMaxSeqs || batch->num_tokens < 0 ||
+        batch->num_tokens > kMaxTokens || prefix_len < 0 || prefix_len > kMaxKeys || mask_words < 1 ||
+        mask_words > GEMM_TREE_MAX_WORDS || mask_stride < 0 || mask_stride > kMaxStride ||
+        static_cast<i128>(batch->num_tokens) * mask_stride > (i128(1) << 59))
+        return GEMM_ERR_ARG;
+    const int64_t tokens = batch->num_tokens;
+    if (tokens == 0 || batch->num_seqs == 0)
+        return GEMM_OK;
+    if (!batch->q_start || !batch->kv_lens || !parents || !mask || (tokens > 1 && mask_stride < mask_words))
+        return GEMM_ERR_ARG;
+    const Range in[3] = {{batch->q_start, words(batch->num_seqs + 1)}, {batch->kv_lens, words(batch->num_seqs)}, {parents, words(tokens)}};
+    const Range out[2] = {{mask, words((tokens - 1) * mask_stride + mask_words)}, {positions, positions ? words(tokens) : 0}};
+    for (const Range &r : in)
+        if (!aligned_to(r.base, 4))
+            return GEMM_ERR_ALIGN;
+    for (const Range &r : out)
+        if (!aligned_to(r.base, 4))
+            return GEMM_ERR_ALIGN;
+    if (overlap(out[0], out[1]))
+        return GEMM_ERR_ARG;
+    for (const Range &r : in)
+        if (overlap(out[0], r) || overlap(out[1], r))
+            return GEMM_ERR_ARG;
+    for (const Range &r : in)
+        if (!on_ctx(ctx, r.base))
+            return GEMM_ERR_DEVICE;
+    if (!on_ctx(ctx, mask) || (positions && !on_ctx(ctx, positions)))
+        return GEMM_ERR_DEVICE;
+    gb300::TreeMaskParams p = {};
+    p.q_start = batch->q_start;
+    p.kv_lens = batch->kv_lens;
+    p.parents = parents;
+    p.num_tokens = static_cast<int>(tokens);
+    p.prefix_len = static_cast<int>(prefix_len);
+    p.mask = mask;
+    p.mask_stride = mask_stride;
+    p.mask_words = static_cast<int>(mask_words);
+    p.positions = positions;
+    p.err = ctx->d_err;
+    DeviceGuard guard(ctx->device);
+    return launched(ctx, launch_serving(gb300::tree_mask_kernel, batch->num_seqs, gb300::kTreeThreads, 0,
+                                        static_cast<cudaStream_t>(stream), p));
+}
+
+int gemm_kv_weigh(gemm_ctx *ctx, const gemm_kv_cache *cache, const gemm_kv_batch *batch, const gemm_heads *q, float scale,
+                  const float *lse, int64_t lse_stride, int64_t window, float decay, const gemm_kv_weights *weights,
+                  void *stream)
+{
+    const float scale_log2 = scale_in_base_2(scale);
+    if (!ctx || !cache || !q || !std::isfinite(scale_log2) || !(decay >= 0.0f && decay <= 1.0f) || window < 0 || lse_stride < 0 ||
+        lse_stride > kMaxStride || (batch && static_cast<i128>(batch->num_tokens) * lse_stride > (i128(1) << 59)))
+        return GEMM_ERR_ARG;
+    int rc = check_cache(ctx, cache, false);
+    if (rc == GEMM_OK)
+        rc = check_batch(ctx, cache, batch, true, false);
+    if (rc == GEMM_OK)
+        rc = check_heads(q, batch->num_tokens, cache->head_dim, false);
+    if (rc != GEMM_OK)
+        return rc;
+    const int64_t tokens = batch->num_tokens, heads = cache->kv_heads, group = q->heads / heads;
+    if (q->heads < heads || q->heads % heads != 0 || group > 128 || tokens * group > kMaxTokens)
+        return GEMM_ERR_ARG;
+    rc = check_weights(ctx, weights, cache->num_pages, cache->page_size, heads);
+    if (rc != GEMM_OK)
+        return rc;
+    if (batch->num_seqs == 0 || tokens == 0)
+        return GEMM_OK;
+    if (!lse || (tokens > 1 && lse_stride < q->heads))
+        return GEMM_ERR_ARG;
+    if (!aligned_to(lse, 4))
+        return GEMM_ERR_ALIGN;
+    const Range out = weights_range(*weights, cache->num_pages, cache->page_size, heads);
+    const Layout kc = cache_layout(*cache, cache->k), lq = heads_layout(*q, tokens, cache->head_dim);
+    const gemm_kv_seqs seqs = {batch->num_seqs, batch->kv_lens, batch->page_table, batch->table_width, batch->table_stride};
+    if (overlap(out, range_of(kc)) || overlap(out, range_of(lq)) || overlap(out, {lse, words((tokens - 1) * lse_stride + q->heads)}) ||
+        overlap(out, {batch->q_start, words(batch->num_seqs + 1)}) || overlap(out, {batch->kv_lens, words(batch->num_seqs)}) ||
+        overlap(out, table_range(seqs)))
+        return GEMM_ERR_ARG;
+    if (!on_ctx(ctx, q->data) || !on_ctx(ctx, lse))
+        return GEMM_ERR_DEVICE;
+    gb300::WeighParams p = {};
+    p.batch = batch_view(*cache, *batch);
+    p.q = q->data;
+    p.q_token = q->token_stride;
+    p.q_head = q->head_stride;
+    p.k = cache->k;
+    p.page_stride = cache->page_stride;
+    p.head_stride = cache->head_stride;
+    p.row_stride = cache->row_stride;
+    p.lse = lse;
+    p.lse_token = lse_stride;
+    p.w = weights->data;
+    p.w_page = weights->page_stride;
+    p.w_head = weights->head_stride;
+    p.kv_heads = static_cast<int>(heads);
+    p.group = static_cast<int>(group);
+    p.window = static_cast<int>(std::min<int64_t>(window, INT32_MAX));
+    p.scale_log2 = scale_log2;
+    p.decay = decay;
+    p.err = ctx->d_err;
+    const int64_t blocks = batch->num_seqs * heads * ((batch->table_width * cache->page_size + gb300::kWeighKeys - 1) / gb300::kWeighKeys);
+    const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(blocks, 2 * static_cast<int64_t>(ctx->num_sms)));
+    DeviceGuard guard(ctx->device);
+    auto run = [&](auto kernel) {
+        return launch_serving(kernel, grid, gb300::kWeighThreads, 0, static_cast<cudaStream_t>(stream), p);
+    };
+    if (cache->dtype == GEMM_F16)
+        return launched(ctx, cache->head_dim == 64 ? run(gb300::kv_weigh_kernel<__half, 64>) : run(gb300::kv_weigh_kernel<__half, 128>));
+    return launched(ctx, cache->head_dim == 64 ? run(gb300::kv_weigh_kernel<__nv_bfloat16, 64>)
+                                               : run(gb300::kv_weigh_kernel<__nv_bfloat16, 128>));
+}
+
+int gemm_kv_select(gemm_ctx *ctx, const gemm_kv_seqs *seqs, int64_t num_pages, int64_t page_size, int64_t kv_heads,
+                   const gemm_kv_weights *weights, int64_t keep, int64_t first, int64_t recent, int32_t *index,
+                   int64_t seq_stride, int64_t head_stride, int32_t *counts, void *stream)
+{
+    if (!ctx || !valid_pages(num_pages, page_size, kv_heads) || keep < 0 || keep > kMaxKeys || first < 0 || recent < 0 ||
+        first > keep || recent > keep || first + recent > keep)
+        return GEMM_ERR_ARG;
+    int rc = check_seqs(ctx, seqs, page_size);
+    if (rc == GEMM_OK)
+        rc = check_weights(ctx, weights, num_pages, page_size, kv_heads);
+    if (rc != GEMM_OK)
+        return rc;
+    const int64_t n = seqs->num_seqs, items = n * kv_heads;
+    if (!valid_lists(n, kv_heads, keep, seq_stride, head_stride, keep > 0 && n > 0))
+        return GEMM_ERR_ARG;
+    if (n == 0)
+        return GEMM_OK;
+    if (!counts || (keep > 0 && !index))
+        return GEMM_ERR_ARG;
+    if (!aligned_to(counts, 4) || !aligned_to(index, 4))
+        return GEMM_ERR_ALIGN;
+    const Range out[2] = {{counts, words(n)}, {index, keep > 0 ? words((n - 1) * seq_stride + (kv_heads - 1) * head_stride + keep) : 0}};
+    const Range in[3] = {{seqs->kv_lens, words(n)}, table_range(*seqs), weights_range(*weights, num_pages, page_size, kv_heads)};
+    if (overlap(out[0], out[1]))
+        return GEMM_ERR_ARG;
+    for (const Range &r : in)
+        if (overlap(out[0], r) || overlap(out[1], r))
+            return GEMM_ERR_ARG;
+    if (!on_ctx(ctx, counts) || (keep > 0 && !on_ctx(ctx, index)))
+        return GEMM_ERR_DEVICE;
+    gb300::SelectParams p = {};
+    p.kv_lens = seqs->kv_lens;
+    p.table = seqs->page_table;
+    p.table_stride = seqs->table_stride;
+    p.table_width = static_cast<int>(seqs->table_width);
+    p.num_pages = static_cast<int>(num_pages);
+    p.page_shift = page_shift(page_size);
+    p.kv_heads = static_cast<int>(kv_heads);
+    p.w = weights->data;
+    p.w_page = weights->page_stride;
+    p.w_head = weights->head_stride;
+    p.keep = static_cast<int>(keep);
+    p.first = static_cast<int>(first);
+    p.recent = static_cast<int>(recent);
+    p.index = index;
+    p.seq_stride = seq_stride;
+    p.head_stride = head_stride;
+    p.counts = counts;
+    p.err = ctx->d_err;
+    // More CTAs for a long list, as long as they fit the GPU at once and have some thousand keys each.
+    const int64_t room = seqs->table_width * page_size;
+    int cluster = 1;
+    while (cluster < 8 && items * cluster * 2 <= 2 * static_cast<int64_t>(ctx->num_sms) && room >= 4096 * cluster)
+        cluster *= 2;
+    if (items * cluster > INT32_MAX)
+        return GEMM_ERR_ARG;
+    p.held = static_cast<int>(std::min<int64_t>(kSelectHeldMax, (room + cluster - 1) / cluster + 16));
+    DeviceGuard guard(ctx->device);
+    return launched(ctx, launch_cluster(gb300::kv_select_kernel, dim3(static_cast<unsigned>(items * cluster)), gb300::kSelectThreads,
+                                        p.held * 4, cluster, static_cast<cudaStream_t>(stream), p));
+}
+
+int gemm_kv_compact(gemm_ctx *ctx, const gemm_kv_cache *cache, const gemm_kv_seqs *seqs, const gemm_kv_weights *weights,
+                    const int32_t *index, int64_t seq_stride, int64_t head_stride, int64_t most, const int32_t *start,
+                    const int32_t *counts, int32_t *new_lens, void *stream)
+{
+    if (!ctx || most < 0 || most > kMaxKeys)
+        return GEMM_ERR_ARG;
+    int rc = check_cache(ctx, cache);
+    if (rc == GEMM_OK)
+        rc = check_seqs(ctx, seqs, cache->page_size);
+    if (rc == GEMM_OK && weights)
+        rc = check_weights(ctx, weights, cache->num_pages, cache->page_size, cache->kv_heads);
+    if (rc != GEMM_OK)
+        return rc;
+    const int64_t n = seqs->num_seqs, heads = cache->kv_heads;
+    if (!valid_lists(n, heads, most, seq_stride, head_stride, false))
+        return GEMM_ERR_ARG;
+    if (n == 0)
+        return GEMM_OK;
+    if (!counts || (most > 0 && !index))
+        return GEMM_ERR_ARG;
+    if (!aligned_to(counts, 4) || !aligned_to(index, 4) || !aligned_to(start, 4) || !aligned_to(new_lens, 4))
+        return GEMM_ERR_ALIGN;
+    const Range w = weights ? weights_range(*weights, cache->num_pages, cache->page_size, heads) : Range{nullptr, 0};
+    const Range out[4] = {range_of(cache_layout(*cache, cache->k)), range_of(cache_layout(*cache, cache->v)), w,
+                          {new_lens, new_lens ? words(n) : 0}};
+    const Range in[5] = {{seqs->kv_lens, words(n)},
+                         table_range(*seqs),
+                         {index, most > 0 ? words((n - 1) * seq_stride + (heads - 1) * head_stride + most) : 0},
+                         {start, start ? words(n) : 0},
+                         {counts, words(n)}};
+    for (const Range &o : out)
+        for (const Range &r : in)
+            if (overlap(o, r))
+                return GEMM_ERR_ARG;
+    for (int i = 0; i < 4; ++i)   // (keys and values may lie between each other)
+        for (int j = std::max(2, i + 1); j < 4; ++j)
+            if (overlap(out[i], out[j]))
+                return GEMM_ERR_ARG;
+    if ((most > 0 && !on_ctx(ctx, index)) || (start && !on_ctx(ctx, start)) || !on_ctx(ctx, counts) || (new_lens && !on_ctx(ctx, new_lens)))
+        return GEMM_ERR_DEVICE;
+    gb300::CompactParams p = {};
+    p.k = cache->k;
+    p.v = cache->v;
+    p.page_stride = cache->page_stride;
+    p.head_stride = cache->head_stride;
+    p.row_stride = cache->row_stride;
+    p.kv_lens = seqs->kv_lens;
+    p.table = seqs->page_table;
+    p.table_stride = seqs->table_stride;
+    p.table_width = static_cast<int>(seqs->table_width);
+    p.num_pages = static_cast<int>(cache->num_pages);
+    p.page_shift = page_shift(cache->page_size);
+    p.kv_heads = static_cast<int>(heads);
+    if (weights) {
+        p.w = weights->data;
+        p.w_page = weights->page_stride;
+        p.w_head = weights->head_stride;
+    }
+    p.index = index;
+    p.seq_index = seq_stride;
+    p.head_index = head_stride;
+    p.most = static_cast<int>(most);
+    p.start = start;
+    p.counts = counts;
+    p.new_lens = new_lens;
+    p.err = ctx->d_err;
+    // A CTA takes several heads where their rows fit its round (accepted drafts); several CTAs take the rows of one
+    // head where there are more of them than fit.
+    const int pairs = cache->head_dim == 64 ? gb300::CompactShape<64>::PAIRS : gb300::CompactShape<128>::PAIRS;
+    p.heads = 1;
+    while (p.heads < heads && p.heads < pairs && most * p.heads * 2 <= pairs)
+        p.heads *= 2;
+    p.groups = static_cast<int>((heads + p.heads - 1) / p.heads);
+    const int64_t items = n * p.groups;
+    int cluster = 1;
+    while (cluster < 8 && items * cluster * 2 <= 4 * static_cast<int64_t>(ctx->num_sms) && most > static_cast<int64_t>(cluster) * (pairs / p.heads))
+        cluster *= 2;
+    if (items * cluster > INT32_MAX)
+        return GEMM_ERR_ARG;
+    DeviceGuard guard(ctx->device);
+    auto run = [&](auto kernel) {
+        return launch_cluster(kernel, dim3(static_cast<unsigned>(items * cluster)), gb300::kCompactThreads, 0, cluster,
+                              static_cast<cudaStream_t>(stream), p);
+    };
+    return launched(ctx, cache->head_dim == 64 ? run(gb300::kv_compact_kernel<64>) : run(gb300::kv_compact_kernel<128>));
+}
+
+int gemm_w4_run(gemm_ctx *ctx, int dtype, int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, const gemm_w4 *w,
+                const void *bias, void *C, int64_t ldc, int epilogue, void *stream)
+{
+    if (!ctx || !w || (dtype != GEMM_F16 && dtype != GEMM_BF16) || M < 0 || N < 0 || K < 0 || M > kMaxW4Rows || N > kMaxW4Size ||
+        K > kMaxW4Size || (epilogue != GEMM_EPI_NONE && epilogue != GEMM_EPI_GELU && epilogue != GEMM_EPI_RELU) ||
+        (w->group != 32 && w->group != 64 && w->group != 128) || K % w->group != 0 || lda < K || ldc < N || lda > kMaxStride || ldc > kMaxStride)
+        return GEMM_ERR_ARG;
+    if (N % 8 != 0 || (K > 0 && lda % 8 != 0) || ldc % 8 != 0)
+        return GEMM_ERR_ALIGN;
+    if (M == 0 || N == 0)
+        return GEMM_OK;
+    if (!C || (K > 0 && (!A || !w->codes || !w->scales)))
+        return GEMM_ERR_ARG;
+    if (!aligned16(C) || !aligned16(bias) || (K > 0 && (!aligned16(A) || !aligned16(w->codes) || !aligned_to(w->scales, 2))))
+        return GEMM_ERR_ALIGN;
+    const size_t n = static_cast<size_t>(N), k = static_cast<size_t>(K), groups = k / static_cast<size_t>(w->group);
+    const Range out = {C, static_cast<size_t>((M - 1) * ldc + N) * 2};
+    const Range in[5] = {{A, K > 0 ? static_cast<size_t>((M - 1) * lda + K) * 2 : 0},
+                         {w->codes, n * k / 2},
+                         {w->scales, n * groups * 2},
+                         {w->zeros, n * groups},
+                         {bias, n * 2}};
+    for (const Range &r : in)
+        if (overlap(out, r))
+            return GEMM_ERR_ARG;
+    for (const Range &r : in)
+        if (r.base && r.bytes > 0 && !on_ctx(ctx, r.base))
+            return GEMM_ERR_DEVICE;
+    if (!on_ctx(ctx, C))
+        return GEMM_ERR_DEVICE;
+    gb300::W4Params p = {};
+    p.M = static_cast<int>(M);
+    p.N = static_cast<int>(N);
+    p.K = static_cast<int>(K);
+    p.a = A;
+    p.lda = lda;
+    p.codes = w->codes;
+    p.scales = w->scales;
+    p.zeros = w->zeros;
+    p.bias = bias;
+    p.c = C;
+    p.ldc = ldc;
+    p.epilogue = epilogue;
+    p.steps = static_cast<int>((K + 127) / 128);
+    const int tiles = M <= 8 ? 1 : M <= 16 ? 2 : M <= 32 ? 4 : 8;
+    const int64_t blocks_m = (M + tiles * 8 - 1) / (tiles * 8);
+    p.row_warps = 8;
+    int cluster = 1;
+    auto blocks = [&] { return (N + 16 * p.row_warps - 1) / (16 * p.row_warps) * blocks_m; };
+    while (cluster < 8 && blocks() * cluster * 2 <= 4 * static_cast<int64_t>(ctx->num_sms) && p.steps >= 2 * cluster * gb300::kW4Ahead)
+        cluster *= 2;
+    while (p.row_warps > 1 && tiles <= 2 && blocks() * cluster < ctx->num_sms)
+        p.row_warps /= 2;
+    const int64_t grid = (N + 16 * p.row_warps - 1) / (16 * p.row_warps) * cluster;
+    DeviceGuard guard(ctx->device);
+    return launched(ctx, with_w4(dtype, tiles, w->group, [&](auto kernel) {
+                        return launch_cluster(kernel, dim3(static_cast<unsigned>(grid), static_cast<unsigned>(blocks_m)),
+                                              gb300::kW4Threads, w4_smem(tiles, p.row_warps), cluster,
+                                              static_cast<cudaStream_t>(stream), p);
+                    }));
+}
+
+}  // extern "C"

@@ -531,6 +531,8 @@ int gemm_create(gemm_ctx **out, int device)
         return cuda_fail(nullptr, e, GEMM_ERR_DEVICE);
     }
     e = serving_init(ctx);
+    if (e == cudaSuccess)
+        e = decode_init(ctx);
     if (e != cudaSuccess) {
         delete ctx;
         return cuda_fail(nullptr, e, GEMM_ERR_DEVICE);

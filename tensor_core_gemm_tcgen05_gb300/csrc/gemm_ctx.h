@@ -1,5 +1,5 @@
 // Host-side state and helpers shared by the translation units of the C ABI (gemm_api.cu,
-// serving_api.cu).
+// serving_api.cu, decode_api.cu).
 #pragma once
 
 #include <cuda.h>
@@ -108,5 +108,7 @@ inline bool overlaps(const void *a, size_t na, const void *b, size_t nb)
 
 // Sets the attributes of the serving kernels (serving_api.cu); called by gemm_create.
 cudaError_t serving_init(gemm_ctx *ctx);
+// The same for those of decode_api.cu.
+cudaError_t decode_init(gemm_ctx *ctx);
 
 }  // namespace gb300_host

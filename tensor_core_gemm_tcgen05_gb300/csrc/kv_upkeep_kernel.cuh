@@ -1,0 +1,563 @@
+// What keeps a paged key/value cache in order while it is decoded from (gemm_decode.h): masks and
+// positions of drafted trees, attention weight added up per key, the keys to keep chosen by it,
+// and rows moved up.
+#pragma once
+
+#include "mma_sync.cuh"
+#include "serving_common.cuh"
+
+namespace gb300 {
+
+// Words of the shared memory of a CTA of this cluster. `addr` is what mapa_shared returned, with nothing added
+// to it: such loads take 64-bit addresses, and where the compiler splits a 32-bit sum into a register that
+// has wrapped below zero and a positive offset, the sum ends up outside shared memory (a fault).
+__device__ __forceinline__ uint2 ld_shared_cluster_u2(uint32_t addr)
+{
+    uint2 v;
+    asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ uint4 ld_shared_cluster_u4(uint32_t addr)
+{
+    uint4 v;
+    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+__device__ __forceinline__ uint32_t cluster_size()
+{
+    uint32_t v;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(v));
+    return v;
+}
+
+__device__ __forceinline__ void report_index(uint32_t *err)
+{
+    atomicCAS(err, 0u, static_cast<uint32_t>(ERR_BATCH_INDEX));
+}
+
+// ---- trees -----------------------------------------------------------------------------------
+//
+// A node's bits are its own and those of the nodes on its way up, whose indexes fall: one walk in
+// shared memory writes the words from the last to the first. A CTA per sequence; bound by the
+// launch and one trip to memory.
+constexpr int kTreeThreads = 128, kTreeMaxNodes = 2048;   // (32 * GEMM_TREE_MAX_WORDS)
+
+struct TreeMaskParams {
+    const int *q_start, *kv_lens, *parents;
+    int num_tokens, prefix_len;
+    uint32_t *mask;
+    int64_t mask_stride;
+    int mask_words;
+    int *positions;
+    uint32_t *err;
+};
+
+__global__ void __launch_bounds__(kTreeThreads) tree_mask_kernel(const TreeMaskParams p)
+{
+    __shared__ int16_t up[kTreeMaxNodes];
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const int s = blockIdx.x;
+    const int raw0 = __ldg(p.q_start + s), raw1 = __ldg(p.q_start + s + 1), raw_kv = __ldg(p.kv_lens + s);
+    const int q0 = min(max(raw0, 0), p.num_tokens), n = min(max(raw1, q0), p.num_tokens) - q0, kv = max(raw_kv, 0);
+    const int nodes = min(n, 32 * p.mask_words);
+    bool bad = q0 != raw0 || q0 + n != raw1 || kv != raw_kv || n > kv || nodes < n || kv > INT32_MAX - 1024 - p.prefix_len;
+    for (int i = threadIdx.x; i < nodes; i += kTreeThreads) {
+        const int parent = __ldg(p.parents + q0 + i);
+        bad = bad || parent < -1 || parent >= i;
+        up[i] = static_cast<int16_t>(parent < -1 || parent >= i ? -1 : parent);
+    }
+    if (bad)
+        report_index(p.err);
+    __syncthreads();
+    const int base = static_cast<int>(min(static_cast<int64_t>(p.prefix_len) + max(kv - n, 0), static_cast<int64_t>(INT32_MAX - 2048)));
+    for (int i = threadIdx.x; i < n; i += kTreeThreads) {
+        uint32_t *row = p.mask + (q0 + i) * p.mask_stride;
+        int at = i < nodes ? i : -1, above = -1;
+        for (int w = p.mask_words - 1; w >= 0; --w) {
+            uint32_t bits = 0;
+            for (; at >= 32 * w && at >= 0; at = up[at]) {
+                bits |= 1u << (at & 31);
+                ++above;
+            }
+            row[w] = bits;
+        }
+        if (p.positions)
+            p.positions[q0 + i] = base + max(above, 0);
+    }
+}
+
+// ---- attention weight per key ------------------------------------------------------------------
+//
+//     w[j] = decay w[j] + sum over rows r (tokens of the window x heads of the group) of 2^(s_rj - lse_r)
+//
+// Keys are the rows of 16 x 8 x 16 products, 32 to a warp, loaded once straight into registers; the
+// queries are the columns, brought to shared memory 64 rows at a time in the order the products
+// take them. Each key's sum stays in one warp (no atomics: the same bits each time). Blocks of 256
+// keys of all sequences and heads are dealt to the CTAs in turn. For a decoding token the time is the
+// reading of K.
+constexpr int kWeighThreads = 256, kWeighKeys = 256, kWeighRows = 64;
+
+struct WeighParams {
+    BatchView batch;
+    const void *q, *k;
+    int64_t q_token, q_head, page_stride, head_stride, row_stride;
+    const float *lse;
+    int64_t lse_token;
+    float *w;
+    int64_t w_page, w_head;
+    int kv_heads, group, window;
+    float scale_log2, decay;
+    uint32_t *err;
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kWeighThreads, 2) kv_weigh_kernel(const __grid_constant__ WeighParams p)
+{
+    constexpr int C = D / 32;   // 16-byte pieces of a key row per lane
+    __shared__ uint4 queries[kWeighRows * D / 8];   // [tile of 8 rows][piece][lane]
+    __shared__ float minus_lse[kWeighRows];         // in base 2
+    __shared__ int last_key[kWeighRows];            // that the row sees; -1: the row gives nothing
+    __shared__ int64_t ahead[kWeighThreads];        // blocks up to and with each sequence of the chunk
+    __shared__ int64_t warp_sum[kWeighThreads / 32];
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    int64_t before = 0;   // blocks of the chunks before
+    for (int s0 = 0; s0 < p.batch.num_seqs; s0 += kWeighThreads) {
+        // the blocks of this chunk's sequences
+        int64_t blocks = 0;
+        if (s0 + static_cast<int>(threadIdx.x) < p.batch.num_seqs) {
+            const SeqView v = load_seq(p.batch, s0 + threadIdx.x);
+            if (v.bad)
+                report_index(p.err);
+            if (v.n > 0 || p.decay != 1.0f)
+                blocks = static_cast<int64_t>((v.kv + kWeighKeys - 1) / kWeighKeys) * p.kv_heads;
+        }
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+            const int64_t x = __shfl_up_sync(0xffffffffu, blocks, o);
+            blocks += lane >= o ? x : 0;
+        }
+        if (lane == 31)
+            warp_sum[warp] = blocks;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w)
+            blocks += warp_sum[w];
+        ahead[threadIdx.x] = blocks;
+        __syncthreads();
+        const int64_t total = ahead[kWeighThreads - 1];
+        // this CTA's: block b of all with b mod CTAs = its number
+        int64_t b = static_cast<int64_t>(blockIdx.x) - before % gridDim.x;
+        b += b < 0 ? gridDim.x : 0;
+        for (; b < total; b += gridDim.x) {
+            int lo = 0;   // the first sequence with ahead > b
+            for (int step = kWeighThreads / 2; step > 0; step /= 2)
+                lo += ahead[lo + step - 1] <= b ? step : 0;
+            const SeqView v = load_seq(p.batch, s0 + lo);
+            const int64_t at = b - (lo > 0 ? ahead[lo - 1] : 0);
+            const int per_head = (v.kv + kWeighKeys - 1) / kWeighKeys;
+            const int head = static_cast<int>(at / per_head), key0 = static_cast<int>(at % per_head) * kWeighKeys + 32 * warp;
+            // ---- the warp's keys
+            uint4 k[2][2][C];   // [tile of 16 keys][row g, g + 8][piece]
+            int64_t page_of[2];   // -1: none
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                const int key = key0 + 16 * m;
+                page_of[m] = -1;
+                if (key < v.kv) {
+                    const int id = __ldg(p.batch.table + (s0 + lo) * p.batch.table_stride + (key >> p.batch.page_shift));
+                    if (id >= 0 && id < p.batch.num_pages)
+                        page_of[m] = id;
+                    else
+                        report_index(p.err);
+                }
+                const int row = key & ((1 << p.batch.page_shift) - 1);
+                const T *src = static_cast<const T *>(p.k) + page_of[m] * p.page_stride + head * p.head_stride + (row + g) * p.row_stride + 8 * t;
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+#pragma unroll
+                    for (int c = 0; c < C; ++c)
+                        k[m][half][c] = page_of[m] >= 0
+                                            ? __ldg(reinterpret_cast<const uint4 *>(src + half * 8 * p.row_stride + 32 * c))
+                                            : make_uint4(0, 0, 0, 0);
+            }
+            // ---- rows of queries, 64 at a time
+            const int tokens = p.window > 0 ? min(p.window, v.n) : v.n;
+            const int rows = tokens * p.group;   // (fits: the host sees to it)
+            float sum[2][2] = {};
+            for (int r0 = 0; r0 < rows; r0 += kWeighRows) {
+                const int tiles = (min(rows - r0, kWeighRows) + 7) / 8;
+                __syncthreads();   // the rows before are done with
+                for (int i = threadIdx.x; i < tiles * 8 * (D / 8); i += kWeighThreads) {
+                    const int r = i / (D / 8), piece = i % (D / 8), row = r0 + r;
+                    uint4 x = make_uint4(0, 0, 0, 0);
+                    if (row < rows) {
+                        const int64_t token = v.q0 + v.n - tokens + row / p.group;
+                        x = __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(p.q) + token * p.q_token +
+                                                                  (head * p.group + row % p.group) * p.q_head + 8 * piece));
+                    }
+                    queries[((r / 8) * C + piece / 4) * 32 + (r % 8) * 4 + piece % 4] = x;
+                }
+                if (threadIdx.x < static_cast<unsigned>(tiles * 8)) {
+                    const int row = r0 + threadIdx.x;
+                    float off = 0.0f;
+                    int last = -1;
+                    if (row < rows) {
+                        const int i = v.n - tokens + row / p.group;   // of the sequence's new tokens
+                        const float l = __ldg(p.lse + (v.q0 + i) * p.lse_token + head * p.group + row % p.group);
+                        off = -l * 1.4426950408889634f;
+                        last = l == -INFINITY ? -1 : v.kv - v.n + i;
+                    }
+                    minus_lse[threadIdx.x] = off;
+                    last_key[threadIdx.x] = last;
+                }
+                __syncthreads();
+                if (key0 >= v.kv)
+                    continue;
+                for (int i = 0; i < tiles; ++i) {
+                    float s[2][4] = {};
+#pragma unroll
+                    for (int c = 0; c < C; ++c) {
+                        const uint4 q = queries[(i * C + c) * 32 + lane];
+#pragma unroll
+                        for (int m = 0; m < 2; ++m) {
+                            mma_16x8x16<T>(s[m], k[m][0][c].x, k[m][1][c].x, k[m][0][c].y, k[m][1][c].y, q.x, q.y);
+                            mma_16x8x16<T>(s[m], k[m][0][c].z, k[m][1][c].z, k[m][0][c].w, k[m][1][c].w, q.z, q.w);
+                        }
+                    }
+                    const float2 off = *reinterpret_cast<const float2 *>(minus_lse + 8 * i + 2 * t);
+                    const int2 last = *reinterpret_cast<const int2 *>(last_key + 8 * i + 2 * t);
+#pragma unroll
+                    for (int m = 0; m < 2; ++m)
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            const int key = key0 + 16 * m + 8 * half + g;
+                            const float a = ex2_approx(fmaf(s[m][2 * half], p.scale_log2, off.x));
+                            const float c = ex2_approx(fmaf(s[m][2 * half + 1], p.scale_log2, off.y));
+                            sum[m][half] += (key <= last.x ? a : 0.0f) + (key <= last.y ? c : 0.0f);
+                        }
+                }
+            }
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    float x = sum[m][half];
+                    x += __shfl_xor_sync(0xffffffffu, x, 1);
+                    x += __shfl_xor_sync(0xffffffffu, x, 2);
+                    const int key = key0 + 16 * m + 8 * half + g;
+                    if (t == 0 && key < v.kv && page_of[m] >= 0) {
+                        float *dst = p.w + page_of[m] * p.w_page + head * p.w_head + (key & ((1 << p.batch.page_shift) - 1));
+                        *dst = p.decay != 0.0f && key < v.kv - v.n ? fmaf(p.decay, *dst, x) : x;
+                    }
+                }
+        }
+        before += total;
+        __syncthreads();   // ahead may be written again
+    }
+}
+
+// ---- choosing what to keep ---------------------------------------------------------------------
+//
+// The m heaviest of the keys between the first and the recent ones, exactly: the weight at the border
+// is found digit by digit (11, 11 and 10 bits of an order-preserving integer), each from a histogram
+// of the keys that agree with the digits before; then one pass over the keys in order writes those above the
+// border and the first of those on it. A cluster of CTAs per sequence and key head, each with a
+// slice of the keys, which it holds in shared memory; the histograms are summed over distributed
+// shared memory. Reads each weight once.
+constexpr int kSelectThreads = 512, kSelectBins = 2048;
+
+struct SelectParams {
+    const int *kv_lens, *table;
+    int64_t table_stride;
+    int table_width, num_pages, page_shift, kv_heads;
+    const float *w;
+    int64_t w_page, w_head;
+    int keep, first, recent;
+    int *index;
+    int64_t seq_stride, head_stride;
+    int *counts;
+    int held;   // keys of a slice that are held in shared memory
+    uint32_t *err;
+};
+
+__global__ void __launch_bounds__(kSelectThreads) kv_select_kernel(const __grid_constant__ SelectParams p)
+{
+    extern __shared__ uint32_t held[];
+    __shared__ uint4 bins[kSelectThreads];   // the highest digit's first, four to a thread
+    __shared__ uint32_t warp_sum[2][kSelectThreads / 32];
+    __shared__ uint32_t digit, above;
+    __shared__ uint2 mine;   // keys above the border, on it
+    uint32_t *const hist = reinterpret_cast<uint32_t *>(bins);
+    static_assert(kSelectBins == 4 * kSelectThreads, "four bins to a thread");
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int ctas = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_ctarank());
+    const int item = static_cast<int>(blockIdx.x) / ctas, s = item / p.kv_heads, head = item % p.kv_heads;
+    const int raw = __ldg(p.kv_lens + s), kv = min(max(raw, 0), p.table_width << p.page_shift);
+    if (raw != kv && threadIdx.x == 0)
+        report_index(p.err);
+    int *index = p.index + s * p.seq_stride + head * p.head_stride;
+    const int count = min(kv, p.keep);
+    if (head == 0 && rank == 0 && threadIdx.x == 0)
+        p.counts[s] = count;
+    for (int64_t i = count + rank * kSelectThreads + static_cast<int>(threadIdx.x); i < p.keep; i += ctas * kSelectThreads)
+        index[i] = -1;
+    if (kv <= p.keep) {   // (the same for all CTAs of the cluster)
+        for (int64_t i = rank * kSelectThreads + static_cast<int>(threadIdx.x); i < kv; i += ctas * kSelectThreads)
+            index[i] = static_cast<int>(i);
+        return;
+    }
+    // candidates [lo, hi), of which m are kept; this CTA's keys [a, b)
+    const int lo = p.first, hi = kv - p.recent, m = p.keep - p.first - p.recent;
+    const int slice = static_cast<int>(((static_cast<int64_t>(kv) + ctas - 1) / ctas + 15) / 16 * 16);
+    const int a = static_cast<int>(min(static_cast<int64_t>(rank) * slice, static_cast<int64_t>(kv)));
+    const int b = static_cast<int>(min(static_cast<int64_t>(a) + slice, static_cast<int64_t>(kv)));
+    auto fetch = [&](int i) -> uint32_t {
+        const int id = __ldg(p.table + s * p.table_stride + (i >> p.page_shift));
+        float x = 0.0f;
+        if (id >= 0 && id < p.num_pages)
+            x = __ldg(p.w + id * p.w_page + head * p.w_head + (i & ((1 << p.page_shift) - 1))) + 0.0f;   // (-0 becomes 0)
+        else
+            report_index(p.err);
+        const uint32_t u = __float_as_uint(x);
+        return x != x ? 0u : u ^ (u >> 31 ? 0xffffffffu : 0x80000000u);
+    };
+    auto key_of = [&](int i) -> uint32_t { return i - a < p.held ? held[i - a] : fetch(i); };
+    if (m > 0)
+        for (int i = a + static_cast<int>(threadIdx.x); i < min(b, a + p.held); i += kSelectThreads)
+            held[i - a] = fetch(i);
+    // ---- the border
+    uint32_t border = 0xffffffffu, left = 0;   // all above it (nothing is) and the first `left` on it
+    if (m > 0) {
+        border = 0;
+        left = static_cast<uint32_t>(m);
+        for (int pass = 0; pass < 3; ++pass) {
+            const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
+            bins[threadIdx.x] = make_uint4(0, 0, 0, 0);
+            __syncthreads();
+            for (int i = max(a, lo) + static_cast<int>(threadIdx.x); i < min(b, hi); i += kSelectThreads) {
+                const uint32_t key = key_of(i);
+                if (pass == 0 || (key ^ border) >> (shift + bits) == 0)
+                    atomicAdd(&hist[(~key >> shift) & ((1u << bits) - 1u)], 1u);
+            }
+            __syncthreads();
+            if (ctas > 1)
+                cluster_sync();
+            // digits from the highest down: complement 4 t + e of the low bits
+            uint4 n = bins[threadIdx.x];
+            for (int r = 0; r < ctas; ++r) {
+                if (r == rank)
+                    continue;
+                const uint4 x = ld_shared_cluster_u4(mapa_shared(smem_u32(bins + threadIdx.x), static_cast<uint32_t>(r)));
+                n = make_uint4(n.x + x.x, n.y + x.y, n.z + x.z, n.w + x.w);
+            }
+            const uint32_t sum = n.x + n.y + n.z + n.w;
+            uint32_t scan = sum;
+#pragma unroll
+            for (int o = 1; o < 32; o *= 2) {
+                const uint32_t x = __shfl_up_sync(0xffffffffu, scan, o);
+                scan += lane >= o ? x : 0;
+            }
+            if (lane == 31)
+                warp_sum[0][warp] = scan;
+            __syncthreads();
+            scan -= sum;
+            for (int w = 0; w < warp; ++w)
+                scan += warp_sum[0][w];
+            const uint32_t each[4] = {n.x, n.y, n.z, n.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (scan < left && left <= scan + each[e]) {   // one thread, one digit
+                    digit = ~(4 * threadIdx.x + e) & ((1u << bits) - 1u);
+                    above = scan;
+                }
+                scan += each[e];
+            }
+            __syncthreads();
+            if (ctas > 1)
+                cluster_sync();   // the other CTAs have read this one's histogram
+            border |= digit << shift;
+            left -= above;
+        }
+    }
+    // ---- how many of each kind the slices before this one have
+    auto above_it = [&](int i, uint32_t key) { return i < lo || i >= hi || key > border; };
+    uint32_t gt = 0, eq = 0;
+    for (int i = a + static_cast<int>(threadIdx.x); i < b; i += kSelectThreads) {
+        const uint32_t key = m > 0 ? key_of(i) : 0u;
+        const bool up = above_it(i, key);
+        gt += up;
+        eq += !up && key == border;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) {
+        gt += __shfl_xor_sync(0xffffffffu, gt, o);
+        eq += __shfl_xor_sync(0xffffffffu, eq, o);
+    }
+    if (threadIdx.x == 0)
+        mine = make_uint2(0, 0);
+    __syncthreads();
+    if (lane == 0) {
+        atomicAdd(&mine.x, gt);
+        atomicAdd(&mine.y, eq);
+    }
+    __syncthreads();
+    if (ctas > 1)
+        cluster_sync();
+    gt = eq = 0;
+    for (int r = 0; r < rank; ++r) {
+        const uint2 x = ld_shared_cluster_u2(mapa_shared(smem_u32(&mine), static_cast<uint32_t>(r)));
+        gt += x.x;
+        eq += x.y;
+    }
+    // ---- the kept keys in order
+    for (int i0 = a, buf = 0; i0 < b; i0 += kSelectThreads, buf ^= 1) {
+        const int i = i0 + static_cast<int>(threadIdx.x);
+        const uint32_t key = i < b && m > 0 ? key_of(i) : 0u;
+        const bool up = i < b && above_it(i, key), on = i < b && !up && key == border;
+        const uint32_t ups = __ballot_sync(0xffffffffu, up), ons = __ballot_sync(0xffffffffu, on);
+        if (lane == 0)
+            warp_sum[buf][warp] = static_cast<uint32_t>(__popc(ups)) | static_cast<uint32_t>(__popc(ons)) << 16;
+        __syncthreads();
+        uint32_t before = 0, all = 0;
+#pragma unroll
+        for (int w = 0; w < kSelectThreads / 32; ++w) {
+            const uint32_t x = warp_sum[buf][w];
+            before += w < warp ? x : 0u;
+            all += x;
+        }
+        const uint32_t lower = (1u << lane) - 1u;
+        const uint32_t g = gt + (before & 0xffffu) + __popc(ups & lower), e = eq + (before >> 16) + __popc(ons & lower);
+        const uint32_t to = g + min(e, left);
+        if ((up || (on && e < left)) && to < static_cast<uint32_t>(p.keep))   // (always, unless weights change meanwhile)
+            index[to] = i;
+        gt += all & 0xffffu;
+        eq += all >> 16;
+    }
+    __syncthreads();
+    if (ctas > 1)
+        cluster_sync();   // the other CTAs have read this one's counts
+}
+
+// ---- moving rows up ------------------------------------------------------------------------------
+//
+// Row j <- row index[j] >= j, in order, so a round of consecutive rows j is safe once all of its own
+// sources are read: sources of later rounds lie behind the rows that it writes, and those of
+// earlier ones are read already. A cluster of CTAs takes a round together (loads into registers, a
+// cluster barrier, stores); each CTA moves keys and values of a few heads. Bound by HBM for long lists,
+// by the chain of lookups for a few accepted drafts.
+constexpr int kCompactThreads = 256, kCompactVecs = 8;   // 16-byte pieces a thread holds
+
+struct CompactParams {
+    void *k, *v;
+    int64_t page_stride, head_stride, row_stride;   // elements of 2 bytes
+    const int *kv_lens, *table;
+    int64_t table_stride;
+    int table_width, num_pages, page_shift, kv_heads;
+    float *w;   // or nullptr
+    int64_t w_page, w_head;
+    const int *index;
+    int64_t seq_index, head_index;
+    int most;
+    const int *start, *counts;
+    int *new_lens;
+    int heads, groups;   // heads of a CTA (a power of two), groups of such heads
+    uint32_t *err;
+};
+
+template <int D>
+struct CompactShape {
+    static constexpr int PIECES = D / 8;                                          // of a row
+    static constexpr int PAIRS = kCompactThreads * kCompactVecs / (2 * PIECES);   // (head, row) of a CTA's round, key and value each
+};
+
+template <int D>
+__global__ void __launch_bounds__(kCompactThreads) kv_compact_kernel(const __grid_constant__ CompactParams p)
+{
+    using Shape = CompactShape<D>;
+    constexpr int PIECES = Shape::PIECES, PAIRS = Shape::PAIRS;
+    __shared__ int64_t from[2][PAIRS], to[2][PAIRS];   // elements of the cache; from < 0: not moved
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const int ctas = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_ctarank());
+    const int item = static_cast<int>(blockIdx.x) / ctas, s = item / p.groups, head0 = item % p.groups * p.heads;
+    const int rows = PAIRS / p.heads;   // of each head in a CTA's round
+    const int raw_kv = __ldg(p.kv_lens + s), kv = min(max(raw_kv, 0), p.table_width << p.page_shift);
+    const int raw_start = p.start ? __ldg(p.start + s) : 0, start = min(max(raw_start, 0), kv);
+    const int raw_count = __ldg(p.counts + s), count = raw_start == start ? min(max(raw_count, 0), p.most) : 0;
+    if (threadIdx.x == 0 && rank == 0 && head0 == 0) {
+        if (raw_kv != kv || raw_start != start || raw_count < 0 || raw_count > p.most)
+            report_index(p.err);
+        if (p.new_lens)
+            p.new_lens[s] = static_cast<int>(min(static_cast<int64_t>(start) + count, static_cast<int64_t>(INT32_MAX)));
+    }
+    const int mask = (1 << p.page_shift) - 1;
+    int buf = 0;
+    for (int64_t round = 0; round < count; round += static_cast<int64_t>(ctas) * rows, buf ^= 1) {
+        const int64_t j0 = round + static_cast<int64_t>(rank) * rows;
+        // ---- where the round's rows are and go to
+        float weight = 0.0f;
+        float *weight_to = nullptr;
+        if (threadIdx.x < PAIRS) {
+            const int head = head0 + static_cast<int>(threadIdx.x) / rows;
+            const int64_t j = j0 + static_cast<int>(threadIdx.x) % rows;
+            int64_t src = -1, dst = 0;
+            if (head < p.kv_heads && j < count) {
+                const int i = __ldg(p.index + s * p.seq_index + head * p.head_index + j);
+                const int64_t row = static_cast<int64_t>(start) + i;
+                if (i < j || row >= kv) {
+                    report_index(p.err);
+                } else if (i > j) {
+                    const int to_row = start + static_cast<int>(j), from_row = static_cast<int>(row);
+                    const int *table = p.table + s * p.table_stride;
+                    const int a = __ldg(table + (from_row >> p.page_shift)), b = __ldg(table + (to_row >> p.page_shift));
+                    if (a < 0 || a >= p.num_pages || b < 0 || b >= p.num_pages) {
+                        report_index(p.err);
+                    } else {
+                        src = a * p.page_stride + head * p.head_stride + (from_row & mask) * p.row_stride;
+                        dst = b * p.page_stride + head * p.head_stride + (to_row & mask) * p.row_stride;
+                        if (p.w) {
+                            weight = p.w[a * p.w_page + head * p.w_head + (from_row & mask)];
+                            weight_to = p.w + b * p.w_page + head * p.w_head + (to_row & mask);
+                        }
+                    }
+                }
+            }
+            from[buf][threadIdx.x] = src;
+            to[buf][threadIdx.x] = dst;
+        }
+        __syncthreads();
+        // ---- read, wait for the others, write
+        uint4 x[kCompactVecs];
+#pragma unroll
+        for (int e = 0; e < kCompactVecs; ++e) {
+            const int at = e * kCompactThreads + static_cast<int>(threadIdx.x), row = at / PIECES, piece = at % PIECES;
+            const int64_t src = from[buf][row / 2];
+            const uint16_t *base = static_cast<const uint16_t *>(row % 2 ? p.v : p.k);
+            if (src >= 0)
+                x[e] = *reinterpret_cast<const uint4 *>(base + src + 8 * piece);
+        }
+        __syncthreads();
+        if (ctas > 1)
+            cluster_sync();
+#pragma unroll
+        for (int e = 0; e < kCompactVecs; ++e) {
+            const int at = e * kCompactThreads + static_cast<int>(threadIdx.x), row = at / PIECES, piece = at % PIECES;
+            uint16_t *base = static_cast<uint16_t *>(row % 2 ? p.v : p.k);
+            if (from[buf][row / 2] >= 0)
+                *reinterpret_cast<uint4 *>(base + to[buf][row / 2] + 8 * piece) = x[e];
+        }
+        if (weight_to)
+            *weight_to = weight;
+    }
+}
+
+}  // namespace gb300

@@ -26,6 +26,9 @@
 //    few rows: bound by HBM; one CTA's latencies overlap the other's). NT = 2: two tiles share
 //    each block of 128 keys, one CTA per SM (for many rows: bound by the tensor cores; one
 //    tile's softmax runs during the other's products).
+//  * Trees (PagedConfig's TREE, gemm_decode.h): a token sees every key before its sequence's new ones and, of
+//    those, the ones that its row of a bit mask names. Every tile then covers all of its sequence's keys, and the
+//    bits decide where the position does otherwise.
 //  * Warps: four softmax warps per tile, a row per thread, an MMA issuer and a producer (TMA), as
 //    in attention_fwd_kernel. Every wait is bounded.
 #pragma once
@@ -85,14 +88,19 @@ struct PagedParams {
     // what repair_stretches reads: the operands as the tensor maps have them, strides in elements
     const void *q, *k, *v;
     int64_t q_token, q_head, page_stride, head_stride, row_stride;
+    // TREE: bit j of token t's mask_words words at mask + t * mask_stride: t sees its sequence's new token j
+    const uint32_t *mask;
+    int64_t mask_stride;
+    int mask_words;
     uint32_t *err;
     uint64_t timeout_ns;
     int debug;                          // DEBUG_WITHHOLD_FIRST_LOAD
 };
 
-template <typename T, int D_, int NT_>
+template <typename T, int D_, int NT_, bool TREE_ = false>
 struct PagedConfig {
     using Type = T;
+    static constexpr bool TREE = TREE_;
     static constexpr int D = D_;
     static constexpr int NT = NT_;                  // query tiles per item
     static constexpr int BQ = 128;                  // rows per tile (= TMEM lanes)
@@ -176,8 +184,8 @@ __host__ __device__ __noinline__ int64_t sum_of_shares(int64_t n, int k, int a, 
 
 // The items of one sequence (or the prefix items, of all tokens together): tiles of `step` tokens
 // for each key head. `edge`: keys that the token before the first would see, counted from the
-// items' first key (token i sees the edge + i + 1 first of them); fixed >= 0: every tile has
-// `fixed` blocks instead.
+// items' first key (token i sees the edge + i + 1 first of them; TREE: every token sees the edge first of
+// them and some of the keys of the new tokens, which follow); fixed >= 0: every tile has `fixed` blocks instead.
 struct SeqItems {
     int q0, n, kv, tiles, fixed;
     int edge, step;
@@ -213,9 +221,9 @@ __host__ __device__ __noinline__ SeqItems seq_items(const PagedParams &p, int s)
     q.n = v.n;
     q.kv = v.kv;
     q.fixed = -1;
-    q.edge = (p.keys == KEYS_ALL ? p.batch.prefix_len : 0) + v.kv - v.n;
+    q.edge = (p.keys == KEYS_ALL ? p.batch.prefix_len : 0) + v.kv - (Cfg::TREE ? min(v.n, v.kv) : v.n);
     q.step = Cfg::NT * p.tile_tokens;
-    q.bad = v.bad;
+    q.bad = v.bad || (Cfg::TREE && (v.n > v.kv || (v.n + 31) / 32 > p.mask_words));
     const bool mine = p.seqs == SEQS_ALL || (v.n > p.long_tokens) == (p.seqs == SEQS_LONG);
     q.tiles = mine ? (v.n + q.step - 1) / q.step : 0;
     return q;
@@ -227,6 +235,8 @@ __host__ __device__ __forceinline__ int blocks_upto(const SeqItems &q, int last)
 {
     if (q.fixed >= 0)
         return q.fixed;
+    if (Cfg::TREE)
+        last = min(q.n, q.kv) - 1;
     return max(1, (q.edge + last + Cfg::BKV) / Cfg::BKV);
 }
 
@@ -254,7 +264,7 @@ __host__ __device__ inline int64_t units_of_head(const SeqItems &q, int quantum)
     if (q.tiles == 0)
         return 0;
     const int last = units_upto<Cfg>(q, quantum, q.n - 1);
-    if (q.fixed >= 0 || q.tiles == 1)
+    if (q.fixed >= 0 || q.tiles == 1 || Cfg::TREE)
         return static_cast<int64_t>(q.tiles) * last;
     // the tiles before the last: tile t sees the edge + (t + 1) step first keys, at least one block's
     const int whole = q.tiles - 1, keys = Cfg::BKV * quantum;
@@ -295,14 +305,14 @@ struct Segment {
         return NT == 2 && tile == 0 && toks <= tile_tokens ? 0 : min(tile_tokens, toks - tile_first<NT>(tile));
     }
     // Its blocks: the first tile of two may see fewer keys than the second.
-    template <int NT, int BKV>
+    template <int NT, int BKV, bool TREE = false>
     __host__ __device__ int tile_blocks(int tile) const
     {
         if (NT == 1 || tile == 1)
             return blocks;
         if (toks <= tile_tokens)
             return 0;
-        return prefix ? blocks : max(1, (edge + (tok0 + tile_tokens - 1 - q0) + BKV) / BKV);
+        return prefix || TREE ? blocks : max(1, (edge + (tok0 + tile_tokens - 1 - q0) + BKV) / BKV);
     }
 };
 
@@ -462,6 +472,22 @@ __device__ __forceinline__ void store_rows(uint32_t stage, int lane, const uint4
     __syncwarp();
 }
 
+// Bit e: whether a row that sees the new tokens which the `words` words at `row` name (of n there are keys
+// of) sees the key `at` + e, counted from the first new token's; all keys before that one are seen.
+__device__ __forceinline__ uint32_t tree_bits(const uint32_t *row, int words, int n, int at)
+{
+    if (at <= -32)
+        return 0xffffffffu;
+    auto word = [&](int i) -> uint32_t {
+        const int left = n - 32 * i;
+        const uint32_t w = i < words && left > 0 ? __ldg(row + i) : 0u;
+        return left < 32 && left > 0 ? w & ((1u << left) - 1u) : w;
+    };
+    if (at < 0)
+        return ((1u << -at) - 1u) | (word(0) << -at);
+    return __funnelshift_r(word(at >> 5), (at & 31) ? word((at >> 5) + 1) : 0u, static_cast<uint32_t>(at & 31));
+}
+
 struct PagedBars {
     uint32_t q_full0, q_empty0, drain, full0, empty0, s_full, pv_done, p_half0, p_full0;
 };
@@ -519,6 +545,17 @@ __device__ __forceinline__ float sum_rows(float (&x)[8], int lane)
     return x[0] + __shfl_xor_sync(0xffffffffu, x[0], 1);
 }
 
+// Keys of an item, counted from its first, that any of its rows sees.
+template <class Cfg>
+__device__ __forceinline__ int keys_alive(const PagedParams &p, const Segment &g)
+{
+    if (g.prefix)
+        return p.batch.prefix_len;
+    if (Cfg::TREE)
+        return (p.keys == KEYS_ALL ? p.batch.prefix_len : 0) + g.kv;
+    return max(0, g.edge + (g.tok0 + g.toks - g.q0));
+}
+
 template <class Cfg>
 __device__ __noinline__ void repair_stretches(const PagedParams &p, const Walk &start, int tile, int quarter, int lane)
 {
@@ -551,8 +588,8 @@ __device__ __noinline__ void repair_stretches(const PagedParams &p, const Walk &
     Segment g;
     while (next_segment<Cfg>(p, walk, g)) {
         const int first = g.tile_first<Cfg::NT>(tile), toks = g.tile_toks<Cfg::NT>(tile);
-        const int alive = g.prefix ? p.batch.prefix_len : max(0, g.edge + (g.tok0 + g.toks - g.q0));
-        const int begin = g.b0 * BKV, end = min(min(g.b1, g.tile_blocks<Cfg::NT, BKV>(tile)) * BKV, alive);
+        const int alive = keys_alive<Cfg>(p, g);
+        const int begin = g.b0 * BKV, end = min(min(g.b1, g.tile_blocks<Cfg::NT, BKV, Cfg::TREE>(tile)) * BKV, alive);
         const int key_base = g.prefix || p.keys == KEYS_ALL ? 0 : p.batch.prefix_len;
         const bool starts = g.b0 == 0, whole = starts && g.b1 == g.blocks;
         const bool final_row = whole && p.keys == KEYS_ALL;
@@ -571,11 +608,20 @@ __device__ __noinline__ void repair_stretches(const PagedParams &p, const Walk &
         const int r = quarter * 32 + lane, token = g.tok0 + first + r / p.group, head = g.head * p.group + r % p.group;
         const bool on = r / p.group < toks;
         int seen;
-        if (g.prefix)
-            seen = prefix_seen(p.batch, token, on);
-        else
-            seen = on ? max(0, g.edge + (token - g.q0) + 1) : 0;
-        const uint32_t some = __ballot_sync(ALL, on && seen > begin && seen < end);   // not all of the stretch, and not none
+        bool part_of_it;   // the row sees not all of the stretch, and not none (TREE: maybe all)
+        if constexpr (Cfg::TREE) {
+            seen = g.prefix ? p.batch.prefix_len : g.edge;
+            part_of_it = on && seen < end && seen > begin;
+            for (int j = begin; on && seen <= begin && j < end && !part_of_it; j += 32)
+                part_of_it = tree_bits(p.mask + token * p.mask_stride, p.mask_words, alive - g.edge, j - g.edge) != 0;
+        } else {
+            if (g.prefix)
+                seen = prefix_seen(p.batch, token, on);
+            else
+                seen = on ? max(0, g.edge + (token - g.q0) + 1) : 0;
+            part_of_it = on && seen > begin && seen < end;
+        }
+        const uint32_t some = __ballot_sync(ALL, part_of_it);
         if (some == 0)
             continue;
         const int64_t row =
@@ -590,7 +636,7 @@ __device__ __noinline__ void repair_stretches(const PagedParams &p, const Walk &
         for (int e = 0; e < V; ++e)
             bad[e] = -1;
         const int hidden = __reduce_min_sync(ALL, some >> lane & 1u ? seen : INT32_MAX);
-        for (int j0 = hidden; j0 < end; j0 += 32) {
+        for (int j0 = hidden; !Cfg::TREE && j0 < end; j0 += 32) {   // (TREE: a row may see some and not others)
             const int64_t mine = place(j0 + lane, end);
 #pragma unroll 4
             for (int i = 0; i < 32; ++i) {
@@ -619,7 +665,7 @@ __device__ __noinline__ void repair_stretches(const PagedParams &p, const Walk &
             bool spoilt = false;
 #pragma unroll
             for (int e = 0; e < V; ++e)
-                spoilt = spoilt || (bad[e] >= n && !(fabsf(x[e]) < INFINITY));
+                spoilt = spoilt || ((Cfg::TREE || bad[e] >= n) && !(fabsf(x[e]) < INFINITY));
             rows |= __any_sync(ALL, spoilt) && (some >> i & 1u) ? 1u << i : 0u;
         }
         while (rows) {
@@ -643,10 +689,16 @@ __device__ __noinline__ void repair_stretches(const PagedParams &p, const Walk &
                     acc[i][e] = 0.0f;
             }
             // of row lane / 4: keys it sees, running maximum (raised beyond 2^8, as in the softmax) and sum
-            const int sees = __shfl_sync(ALL, seen, mine), last = __reduce_max_sync(ALL, sees);
+            const int sees = __shfl_sync(ALL, seen, mine), last = Cfg::TREE ? end : __reduce_max_sync(ALL, sees);
+            const int sees_token = __shfl_sync(ALL, token, mine);
             float m = -INFINITY, l = 0.0f;
             for (int j0 = begin; j0 < last; j0 += 32) {
                 const int64_t at = place(j0 + lane, last);
+                uint32_t bits = 0;   // TREE: of these 32 keys, those that row lane / 4 sees
+                if constexpr (Cfg::TREE)
+                    bits = tree_bits(p.mask + sees_token * p.mask_stride, p.mask_words, alive - g.edge, j0 - g.edge) &
+                           (last - j0 >= 32 ? ALL : (1u << (last - j0)) - 1u);
+                auto visible = [&](int i) { return Cfg::TREE ? (bits >> i & 1u) != 0 : j0 + i < sees; };
                 Vec k[KEYS], v[KEYS];
 #pragma unroll
                 for (int u = 0; u < KEYS; ++u) {
@@ -670,7 +722,7 @@ __device__ __noinline__ void repair_stretches(const PagedParams &p, const Walk &
                                 x[i] = fmaf(q[i][e], kf[e], x[i]);
                         }
                         score[u] = sum_rows(x, lane) * p.scale_log2;
-                        top = j0 + i0 + u < sees ? fmaxf(top, score[u]) : top;   // (a NaN score leaves it alone)
+                        top = visible(i0 + u) ? fmaxf(top, score[u]) : top;   // (a NaN score leaves it alone)
                         // the same of the next KEYS keys (past this step's 32: fetched above, when it comes)
                         const int64_t next = __shfl_sync(ALL, at, (i0 + KEYS + u) & 31);
                         if (i0 + KEYS < 32) {
@@ -694,7 +746,7 @@ __device__ __noinline__ void repair_stretches(const PagedParams &p, const Walk &
                     const float from = m == -INFINITY ? 0.0f : m;
 #pragma unroll
                     for (int u = 0; u < KEYS; ++u) {
-                        const bool on_key = j0 + i0 + u < sees;
+                        const bool on_key = visible(i0 + u);
                         const float w = on_key ? exp2f(score[u] - from) : -1.0f;   // -1: not seen
                         l += on_key ? w : 0.0f;
                         float vf[V];
@@ -765,7 +817,10 @@ __device__ __forceinline__ void paged_softmax_warp(const PagedParams &p, const P
         const bool row_ok = row_tok < toks;
         const int token = g.tok0 + first + row_tok;
         int seen = INT32_MAX;   // keys, from the item's first, that the row sees (idle rows: as if all)
-        if (g.prefix) {
+        if constexpr (Cfg::TREE) {   // (of the new tokens' keys, which follow, the mask's)
+            if (row_ok)
+                seen = g.prefix ? p.batch.prefix_len : g.edge;
+        } else if (g.prefix) {
             const int n = prefix_seen(p.batch, token, row_ok);
             seen = row_ok ? n : seen;
         } else if (row_ok) {
@@ -773,8 +828,9 @@ __device__ __forceinline__ void paged_softmax_warp(const PagedParams &p, const P
         }
         const bool active = __any_sync(0xffffffffu, row_ok);
         // keys that any row of the item sees: rows of V past them are zeroed
-        const int alive = g.prefix ? p.batch.prefix_len : max(0, g.edge + (g.tok0 + g.toks - g.q0));
-        const int mine = g.tile_blocks<Cfg::NT, BKV>(tile);
+        const int alive = keys_alive<Cfg>(p, g);
+        bool sees = seen > g.b0 * BKV;   // a key of the stretch
+        const int mine = g.tile_blocks<Cfg::NT, BKV, Cfg::TREE>(tile);
         float m = -INFINITY, l = 0.0f;
         bool any_block = false;
         RingPos<Cfg::STAGES> prev_v = ring_k;
@@ -817,6 +873,23 @@ __device__ __forceinline__ void paged_softmax_warp(const PagedParams &p, const P
                         const int lim = seen - k0 - 32 * c;   // keys of these 32 that the row sees
                         if (__all_sync(0xffffffffu, lim >= 32))
                             continue;
+                        if constexpr (Cfg::TREE) {
+                            uint32_t bits = lim >= 32 ? 0xffffffffu : lim > 0 ? (1u << lim) - 1u : 0u;
+                            if (row_ok && !g.prefix)
+                                bits = tree_bits(p.mask + token * p.mask_stride, p.mask_words, alive - g.edge, -lim);
+                            sees = sees || bits != 0;
+                            if (__all_sync(0xffffffffu, bits == 0xffffffffu))
+                                continue;
+                            if (__any_sync(0xffffffffu, row_ok && bits != 0)) {
+                                tmem_ld_32x32b_x32(s_addr + 32u * c, va);
+                                tmem_ld_wait_regs(va);
+                            }
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                va[e] = bits >> e & 1u ? va[e] : hidden;
+                            tmem_st_32x32b_x32(s_addr + 32u * c, va);
+                            continue;
+                        }
                         if (__any_sync(0xffffffffu, row_ok && lim > 0)) {
                             tmem_ld_32x32b_x32(s_addr + 32u * c, va);
                             tmem_ld_wait_regs(va);
@@ -993,7 +1066,7 @@ __device__ __forceinline__ void paged_softmax_warp(const PagedParams &p, const P
                     for (int e = 0; e < 4; ++e) {
                         const int k = 8 * (i & 3) + 2 * e;
                         const float a = __uint_as_float(i < 4 ? va[k] : vb[k]), bb = __uint_as_float(i < 4 ? va[k + 1] : vb[k + 1]);
-                        w[e] = seen == 0 ? 0u : pack2<T>(a * inv, bb * inv);
+                        w[e] = (Cfg::TREE ? !sees : seen == 0) ? 0u : pack2<T>(a * inv, bb * inv);
                     }
                     piece[i] = make_uint4(w[0], w[1], w[2], w[3]);
                 }
@@ -1040,7 +1113,7 @@ __device__ __forceinline__ void paged_softmax_warp(const PagedParams &p, const P
             }
         }
         if (row_ok)
-            *ml = part_ml(m, l, seen > g.b0 * BKV);
+            *ml = part_ml(m, l, Cfg::TREE ? sees : seen > g.b0 * BKV);
     }
     __syncwarp();
     if (__builtin_expect(spoilt[warp], 0))
@@ -1412,7 +1485,7 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, Cfg::CTAS_PER_SM)
                 bool more = next_segment<Cfg>(p, walk, next);
                 while (ok && more) {
                     g = next;
-                    const int mine = g.tile_blocks<NT, BKV>(0);   // the first tile's blocks
+                    const int mine = g.tile_blocks<NT, BKV, Cfg::TREE>(0);   // the first tile's blocks
                     ok = wait_bounded(bar.q_full0, qp.parity, wc, ERR_MMA_OPERANDS);
                     qp.step();
                     auto product = [&](int t, int slot, bool add) -> bool {

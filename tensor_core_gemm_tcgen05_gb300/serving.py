@@ -156,6 +156,15 @@ def _weights(w, what, d, dtype, device):
     return w.data_ptr()
 
 
+def _lse(lse, shape, device):
+    """Address and token stride of ``lse`` for queries of ``shape``; None: no address."""
+    if lse is None:
+        return None, 0
+    if lse.dtype != torch.float32 or lse.device != device or lse.shape != shape[:2] or shape[1] > 1 and lse.stride(1) != 1:
+        raise ValueError(f"lse: a float32 tensor of shape {tuple(shape[:2])} on {device}, heads contiguous, expected")
+    return lse.data_ptr(), lse.stride(0) if shape[0] > 1 else shape[1]
+
+
 def _rope(q_norm, k_norm, eps, table, interleaved, scale, d, dtype, device):
     words, half = 0, 0
     if table is not None:
@@ -289,11 +298,7 @@ def paged_attention(ctx, q, k_cache, v_cache, q_start, kv_lens, page_table, max_
     if q_dim != d:
         raise ValueError(f"q: head_dim {d} expected, got {q_dim}")
     b = _batch(tokens, q_start, kv_lens, page_table, device, max_q, prefix_pages)
-    lse_ptr, lse_stride = None, 0
-    if lse is not None:
-        if lse.dtype != torch.float32 or lse.device != device or lse.shape != shape[:2] or heads > 1 and lse.stride(1) != 1:
-            raise ValueError(f"lse: a float32 tensor of shape {tuple(shape[:2])} on {device}, heads contiguous, expected")
-        lse_ptr, lse_stride = lse.data_ptr(), lse.stride(0) if tokens > 1 else heads
+    lse_ptr, lse_stride = _lse(lse, shape, device)
     if workspace is not None and (workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != device):
         raise ValueError(f"workspace: a contiguous uint8 tensor on {device} expected")
     if workspace is None:
