@@ -136,7 +136,7 @@ typedef struct gemm_w4 {
 } gemm_w4;
 
 /* C[M][N] = act(A[M][K] W^T + bias[N]): gemm_run's product and epilogues (GEMM_EPI_SOFTMAX excepted)
- * for few rows, which its time is the reading of W for. Any M up to 2^20 (0: nothing to do); it is
+ * for few rows, which its time is the reading of W for. Any M up to 2^18 (0: nothing to do); it is
  * made for M up to 64. N a multiple of 8, K of the group, both up to 2^24 (K = 0: act(bias)). A and C have rows of lda and
  * ldc elements (multiples of 8, at least K and N), all pointers 16-byte aligned (scales 2, zeros 1). dtype: type of A, scales,
  * bias and C. Codes minus zeros enter the tensor cores exactly; each group is summed in FP32 before its scale

@@ -11,13 +11,18 @@
 #include "gemm_decode.h"
 #include "kv_upkeep_kernel.cuh"
 #include "serving_host.h"
-#include "w4_kernel.cuh"
+#include "w4_umma_kernel.cuh"
 
 using namespace gb300_host;
 
 namespace {
 
-constexpr int64_t kMaxW4Rows = 1 << 20, kMaxW4Size = 1 << 24;
+constexpr int64_t kMaxW4Rows = 1 << 18, kMaxW4Size = 1 << 24;
+// Rows of A up to which w4_kernel is used. Both forms, in us (4096 x 4096, 16384 x 4096, 1024 x 1024, 512 x 8192, groups of 128):
+// eight rows 8.2, 17.0, 4.2, 7.7 against w4_umma_kernel's 8.3, 16.9, 5.0, 10.5; one row 6.3, 14.9, 3.7, 5.7 against 8.1, 16.9,
+// 4.9, 10.3; sixteen (of a w4_kernel that took them) 12.0, 23.2, 5.1, 11.2 against 8.4, 17.1, 5.1, 10.5.
+constexpr int64_t kW4MmaRows = 8;
+constexpr int kW4SmemMax = 227 * 1024;
 constexpr int kSelectHeldMax = 48 * 1024;   // keys: 192 KB of shared memory
 
 // launch_serving in clusters of `cluster` CTAs along x.
@@ -118,51 +123,89 @@ int page_shift(int64_t page_size)
 
 int launched(gemm_ctx *ctx, cudaError_t e) { return e == cudaSuccess ? GEMM_OK : cuda_fail(ctx, e, GEMM_ERR_LAUNCH); }
 
-template <typename T, int TILES, class Fn>
+template <typename T, class Fn>
 cudaError_t with_group(int64_t group, Fn &&fn)
 {
-    return group == 128 ? fn(gb300::w4_kernel<T, TILES, 4>) : group == 64 ? fn(gb300::w4_kernel<T, TILES, 2>) : fn(gb300::w4_kernel<T, TILES, 1>);
-}
-
-template <typename T, class Fn>
-cudaError_t with_tiles(int tiles, int64_t group, Fn &&fn)
-{
-    switch (tiles) {
-    case 1: return with_group<T, 1>(group, fn);
-    case 2: return with_group<T, 2>(group, fn);
-    case 4: return with_group<T, 4>(group, fn);
-    default: return with_group<T, 8>(group, fn);
-    }
+    return group == 128 ? fn(gb300::w4_kernel<T, 4>) : group == 64 ? fn(gb300::w4_kernel<T, 2>) : fn(gb300::w4_kernel<T, 1>);
 }
 
 template <class Fn>
-cudaError_t with_w4(int dtype, int tiles, int64_t group, Fn &&fn)
+cudaError_t with_w4(int dtype, int64_t group, Fn &&fn)
 {
-    return dtype == GEMM_F16 ? with_tiles<__half>(tiles, group, fn) : with_tiles<__nv_bfloat16>(tiles, group, fn);
+    return dtype == GEMM_F16 ? with_group<__half>(group, fn) : with_group<__nv_bfloat16>(group, fn);
 }
 
-// Shared memory of a CTA: the chunk of A, or the partial sums.
-int w4_smem(int tiles, int row_warps)
+template <typename T, int TOK, class Fn>
+cudaError_t with_umma_group(int64_t group, Fn &&fn)
 {
-    const int k_warps = gb300::kW4Warps / row_warps;
-    return std::max(gb300::kW4Ahead * k_warps * 4 * tiles * 32 * 16, k_warps * tiles * 8 * (16 * row_warps + 4) * 4);
+    return group == 128  ? fn(gb300::W4UmmaConfig<T, TOK, 128>{})
+           : group == 64 ? fn(gb300::W4UmmaConfig<T, TOK, 64>{})
+                         : fn(gb300::W4UmmaConfig<T, TOK, 32>{});
+}
+
+template <typename T, class Fn>
+cudaError_t with_umma_tokens(int tokens, int64_t group, Fn &&fn)
+{
+    return tokens == 16 ? with_umma_group<T, 16>(group, fn) : tokens == 32 ? with_umma_group<T, 32>(group, fn) : with_umma_group<T, 64>(group, fn);
+}
+
+template <class Fn>
+cudaError_t with_w4_umma(int dtype, int tokens, int64_t group, Fn &&fn)
+{
+    return dtype == GEMM_F16 ? with_umma_tokens<__half>(tokens, group, fn) : with_umma_tokens<__nv_bfloat16>(tokens, group, fn);
+}
+
+bool encode_2d(const gemm_ctx *ctx, CUtensorMap *map, CUtensorMapDataType type, int bytes, const void *ptr, int64_t cols, int64_t rows,
+               int64_t stride, uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swizzle)
+{
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride * bytes)};
+    const cuuint32_t box[2] = {box_cols, box_rows}, ones[2] = {1, 1};
+    return ctx->encode(map, type, 2, const_cast<void *>(ptr), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
 
 namespace gb300_host {
 
-cudaError_t decode_init(gemm_ctx *)
+cudaError_t decode_init(gemm_ctx *ctx)
 {
     for (int dtype : {GEMM_F16, GEMM_BF16})
-        for (int tiles : {1, 2, 4, 8})
+        for (int64_t group : {32, 64, 128}) {
+            const cudaError_t e = with_w4(dtype, group, [&](auto kernel) {
+                return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kW4SmemMax);
+            });
+            if (e != cudaSuccess)
+                return e;
+        }
+    for (int dtype : {GEMM_F16, GEMM_BF16})
+        for (int tokens : {16, 32, 64})
             for (int64_t group : {32, 64, 128}) {
-                const cudaError_t e = with_w4(dtype, tiles, group, [&](auto kernel) {
-                    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+                const cudaError_t e = with_w4_umma(dtype, tokens, group, [&](auto cfg) {
+                    using Cfg = decltype(cfg);
+                    return cudaFuncSetAttribute(gb300::w4_umma_kernel<Cfg>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES);
                 });
                 if (e != cudaSuccess)
                     return e;
             }
+    // clusters of the 4-bit product that run at once, a CTA to an SM
+    ctx->w4_clusters[1] = ctx->num_sms;
+    for (int size : {2, 4, 8}) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(size));
+        cfg.blockDim = dim3(gb300::kW4Threads);
+        cfg.dynamicSmemBytes = kW4SmemMax;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = static_cast<unsigned>(size);
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        const cudaError_t e = cudaOccupancyMaxActiveClusters(&ctx->w4_clusters[size], gb300::w4_kernel<__half, 4>, &cfg);
+        if (e != cudaSuccess)
+            return e;
+    }
     return cudaFuncSetAttribute(gb300::kv_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelectHeldMax * 4);
 }
 
@@ -269,6 +312,9 @@ int gemm_kv_weigh(gemm_ctx *ctx, const gemm_kv_cache *cache, const gemm_kv_batch
     p.w_head = weights->head_stride;
     p.kv_heads = static_cast<int>(heads);
     p.group = static_cast<int>(group);
+    auto magic = [](int64_t x) { return static_cast<uint32_t>(((uint64_t(1) << 32) + x - 1) / x); };   // (of 1: 0, a plain division)
+    p.group_magic = tokens * group <= (1 << 25) ? magic(group) : 0;
+    p.heads_magic = heads <= 128 ? magic(heads) : 0;
     p.window = static_cast<int>(std::min<int64_t>(window, INT32_MAX));
     p.scale_log2 = scale_log2;
     p.decay = decay;
@@ -341,7 +387,7 @@ int gemm_kv_select(gemm_ctx *ctx, const gemm_kv_seqs *seqs, int64_t num_pages, i
         cluster *= 2;
     if (items * cluster > INT32_MAX)
         return GEMM_ERR_ARG;
-    p.held = static_cast<int>(std::min<int64_t>(kSelectHeldMax, (room + cluster - 1) / cluster + 16));
+    p.held = static_cast<int>(std::min<int64_t>(kSelectHeldMax, ((room + cluster - 1) / cluster + 16 + 3) / 4 * 4));
     DeviceGuard guard(ctx->device);
     return launched(ctx, launch_cluster(gb300::kv_select_kernel, dim3(static_cast<unsigned>(items * cluster)), gb300::kSelectThreads,
                                         p.held * 4, cluster, static_cast<cudaStream_t>(stream), p));
@@ -477,21 +523,49 @@ int gemm_w4_run(gemm_ctx *ctx, int dtype, int64_t M, int64_t N, int64_t K, const
     p.c = C;
     p.ldc = ldc;
     p.epilogue = epilogue;
-    p.steps = static_cast<int>((K + 127) / 128);
-    const int tiles = M <= 8 ? 1 : M <= 16 ? 2 : M <= 32 ? 4 : 8;
-    const int64_t blocks_m = (M + tiles * 8 - 1) / (tiles * 8);
-    p.row_warps = 8;
+    p.steps = static_cast<int>((K + 255) / 256);
+    p.err = ctx->d_err;
+    p.timeout_ns = ctx->timeout_ns;
+    // w4_kernel: A's columns have to fit the shared memory of a cluster.
+    const int groups_128 = static_cast<int>(128 / w->group);
     int cluster = 1;
-    auto blocks = [&] { return (N + 16 * p.row_warps - 1) / (16 * p.row_warps) * blocks_m; };
-    while (cluster < 8 && blocks() * cluster * 2 <= 4 * static_cast<int64_t>(ctx->num_sms) && p.steps >= 2 * cluster * gb300::kW4Ahead)
+    auto slice = [&] { return (p.steps + cluster - 1) / cluster; };
+    auto fits = [&] { return gb300::w4_smem(groups_128, slice(), cluster > 1) <= kW4SmemMax; };
+    while (cluster < 8 && !fits())
         cluster *= 2;
-    while (p.row_warps > 1 && tiles <= 2 && blocks() * cluster < ctx->num_sms)
-        p.row_warps /= 2;
-    const int64_t grid = (N + 16 * p.row_warps - 1) / (16 * p.row_warps) * cluster;
+    if (K > 0 && (M > kW4MmaRows || !fits())) {
+        p.steps = static_cast<int>((K + 127) / 128);
+        const int tokens = M <= 16 ? 16 : M <= 32 ? 32 : 64;
+        const int64_t tiles = (N + 127) / 128, blocks_m = (M + tokens - 1) / tokens;
+        // as many CTAs share a tile's columns as run at once, with two steps each at least (512 x 8192, 16 rows: 8 of them 7.9
+        // us, 4 10.5; 2048 x 2048, where not all clusters of 8 run at once: 11.1, 6.2)
+        cluster = 1;
+        while (cluster < 8 && tiles * blocks_m <= ctx->w4_clusters[cluster * 2] && p.steps >= 4 * cluster)
+            cluster *= 2;
+        CUtensorMap codes, a;
+        if (!encode_2d(ctx, &codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w->codes, K / 2, N, K / 2, 64, 128, CU_TENSOR_MAP_SWIZZLE_64B) ||
+            !encode_2d(ctx, &a, dtype == GEMM_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, A, K, M, lda, 64,
+                       static_cast<uint32_t>(tokens), CU_TENSOR_MAP_SWIZZLE_128B))
+            return GEMM_ERR_LAUNCH;
+        DeviceGuard guard(ctx->device);
+        return launched(ctx, with_w4_umma(dtype, tokens, w->group, [&](auto cfg) {
+                            using Cfg = decltype(cfg);
+                            return launch_cluster(gb300::w4_umma_kernel<Cfg>,
+                                                  dim3(static_cast<unsigned>(tiles * cluster), static_cast<unsigned>(blocks_m)),
+                                                  Cfg::NUM_THREADS, Cfg::SMEM_BYTES, cluster, static_cast<cudaStream_t>(stream), codes, a, p);
+                        }));
+    }
+    const int64_t blocks_m = (M + gb300::kW4Rows - 1) / gb300::kW4Rows;
+    p.tiles = static_cast<int>((N + 15) / 16);
+    // Fewer tiles than CTAs: the columns shared by more of them, as long as every warp has a step.
+    while (cluster < 8 && int64_t(p.tiles) * blocks_m * cluster * 2 <= ctx->num_sms && p.steps >= 2 * cluster * gb300::kW4Warps)
+        cluster *= 2;
+    p.slice = slice();
+    p.clusters = std::min(p.tiles, std::max(1, ctx->w4_clusters[cluster]));
     DeviceGuard guard(ctx->device);
-    return launched(ctx, with_w4(dtype, tiles, w->group, [&](auto kernel) {
-                        return launch_cluster(kernel, dim3(static_cast<unsigned>(grid), static_cast<unsigned>(blocks_m)),
-                                              gb300::kW4Threads, w4_smem(tiles, p.row_warps), cluster,
+    return launched(ctx, with_w4(dtype, w->group, [&](auto kernel) {
+                        return launch_cluster(kernel, dim3(static_cast<unsigned>(p.clusters * cluster), static_cast<unsigned>(blocks_m)),
+                                              gb300::kW4Threads, static_cast<int>(gb300::w4_smem(groups_128, p.slice, cluster > 1)), cluster,
                                               static_cast<cudaStream_t>(stream), p);
                     }));
 }

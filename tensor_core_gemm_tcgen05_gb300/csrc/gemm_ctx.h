@@ -41,6 +41,8 @@ struct gemm_ctx {
     int softmax_clusters[gb300_host::kSoftmaxClusterMax + 1] = {};
     // split-K: co-resident clusters of 2, 4 and 8 CTAs of the split-K instance, per size
     int split_clusters[9] = {};
+    // 4-bit products: co-resident clusters of 1, 2, 4 and 8 CTAs, per size
+    int w4_clusters[9] = {};
     // gemm_run_host: device staging buffers, two copy streams and the events that order
     // the chunked pipeline (created on first use)
     void *stage = nullptr;

@@ -28,13 +28,6 @@ __device__ __forceinline__ uint4 ld_shared_cluster_u4(uint32_t addr)
     return v;
 }
 
-__device__ __forceinline__ uint32_t cluster_size()
-{
-    uint32_t v;
-    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(v));
-    return v;
-}
-
 __device__ __forceinline__ void report_index(uint32_t *err)
 {
     atomicCAS(err, 0u, static_cast<uint32_t>(ERR_BATCH_INDEX));
@@ -112,9 +105,17 @@ struct WeighParams {
     float *w;
     int64_t w_page, w_head;
     int kv_heads, group, window;
+    uint32_t group_magic, heads_magic;   // ceil(2^32 / x); 0: not used
     float scale_log2, decay;
     uint32_t *err;
 };
+
+// a / b for 0 <= a < 2^25, 0 < b <= 128 with magic = ceil(2^32 / b): the product is off by less than a 2^-32 < 1 / b. (A
+// division costs about thirty instructions, the rest of a warp's 32 keys of a decoding step about three hundred.) magic = 0: any.
+__device__ __forceinline__ int divide(int a, int b, uint32_t magic)
+{
+    return magic ? static_cast<int>(__umulhi(static_cast<uint32_t>(a), magic)) : a / b;
+}
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kWeighThreads, 2) kv_weigh_kernel(const __grid_constant__ WeighParams p)
@@ -155,93 +156,141 @@ __global__ void __launch_bounds__(kWeighThreads, 2) kv_weigh_kernel(const __grid
         // this CTA's: block b of all with b mod CTAs = its number
         int64_t b = static_cast<int64_t>(blockIdx.x) - before % gridDim.x;
         b += b < 0 ? gridDim.x : 0;
-        for (; b < total; b += gridDim.x) {
-            int lo = 0;   // the first sequence with ahead > b
+        // a block, and where the warp's keys are; found while the block before it is worked on
+        struct Unit {
+            SeqView v;
+            int head, key0;
+            int page[2];   // of 16 keys each; -1: none
+        };
+        auto find = [&](int64_t at) {
+            Unit u = {};
+            if (at >= total)
+                return u;
+            int lo = 0;   // the first sequence with ahead > at
             for (int step = kWeighThreads / 2; step > 0; step /= 2)
-                lo += ahead[lo + step - 1] <= b ? step : 0;
-            const SeqView v = load_seq(p.batch, s0 + lo);
-            const int64_t at = b - (lo > 0 ? ahead[lo - 1] : 0);
-            const int per_head = (v.kv + kWeighKeys - 1) / kWeighKeys;
-            const int head = static_cast<int>(at / per_head), key0 = static_cast<int>(at % per_head) * kWeighKeys + 32 * warp;
-            // ---- the warp's keys
-            uint4 k[2][2][C];   // [tile of 16 keys][row g, g + 8][piece]
-            int64_t page_of[2];   // -1: none
+                lo += ahead[lo + step - 1] <= at ? step : 0;
+            u.v = load_seq(p.batch, s0 + lo);
+            const int64_t in_seq = at - (lo > 0 ? ahead[lo - 1] : 0);   // block of keys by block, its heads one after the other
+            const int block = in_seq < (1 << 25) ? divide(static_cast<int>(in_seq), p.kv_heads, p.heads_magic)
+                                                 : static_cast<int>(in_seq / p.kv_heads);
+            u.head = static_cast<int>(in_seq - static_cast<int64_t>(block) * p.kv_heads);
+            u.key0 = block * kWeighKeys + 32 * warp;
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
-                const int key = key0 + 16 * m;
-                page_of[m] = -1;
-                if (key < v.kv) {
-                    const int id = __ldg(p.batch.table + (s0 + lo) * p.batch.table_stride + (key >> p.batch.page_shift));
-                    if (id >= 0 && id < p.batch.num_pages)
-                        page_of[m] = id;
-                    else
-                        report_index(p.err);
-                }
-                const int row = key & ((1 << p.batch.page_shift) - 1);
-                const T *src = static_cast<const T *>(p.k) + page_of[m] * p.page_stride + head * p.head_stride + (row + g) * p.row_stride + 8 * t;
-#pragma unroll
-                for (int half = 0; half < 2; ++half)
-#pragma unroll
-                    for (int c = 0; c < C; ++c)
-                        k[m][half][c] = page_of[m] >= 0
-                                            ? __ldg(reinterpret_cast<const uint4 *>(src + half * 8 * p.row_stride + 32 * c))
-                                            : make_uint4(0, 0, 0, 0);
+                const int key = u.key0 + 16 * m;
+                u.page[m] = key < u.v.kv ? __ldg(p.batch.table + (s0 + lo) * p.batch.table_stride + (key >> p.batch.page_shift)) : -1;
             }
-            // ---- rows of queries, 64 at a time
+            return u;
+        };
+        Unit next = find(b);
+        for (; b < total; b += gridDim.x) {
+            const Unit u = next;
+            const SeqView &v = u.v;
+            const int head = u.head, key0 = u.key0;
+            // ---- the warp's keys, and their weights before (lanes of t = 0)
+            uint4 k[2][2][C];   // [tile of 16 keys][row g, g + 8][piece]
+            float *weight[2];   // of key g of the tile
+            float old[2][2];
+            bool there[2];
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                const int key = key0 + 16 * m, row = key & ((1 << p.batch.page_shift) - 1);
+                there[m] = u.page[m] >= 0 && u.page[m] < p.batch.num_pages;
+                if (key < v.kv && !there[m])
+                    report_index(p.err);
+                const T *src = static_cast<const T *>(p.k) + u.page[m] * p.page_stride + head * p.head_stride + (row + g) * p.row_stride + 8 * t;
+                weight[m] = p.w + u.page[m] * p.w_page + head * p.w_head + row + g;
+                old[m][0] = old[m][1] = 0.0f;
+                if (there[m]) {   // (the sums of keys that are not there are not written)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+#pragma unroll
+                        for (int c = 0; c < C; ++c)
+                            k[m][half][c] = __ldg(reinterpret_cast<const uint4 *>(src + half * 8 * p.row_stride + 32 * c));
+                        if (t == 0 && p.decay != 0.0f && key + 8 * half + g < v.kv - v.n)
+                            old[m][half] = weight[m][8 * half];
+                    }
+                }
+            }
             const int tokens = p.window > 0 ? min(p.window, v.n) : v.n;
             const int rows = tokens * p.group;   // (fits: the host sees to it)
+            // row r of the queries: -lse in base 2, and the last key that it sees (-1: it gives nothing)
+            auto row_of = [&](int r, float &off, int &last) {
+                off = 0.0f;
+                last = -1;
+                if (r < rows) {
+                    const int token = divide(r, p.group, p.group_magic), i = v.n - tokens + token;   // of the sequence's new tokens
+                    const float l = __ldg(p.lse + (v.q0 + i) * p.lse_token + head * p.group + (r - token * p.group));
+                    off = -l * 1.4426950408889634f;
+                    last = l == -INFINITY ? -1 : v.kv - v.n + i;
+                }
+            };
+            auto query = [&](int r, int piece) -> uint4 {   // 8 dims of row r
+                if (r >= rows)
+                    return make_uint4(0, 0, 0, 0);
+                const int token = divide(r, p.group, p.group_magic);
+                return __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(p.q) + static_cast<int64_t>(v.q0 + v.n - tokens + token) * p.q_token +
+                                                             (head * p.group + r - token * p.group) * p.q_head + 8 * piece));
+            };
             float sum[2][2] = {};
-            for (int r0 = 0; r0 < rows; r0 += kWeighRows) {
-                const int tiles = (min(rows - r0, kWeighRows) + 7) / 8;
-                __syncthreads();   // the rows before are done with
-                for (int i = threadIdx.x; i < tiles * 8 * (D / 8); i += kWeighThreads) {
-                    const int r = i / (D / 8), piece = i % (D / 8), row = r0 + r;
-                    uint4 x = make_uint4(0, 0, 0, 0);
-                    if (row < rows) {
-                        const int64_t token = v.q0 + v.n - tokens + row / p.group;
-                        x = __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(p.q) + token * p.q_token +
-                                                                  (head * p.group + row % p.group) * p.q_head + 8 * piece));
-                    }
-                    queries[((r / 8) * C + piece / 4) * 32 + (r % 8) * 4 + piece % 4] = x;
-                }
-                if (threadIdx.x < static_cast<unsigned>(tiles * 8)) {
-                    const int row = r0 + threadIdx.x;
-                    float off = 0.0f;
-                    int last = -1;
-                    if (row < rows) {
-                        const int i = v.n - tokens + row / p.group;   // of the sequence's new tokens
-                        const float l = __ldg(p.lse + (v.q0 + i) * p.lse_token + head * p.group + row % p.group);
-                        off = -l * 1.4426950408889634f;
-                        last = l == -INFINITY ? -1 : v.kv - v.n + i;
-                    }
-                    minus_lse[threadIdx.x] = off;
-                    last_key[threadIdx.x] = last;
-                }
-                __syncthreads();
-                if (key0 >= v.kv)
-                    continue;
-                for (int i = 0; i < tiles; ++i) {
-                    float s[2][4] = {};
+            // weight of eight rows: the pieces of their queries, and of rows 2 t, 2 t + 1 the other two
+            auto weigh = [&](const uint4 (&q)[C], float2 off, int2 last) {
+                float s[2][4] = {};
 #pragma unroll
-                    for (int c = 0; c < C; ++c) {
-                        const uint4 q = queries[(i * C + c) * 32 + lane];
+                for (int c = 0; c < C; ++c)
 #pragma unroll
-                        for (int m = 0; m < 2; ++m) {
-                            mma_16x8x16<T>(s[m], k[m][0][c].x, k[m][1][c].x, k[m][0][c].y, k[m][1][c].y, q.x, q.y);
-                            mma_16x8x16<T>(s[m], k[m][0][c].z, k[m][1][c].z, k[m][0][c].w, k[m][1][c].w, q.z, q.w);
+                    for (int m = 0; m < 2; ++m) {
+                        mma_16x8x16<T>(s[m], k[m][0][c].x, k[m][1][c].x, k[m][0][c].y, k[m][1][c].y, q[c].x, q[c].y);
+                        mma_16x8x16<T>(s[m], k[m][0][c].z, k[m][1][c].z, k[m][0][c].w, k[m][1][c].w, q[c].z, q[c].w);
+                    }
+                const bool all = __all_sync(0xffffffffu, min(last.x, last.y) >= key0 + 31);   // the rows see all of the warp's keys
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const int key = key0 + 16 * m + 8 * half + g;
+                        float x = ex2_approx(fmaf(s[m][2 * half], p.scale_log2, off.x));
+                        float y = ex2_approx(fmaf(s[m][2 * half + 1], p.scale_log2, off.y));
+                        if (!all) {
+                            x = key <= last.x ? x : 0.0f;
+                            y = key <= last.y ? y : 0.0f;
                         }
+                        sum[m][half] += x + y;
                     }
-                    const float2 off = *reinterpret_cast<const float2 *>(minus_lse + 8 * i + 2 * t);
-                    const int2 last = *reinterpret_cast<const int2 *>(last_key + 8 * i + 2 * t);
+            };
+            if (rows <= 8) {   // (a decoding step: the queries straight into registers, no warp waits for another)
+                uint4 q[C];
+                float2 off;
+                int2 last;
 #pragma unroll
-                    for (int m = 0; m < 2; ++m)
+                for (int c = 0; c < C; ++c)
+                    q[c] = query(g, 4 * c + t);
+                row_of(2 * t, off.x, last.x);
+                row_of(2 * t + 1, off.y, last.y);
+                next = find(b + gridDim.x);
+                weigh(q, off, last);
+            } else {
+                next = find(b + gridDim.x);
+                for (int r0 = 0; r0 < rows; r0 += kWeighRows) {   // 64 rows at a time
+                    const int tiles = (min(rows - r0, kWeighRows) + 7) / 8;
+                    __syncthreads();   // the rows before are done with
+                    for (int i = threadIdx.x; i < tiles * 8 * (D / 8); i += kWeighThreads) {
+                        const int r = i / (D / 8), piece = i % (D / 8);
+                        queries[((r / 8) * C + piece / 4) * 32 + (r % 8) * 4 + piece % 4] = query(r0 + r, piece);
+                    }
+                    if (threadIdx.x < static_cast<unsigned>(tiles * 8))
+                        row_of(r0 + threadIdx.x, minus_lse[threadIdx.x], last_key[threadIdx.x]);
+                    __syncthreads();
+                    if (key0 >= v.kv)
+                        continue;
+                    for (int i = 0; i < tiles; ++i) {
+                        uint4 q[C];
 #pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            const int key = key0 + 16 * m + 8 * half + g;
-                            const float a = ex2_approx(fmaf(s[m][2 * half], p.scale_log2, off.x));
-                            const float c = ex2_approx(fmaf(s[m][2 * half + 1], p.scale_log2, off.y));
-                            sum[m][half] += (key <= last.x ? a : 0.0f) + (key <= last.y ? c : 0.0f);
-                        }
+                        for (int c = 0; c < C; ++c)
+                            q[c] = queries[(i * C + c) * 32 + lane];
+                        weigh(q, *reinterpret_cast<const float2 *>(minus_lse + 8 * i + 2 * t),
+                              *reinterpret_cast<const int2 *>(last_key + 8 * i + 2 * t));
+                    }
                 }
             }
 #pragma unroll
@@ -251,11 +300,8 @@ __global__ void __launch_bounds__(kWeighThreads, 2) kv_weigh_kernel(const __grid
                     float x = sum[m][half];
                     x += __shfl_xor_sync(0xffffffffu, x, 1);
                     x += __shfl_xor_sync(0xffffffffu, x, 2);
-                    const int key = key0 + 16 * m + 8 * half + g;
-                    if (t == 0 && key < v.kv && page_of[m] >= 0) {
-                        float *dst = p.w + page_of[m] * p.w_page + head * p.w_head + (key & ((1 << p.batch.page_shift) - 1));
-                        *dst = p.decay != 0.0f && key < v.kv - v.n ? fmaf(p.decay, *dst, x) : x;
-                    }
+                    if (t == 0 && key0 + 16 * m + 8 * half + g < v.kv && there[m])
+                        weight[m][8 * half] = fmaf(p.decay, old[m][half], x);
                 }
         }
         before += total;
@@ -271,7 +317,7 @@ __global__ void __launch_bounds__(kWeighThreads, 2) kv_weigh_kernel(const __grid
 // border and the first of those on it. A cluster of CTAs per sequence and key head, each with a
 // slice of the keys, which it holds in shared memory; the histograms are summed over distributed
 // shared memory. Reads each weight once.
-constexpr int kSelectThreads = 512, kSelectBins = 2048;
+constexpr int kSelectThreads = 512, kSelectBins = 2048, kSelectBatch = 8;
 
 struct SelectParams {
     const int *kv_lens, *table;
@@ -320,20 +366,37 @@ __global__ void __launch_bounds__(kSelectThreads) kv_select_kernel(const __grid_
     const int slice = static_cast<int>(((static_cast<int64_t>(kv) + ctas - 1) / ctas + 15) / 16 * 16);
     const int a = static_cast<int>(min(static_cast<int64_t>(rank) * slice, static_cast<int64_t>(kv)));
     const int b = static_cast<int>(min(static_cast<int64_t>(a) + slice, static_cast<int64_t>(kv)));
-    auto fetch = [&](int i) -> uint32_t {
-        const int id = __ldg(p.table + s * p.table_stride + (i >> p.page_shift));
-        float x = 0.0f;
-        if (id >= 0 && id < p.num_pages)
-            x = __ldg(p.w + id * p.w_page + head * p.w_head + (i & ((1 << p.page_shift) - 1))) + 0.0f;   // (-0 becomes 0)
-        else
-            report_index(p.err);
+    bool bad = false;
+    auto page_of = [&](int i) { return __ldg(p.table + s * p.table_stride + (i >> p.page_shift)); };
+    auto weight_key = [&](int id, int i) -> uint32_t {   // of key i, whose page is id: as an integer that orders as the weights do
+        // (no branch: several loads are in flight)
+        const bool ok = id >= 0 && id < p.num_pages;
+        bad = bad || !ok;
+        float x = __ldg(p.w + (ok ? id : 0) * p.w_page + head * p.w_head + (i & ((1 << p.page_shift) - 1))) + 0.0f;   // (-0 becomes 0)
+        x = ok ? x : 0.0f;
         const uint32_t u = __float_as_uint(x);
         return x != x ? 0u : u ^ (u >> 31 ? 0xffffffffu : 0x80000000u);
     };
-    auto key_of = [&](int i) -> uint32_t { return i - a < p.held ? held[i - a] : fetch(i); };
-    if (m > 0)
-        for (int i = a + static_cast<int>(threadIdx.x); i < min(b, a + p.held); i += kSelectThreads)
-            held[i - a] = fetch(i);
+    auto fetch = [&](int i) { return weight_key(page_of(i), i); };
+    const int in_held = static_cast<int>(min(static_cast<int64_t>(b), static_cast<int64_t>(a) + p.held));
+    auto key_of = [&](int i) -> uint32_t { return i < in_held ? held[i - a] : fetch(i); };
+    if (m > 0) {   // (pages of eight keys at a time, then their weights: two trips to memory for eight)
+        const int end = in_held;
+        for (int i0 = a + static_cast<int>(threadIdx.x); i0 < end; i0 += kSelectBatch * kSelectThreads) {
+            int id[kSelectBatch];
+            uint32_t key[kSelectBatch];
+#pragma unroll
+            for (int e = 0; e < kSelectBatch; ++e)
+                id[e] = page_of(min(i0 + e * kSelectThreads, end - 1));
+#pragma unroll
+            for (int e = 0; e < kSelectBatch; ++e)
+                key[e] = weight_key(id[e], min(i0 + e * kSelectThreads, end - 1));
+#pragma unroll
+            for (int e = 0; e < kSelectBatch; ++e)
+                if (i0 + e * kSelectThreads < end)
+                    held[i0 + e * kSelectThreads - a] = key[e];
+        }
+    }
     // ---- the border
     uint32_t border = 0xffffffffu, left = 0;   // all above it (nothing is) and the first `left` on it
     if (m > 0) {
@@ -343,11 +406,19 @@ __global__ void __launch_bounds__(kSelectThreads) kv_select_kernel(const __grid_
             const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
             bins[threadIdx.x] = make_uint4(0, 0, 0, 0);
             __syncthreads();
-            for (int i = max(a, lo) + static_cast<int>(threadIdx.x); i < min(b, hi); i += kSelectThreads) {
-                const uint32_t key = key_of(i);
-                if (pass == 0 || (key ^ border) >> (shift + bits) == 0)
+            auto count_digit = [&](int i, uint32_t key) {
+                if (static_cast<uint32_t>(i - lo) < static_cast<uint32_t>(hi - lo) && (pass == 0 || (key ^ border) >> (shift + bits) == 0))
                     atomicAdd(&hist[(~key >> shift) & ((1u << bits) - 1u)], 1u);
+            };
+            for (int i = a + 4 * static_cast<int>(threadIdx.x); i < in_held; i += 4 * kSelectThreads) {   // (past the end: keys that are not counted)
+                const uint4 key = *reinterpret_cast<const uint4 *>(held + (i - a));
+                count_digit(i, key.x);
+                count_digit(i + 1, i + 1 < in_held ? key.y : 0u);
+                count_digit(i + 2, i + 2 < in_held ? key.z : 0u);
+                count_digit(i + 3, i + 3 < in_held ? key.w : 0u);
             }
+            for (int i = in_held + static_cast<int>(threadIdx.x); i < b; i += kSelectThreads)
+                count_digit(i, fetch(i));
             __syncthreads();
             if (ctas > 1)
                 cluster_sync();
@@ -388,10 +459,15 @@ __global__ void __launch_bounds__(kSelectThreads) kv_select_kernel(const __grid_
             left -= above;
         }
     }
+    if (bad)
+        report_index(p.err);
     // ---- how many of each kind the slices before this one have
     auto above_it = [&](int i, uint32_t key) { return i < lo || i >= hi || key > border; };
+    const int piece = ((b - a + kSelectThreads - 1) / kSelectThreads) * 32;   // of the slice, to a warp
+    const int wa = static_cast<int>(min(static_cast<int64_t>(a) + static_cast<int64_t>(warp) * piece, static_cast<int64_t>(b)));
+    const int wb = static_cast<int>(min(static_cast<int64_t>(wa) + piece, static_cast<int64_t>(b)));
     uint32_t gt = 0, eq = 0;
-    for (int i = a + static_cast<int>(threadIdx.x); i < b; i += kSelectThreads) {
+    for (int i = wa + lane; i < wb; i += 32) {
         const uint32_t key = m > 0 ? key_of(i) : 0u;
         const bool up = above_it(i, key);
         gt += up;
@@ -402,45 +478,38 @@ __global__ void __launch_bounds__(kSelectThreads) kv_select_kernel(const __grid_
         gt += __shfl_xor_sync(0xffffffffu, gt, o);
         eq += __shfl_xor_sync(0xffffffffu, eq, o);
     }
-    if (threadIdx.x == 0)
-        mine = make_uint2(0, 0);
-    __syncthreads();
     if (lane == 0) {
-        atomicAdd(&mine.x, gt);
-        atomicAdd(&mine.y, eq);
+        warp_sum[0][warp] = gt;
+        warp_sum[1][warp] = eq;
     }
     __syncthreads();
-    if (ctas > 1)
-        cluster_sync();
-    gt = eq = 0;
-    for (int r = 0; r < rank; ++r) {
-        const uint2 x = ld_shared_cluster_u2(mapa_shared(smem_u32(&mine), static_cast<uint32_t>(r)));
-        gt += x.x;
-        eq += x.y;
+    gt = eq = 0;   // of the warps before this one; thread 511: of all
+    for (int w = 0; w < warp; ++w) {
+        gt += warp_sum[0][w];
+        eq += warp_sum[1][w];
     }
-    // ---- the kept keys in order
-    for (int i0 = a, buf = 0; i0 < b; i0 += kSelectThreads, buf ^= 1) {
-        const int i = i0 + static_cast<int>(threadIdx.x);
-        const uint32_t key = i < b && m > 0 ? key_of(i) : 0u;
-        const bool up = i < b && above_it(i, key), on = i < b && !up && key == border;
-        const uint32_t ups = __ballot_sync(0xffffffffu, up), ons = __ballot_sync(0xffffffffu, on);
-        if (lane == 0)
-            warp_sum[buf][warp] = static_cast<uint32_t>(__popc(ups)) | static_cast<uint32_t>(__popc(ons)) << 16;
+    if (ctas > 1) {
+        if (threadIdx.x == kSelectThreads - 1)
+            mine = make_uint2(gt + warp_sum[0][warp], eq + warp_sum[1][warp]);
         __syncthreads();
-        uint32_t before = 0, all = 0;
-#pragma unroll
-        for (int w = 0; w < kSelectThreads / 32; ++w) {
-            const uint32_t x = warp_sum[buf][w];
-            before += w < warp ? x : 0u;
-            all += x;
+        cluster_sync();
+        for (int r = 0; r < rank; ++r) {
+            const uint2 x = ld_shared_cluster_u2(mapa_shared(smem_u32(&mine), static_cast<uint32_t>(r)));
+            gt += x.x;
+            eq += x.y;
         }
-        const uint32_t lower = (1u << lane) - 1u;
-        const uint32_t g = gt + (before & 0xffffu) + __popc(ups & lower), e = eq + (before >> 16) + __popc(ons & lower);
-        const uint32_t to = g + min(e, left);
+    }
+    // ---- the kept keys in order, a piece of the slice per warp
+    for (int i0 = wa; i0 < wb; i0 += 32) {
+        const int i = i0 + lane;
+        const uint32_t key = i < wb && m > 0 ? key_of(i) : 0u;
+        const bool up = i < wb && above_it(i, key), on = i < wb && !up && key == border;
+        const uint32_t ups = __ballot_sync(0xffffffffu, up), ons = __ballot_sync(0xffffffffu, on), lower = (1u << lane) - 1u;
+        const uint32_t g = gt + __popc(ups & lower), e = eq + __popc(ons & lower), to = g + min(e, left);
         if ((up || (on && e < left)) && to < static_cast<uint32_t>(p.keep))   // (always, unless weights change meanwhile)
             index[to] = i;
-        gt += all & 0xffffu;
-        eq += all >> 16;
+        gt += __popc(ups);
+        eq += __popc(ons);
     }
     __syncthreads();
     if (ctas > 1)
@@ -500,42 +569,45 @@ __global__ void __launch_bounds__(kCompactThreads) kv_compact_kernel(const __gri
             p.new_lens[s] = static_cast<int>(min(static_cast<int64_t>(start) + count, static_cast<int64_t>(INT32_MAX)));
     }
     const int mask = (1 << p.page_shift) - 1;
-    int buf = 0;
-    for (int64_t round = 0; round < count; round += static_cast<int64_t>(ctas) * rows, buf ^= 1) {
-        const int64_t j0 = round + static_cast<int64_t>(rank) * rows;
-        // ---- where the round's rows are and go to
-        float weight = 0.0f;
-        float *weight_to = nullptr;
-        if (threadIdx.x < PAIRS) {
-            const int head = head0 + static_cast<int>(threadIdx.x) / rows;
-            const int64_t j = j0 + static_cast<int>(threadIdx.x) % rows;
-            int64_t src = -1, dst = 0;
-            if (head < p.kv_heads && j < count) {
-                const int i = __ldg(p.index + s * p.seq_index + head * p.head_index + j);
-                const int64_t row = static_cast<int64_t>(start) + i;
-                if (i < j || row >= kv) {
+    const int64_t per_round = static_cast<int64_t>(ctas) * rows;
+    float *weight_from = nullptr, *weight_to = nullptr;   // of the row that this thread has looked up last
+    // where the rows of the round from `first` on are and go to
+    auto find = [&](int64_t first, int buf) {
+        if (threadIdx.x >= PAIRS)
+            return;
+        const int head = head0 + static_cast<int>(threadIdx.x) / rows;
+        const int64_t j = first + static_cast<int64_t>(rank) * rows + static_cast<int>(threadIdx.x) % rows;
+        int64_t src = -1, dst = 0;
+        weight_to = nullptr;
+        if (head < p.kv_heads && j < count) {
+            const int i = __ldg(p.index + s * p.seq_index + head * p.head_index + j);
+            const int64_t row = static_cast<int64_t>(start) + i;
+            if (i < j || row >= kv) {
+                report_index(p.err);
+            } else if (i > j) {
+                const int to_row = start + static_cast<int>(j), from_row = static_cast<int>(row);
+                const int *table = p.table + s * p.table_stride;
+                const int a = __ldg(table + (from_row >> p.page_shift)), b = __ldg(table + (to_row >> p.page_shift));
+                if (a < 0 || a >= p.num_pages || b < 0 || b >= p.num_pages) {
                     report_index(p.err);
-                } else if (i > j) {
-                    const int to_row = start + static_cast<int>(j), from_row = static_cast<int>(row);
-                    const int *table = p.table + s * p.table_stride;
-                    const int a = __ldg(table + (from_row >> p.page_shift)), b = __ldg(table + (to_row >> p.page_shift));
-                    if (a < 0 || a >= p.num_pages || b < 0 || b >= p.num_pages) {
-                        report_index(p.err);
-                    } else {
-                        src = a * p.page_stride + head * p.head_stride + (from_row & mask) * p.row_stride;
-                        dst = b * p.page_stride + head * p.head_stride + (to_row & mask) * p.row_stride;
-                        if (p.w) {
-                            weight = p.w[a * p.w_page + head * p.w_head + (from_row & mask)];
-                            weight_to = p.w + b * p.w_page + head * p.w_head + (to_row & mask);
-                        }
+                } else {
+                    src = a * p.page_stride + head * p.head_stride + (from_row & mask) * p.row_stride;
+                    dst = b * p.page_stride + head * p.head_stride + (to_row & mask) * p.row_stride;
+                    if (p.w) {
+                        weight_from = p.w + a * p.w_page + head * p.w_head + (from_row & mask);
+                        weight_to = p.w + b * p.w_page + head * p.w_head + (to_row & mask);
                     }
                 }
             }
-            from[buf][threadIdx.x] = src;
-            to[buf][threadIdx.x] = dst;
         }
-        __syncthreads();
-        // ---- read, wait for the others, write
+        from[buf][threadIdx.x] = src;
+        to[buf][threadIdx.x] = dst;
+    };
+    find(0, 0);
+    __syncthreads();
+    int buf = 0;
+    for (int64_t first = 0; first < count; first += per_round, buf ^= 1) {
+        // ---- read, look up the next round's rows meanwhile, wait for the others, write
         uint4 x[kCompactVecs];
 #pragma unroll
         for (int e = 0; e < kCompactVecs; ++e) {
@@ -545,6 +617,9 @@ __global__ void __launch_bounds__(kCompactThreads) kv_compact_kernel(const __gri
             if (src >= 0)
                 x[e] = *reinterpret_cast<const uint4 *>(base + src + 8 * piece);
         }
+        float *const store_weight = weight_to;
+        const float weight = store_weight ? *weight_from : 0.0f;
+        find(first + per_round, buf ^ 1);
         __syncthreads();
         if (ctas > 1)
             cluster_sync();
@@ -555,8 +630,9 @@ __global__ void __launch_bounds__(kCompactThreads) kv_compact_kernel(const __gri
             if (from[buf][row / 2] >= 0)
                 *reinterpret_cast<uint4 *>(base + to[buf][row / 2] + 8 * piece) = x[e];
         }
-        if (weight_to)
-            *weight_to = weight;
+        if (store_weight)
+            *store_weight = weight;
+        __syncthreads();   // the lookups after the next go over this round's
     }
 }
 

@@ -1,23 +1,36 @@
-// C[M][N] = act(A[M][K] W^T + bias[N]) with W[n][k] = (code - zero) scale, 4-bit codes (gemm_decode.h), for few rows
-// of A: what the time goes to is reading W once.
+// C[M][N] = act(A[M][K] W^T + bias[N]) with W[n][k] = (code - zero) scale, 4-bit codes (gemm_decode.h), for up to eight
+// rows of A: what the time goes to is reading W once. (w4_umma_kernel.cuh has the form for more rows.)
 //
 // The rows of W are the rows of 16 x 8 x 16 products and come straight into registers, the rows of A (tokens) are
-// the columns. Codes become code - zero exactly: the four bits go into the mantissa of 1024 (FP16) or 128 (BF16), from
-// which 1024 + zero or 128 + zero is taken. Each group is summed by itself in FP32 and its sum scaled in FP32, so that
-// no weight is rounded.
+// the columns. With the zero z, the scale s and the columns of a group,
+//     s sum (code - z) x = s (sum code x - z sum x),
+// so the products are of the codes themselves, which cost a mask each (see W4Codes) and are exact, and sum x comes with A. Groups
+// are summed and scaled in FP32: no weight is rounded. Where a sum x is not finite the two terms would cancel to NaN: a CTA
+// that finds one takes code - zero itself to the products.
 //
-// A warp takes 16 rows of W in steps of 128 columns; ROWS_W warps of a CTA stand side by side, the others
-// and (in a cluster) other CTAs share the columns; the partial sums meet in shared and distributed shared memory in a
-// fixed order. A is brought to shared memory a chunk of steps at a time, in the order the products take it.
+// A stays: a CTA (one to an SM, sixteen warps) brings its columns of A to shared memory once, in the order the products take
+// them, and then sees the tiles of 16 rows of W that are its cluster's, four, two or one at a time (a round), the columns
+// of a tile shared by the other warps and by the CTAs of the cluster (several, where A does not fit one). A step is 256 columns
+// of a tile; each lane copies its own codes of the next steps into a ring of its own, across rounds, so nothing but the
+// sums of a round waits for another warp. These meet in shared and distributed shared memory in a fixed order.
+//
+// What bounds it: instruction issue at 1.7 a cycle and SM, of which unpacking is a third, behind a start of about 3.5 us. Measured
+// (captured, weights from HBM): 4096 x 4096 6.3 us for one row, 8.2 for eight, 16384 x 4096 14.9 and 17.0 (33.5 MB: 5.2 at
+// the copy rate), 1024 x 1024 3.7. Steps of 128 columns with a ring of four took 25; codes - zero unpacked for each row 24;
+// 256 threads that brought A anew for each 128 rows 23.
 #pragma once
+
+#include <type_traits>
 
 #include "mma_sync.cuh"
 #include "serving_common.cuh"
 
 namespace gb300 {
 
-constexpr int kW4Threads = 256, kW4Warps = 8;
-constexpr int kW4Ahead = 4;   // steps whose codes a warp has in flight
+constexpr int kW4Threads = 512, kW4LogWarps = 4, kW4Warps = 1 << kW4LogWarps;
+constexpr int kW4Round = 4;   // tiles of 16 rows of W in a round, at most
+constexpr int kW4Rows = 8;    // of A in a CTA
+constexpr int kW4Ahead = 2;   // steps whose codes a warp has in flight
 
 struct W4Params {
     int M, N, K;
@@ -30,8 +43,11 @@ struct W4Params {
     void *c;
     int64_t ldc;
     int epilogue;
-    int row_warps;   // of a CTA: 1, 2, 4 or 8
-    int steps;       // of 128 columns, the last maybe in part
+    int tiles, clusters;   // w4_kernel: of 16 rows of W; of CTAs
+    int slice;             // w4_kernel: steps of a CTA, at most
+    int steps;             // of 256 (w4_kernel) or 128 columns, the last maybe in part
+    uint32_t *err;
+    uint64_t timeout_ns;
 };
 
 // The activation in FP32 (NaN stays NaN).
@@ -48,61 +64,54 @@ __device__ __forceinline__ void w4_activate(int epilogue, float &x0, float &x1)
     }
 }
 
-// Codes j and j + 4 of a word of eight (the first in the lowest bits), minus zero, as pair j of x. The constants of a
-// zero: what is to be taken from the pairs.
+// Codes j and j + 4 of a word of eight (the first in the lowest bits) as pair j of x, so that the value of a pair's bits
+// times UNIT (j even) or ODD_UNIT (j odd) is BASE + code.
+//  * FP16: bits alone are subnormal numbers, code 2^-24; odd codes are left where they are, 16 code 2^-24.
+//  * BF16: in the mantissa of 128. (As subnormal numbers times x they would leave FP32's range.) The sums then lose
+//    5 of FP32's 24 bits to the base, of which the result keeps 8.
 template <typename T>
 struct W4Codes;
 template <>
 struct W4Codes<__half> {
-    __half2 z, z16;
-    __device__ __forceinline__ explicit W4Codes(uint32_t zero)
+    static constexpr float UNIT = 16777216.0f, ODD_UNIT = 1048576.0f, BASE = 0.0f;
+    static __device__ __forceinline__ void unpack(uint32_t w, uint32_t (&x)[4])
     {
-        const uint32_t one = 0x6400u | zero, sixteenth = 0xd400u | zero << 4;   // 1024 + zero, -(64 + zero)
-        const uint32_t a = one * 0x10001u, b = sixteenth * 0x10001u;
-        z = *reinterpret_cast<const __half2 *>(&a);
-        z16 = *reinterpret_cast<const __half2 *>(&b);
-    }
-    __device__ __forceinline__ void unpack(uint32_t w, uint32_t (&x)[4]) const
-    {
-        const uint32_t one16 = 0x2c002c00u;   // 1 / 16
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint32_t lo = (w & 0x000f000fu) | 0x64006400u;   // 1024 + code
-            const uint32_t hi = (w & 0x00f000f0u) | 0x64006400u;   // 1024 + 16 code
-            const __half2 a = __hsub2(*reinterpret_cast<const __half2 *>(&lo), z);
-            const __half2 b = __hfma2(*reinterpret_cast<const __half2 *>(&hi), *reinterpret_cast<const __half2 *>(&one16), z16);
-            x[2 * h] = *reinterpret_cast<const uint32_t *>(&a);
-            x[2 * h + 1] = *reinterpret_cast<const uint32_t *>(&b);
-            w >>= 8;
-        }
+        x[0] = w & 0x000f000fu;
+        x[1] = w & 0x00f000f0u;
+        w >>= 8;
+        x[2] = w & 0x000f000fu;
+        x[3] = w & 0x00f000f0u;
     }
 };
 template <>
 struct W4Codes<__nv_bfloat16> {
-    __nv_bfloat162 z;
-    __device__ __forceinline__ explicit W4Codes(uint32_t zero)
-    {
-        const uint32_t a = (0x4300u | zero) * 0x10001u;   // 128 + zero
-        z = *reinterpret_cast<const __nv_bfloat162 *>(&a);
-    }
-    __device__ __forceinline__ void unpack(uint32_t w, uint32_t (&x)[4]) const
+    static constexpr float UNIT = 1.0f, ODD_UNIT = 1.0f, BASE = 128.0f;
+    static __device__ __forceinline__ void unpack(uint32_t w, uint32_t (&x)[4])
     {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t v = (w & 0x000f000fu) | 0x43004300u;
-            const __nv_bfloat162 a = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&v), z);
-            x[j] = *reinterpret_cast<const uint32_t *>(&a);
-            w >>= 4;
-        }
+        for (int j = 0; j < 4; ++j)
+            x[j] = ((w >> (4 * j)) & 0x000f000fu) | 0x43004300u;
     }
 };
 
-// A step's codes of a lane: 32 of row g and 32 of row g + 8, and (lane t, t < groups of the step) scale and
-// zero of group t in both rows.
-struct W4Step {
-    uint32_t w[2][4];
-    uint32_t sz[2];   // scale's bits, zero << 16
-};
+// The same with code - zero as the value, a zero for each row.
+template <typename T>
+__device__ __forceinline__ void w4_unpack_minus_zero(uint32_t w, uint32_t zero, uint32_t (&x)[4])
+{
+    constexpr bool HALF = std::is_same<T, __half>::value;
+    const uint32_t base = HALF ? 0x64006400u : 0x43004300u, less = base | zero * 0x10001u;   // 1024 or 128, and with the zero
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t v = ((w >> (4 * j)) & 0x000f000fu) | base;
+        if constexpr (HALF) {
+            const __half2 y = __hsub2(*reinterpret_cast<const __half2 *>(&v), *reinterpret_cast<const __half2 *>(&less));
+            x[j] = *reinterpret_cast<const uint32_t *>(&y);
+        } else {
+            const __nv_bfloat162 y = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&v), *reinterpret_cast<const __nv_bfloat162 *>(&less));
+            x[j] = *reinterpret_cast<const uint32_t *>(&y);
+        }
+    }
+}
 
 template <typename T>
 __device__ __forceinline__ float w4_scale(uint32_t sz)
@@ -110,167 +119,301 @@ __device__ __forceinline__ float w4_scale(uint32_t sz)
     return unpack2<T>(sz & 0xffffu).x;
 }
 
-// GW: words of eight codes that a lane has of a group (1, 2, 4: groups of 32, 64, 128). TILES: of eight rows of A.
-template <typename T, int TILES, int GW>
-__global__ void __launch_bounds__(kW4Threads) w4_kernel(const __grid_constant__ W4Params p)
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void *src)
 {
-    constexpr int GROUPS = 4 / GW, GROUP = 32 * GW;   // groups of a step
-    extern __shared__ uint4 act[];                    // [step of the chunk][word][tile][lane]
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
+}
+
+// A warp's way through the rounds of its cluster's tiles: 2^log_rows tiles from `tile` on; of a tile its steps w, w + warps, ...,
+// in `turns` turns, a multiple of kW4Ahead (so that a turn's slot of the ring is known when compiling; the last may be empty).
+struct W4Walk {
+    int tile, left, log_rows, step, turns;
+    __device__ __forceinline__ void begin(int warp, int count)
+    {
+        static_assert(kW4Round == 4 && kW4Ahead == 2, "powers of two below");
+        log_rows = left >= 4 ? 2 : left >= 2 ? 1 : 0;
+        step = warp >> log_rows;
+        turns = ((count + (2 * kW4Warps >> log_rows) - 1) >> (kW4LogWarps + 1 - log_rows)) * kW4Ahead;
+    }
+    __device__ __forceinline__ void end_round(int warp, int count)
+    {
+        tile += 1 << log_rows;
+        left -= 1 << log_rows;
+        begin(warp, count);
+    }
+    __device__ __forceinline__ int row_warp(int warp) const { return warp & ((1 << log_rows) - 1); }
+    __device__ __forceinline__ int warps() const { return kW4Warps >> log_rows; }   // of a tile
+};
+
+// Bytes of shared memory: A's columns of the slice and (by group) their sums, the rings, the partial sums, and in clusters the
+// CTA's sums (two rounds').
+__host__ __device__ constexpr int64_t w4_smem(int groups, int64_t slice, bool cluster)
+{
+    return slice * 2 * (2048 + 32 * groups) + kW4Warps * (kW4Ahead * 2048 + 512) + (cluster ? 2 * kW4Round * 512 : 0);
+}
+
+// GW: words of eight codes that a lane has of a group (1, 2, 4: groups of 32, 64, 128).
+template <typename T, int GW>
+__global__ void __launch_bounds__(kW4Threads, 1) w4_kernel(const __grid_constant__ W4Params p)
+{
+    constexpr int GROUP = 32 * GW, GROUPS = 256 / GROUP;   // groups of a step
+    constexpr int OWN = (GROUPS + 3) / 4;                  // of a row's groups, those whose scale and zero a lane brings: t, t + 4
+    extern __shared__ uint4 act[];                         // [128 columns][word][lane]
     grid_dependency_wait();
     grid_dependents_launch();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    uint32_t ctas, rank = cluster_ctarank();
-    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
-    const int row_warp = warp % p.row_warps, k_warp = warp / p.row_warps, k_warps = kW4Warps / p.row_warps;
-    const int rows = 16 * p.row_warps;   // of W in this CTA
-    const int n0 = static_cast<int>(blockIdx.x / ctas) * rows, m0 = static_cast<int>(blockIdx.y) * TILES * 8;
+    const int ctas = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_ctarank());
+    const int cluster = static_cast<int>(blockIdx.x) / ctas, m0 = static_cast<int>(blockIdx.y) * kW4Rows;
     const int step0 = static_cast<int>(static_cast<int64_t>(p.steps) * rank / ctas);
-    const int step1 = static_cast<int>(static_cast<int64_t>(p.steps) * (rank + 1) / ctas);
-    const int chunk = kW4Ahead * k_warps;   // steps
-    const int groups = p.K / GROUP;
-    // ---- codes
-    int64_t row[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-        row[h] = min(n0 + 16 * row_warp + 8 * h + g, p.N - 1);   // (rows past the last are not written)
-    auto load = [&](int step, W4Step &x) {
-        const bool on = step < step1;
+    const int count = static_cast<int>(static_cast<int64_t>(p.steps) * (rank + 1) / ctas) - step0;
+    const int groups = p.K / GROUP, my_groups = groups - step0 * GROUPS;   // of a row, in all and from this slice on
+    float *const xsum = reinterpret_cast<float *>(act + p.slice * 256);                        // [group of the slice][row of A]
+    uint4 *const rings = reinterpret_cast<uint4 *>(xsum + p.slice * GROUPS * kW4Rows);
+    uint4 *const ring = rings + warp * (kW4Ahead * 128) + lane;                                // [slot][128 columns][row g, g + 8] of this lane
+    float4 *const red = reinterpret_cast<float4 *>(rings + kW4Warps * kW4Ahead * 128);         // [warp][lane]
+    float4 *const part = red + kW4Warps * 32;                                                  // [round mod 2][tile of W][lane]
+    W4Walk now;
+    now.tile = static_cast<int>(static_cast<int64_t>(p.tiles) * cluster / p.clusters);
+    now.left = static_cast<int>(static_cast<int64_t>(p.tiles) * (cluster + 1) / p.clusters) - now.tile;
+    now.begin(warp, count);
+    // ---- the codes of a turn into a slot of the ring, scales and zeros into registers (as they are: whatever used them
+    // here would wait for them)
+    struct Scales {
+        uint16_t s[2][OWN];
+        uint8_t z[2][OWN];
+    } scales[kW4Ahead];
+    W4Walk ahead = now;
+    const uint8_t *codes_at[2], *zeros_at[2];   // of this lane's rows, from the slice's first step on
+    const uint16_t *scales_at[2];
+    auto rows_of_round = [&]() {
+        const int row = (ahead.tile + ahead.row_warp(warp)) * 16 + g;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const uint8_t *src = p.codes + row[h] * (p.K / 2) + static_cast<int64_t>(step) * 64;
-            if constexpr (GW == 4) {
-                const uint4 v = on ? __ldg(reinterpret_cast<const uint4 *>(src + 16 * t)) : make_uint4(0, 0, 0, 0);
-                x.w[h][0] = v.x, x.w[h][1] = v.y, x.w[h][2] = v.z, x.w[h][3] = v.w;
-            } else {
-#pragma unroll
-                for (int i = 0; i < GROUPS; ++i) {
-                    const bool in = on && step * GROUPS + i < groups;
-                    if constexpr (GW == 2) {
-                        const uint2 v = in ? __ldg(reinterpret_cast<const uint2 *>(src + 32 * i + 8 * t)) : make_uint2(0, 0);
-                        x.w[h][2 * i] = v.x, x.w[h][2 * i + 1] = v.y;
-                    } else {
-                        x.w[h][i] = in ? __ldg(reinterpret_cast<const uint32_t *>(src + 16 * i + 4 * t)) : 0u;
-                    }
-                }
-            }
-            uint32_t sz = 8u << 16;   // past the last group: scale 0
-            if (on && t < GROUPS && step * GROUPS + t < groups) {
-                const int64_t at = row[h] * groups + step * GROUPS + t;
-                const uint32_t zero = p.zeros ? __ldg(p.zeros + at) & 15u : 8u;
-                sz = __ldg(static_cast<const uint16_t *>(p.scales) + at) | zero << 16;
-            }
-            x.sz[h] = sz;
+            const int64_t r = min(row + 8 * h, p.N - 1);   // (rows past the last are not written)
+            codes_at[h] = p.codes + r * (p.K / 2) + static_cast<int64_t>(step0) * 128 + 4 * GW * t;
+            const int64_t at = r * groups + static_cast<int64_t>(step0) * GROUPS + t;
+            scales_at[h] = static_cast<const uint16_t *>(p.scales) + at;
+            zeros_at[h] = p.zeros + at;
         }
     };
-    float acc[TILES][4] = {};
-    W4Step x[kW4Ahead];
-#pragma unroll
-    for (int u = 0; u < kW4Ahead; ++u)
-        load(step0 + u * k_warps + k_warp, x[u]);
-    for (int first = step0; first < step1; first += chunk) {
-        // ---- A's columns of this chunk
-        if (first > step0)
-            __syncthreads();
-        const int steps = min(chunk, step1 - first);
-        for (int i = threadIdx.x; i < TILES * 8 * steps * 16; i += kW4Threads) {
-            const int k8 = i % (steps * 16), m = i / (steps * 16), at = k8 % 16;
-            const int64_t k = static_cast<int64_t>(first) * 128 + 8 * k8;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (m0 + m < p.M && k < p.K)
-                v = __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(p.a) + (m0 + m) * p.lda + k));
-            // eight columns belong to one lane's word; the word's pairs are columns j and j + 4
-            const int lane_t = GW == 4 ? at / 4 : GW == 2 ? at / 2 % 4 : at % 4;
-            const int word = GW == 4 ? at % 4 : GW == 2 ? at / 8 * 2 + at % 2 : at / 4;
-            act[((k8 / 16 * 4 + word) * TILES + m / 8) * 32 + m % 8 * 4 + lane_t] =
-                make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
-                           __byte_perm(v.y, v.w, 0x7632));
+    rows_of_round();
+    const uint32_t ring_at = smem_u32(ring);
+    auto load = [&](int slot, Scales &x) {
+        if (ahead.turns == 0 && ahead.left > 0) {
+            ahead.end_round(warp, count);
+            if (ahead.left > 0)
+                rows_of_round();
         }
-        __syncthreads();
-        // ---- products
+        --ahead.turns;
+        const int step = ahead.step, have = my_groups - step * GROUPS;   // groups from this step on
+        ahead.step += ahead.warps();
+        if (ahead.left > 0 && step < count) {
 #pragma unroll
-        for (int u = 0; u < kW4Ahead; ++u) {
-            const int at = u * k_warps + k_warp;   // step of the chunk
-            if (at < steps) {
+            for (int h = 0; h < 2; ++h) {
 #pragma unroll
-                for (int i = 0; i < GROUPS; ++i) {
-                    const uint32_t sz0 = __shfl_sync(0xffffffffu, x[u].sz[0], (lane & ~3) | i);
-                    const uint32_t sz1 = __shfl_sync(0xffffffffu, x[u].sz[1], (lane & ~3) | i);
-                    const W4Codes<T> z0(sz0 >> 16), z1(sz1 >> 16);
-                    float sum[TILES][4] = {};
+                for (int i = 0; i < GROUPS; ++i)
+                    if (i < have)   // (past the last group what is there counts with columns of 0)
+                        copy_async<4 * GW>(ring_at + (slot * 128u + (i * GW / 4) * 64u + 32u * h) * 16u + 4u * (i * GW % 4),
+                                           codes_at[h] + step * 128 + 16 * GW * i);
 #pragma unroll
-                    for (int w = i * GW; w < (i + 1) * GW; ++w) {
-                        uint32_t a0[4], a1[4];
-                        z0.unpack(x[u].w[0][w], a0);
-                        z1.unpack(x[u].w[1][w], a1);
-#pragma unroll
-                        for (int n = 0; n < TILES; ++n) {
-                            const uint4 b = act[((at * 4 + w) * TILES + n) * 32 + lane];
-                            mma_16x8x16<T>(sum[n], a0[0], a1[0], a0[1], a1[1], b.x, b.y);
-                            mma_16x8x16<T>(sum[n], a0[2], a1[2], a0[3], a1[3], b.z, b.w);
-                        }
-                    }
-                    const float s0 = w4_scale<T>(sz0), s1 = w4_scale<T>(sz1);
-#pragma unroll
-                    for (int n = 0; n < TILES; ++n) {
-                        acc[n][0] = fmaf(sum[n][0], s0, acc[n][0]);
-                        acc[n][1] = fmaf(sum[n][1], s0, acc[n][1]);
-                        acc[n][2] = fmaf(sum[n][2], s1, acc[n][2]);
-                        acc[n][3] = fmaf(sum[n][3], s1, acc[n][3]);
+                for (int j = 0; j < OWN; ++j) {
+                    x.s[h][j] = 0;
+                    x.z[h][j] = 8;
+                    if (t + 4 * j < min(GROUPS, have)) {
+                        x.s[h][j] = __ldg(scales_at[h] + step * GROUPS + 4 * j);
+                        if (p.zeros)
+                            x.z[h][j] = __ldg(zeros_at[h] + step * GROUPS + 4 * j);
                     }
                 }
             }
-            load(first + chunk + at, x[u]);
         }
-    }
-    // ---- partial sums: [k warp][token][row of W], tokens 4 words further apart than a row is long
-    const int pitch = rows + 4;
-    float *part = reinterpret_cast<float *>(act);
-    __syncthreads();
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
 #pragma unroll
-    for (int n = 0; n < TILES; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            part[(k_warp * TILES * 8 + 8 * n + 2 * t + e % 2) * pitch + 16 * row_warp + g + e / 2 * 8] = acc[n][e];
-    __syncthreads();
-    if (k_warps > 1) {
-        for (int i = threadIdx.x; i < TILES * 8 * rows; i += kW4Threads) {
-            const int at = i / rows * pitch + i % rows;
-            float sum = part[at];
-            for (int w = 1; w < k_warps; ++w)
-                sum += part[w * TILES * 8 * pitch + at];
-            part[at] = sum;
+    for (int u = 0; u < kW4Ahead; ++u)
+        load(u, scales[u]);
+    // ---- A's columns and their sums, a warp 256 columns of a row at a time, four rows or pieces of one in flight (what stands
+    // in rows past the last stays in columns of the products that are not written)
+    const int rows = min(p.M - m0, kW4Rows);
+    bool finite = true;
+    int m = 0, piece = warp;   // (no division: it would cost as much as the rest)
+    auto settle = [&] {
+        while (piece >= count && m < rows) {
+            piece -= count;
+            ++m;
         }
-        __syncthreads();
-    }
-    if (ctas > 1)
-        cluster_sync();
-    // this CTA's share of the outputs: pairs of rows of W for one token
-    const int pairs = TILES * 8 * rows / 2, share = (pairs + static_cast<int>(ctas) - 1) / static_cast<int>(ctas);
-    const uint32_t base = smem_u32(part);
-    for (int i = static_cast<int>(rank) * share + static_cast<int>(threadIdx.x); i < min(pairs, (static_cast<int>(rank) + 1) * share);
-         i += kW4Threads) {
-        const int m = i / (rows / 2), r = i % (rows / 2) * 2;
-        if (m0 + m >= p.M || n0 + r >= p.N)
-            continue;
-        float2 y = make_float2(0.0f, 0.0f);
-        if (ctas == 1) {   // (shared::cluster addresses only come from mapa, in a cluster)
-            y = *reinterpret_cast<const float2 *>(part + m * pitch + r);
-        } else {
-            for (uint32_t c = 0; c < ctas; ++c) {
-                const float2 v = ld_shared_cluster_f2(mapa_shared(base + static_cast<uint32_t>(m * pitch + r) * 4u, c));
-                y.x += v.x;
-                y.y += v.y;
+    };
+    settle();
+    while (m < rows) {
+        uint4 v[4];
+        int at_m[4], at_piece[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            at_m[u] = m;
+            at_piece[u] = piece;
+            const int64_t k = (static_cast<int64_t>(step0) + piece) * 256 + 8 * lane;
+            v[u] = make_uint4(0, 0, 0, 0);
+            if (m < rows && k < p.K)
+                v[u] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(p.a) + (m0 + m) * p.lda + k));
+            piece += kW4Warps;
+            settle();
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int k8 = at_piece[u] * 32 + lane, at = lane % 16;
+            float sum = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 x = unpack2<T>(e == 0 ? v[u].x : e == 1 ? v[u].y : e == 2 ? v[u].z : v[u].w);
+                sum += x.x + x.y;
+            }
+#pragma unroll
+            for (int o = GROUP / 16; o > 0; o /= 2)
+                sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            finite = finite && fabsf(sum) < INFINITY;
+            if (at_m[u] < rows) {
+                const int row = at_m[u];
+                // eight columns belong to one lane's word; the word's pairs are columns j and j + 4
+                const int lane_t = GW == 4 ? at / 4 : GW == 2 ? at / 2 % 4 : at % 4;
+                const int word = GW == 4 ? at % 4 : GW == 2 ? at / 8 * 2 + at % 2 : at / 4;
+                act[(k8 / 16 * 4 + word) * 32 + row * 4 + lane_t] =
+                    make_uint4(__byte_perm(v[u].x, v[u].z, 0x5410), __byte_perm(v[u].x, v[u].z, 0x7632),
+                               __byte_perm(v[u].y, v[u].w, 0x5410), __byte_perm(v[u].y, v[u].w, 0x7632));
+                if (k8 % (GROUP / 8) == 0)
+                    xsum[k8 / (GROUP / 8) * kW4Rows + row] = sum;
             }
         }
+    }
+    finite = __syncthreads_and(finite);
+    // ---- bias, activation and one rounding of a tile of sums (rows g and g + 8 of the tile, rows 2 t and 2 t + 1 of A)
+    auto finish = [&](float4 y, int tile) {
+        const int row = tile * 16 + g;
         if (p.bias) {
-            const float2 b = unpack2<T>(__ldg(reinterpret_cast<const uint32_t *>(static_cast<const T *>(p.bias) + n0 + r)));
-            y.x += b.x;
-            y.y += b.y;
+            const T *bias = static_cast<const T *>(p.bias);
+            const float b0 = row < p.N ? static_cast<float>(bias[row]) : 0.0f, b1 = row + 8 < p.N ? static_cast<float>(bias[row + 8]) : 0.0f;
+            y = make_float4(y.x + b0, y.y + b0, y.z + b1, y.w + b1);
         }
         w4_activate(p.epilogue, y.x, y.y);
-        *reinterpret_cast<uint32_t *>(static_cast<T *>(p.c) + (m0 + m) * p.ldc + n0 + r) = pack2<T>(y.x, y.y);
+        w4_activate(p.epilogue, y.z, y.w);
+        // lanes of even g take token 2 t of rows g and g + 1, those of odd g token 2 t + 1: two rows to a store
+        const bool odd = g & 1;
+        const float a = __shfl_xor_sync(0xffffffffu, odd ? y.x : y.y, 4), b = __shfl_xor_sync(0xffffffffu, odd ? y.z : y.w, 4);
+        const uint32_t lo = odd ? pack2<T>(a, y.y) : pack2<T>(y.x, a), hi = odd ? pack2<T>(b, y.w) : pack2<T>(y.z, b);
+        const int m = m0 + 2 * t + odd, first = row & ~1;
+        if (m < p.M) {
+            T *dst = static_cast<T *>(p.c) + m * p.ldc + first;
+            if (first < p.N)
+                *reinterpret_cast<uint32_t *>(dst) = lo;
+            if (first + 8 < p.N)
+                *reinterpret_cast<uint32_t *>(dst + 8) = hi;
+        }
+    };
+    for (int buf = 0; now.left > 0; now.end_round(warp, count), buf ^= 1) {
+        const int row_warp = now.row_warp(warp), k_warp = warp >> now.log_rows, k_warps = now.warps();
+        float acc[4] = {};
+        // codes of the turn's step (in slot `slot`) times A's columns
+        auto products = [&](int slot, int step, const Scales &mine, auto all_finite) {
+            constexpr bool FINITE = decltype(all_finite)::value;
+            const uint4 *b = act + step * 256 + lane;
+            const float *xs = xsum + step * (GROUPS * kW4Rows) + 2 * t;
+            // s (UNIT sum + ODD_UNIT odd - (BASE + z) xsum), the unit with the scale
+            constexpr float PER_ODD = W4Codes<T>::ODD_UNIT / W4Codes<T>::UNIT;
+            float s[2][OWN], z[2][OWN];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int j = 0; j < OWN; ++j) {
+                    const float zero = static_cast<float>(mine.z[h][j] & 15);
+                    s[h][j] = unpack2<T>(mine.s[h][j]).x * (FINITE ? W4Codes<T>::UNIT : 1.0f);
+                    z[h][j] = FINITE ? (W4Codes<T>::BASE + zero) * (-1.0f / W4Codes<T>::UNIT) : zero;
+                }
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const uint4 w0 = ring[slot * 128 + half * 64], w1 = ring[slot * 128 + half * 64 + 32];
+                const uint32_t codes[2][4] = {{w0.x, w0.y, w0.z, w0.w}, {w1.x, w1.y, w1.z, w1.w}};
+#pragma unroll
+                for (int i = half * (GROUPS / 2); i < (half + 1) * (GROUPS / 2); ++i) {
+                    float sum[4] = {}, odd[4] = {};
+                    const int from = (lane & ~3) | (i & 3);
+                    const float s0 = __shfl_sync(0xffffffffu, s[0][i / 4], from), s1 = __shfl_sync(0xffffffffu, s[1][i / 4], from);
+                    const float z0 = __shfl_sync(0xffffffffu, z[0][i / 4], from), z1 = __shfl_sync(0xffffffffu, z[1][i / 4], from);
+#pragma unroll
+                    for (int w = i * GW; w < (i + 1) * GW; ++w) {   // of the step's eight words
+                        uint32_t a0[4], a1[4];
+                        if constexpr (FINITE) {
+                            W4Codes<T>::unpack(codes[0][w % 4], a0);
+                            W4Codes<T>::unpack(codes[1][w % 4], a1);
+                        } else {
+                            w4_unpack_minus_zero<T>(codes[0][w % 4], static_cast<uint32_t>(z0), a0);
+                            w4_unpack_minus_zero<T>(codes[1][w % 4], static_cast<uint32_t>(z1), a1);
+                        }
+                        const uint4 x = b[w * 32];
+                        mma_16x8x16<T>(sum, a0[0], a1[0], a0[2], a1[2], x.x, x.z);
+                        mma_16x8x16<T>(odd, a0[1], a1[1], a0[3], a1[3], x.y, x.w);
+                    }
+                    if constexpr (FINITE) {
+                        const float2 x = *reinterpret_cast<const float2 *>(xs + i * kW4Rows);
+                        acc[0] = fmaf(fmaf(z0, x.x, fmaf(odd[0], PER_ODD, sum[0])), s0, acc[0]);
+                        acc[1] = fmaf(fmaf(z0, x.y, fmaf(odd[1], PER_ODD, sum[1])), s0, acc[1]);
+                        acc[2] = fmaf(fmaf(z1, x.x, fmaf(odd[2], PER_ODD, sum[2])), s1, acc[2]);
+                        acc[3] = fmaf(fmaf(z1, x.y, fmaf(odd[3], PER_ODD, sum[3])), s1, acc[3]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            acc[e] = fmaf(sum[e] + odd[e], e < 2 ? s0 : s1, acc[e]);
+                    }
+                }
+            }
+        };
+        for (int turn = 0; turn < now.turns; turn += kW4Ahead) {
+#pragma unroll
+            for (int u = 0; u < kW4Ahead; ++u) {
+                asm volatile("cp.async.wait_group %0;" ::"n"(kW4Ahead - 1) : "memory");   // (a lane reads only what it has copied)
+                const int step = now.step + (turn + u) * k_warps;
+                if (step < count) {
+                    if (finite)
+                        products(u, step, scales[u], std::true_type{});
+                    else
+                        products(u, step, scales[u], std::false_type{});
+                }
+                load(u, scales[u]);
+            }
+        }
+        // ---- the round's sums: the warps of a tile, then the CTAs, in order
+        if (k_warp > 0)
+            red[warp * 32 + lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        __syncthreads();
+        if (k_warp == 0) {
+            float4 y = make_float4(acc[0], acc[1], acc[2], acc[3]);
+            for (int k = 1; k < k_warps; ++k) {
+                const float4 v = red[(warp + (k << now.log_rows)) * 32 + lane];
+                y = make_float4(y.x + v.x, y.y + v.y, y.z + v.z, y.w + v.w);
+            }
+            if (ctas == 1)
+                finish(y, now.tile + row_warp);
+            else
+                part[(buf * kW4Round + row_warp) * 32 + lane] = y;
+        }
+        __syncthreads();   // red may be written again
+        if (ctas > 1) {
+            cluster_sync();   // (and the CTAs' sums of the round before have been read: those two rounds on go over them)
+            const int f = warp * ctas + rank;   // one tile at most: the round has no more than kW4Round
+            if (f < 1 << now.log_rows) {
+                float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                for (int c = 0; c < ctas; ++c) {
+                    const float4 v =
+                        ld_shared_cluster_f4(mapa_shared(smem_u32(part + (buf * kW4Round + f) * 32 + lane), static_cast<uint32_t>(c)));
+                    y = make_float4(y.x + v.x, y.y + v.y, y.z + v.z, y.w + v.w);
+                }
+                finish(y, now.tile + f);
+            }
+            __syncthreads();
+        }
     }
-    __syncthreads();
     if (ctas > 1)
         cluster_sync();   // the other CTAs have read this one's sums
 }

@@ -35,6 +35,8 @@ _i64, _i32, _vp, _f32 = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.
 
 GEMM_TREE_MAX_WORDS = 64
 
+_int32, _float32, _uint8 = torch.int32, torch.float32, torch.uint8
+
 
 class Tree(ctypes.Structure):
     """``gemm_tree``"""
@@ -82,18 +84,20 @@ def _declare(L):
 
 def _seqs(kv_lens, page_table, device):
     """``gemm_kv_seqs`` and the number of sequences."""
-    n = kv_lens.shape[0] if kv_lens.dim() else -1
-    lens, table = _s._ints(kv_lens, "kv_lens", (n,), device), _s._ints(page_table, "page_table", (n, None), device)
+    s = kv_lens.shape
+    n = s[0] if s else -1
+    lens, table = _s._vector(kv_lens, "kv_lens", n, device), _s._ints(page_table, "page_table", (n, None), device)
     width = page_table.shape[1]
-    return _SEQS.pack(n, lens, table, width, page_table.stride(0) if n > 1 else width), n
+    return _SEQS.pack(n, lens, table, width, page_table.stride()[0] if n > 1 else width), n
 
 
 def _weights(w, device, shape=None):
     """``gemm_kv_weights``"""
-    if w.dtype != torch.float32 or w.device != device or w.dim() != 3 or (shape is not None and w.shape != shape):
+    s = w.shape
+    if w.dtype is not _float32 or w.device != device or len(s) != 3 or (shape is not None and s != shape):
         raise ValueError(f"weights: a float32 tensor [pages, kv_heads, page_size]{'' if shape is None else f' = {tuple(shape)}'} on "
                          f"{device} expected")
-    n, h, p = w.shape
+    n, h, p = s
     sn, sh, sp = w.stride()
     if sp != 1 and p > 1:
         raise ValueError("weights: the rows of a page must be contiguous")
@@ -101,22 +105,23 @@ def _weights(w, device, shape=None):
 
 
 def _mask(mask, tokens, device):
-    """``gemm_tree``"""
-    if mask.dtype not in (torch.int32, torch.uint32) or mask.device != device or mask.dim() != 2 or mask.shape[0] != tokens or (
-            mask.shape[1] > 1 and mask.stride(1) != 1):
+    """Address, words and stride of a mask."""
+    s = mask.shape
+    if (mask.dtype is not _int32 and mask.dtype is not torch.uint32) or len(s) != 2 or s[0] != tokens or mask.device != device or (
+            s[1] > 1 and mask.stride()[1] != 1):
         raise ValueError(f"mask: an int32 tensor [{tokens}, words] on {device}, words contiguous, expected")
-    words = mask.shape[1]
-    return _TREE.pack(mask.data_ptr(), words, mask.stride(0) if tokens > 1 else words)
+    return mask.data_ptr(), s[1], mask.stride()[0] if tokens > 1 else s[1]
 
 
 def _lists(index, n, heads, device):
     """Address, strides and length of index lists [seqs, most] or [seqs, kv_heads, most]."""
-    if index.dtype != torch.int32 or index.device != device or index.dim() not in (2, 3) or index.shape[0] != n or (
-            index.dim() == 3 and index.shape[1] != heads) or (index.shape[-1] > 1 and index.stride(-1) != 1):
+    s, strides = index.shape, index.stride()
+    dims = len(s)
+    if index.dtype is not _int32 or index.device != device or (dims != 2 and dims != 3) or s[0] != n or (
+            dims == 3 and s[1] != heads) or (s[-1] > 1 and strides[-1] != 1):
         raise ValueError(f"index: an int32 tensor [{n}, most] or [{n}, {heads}, most] on {device}, the last dimension contiguous, expected")
-    most = index.shape[-1]
-    per_head = index.dim() == 3 and heads > 1
-    return index.data_ptr(), index.stride(0) if n > 1 else most * heads, index.stride(1) if per_head else 0 if index.dim() == 2 else most, most
+    most = s[-1]
+    return index.data_ptr(), strides[0] if n > 1 else most * heads, 0 if dims == 2 else strides[1] if heads > 1 else most, most
 
 
 # --------------------------------------------------------------------------------- the calls
@@ -126,22 +131,22 @@ def tree_mask(ctx, parents, q_start, kv_lens, max_nodes, prefix_len=0, mask=None
     the nodes that it sees (int32 [tokens, words], room for ``max_nodes`` nodes of a sequence) and
     its position (int32). ``kv_lens`` counts the new tokens, ``prefix_len`` the keys of a shared
     prefix before the sequence's own."""
-    device = parents.device
-    if parents.dim() != 1:
+    device, s = parents.device, parents.shape
+    if len(s) != 1:
         raise ValueError("parents: one int32 per token expected")
-    tokens = parents.shape[0]
+    tokens = s[0]
     if mask is None:
         if not 0 <= max_nodes <= 32 * GEMM_TREE_MAX_WORDS:
             raise ValueError(f"max_nodes: up to {32 * GEMM_TREE_MAX_WORDS} expected, got {max_nodes}")
-        mask = _s._empty((tokens, max(1, -(-max_nodes // 32))), torch.int32, device, stream)
+        mask = _s._empty((tokens, (max_nodes + 31) // 32 or 1), _int32, device, stream)
     if positions is None:
-        positions = _s._empty((tokens,), torch.int32, device, stream)
-    words, row = mask.shape[-1], _mask(mask, tokens, device)
-    n = kv_lens.shape[0] if kv_lens.dim() else -1
-    b = _s._BATCH.pack(n, tokens, 0, _s._ints(q_start, "q_start", (n + 1,), device), _s._ints(kv_lens, "kv_lens", (n,), device), 0, 0, 0, 0, 0)
-    p = _s._ints(parents, "parents", (tokens,), device)
-    _g._check(_s._lib().gemm_tree_mask(_g._h(ctx), b, prefix_len, p, mask.data_ptr(), words, _TREE.unpack(row)[2],
-                                       _s._ints(positions, "positions", (tokens,), device), _s._on(stream, device)), "gemm_tree_mask")
+        positions = _s._empty((tokens,), _int32, device, stream)
+    at, words, stride = _mask(mask, tokens, device)
+    vector, s = _s._vector, kv_lens.shape
+    n = s[0] if s else -1
+    b = _s._BATCH.pack(n, tokens, 0, vector(q_start, "q_start", n + 1, device), vector(kv_lens, "kv_lens", n, device), 0, 0, 0, 0, 0)
+    _g._check(_s._lib().gemm_tree_mask(_g._h(ctx), b, prefix_len, vector(parents, "parents", tokens, device), at, words, stride,
+                                       vector(positions, "positions", tokens, device), _s._on(stream, device)), "gemm_tree_mask")
     return mask, positions
 
 
@@ -160,7 +165,7 @@ def tree_attention(ctx, q, k_cache, v_cache, q_start, kv_lens, page_table, mask,
     if q_dim != d:
         raise ValueError(f"q: head_dim {d} expected, got {q_dim}")
     b = _s._batch(tokens, q_start, kv_lens, page_table, device, max_q, prefix_pages)
-    tree = _mask(mask, tokens, device)
+    tree = _TREE.pack(*_mask(mask, tokens, device))
     lse_ptr, lse_stride = _s._lse(lse, shape, device)
     if workspace is not None and (workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != device):
         raise ValueError(f"workspace: a contiguous uint8 tensor on {device} expected")
@@ -192,15 +197,13 @@ def kv_weigh(ctx, q, k_cache, q_start, kv_lens, page_table, lse, weights, scale=
     before are multiplied by ``decay``, those of the new tokens' keys start from 0. ``lse`` is what
     ``paged_attention`` filled for these queries. Returns ``weights``."""
     dtype, device = k_cache.dtype, k_cache.device
-    if k_cache.dim() != 4:
-        raise ValueError("k_cache: [pages, kv_heads, page_size, head_dim] expected")
     c, page, heads, d = _s._cache(k_cache, k_cache)
-    hq = _s._heads(q, "q", dtype, device)
-    if q.shape[2] != d:
-        raise ValueError(f"q: head_dim {d} expected, got {q.shape[2]}")
-    b = _s._batch(q.shape[0], q_start, kv_lens, page_table, device)
+    hq, s = _s._heads(q, "q", dtype, device), q.shape
+    if s[2] != d:
+        raise ValueError(f"q: head_dim {d} expected, got {s[2]}")
+    b = _s._batch(s[0], q_start, kv_lens, page_table, device)
     w = _weights(weights, device, (k_cache.shape[0], heads, page))
-    lse_ptr, lse_stride = _s._lse(lse, q.shape, device)
+    lse_ptr, lse_stride = _s._lse(lse, s, device)
     if scale is None:
         scale = 1.0 / math.sqrt(d) if d else 1.0
     _g._check(_s._lib().gemm_kv_weigh(_g._h(ctx), c, b, hq, scale, lse_ptr, lse_stride, window, decay, w, _s._on(stream, device)),
@@ -220,14 +223,14 @@ def kv_select(ctx, weights, kv_lens, page_table, keep, first=0, recent=0, index=
     if index is None:
         if keep < 0:
             raise ValueError(f"keep: at least 0 expected, got {keep}")
-        index = _s._empty((n, heads, keep), torch.int32, device, stream)
+        index = _s._empty((n, heads, keep), _int32, device, stream)
     elif index.shape != (n, heads, keep):
         raise ValueError(f"index: shape {(n, heads, keep)} expected, got {tuple(index.shape)}")
     if counts is None:
-        counts = _s._empty((n,), torch.int32, device, stream)
+        counts = _s._empty((n,), _int32, device, stream)
     at, seq_stride, head_stride, _ = _lists(index, n, heads, device)
     _g._check(_s._lib().gemm_kv_select(_g._h(ctx), s, pages, page, heads, w, keep, first, recent, at, seq_stride, head_stride,
-                                       _s._ints(counts, "counts", (n,), device), _s._on(stream, device)), "gemm_kv_select")
+                                       _s._vector(counts, "counts", n, device), _s._on(stream, device)), "gemm_kv_select")
     return index, counts
 
 
@@ -243,10 +246,11 @@ def kv_compact(ctx, k_cache, v_cache, kv_lens, page_table, index, counts, start=
     at, seq_stride, head_stride, most = _lists(index, n, heads, device)
     w = None if weights is None else _weights(weights, device, (k_cache.shape[0], heads, page))
     if new_lens is None:
-        new_lens = _s._empty((n,), torch.int32, device, stream)
+        new_lens = _s._empty((n,), _int32, device, stream)
+    vector = _s._vector
     _g._check(_s._lib().gemm_kv_compact(_g._h(ctx), c, s, w, at, seq_stride, head_stride, most,
-                                        None if start is None else _s._ints(start, "start", (n,), device),
-                                        _s._ints(counts, "counts", (n,), device), _s._ints(new_lens, "new_lens", (n,), device),
+                                        None if start is None else vector(start, "start", n, device),
+                                        vector(counts, "counts", n, device), vector(new_lens, "new_lens", n, device),
                                         _s._on(stream, device)), "gemm_kv_compact")
     return new_lens
 
@@ -257,27 +261,35 @@ def w4_gemm(ctx, a, codes, scales, zeros=None, bias=None, epilogue=0, out=None, 
     group] of ``a``'s type, ``zeros`` uint8 [N, K / group] or None (8): W = (code - zero) * scale, groups
     of 32, 64 or 128 columns. Returns ``out`` (allocated when not given)."""
     dtype, device = a.dtype, a.device
-    if a.dim() != 2 or codes.dim() != 2 or scales.dim() != 2:
+    size, wide = a.shape, scales.shape
+    if len(size) != 2 or len(wide) != 2:
         raise ValueError("a [rows, K], codes [N, K / 2] and scales [N, K / group] expected")
-    m, k = a.shape
-    n, groups = scales.shape
-    if codes.dtype != torch.uint8 or codes.shape != (n, k // 2) or codes.device != device or not codes.is_contiguous():
+    (m, k), (n, groups) = size, wide
+    if codes.dtype is not _uint8 or codes.shape != (n, k // 2) or codes.device != device or not codes.is_contiguous():
         raise ValueError(f"codes: a contiguous uint8 tensor of shape {(n, k // 2)} on {device} expected")
-    if scales.dtype != dtype or scales.device != device or not scales.is_contiguous():
+    if scales.dtype is not dtype or scales.device != device or not scales.is_contiguous():
         raise ValueError(f"scales: a contiguous tensor of {dtype} on {device} expected")
-    if zeros is not None and (zeros.dtype != torch.uint8 or zeros.shape != (n, groups) or zeros.device != device or not zeros.is_contiguous()):
+    if zeros is None:
+        zeros_ptr = 0
+    elif zeros.dtype is not _uint8 or zeros.shape != wide or zeros.device != device or not zeros.is_contiguous():
         raise ValueError(f"zeros: a contiguous uint8 tensor of shape {(n, groups)} on {device} expected")
+    else:
+        zeros_ptr = zeros.data_ptr()
     if k and (not groups or k % groups):
         raise ValueError(f"scales: one for each group of the {k} columns expected, got {groups} a row")
+    lda, ca = a.stride()
+    if ca != 1 and k > 1:
+        raise ValueError("a: the values of a row must be contiguous")
     if out is None:
-        out = _s._empty((m, n), dtype, device, stream)
-    for t, what, cols in ((a, "a", k), (out, "out", n)):
-        if t.dtype != dtype or t.device != device or t.shape != (m, cols) or (cols > 1 and t.stride(1) != 1):
-            raise ValueError(f"{what}: {m} rows of {cols} contiguous values of {dtype} on {device} expected")
-    if bias is not None and (bias.dtype != dtype or bias.shape != (n,) or bias.device != device or not bias.is_contiguous()):
+        out, ldc = _s._empty((m, n), dtype, device, stream), n
+    elif out.dtype is not dtype or out.shape != (m, n) or out.device != device or (n > 1 and out.stride()[1] != 1):
+        raise ValueError(f"out: {m} rows of {n} contiguous values of {dtype} on {device} expected")
+    else:
+        ldc = out.stride()[0]
+    if bias is not None and (bias.dtype is not dtype or bias.shape != (n,) or bias.device != device or not bias.is_contiguous()):
         raise ValueError(f"bias: {n} contiguous values of {dtype} on {device} expected")
-    w = _W4.pack(codes.data_ptr(), scales.data_ptr(), 0 if zeros is None else zeros.data_ptr(), k // groups if groups else 128)
-    _g._check(_s._lib().gemm_w4_run(_g._h(ctx), _s._dtype_code(dtype), m, n, k, a.data_ptr(), a.stride(0) if m > 1 else k, w,
-                                    None if bias is None else bias.data_ptr(), out.data_ptr(), out.stride(0) if m > 1 else n, int(epilogue),
+    w = _W4.pack(codes.data_ptr(), scales.data_ptr(), zeros_ptr, k // groups if groups else 128)
+    _g._check(_s._lib().gemm_w4_run(_g._h(ctx), _s._dtype_code(dtype), m, n, k, a.data_ptr(), lda if m > 1 else k, w,
+                                    None if bias is None else bias.data_ptr(), out.data_ptr(), ldc if m > 1 else n, epilogue,
                                     _s._on(stream, device)), "gemm_w4_run")
     return out

@@ -108,13 +108,25 @@ def _heads(t, what, dtype, device, shape=None):
     return _HEADS.pack(t.data_ptr(), h, st if n > 1 else h * d, sh if h > 1 else d)
 
 
+_int32 = torch.int32   # (a global: half of an attribute of torch to look up)
+
+
 def _ints(t, what, shape, device):
     """The address of an int32 tensor of ``shape`` (entries None: any), its last dimension contiguous."""
     s = t.shape
-    if t.dtype != torch.int32 or t.device != device or len(s) != len(shape) or s[0] != shape[0] and shape[0] is not None:
+    if t.dtype is not _int32 or t.device != device or len(s) != len(shape) or s[0] != shape[0] and shape[0] is not None:
         raise ValueError(f"{what}: an int32 tensor of shape {shape} on {device} expected")
-    if s[-1] > 1 and t.stride(-1) != 1:
+    if s[-1] > 1 and t.stride()[-1] != 1:
         raise ValueError(f"{what}: the last dimension must be contiguous")
+    return t.data_ptr()
+
+
+def _vector(t, what, n, device):
+    """The address of a contiguous int32 vector of ``n`` entries."""
+    if t.dtype is not _int32 or t.shape != (n,) or t.device != device:
+        raise ValueError(f"{what}: an int32 tensor of shape {(n,)} on {device} expected")
+    if n > 1 and t.stride() != (1,):
+        raise ValueError(f"{what}: the entries must be contiguous")
     return t.data_ptr()
 
 
@@ -135,9 +147,10 @@ def _cache(k_cache, v_cache):
 
 
 def _batch(tokens, q_start, kv_lens, page_table, device, max_q=None, prefix_pages=None, num_prefix_pages=0):
-    n = kv_lens.shape[0] if kv_lens.dim() else -1
-    ps = _ints(q_start, "q_start", (n + 1,), device)
-    pk = _ints(kv_lens, "kv_lens", (n,), device)
+    s = kv_lens.shape
+    n = s[0] if s else -1
+    ps = _vector(q_start, "q_start", n + 1, device)
+    pk = _vector(kv_lens, "kv_lens", n, device)
     pt = _ints(page_table, "page_table", (n, None), device)
     pre = 0
     if prefix_pages is not None:
@@ -191,11 +204,14 @@ def _on(stream, device):
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
+_torch_empty = torch.empty
+
+
 def _empty(shape, dtype, device, stream):
     """A tensor for a kernel on ``stream`` (None: the current one) to write. The memory comes from what is free
     on that stream: a block that is free on the current one may still be in use by work queued there."""
     if stream is None or device.type != "cuda":   # (the library refuses host memory)
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _torch_empty(shape, dtype=dtype, device=device)
     handle = _on(stream, device)
     if handle == _current(device):
         return torch.empty(shape, dtype=dtype, device=device)
