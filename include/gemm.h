@@ -73,8 +73,8 @@ enum gemm_status {
     GEMM_ERR_TIMEOUT = -5, /* a bounded in-kernel wait ran out; the kernel returned
                               early and C is incomplete (see gemm_last_device_error) */
     GEMM_ERR_NOMEM = -6,   /* host or device allocation failed (create, run_host)     */
-    GEMM_ERR_INDEX = -7    /* a length or page number that a call of gemm_serving.h read
-                              from device memory was out of range (reported by
+    GEMM_ERR_INDEX = -7    /* a length, index or page number that a call of gemm_serving.h or
+                              gemm_decode.h read from device memory was out of range (reported by
                               gemm_last_device_error; no access was made with it)     */
 };
 

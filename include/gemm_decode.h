@@ -51,7 +51,8 @@ typedef struct gemm_tree {
  * among its sequence's new tokens, of the node before it, which is lower than its own, or -1 for
  * a node that follows the sequence's last key before the new ones. A node sees itself and the
  * nodes on its way up; its position (positions[t], int32; NULL: not wanted) is
- * prefix_len + kv_lens[s] - n + the number of nodes above it. A parent out of range counts as -1
+ * prefix_len + kv_lens[s] - n + the number of nodes above it (with fewer own keys than new tokens
+ * prefix_len + that number, and GEMM_ERR_INDEX). A parent out of range counts as -1
  * (GEMM_ERR_INDEX); a node past the 32 * mask_words-th (GEMM_ERR_INDEX) gets no bits and the position
  * of a node without a parent. Of the batch, q_start, kv_lens and the counts are read. Rows of tokens
  * that belong to no sequence are not written. One kernel launch. */
@@ -88,7 +89,8 @@ typedef struct gemm_kv_weights {
 
 /* Adds the attention weight that the batch's new tokens give to each of their sequence's own keys:
  *   w[j][h'] = decay * w[j][h'] + sum over tokens t, query heads h of h' of exp(scale * q[t][h] . K[j][h'] - lse[t][h])
- * over the last `window` new tokens (0: all) that see key j (the order of gemm_serving.h). lse is
+ * over the last `window` new tokens (0: all) that see key j (the order of gemm_serving.h); a sequence
+ * without new tokens keeps its weights. lse is
  * what gemm_paged_attention left for the same q and scale. The rows of the new tokens' own keys start
  * from 0, whatever they held; with decay 0 all do. FP32 scores and sums, in a fixed order (the same
  * bits each time). A token whose lse is -inf gives nothing. decay from 0 to 1. cache->v is not
@@ -139,8 +141,9 @@ typedef struct gemm_w4 {
  * for few rows, which its time is the reading of W for. Any M up to 2^18 (0: nothing to do); it is
  * made for M up to 64. N a multiple of 8, K of the group, both up to 2^24 (K = 0: act(bias)). A and C have rows of lda and
  * ldc elements (multiples of 8, at least K and N), all pointers 16-byte aligned (scales 2, zeros 1). dtype: type of A, scales,
- * bias and C. Codes minus zeros enter the tensor cores exactly; each group is summed in FP32 before its scale
- * is applied, and the result is rounded once. C may not overlap any other operand. One kernel launch. */
+ * bias and C. No weight is rounded: codes enter the products exactly, each group is summed in FP32 before its scale is
+ * applied, and the result is rounded once. (Up to eight rows, code A and zero A are summed apart, so that FP32's errors are
+ * relative to 15 scale |A| - BF16: 143 - not to |W| |A|.) C may not overlap any other operand. One kernel launch. */
 int gemm_w4_run(gemm_ctx *ctx, int dtype, int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, const gemm_w4 *w,
                 const void *bias, void *C, int64_t ldc, int epilogue, void *stream);
 

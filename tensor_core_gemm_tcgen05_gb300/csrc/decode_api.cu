@@ -526,6 +526,7 @@ int gemm_w4_run(gemm_ctx *ctx, int dtype, int64_t M, int64_t N, int64_t K, const
     p.steps = static_cast<int>((K + 255) / 256);
     p.err = ctx->d_err;
     p.timeout_ns = ctx->timeout_ns;
+    p.debug = ctx->debug & GEMM_DEBUG_WITHHOLD_FIRST_LOAD;
     // w4_kernel: A's columns have to fit the shared memory of a cluster.
     const int groups_128 = static_cast<int>(128 / w->group);
     int cluster = 1;
@@ -542,12 +543,12 @@ int gemm_w4_run(gemm_ctx *ctx, int dtype, int64_t M, int64_t N, int64_t K, const
         cluster = 1;
         while (cluster < 8 && tiles * blocks_m <= ctx->w4_clusters[cluster * 2] && p.steps >= 4 * cluster)
             cluster *= 2;
+        DeviceGuard guard(ctx->device);
         CUtensorMap codes, a;
         if (!encode_2d(ctx, &codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w->codes, K / 2, N, K / 2, 64, 128, CU_TENSOR_MAP_SWIZZLE_64B) ||
             !encode_2d(ctx, &a, dtype == GEMM_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, A, K, M, lda, 64,
                        static_cast<uint32_t>(tokens), CU_TENSOR_MAP_SWIZZLE_128B))
             return GEMM_ERR_LAUNCH;
-        DeviceGuard guard(ctx->device);
         return launched(ctx, with_w4_umma(dtype, tokens, w->group, [&](auto cfg) {
                             using Cfg = decltype(cfg);
                             return launch_cluster(gb300::w4_umma_kernel<Cfg>,

@@ -121,9 +121,9 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kWeighThreads, 2) kv_weigh_kernel(const __grid_constant__ WeighParams p)
 {
     constexpr int C = D / 32;   // 16-byte pieces of a key row per lane
-    __shared__ uint4 queries[kWeighRows * D / 8];   // [tile of 8 rows][piece][lane]
-    __shared__ float minus_lse[kWeighRows];         // in base 2
-    __shared__ int last_key[kWeighRows];            // that the row sees; -1: the row gives nothing
+    __shared__ uint4 queries[2][kWeighRows * D / 8];   // of two runs of rows: [tile of 8 rows][piece][lane]
+    __shared__ float minus_lse[2][kWeighRows];         // in base 2
+    __shared__ int last_key[2][kWeighRows];            // that the row sees; -1: the row gives nothing
     __shared__ int64_t ahead[kWeighThreads];        // blocks up to and with each sequence of the chunk
     __shared__ int64_t warp_sum[kWeighThreads / 32];
     grid_dependency_wait();
@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(kWeighThreads, 2) kv_weigh_kernel(const __grid
             const SeqView v = load_seq(p.batch, s0 + threadIdx.x);
             if (v.bad)
                 report_index(p.err);
-            if (v.n > 0 || p.decay != 1.0f)
+            if (v.n > 0)   // (without new tokens: as it is)
                 blocks = static_cast<int64_t>((v.kv + kWeighKeys - 1) / kWeighKeys) * p.kv_heads;
         }
 #pragma unroll
@@ -225,12 +225,10 @@ __global__ void __launch_bounds__(kWeighThreads, 2) kv_weigh_kernel(const __grid
                     last = l == -INFINITY ? -1 : v.kv - v.n + i;
                 }
             };
-            auto query = [&](int r, int piece) -> uint4 {   // 8 dims of row r
-                if (r >= rows)
-                    return make_uint4(0, 0, 0, 0);
+            auto query_at = [&](int r, int piece) {   // 8 dims of row r
                 const int token = divide(r, p.group, p.group_magic);
-                return __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(p.q) + static_cast<int64_t>(v.q0 + v.n - tokens + token) * p.q_token +
-                                                             (head * p.group + r - token * p.group) * p.q_head + 8 * piece));
+                return reinterpret_cast<const uint4 *>(static_cast<const T *>(p.q) + static_cast<int64_t>(v.q0 + v.n - tokens + token) * p.q_token +
+                                                       (head * p.group + r - token * p.group) * p.q_head + 8 * piece);
             };
             float sum[2][2] = {};
             // weight of eight rows: the pieces of their queries, and of rows 2 t, 2 t + 1 the other two
@@ -264,33 +262,48 @@ __global__ void __launch_bounds__(kWeighThreads, 2) kv_weigh_kernel(const __grid
                 int2 last;
 #pragma unroll
                 for (int c = 0; c < C; ++c)
-                    q[c] = query(g, 4 * c + t);
+                    q[c] = g < rows ? __ldg(query_at(g, 4 * c + t)) : make_uint4(0, 0, 0, 0);
                 row_of(2 * t, off.x, last.x);
                 row_of(2 * t + 1, off.y, last.y);
                 next = find(b + gridDim.x);
                 weigh(q, off, last);
             } else {
-                next = find(b + gridDim.x);
-                for (int r0 = 0; r0 < rows; r0 += kWeighRows) {   // 64 rows at a time
-                    const int tiles = (min(rows - r0, kWeighRows) + 7) / 8;
-                    __syncthreads();   // the rows before are done with
-                    for (int i = threadIdx.x; i < tiles * 8 * (D / 8); i += kWeighThreads) {
+                // 64 rows at a time, the next ones on their way meanwhile
+                auto bring = [&](int r0, int buf) {
+                    const int count = (min(rows - r0, kWeighRows) + 7) / 8 * 8;
+                    for (int i = threadIdx.x; i < count * (D / 8); i += kWeighThreads) {
                         const int r = i / (D / 8), piece = i % (D / 8);
-                        queries[((r / 8) * C + piece / 4) * 32 + (r % 8) * 4 + piece % 4] = query(r0 + r, piece);
+                        uint4 *dst = queries[buf] + ((r / 8) * C + piece / 4) * 32 + (r % 8) * 4 + piece % 4;
+                        if (r0 + r < rows)
+                            copy_async<16>(smem_u32(dst), query_at(r0 + r, piece));
+                        else
+                            *dst = make_uint4(0, 0, 0, 0);
                     }
-                    if (threadIdx.x < static_cast<unsigned>(tiles * 8))
-                        row_of(r0 + threadIdx.x, minus_lse[threadIdx.x], last_key[threadIdx.x]);
+                    asm volatile("cp.async.commit_group;" ::: "memory");
+                    if (threadIdx.x < static_cast<unsigned>(count))
+                        row_of(r0 + threadIdx.x, minus_lse[buf][threadIdx.x], last_key[buf][threadIdx.x]);
+                };
+                __syncthreads();   // the rows of the block before are done with
+                bring(0, 0);
+                next = find(b + gridDim.x);
+                for (int r0 = 0, buf = 0; r0 < rows; r0 += kWeighRows, buf ^= 1) {
+                    if (r0 + kWeighRows < rows) {
+                        bring(r0 + kWeighRows, buf ^ 1);
+                        asm volatile("cp.async.wait_group 1;" ::: "memory");
+                    } else {
+                        asm volatile("cp.async.wait_group 0;" ::: "memory");
+                    }
                     __syncthreads();
-                    if (key0 >= v.kv)
-                        continue;
+                    const int tiles = key0 < v.kv ? (min(rows - r0, kWeighRows) + 7) / 8 : 0;
                     for (int i = 0; i < tiles; ++i) {
                         uint4 q[C];
 #pragma unroll
                         for (int c = 0; c < C; ++c)
-                            q[c] = queries[(i * C + c) * 32 + lane];
-                        weigh(q, *reinterpret_cast<const float2 *>(minus_lse + 8 * i + 2 * t),
-                              *reinterpret_cast<const int2 *>(last_key + 8 * i + 2 * t));
+                            q[c] = queries[buf][(i * C + c) * 32 + lane];
+                        weigh(q, *reinterpret_cast<const float2 *>(minus_lse[buf] + 8 * i + 2 * t),
+                              *reinterpret_cast<const int2 *>(last_key[buf] + 8 * i + 2 * t));
                     }
+                    __syncthreads();   // these rows are done with
                 }
             }
 #pragma unroll
@@ -336,11 +349,10 @@ struct SelectParams {
 __global__ void __launch_bounds__(kSelectThreads) kv_select_kernel(const __grid_constant__ SelectParams p)
 {
     extern __shared__ uint32_t held[];
-    __shared__ uint4 bins[kSelectThreads];   // the highest digit's first, four to a thread
+    __shared__ uint4 histograms[3][kSelectThreads];   // of each digit, the highest value first, four to a thread
     __shared__ uint32_t warp_sum[2][kSelectThreads / 32];
     __shared__ uint32_t digit, above;
     __shared__ uint2 mine;   // keys above the border, on it
-    uint32_t *const hist = reinterpret_cast<uint32_t *>(bins);
     static_assert(kSelectBins == 4 * kSelectThreads, "four bins to a thread");
     grid_dependency_wait();
     grid_dependents_launch();
@@ -404,6 +416,8 @@ __global__ void __launch_bounds__(kSelectThreads) kv_select_kernel(const __grid_
         left = static_cast<uint32_t>(m);
         for (int pass = 0; pass < 3; ++pass) {
             const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
+            uint4 *const bins = histograms[pass];   // (one for each: the other CTAs may still be reading the last)
+            uint32_t *const hist = reinterpret_cast<uint32_t *>(bins);
             bins[threadIdx.x] = make_uint4(0, 0, 0, 0);
             __syncthreads();
             auto count_digit = [&](int i, uint32_t key) {
@@ -453,8 +467,6 @@ __global__ void __launch_bounds__(kSelectThreads) kv_select_kernel(const __grid_
                 scan += each[e];
             }
             __syncthreads();
-            if (ctas > 1)
-                cluster_sync();   // the other CTAs have read this one's histogram
             border |= digit << shift;
             left -= above;
         }

@@ -40,6 +40,16 @@ __device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t v)
     return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
 }
 
+// BYTES (4, 8 or 16) from global to shared memory, on their way until the thread waits for its cp.async group.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void *src)
+{
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
+}
+
 // The batch as gemm_serving.h describes it. Sizes are checked on the host so that every
 // combined key index (prefix + own) fits an int.
 struct BatchView {

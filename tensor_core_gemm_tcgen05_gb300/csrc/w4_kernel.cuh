@@ -48,6 +48,7 @@ struct W4Params {
     int steps;             // of 256 (w4_kernel) or 128 columns, the last maybe in part
     uint32_t *err;
     uint64_t timeout_ns;
+    int debug;             // DEBUG_WITHHOLD_FIRST_LOAD (w4_umma_kernel)
 };
 
 // The activation in FP32 (NaN stays NaN).
@@ -117,15 +118,6 @@ template <typename T>
 __device__ __forceinline__ float w4_scale(uint32_t sz)
 {
     return unpack2<T>(sz & 0xffffu).x;
-}
-
-template <int BYTES>
-__device__ __forceinline__ void copy_async(uint32_t dst, const void *src)
-{
-    if constexpr (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
 }
 
 // A warp's way through the rounds of its cluster's tiles: 2^log_rows tiles from `tile` on; of a tile its steps w, w + warps, ...,

@@ -232,6 +232,8 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
                 const uint32_t stage = static_cast<uint32_t>(i % STAGES), at = base + stage * Cfg::STAGE, full = full0 + 8u * stage;
                 if (!(ok = wait_bounded(empty0 + 8u * stage, (static_cast<uint32_t>(i / STAGES) & 1u) ^ 1u, wc, ERR_PRODUCER_SLOT)))
                     break;
+                if (p.debug & DEBUG_WITHHOLD_FIRST_LOAD)   // test hook: never loaded
+                    break;
                 mbar_arrive_expect_tx(full, Cfg::STAGE);
                 tma_load_2d(at, &tmap_codes, full, (step0 + i) * 64, n0);
                 tma_load_2d(at + Cfg::CODES, &tmap_a, full, (step0 + i) * 128, m0);

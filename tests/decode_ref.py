@@ -91,7 +91,7 @@ def weigh(q, k_cache, b, lse, weights, scale, window, decay):
     w, bound = weights.double().clone(), torch.zeros_like(weights, dtype=torch.float64)
     for s, n in enumerate(b["n_q"]):
         end, kv = int(b["q_start"][s]) + n, b["kv"][s]
-        if kv == 0:
+        if kv == 0 or n == 0:   # (without new tokens: as it is)
             continue
         rows = min(n, window) if window else n
         k = keys_of(k_cache, {**b, "prefix_pages": None}, s).double()   # [keys, hk, d]
