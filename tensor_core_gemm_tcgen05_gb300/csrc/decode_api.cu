@@ -18,12 +18,26 @@ using namespace gb300_host;
 namespace {
 
 constexpr int64_t kMaxW4Rows = 1 << 18, kMaxW4Size = 1 << 24;
-// Rows of A up to which w4_kernel is used. Both forms, in us (4096 x 4096, 16384 x 4096, 1024 x 1024, 512 x 8192, groups of 128):
-// eight rows 8.2, 17.0, 4.2, 7.7 against w4_umma_kernel's 8.3, 16.9, 5.0, 10.5; one row 6.3, 14.9, 3.7, 5.7 against 8.1, 16.9,
-// 4.9, 10.3; sixteen (of a w4_kernel that took them) 12.0, 23.2, 5.1, 11.2 against 8.4, 17.1, 5.1, 10.5.
-constexpr int64_t kW4MmaRows = 8;
 constexpr int kW4SmemMax = 227 * 1024;
 constexpr int kSelectHeldMax = 48 * 1024;   // keys: 192 KB of shared memory
+
+// Which of the two 4-bit products takes up to eight rows of A: the one that these estimates (ns) give less. w4_kernel's time goes by the
+// tiles of 16 rows of W and 256 columns that an SM sees and by the values of A that it lays out; w4_umma_kernel's by the
+// steps of 128 x 128 an SM sees, in waves, whatever the rows. Over eight shapes from 6144 x 4096 to 65536 x 1024, groups, types and 1 to 8
+// rows the choice takes 0.5 % longer than the faster of both in the mean, w4_kernel alone 5 %. Both sides, us (w4_kernel, the other):
+//  * 1024 x 1024, eight rows, groups of 128: 4.3, 5.0; 4096 x 4096: 8.2, 8.2 (one row 6.4, 8.1); 32768 x 4096: 25.9, 33.4
+//  * 16384 x 4096: one row 15.1, 16.9, eight 17.2, 17.0; groups of 64 in BF16 19.9, 19.1 and 21.2, 19.1; of 32 24.8, 23.3 and 26.2, 23.4
+//  * 4096 x 16384: one row 15.5, 17.9, eight 20.2, 18.1; groups of 64 in BF16 23.0, 20.1 and 27.2, 20.2
+// Of sixteen rows (of a w4_kernel that took them) 16384 x 4096 took 23.2, 17.0 and 1024 x 1024 5.1, 5.1.
+int64_t w4_kernel_ns(int dtype, int64_t group, int64_t tile_steps, int64_t a_steps)
+{
+    const int64_t per_step = dtype == GEMM_F16 ? (group == 128 ? 98 : group == 64 ? 132 : 184) : (group == 128 ? 114 : group == 64 ? 140 : 190);
+    return 3300 + tile_steps * per_step + a_steps * 14;
+}
+int64_t w4_umma_ns(int64_t group, int64_t waves, int64_t steps)
+{
+    return 2400 + waves * (3000 + steps * (group == 128 ? 375 : group == 64 ? 440 : 570));
+}
 
 // launch_serving in clusters of `cluster` CTAs along x.
 template <typename... P, typename... A>
@@ -529,21 +543,32 @@ int gemm_w4_run(gemm_ctx *ctx, int dtype, int64_t M, int64_t N, int64_t K, const
     p.debug = ctx->debug & GEMM_DEBUG_WITHHOLD_FIRST_LOAD;
     // w4_kernel: A's columns have to fit the shared memory of a cluster.
     const int groups_128 = static_cast<int>(128 / w->group);
+    const int64_t blocks_m = (M + gb300::kW4Rows - 1) / gb300::kW4Rows;
+    p.tiles = static_cast<int>((N + 15) / 16);
     int cluster = 1;
     auto slice = [&] { return (p.steps + cluster - 1) / cluster; };
     auto fits = [&] { return gb300::w4_smem(groups_128, slice(), cluster > 1) <= kW4SmemMax; };
     while (cluster < 8 && !fits())
         cluster *= 2;
-    if (K > 0 && (M > kW4MmaRows || !fits())) {
-        p.steps = static_cast<int>((K + 127) / 128);
-        const int tokens = M <= 16 ? 16 : M <= 32 ? 32 : 64;
-        const int64_t tiles = (N + 127) / 128, blocks_m = (M + tokens - 1) / tokens;
-        // as many CTAs share a tile's columns as run at once, with two steps each at least (512 x 8192, 16 rows: 8 of them 7.9
-        // us, 4 10.5; 2048 x 2048, where not all clusters of 8 run at once: 11.1, 6.2)
-        cluster = 1;
-        while (cluster < 8 && tiles * blocks_m <= ctx->w4_clusters[cluster * 2] && p.steps >= 4 * cluster)
-            cluster *= 2;
-        DeviceGuard guard(ctx->device);
+    // Fewer tiles than CTAs: the columns shared by more of them, as long as every warp has a step.
+    while (cluster < 8 && int64_t(p.tiles) * blocks_m * cluster * 2 <= ctx->num_sms && p.steps >= 2 * cluster * gb300::kW4Warps)
+        cluster *= 2;
+    p.slice = slice();
+    p.clusters = std::min(p.tiles, std::max(1, ctx->w4_clusters[cluster]));
+    // w4_umma_kernel: as many CTAs share a tile's columns as run at once, with two steps each at least (512 x 8192, 16 rows: 8 of
+    // them 7.9 us, 4 10.5; 2048 x 2048, where not all clusters of 8 run at once: 11.1, 6.2)
+    const int tokens = M <= 16 ? 16 : M <= 32 ? 32 : 64, umma_steps = static_cast<int>((K + 127) / 128);
+    const int64_t umma_tiles = (N + 127) / 128 * ((M + tokens - 1) / tokens);
+    int umma_cluster = 1;
+    while (umma_cluster < 8 && umma_tiles <= ctx->w4_clusters[umma_cluster * 2] && umma_steps >= 4 * umma_cluster)
+        umma_cluster *= 2;
+    const bool umma =
+        K > 0 && (M > gb300::kW4Rows || !fits() ||
+                  w4_umma_ns(w->group, (umma_tiles * umma_cluster + ctx->num_sms - 1) / ctx->num_sms, (umma_steps + umma_cluster - 1) / umma_cluster) <
+                      w4_kernel_ns(dtype, w->group, int64_t((p.tiles + p.clusters - 1) / p.clusters) * p.slice, M * p.slice));
+    DeviceGuard guard(ctx->device);
+    if (umma) {
+        p.steps = umma_steps;
         CUtensorMap codes, a;
         if (!encode_2d(ctx, &codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w->codes, K / 2, N, K / 2, 64, 128, CU_TENSOR_MAP_SWIZZLE_64B) ||
             !encode_2d(ctx, &a, dtype == GEMM_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, A, K, M, lda, 64,
@@ -552,18 +577,11 @@ int gemm_w4_run(gemm_ctx *ctx, int dtype, int64_t M, int64_t N, int64_t K, const
         return launched(ctx, with_w4_umma(dtype, tokens, w->group, [&](auto cfg) {
                             using Cfg = decltype(cfg);
                             return launch_cluster(gb300::w4_umma_kernel<Cfg>,
-                                                  dim3(static_cast<unsigned>(tiles * cluster), static_cast<unsigned>(blocks_m)),
-                                                  Cfg::NUM_THREADS, Cfg::SMEM_BYTES, cluster, static_cast<cudaStream_t>(stream), codes, a, p);
+                                                  dim3(static_cast<unsigned>((N + 127) / 128 * umma_cluster),
+                                                       static_cast<unsigned>((M + tokens - 1) / tokens)),
+                                                  Cfg::NUM_THREADS, Cfg::SMEM_BYTES, umma_cluster, static_cast<cudaStream_t>(stream), codes, a, p);
                         }));
     }
-    const int64_t blocks_m = (M + gb300::kW4Rows - 1) / gb300::kW4Rows;
-    p.tiles = static_cast<int>((N + 15) / 16);
-    // Fewer tiles than CTAs: the columns shared by more of them, as long as every warp has a step.
-    while (cluster < 8 && int64_t(p.tiles) * blocks_m * cluster * 2 <= ctx->num_sms && p.steps >= 2 * cluster * gb300::kW4Warps)
-        cluster *= 2;
-    p.slice = slice();
-    p.clusters = std::min(p.tiles, std::max(1, ctx->w4_clusters[cluster]));
-    DeviceGuard guard(ctx->device);
     return launched(ctx, with_w4(dtype, w->group, [&](auto kernel) {
                         return launch_cluster(kernel, dim3(static_cast<unsigned>(p.clusters * cluster), static_cast<unsigned>(blocks_m)),
                                               gb300::kW4Threads, static_cast<int>(gb300::w4_smem(groups_128, p.slice, cluster > 1)), cluster,

@@ -471,6 +471,18 @@ def test_w4_large(ctx, dtype, m, n, k):
     ref.check_w4(got.cpu(), y, slack, (dtype, m, n, k))
 
 
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("m,n,k,group", [(1, 4096, 16384, 64), (3, 8192, 4096, 128), (5, 4096, 8192, 128), (8, 2048, 16384, 32)])
+def test_w4_few_rows(ctx, dtype, m, n, k, group):
+    """Where the faster kernel for up to eight rows depends on the sizes, the group and the type."""
+    dt = TYPES[dtype]
+    a, codes, scales, zeros, bias = w4_inputs(m, n, k, group, dt, True, seed=m)
+    y, slack = ref.w4(a, codes, scales, zeros, bias, "relu")
+    got = g.w4_gemm(ctx, a.cuda(), codes.cuda(), scales.cuda(), zeros.cuda(), bias.cuda(), g.EPI_RELU)
+    clean(ctx)
+    ref.check_w4(got.cpu(), y, slack, (dtype, m, n, k, group))
+
+
 def test_w4_rows_of_any_stride(ctx):
     a, codes, scales, zeros, bias = w4_inputs(5, 64, 256, 64, torch.float16, True)
     wide = torch.full((5, 300 + 4), 7.0, dtype=torch.float16, device="cuda")

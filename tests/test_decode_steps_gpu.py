@@ -9,7 +9,7 @@ import decode_ref as ref
 import serving_ref
 import tensor_core_gemm_tcgen05_gb300 as g
 from serving_ref import attention, batch, check_attention, check_rope
-from test_decode_gpu import cache_of, clean, complains, heavy, normal, on_gpu, w4_inputs
+from test_decode_gpu import cache_of, clean, heavy, normal, on_gpu, w4_inputs
 
 pytestmark = pytest.mark.gpu
 F16 = torch.float16
