@@ -141,11 +141,11 @@ struct W4Walk {
     __device__ __forceinline__ int warps() const { return kW4Warps >> log_rows; }   // of a tile
 };
 
-// Bytes of shared memory: A's columns of the slice and (by group) their sums, the rings, the partial sums, and in clusters the
-// CTA's sums (two rounds').
+// Bytes of shared memory: A's columns of the slice and (by group) their sums, the rings, the partial sums and in clusters the
+// CTA's sums (two rounds' of both).
 __host__ __device__ constexpr int64_t w4_smem(int groups, int64_t slice, bool cluster)
 {
-    return slice * 2 * (2048 + 32 * groups) + kW4Warps * (kW4Ahead * 2048 + 512) + (cluster ? 2 * kW4Round * 512 : 0);
+    return slice * 2 * (2048 + 32 * groups) + kW4Warps * (kW4Ahead * 2048 + 1024) + (cluster ? 2 * kW4Round * 512 : 0);
 }
 
 // GW: words of eight codes that a lane has of a group (1, 2, 4: groups of 32, 64, 128).
@@ -166,8 +166,8 @@ __global__ void __launch_bounds__(kW4Threads, 1) w4_kernel(const __grid_constant
     float *const xsum = reinterpret_cast<float *>(act + p.slice * 256);                        // [group of the slice][row of A]
     uint4 *const rings = reinterpret_cast<uint4 *>(xsum + p.slice * GROUPS * kW4Rows);
     uint4 *const ring = rings + warp * (kW4Ahead * 128) + lane;                                // [slot][128 columns][row g, g + 8] of this lane
-    float4 *const red = reinterpret_cast<float4 *>(rings + kW4Warps * kW4Ahead * 128);         // [warp][lane]
-    float4 *const part = red + kW4Warps * 32;                                                  // [round mod 2][tile of W][lane]
+    float4 *const reds = reinterpret_cast<float4 *>(rings + kW4Warps * kW4Ahead * 128);        // [round mod 2][warp][lane]
+    float4 *const part = reds + 2 * kW4Warps * 32;                                             // [round mod 2][tile of W][lane]
     W4Walk now;
     now.tile = static_cast<int>(static_cast<int64_t>(p.tiles) * cluster / p.clusters);
     now.left = static_cast<int>(static_cast<int64_t>(p.tiles) * (cluster + 1) / p.clusters) - now.tile;
@@ -375,7 +375,9 @@ __global__ void __launch_bounds__(kW4Threads, 1) w4_kernel(const __grid_constant
                 load(u, scales[u]);
             }
         }
-        // ---- the round's sums: the warps of a tile, then the CTAs, in order
+        // ---- the round's sums: the warps of a tile, then the CTAs, in order. One barrier, after which the others go on: where they
+        // write in the next round nothing is read any more, since who reads passes that barrier first.
+        float4 *const red = reds + buf * (kW4Warps * 32);
         if (k_warp > 0)
             red[warp * 32 + lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
         __syncthreads();
@@ -390,9 +392,8 @@ __global__ void __launch_bounds__(kW4Threads, 1) w4_kernel(const __grid_constant
             else
                 part[(buf * kW4Round + row_warp) * 32 + lane] = y;
         }
-        __syncthreads();   // red may be written again
         if (ctas > 1) {
-            cluster_sync();   // (and the CTAs' sums of the round before have been read: those two rounds on go over them)
+            cluster_sync();
             const int f = warp * ctas + rank;   // one tile at most: the round has no more than kW4Round
             if (f < 1 << now.log_rows) {
                 float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -403,7 +404,6 @@ __global__ void __launch_bounds__(kW4Threads, 1) w4_kernel(const __grid_constant
                 }
                 finish(y, now.tile + f);
             }
-            __syncthreads();
         }
     }
     if (ctas > 1)
