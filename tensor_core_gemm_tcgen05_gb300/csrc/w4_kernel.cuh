@@ -9,15 +9,16 @@
 // that finds one takes code - zero itself to the products.
 //
 // A stays: a CTA (one to an SM, sixteen warps) brings its columns of A to shared memory once, in the order the products take
-// them, and then sees the tiles of 16 rows of W that are its cluster's, four, two or one at a time (a round), the columns
+// them, and then sees the tiles of 16 rows of W that are its cluster's, eight, four, two or one at a time (a round), the columns
 // of a tile shared by the other warps and by the CTAs of the cluster (several, where A does not fit one). A step is 256 columns
 // of a tile; each lane copies its own codes of the next steps into a ring of its own, across rounds, so nothing but the
 // sums of a round waits for another warp. These meet in shared and distributed shared memory in a fixed order.
 //
-// What bounds it: instruction issue at 1.7 a cycle and SM, of which unpacking is a third, behind a start of about 3.5 us. Measured
-// (captured, weights from HBM): 4096 x 4096 6.3 us for one row, 8.2 for eight, 16384 x 4096 14.9 and 17.0 (33.5 MB: 5.2 at
-// the copy rate), 1024 x 1024 3.7. Steps of 128 columns with a ring of four took 25; codes - zero unpacked for each row 24;
-// 256 threads that brought A anew for each 128 rows 23.
+// What bounds it: the chain of a step in its sixteen warps (issue 1.6 a cycle and SM, of which unpacking is a third; HBM at 22 %)
+// behind a start of about 3.5 us. Measured (captured, weights from HBM): 4096 x 4096 6.3 us for one row, 7.9 for eight, 16384 x 4096
+// 14.5 and 16.5 (33.5 MB: 5.2 at the copy rate), 32768 x 4096 21.0 and 22.9, 1024 x 1024 3.8. What it took there before:
+// steps of 128 columns with a ring of four 25 (eight rows, 16384 x 4096); codes - zero unpacked for each row 24; 256 threads that
+// brought A anew for each 128 rows 23; two more barriers to a round 17.2.
 #pragma once
 
 #include <type_traits>
@@ -28,7 +29,7 @@
 namespace gb300 {
 
 constexpr int kW4Threads = 512, kW4LogWarps = 4, kW4Warps = 1 << kW4LogWarps;
-constexpr int kW4Round = 4;   // tiles of 16 rows of W in a round, at most
+constexpr int kW4Round = 8;   // tiles of 16 rows of W in a round, at most (4: 32768 x 4096, one row 22.1 us for 21.0)
 constexpr int kW4Rows = 8;    // of A in a CTA
 constexpr int kW4Ahead = 2;   // steps whose codes a warp has in flight
 
@@ -126,8 +127,8 @@ struct W4Walk {
     int tile, left, log_rows, step, turns;
     __device__ __forceinline__ void begin(int warp, int count)
     {
-        static_assert(kW4Round == 4 && kW4Ahead == 2, "powers of two below");
-        log_rows = left >= 4 ? 2 : left >= 2 ? 1 : 0;
+        static_assert(kW4Round == 8 && kW4Ahead == 2, "powers of two below");
+        log_rows = left >= 8 ? 3 : left >= 4 ? 2 : left >= 2 ? 1 : 0;
         step = warp >> log_rows;
         turns = ((count + (2 * kW4Warps >> log_rows) - 1) >> (kW4LogWarps + 1 - log_rows)) * kW4Ahead;
     }
@@ -154,7 +155,10 @@ __global__ void __launch_bounds__(kW4Threads, 1) w4_kernel(const __grid_constant
 {
     constexpr int GROUP = 32 * GW, GROUPS = 256 / GROUP;   // groups of a step
     constexpr int OWN = (GROUPS + 3) / 4;                  // of a row's groups, those whose scale and zero a lane brings: t, t + 4
-    extern __shared__ uint4 act[];                         // [128 columns][word][lane]
+    extern __shared__ uint4 act[];                         // [128 columns][word][lane ^ turn(word)]
+    // (turned, so that eight neighbouring lanes write pieces of eight different banks when they lay A out: 4096 x 4096, eight rows 8.1 ->
+    // 7.8 us. With smaller groups, where they write two or four, the turn cost more: 65536 x 1024, groups of 64, 18.2 -> 21.5)
+    auto turn = [](int word) { return GW == 4 ? 2 * (word & 3) : 0; };
     grid_dependency_wait();
     grid_dependents_launch();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
@@ -272,7 +276,7 @@ __global__ void __launch_bounds__(kW4Threads, 1) w4_kernel(const __grid_constant
                 // eight columns belong to one lane's word; the word's pairs are columns j and j + 4
                 const int lane_t = GW == 4 ? at / 4 : GW == 2 ? at / 2 % 4 : at % 4;
                 const int word = GW == 4 ? at % 4 : GW == 2 ? at / 8 * 2 + at % 2 : at / 4;
-                act[(k8 / 16 * 4 + word) * 32 + row * 4 + lane_t] =
+                act[(k8 / 16 * 4 + word) * 32 + ((row * 4 + lane_t) ^ turn(word))] =
                     make_uint4(__byte_perm(v[u].x, v[u].z, 0x5410), __byte_perm(v[u].x, v[u].z, 0x7632),
                                __byte_perm(v[u].y, v[u].w, 0x5410), __byte_perm(v[u].y, v[u].w, 0x7632));
                 if (k8 % (GROUP / 8) == 0)
@@ -310,7 +314,7 @@ __global__ void __launch_bounds__(kW4Threads, 1) w4_kernel(const __grid_constant
         // codes of the turn's step (in slot `slot`) times A's columns
         auto products = [&](int slot, int step, const Scales &mine, auto all_finite) {
             constexpr bool FINITE = decltype(all_finite)::value;
-            const uint4 *b = act + step * 256 + lane;
+            const uint4 *b = act + step * 256;
             const float *xs = xsum + step * (GROUPS * kW4Rows) + 2 * t;
             // s (UNIT sum + ODD_UNIT odd - (BASE + z) xsum), the unit with the scale
             constexpr float PER_ODD = W4Codes<T>::ODD_UNIT / W4Codes<T>::UNIT;
@@ -343,7 +347,7 @@ __global__ void __launch_bounds__(kW4Threads, 1) w4_kernel(const __grid_constant
                             w4_unpack_minus_zero<T>(codes[0][w % 4], static_cast<uint32_t>(z0), a0);
                             w4_unpack_minus_zero<T>(codes[1][w % 4], static_cast<uint32_t>(z1), a1);
                         }
-                        const uint4 x = b[w * 32];
+                        const uint4 x = b[w * 32 + (lane ^ turn(w))];
                         mma_16x8x16<T>(sum, a0[0], a1[0], a0[2], a1[2], x.x, x.z);
                         mma_16x8x16<T>(odd, a0[1], a1[1], a0[3], a1[3], x.y, x.w);
                     }
