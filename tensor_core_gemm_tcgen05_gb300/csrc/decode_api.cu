@@ -394,10 +394,12 @@ int gemm_kv_select(gemm_ctx *ctx, const gemm_kv_seqs *seqs, int64_t num_pages, i
     p.head_stride = head_stride;
     p.counts = counts;
     p.err = ctx->d_err;
-    // More CTAs for a long list, as long as they fit the GPU at once and have some thousand keys each.
+    // More CTAs for a long list, as long as they fit the GPU at once and have some thousand keys each (choice and compaction, us:
+    // 12 sequences of up to 16 000 keys, 8 heads, 59.0, with half as many CTAs 62.8; 16 of up to 40 000 109, 114, with twice as
+    // many 165; one sequence, 1090 keys, 12.4, with a CTA's keys down to 512 16.0).
     const int64_t room = seqs->table_width * page_size;
     int cluster = 1;
-    while (cluster < 8 && items * cluster * 2 <= 2 * static_cast<int64_t>(ctx->num_sms) && room >= 4096 * cluster)
+    while (cluster < 8 && items * cluster * 2 <= 4 * static_cast<int64_t>(ctx->num_sms) && room >= 4096 * cluster)
         cluster *= 2;
     if (items * cluster > INT32_MAX)
         return GEMM_ERR_ARG;
@@ -473,8 +475,9 @@ int gemm_kv_compact(gemm_ctx *ctx, const gemm_kv_cache *cache, const gemm_kv_seq
     p.counts = counts;
     p.new_lens = new_lens;
     p.err = ctx->d_err;
-    // A CTA takes several heads where their rows fit its round (accepted drafts); several CTAs take the rows of one
-    // head where there are more of them than fit.
+    // A CTA takes several heads where their rows fit its round (accepted drafts: 4.2 us for 200 sequences x 16 heads x 12 rows, a CTA to
+    // each head 15.4); several CTAs take the rows of one head where there are more of them than fit (12 sequences x 8 heads x 2048 rows
+    // 39.4 us, half as many CTAs 55.0, one to a head 66.4, twice as many 40.9).
     const int pairs = cache->head_dim == 64 ? gb300::CompactShape<64>::PAIRS : gb300::CompactShape<128>::PAIRS;
     p.heads = 1;
     while (p.heads < heads && p.heads < pairs && most * p.heads * 2 <= pairs)

@@ -6,12 +6,18 @@
 //  * producer: TMA, a step's codes (64 bytes of each row) and A's columns into a ring of stages;
 //  * six loaders: a block's scales and zeros, read along the rows of W (a thread for each row, step by step,
 //    touches a line per row and step) and laid out by group;
-//  * two or three groups of four warps, a row of W per thread, take the codes of steps in turn to Tensor Memory as code - zero
+//  * four or two groups of four warps, a row of W per thread, take the codes of steps in turn to Tensor Memory as code - zero
 //    (pairs of consecutive columns, the lower in the low half, as the product wants them), and a thread of each issues
 //    the step's products: several issuers, since one thread's waits and instructions took longer than the products;
 //  * one or two groups of four warps scale and add up the sums of the groups, a row of W per thread.
-// What bounds it is the unpacking (a byte permutation and half a mask per pair on the integer pipe, a fused multiply-add),
-// so nothing that unpacks waits for a product. Every wait is bounded.
+// Every wait is bounded.
+//
+// Measured (captured, weights from HBM; 5.2 us at the copy rate): 16384 x 4096, groups of 128, 16 rows 16.9 us, 64 rows 21.4; 4096 x 16384,
+// groups of 64 in BF16, 64 rows 29.3. What bounds it is the way of a step from group to group, none of its parts alone: of the
+// last, without the loads of weights 27.2, with one product of eight 26.3, without unpacking 27.0, without the loads of scales
+// 27.9, without scaling 29.3, without all but the first 22.6. Tried at 16384 x 4096, 16 rows: two CTAs to an SM, roles merged, 17.5; one
+// issuer and six buffers of codes 22.8; three groups with two buffers 18.9; five groups 16.6 (but 32 rows 18.1 -> 20.1); halves of
+// a step handed over one by one 18.3.
 #pragma once
 
 #include "w4_kernel.cuh"
