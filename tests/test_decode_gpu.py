@@ -472,7 +472,8 @@ def test_w4_large(ctx, dtype, m, n, k):
 
 
 @pytest.mark.parametrize("dtype", list(TYPES))
-@pytest.mark.parametrize("m,n,k,group", [(1, 4096, 16384, 64), (3, 8192, 4096, 128), (5, 4096, 8192, 128), (8, 2048, 16384, 32)])
+@pytest.mark.parametrize("m,n,k,group", [(1, 4096, 16384, 64), (3, 8192, 4096, 128), (5, 4096, 8192, 128), (8, 2048, 16384, 32),
+                                           (1, 24, 65536, 32), (2, 16, 69632, 128), (2, 16, 69888, 128), (8, 8, 131072, 64), (4, 50000, 256, 128)])
 def test_w4_few_rows(ctx, dtype, m, n, k, group):
     """Where the faster kernel for up to eight rows depends on the sizes, the group and the type."""
     dt = TYPES[dtype]
