@@ -138,6 +138,30 @@ def test_any_mask(ctx, dtype, n, ctx_len, words):
     check_attention(out.cpu(), lse.cpu(), *ref.tree_attention(q, k, v, b, mask, 1 / math.sqrt(d)), (dtype, n, ctx_len, words))
 
 
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("n_q,kv,ps,prefix", [([5, 0, 16], [300, 20, 16], 16, 0), ([16, 3, 9], [400, 70, 9], 64, 2), ([64], [5000], 32, 1),
+                                              ([7] * 20, [40 + 13 * i for i in range(20)], 32, 40)])
+def test_tree_attention_leaves_padding_alone(ctx, dtype, n_q, kv, ps, prefix):
+    """Tokens behind the last sequence are of no sequence, whatever their rows of the mask hold."""
+    dt, hq, hk, d, tokens = TYPES[dtype], 8, 2, 128, sum(n_q)
+    b = batch(n_q, kv, ps, prefix_pages=prefix, seed=1)
+    k, kd = cache_of(b["pages"], hk, ps, d, 1, dt, False)
+    v, vd = cache_of(b["pages"], hk, ps, d, 2, dt, False)
+    q = normal(tokens + 37, hq, d, seed=3, dtype=dt)
+    q[tokens:] = math.nan
+    words = max(1, -(-max(n_q) // 32))
+    mask, _ = ref.tree_mask(ref.trees(n_q, seed=2), b, words)
+    rows = torch.full((tokens + 37, words), -1, dtype=torch.int32)
+    rows[:tokens] = mask
+    out = torch.full((tokens + 37, hq, d), 7.0, dtype=dt, device="cuda")
+    lse = torch.full((tokens + 37, hq), 7.0, device="cuda")
+    g.tree_attention(ctx, q.cuda(), kd, vd, *on_gpu(b).values(), rows.cuda(), prefix_pages=b["prefix_pages"].cuda() if prefix else None,
+                     out=out, lse=lse)
+    clean(ctx)
+    check_attention(out[:tokens].cpu(), lse[:tokens].cpu(), *ref.tree_attention(q[:tokens], k, v, b, mask, 1 / math.sqrt(d)), (dtype, n_q, prefix))
+    assert bool((out[tokens:] == 7).all()) and bool((lse[tokens:] == 7).all())
+
+
 @pytest.mark.parametrize("bad", [math.nan, math.inf])
 @pytest.mark.parametrize("n,ctx_len", [(9, 50), (70, 200), (9, 0)])
 def test_unseen_nodes_may_hold_anything(ctx, bad, n, ctx_len):
