@@ -25,14 +25,14 @@ constexpr int kSelectHeldMax = 48 * 1024;   // keys: 192 KB of shared memory
 // tiles of 16 rows of W and 256 columns that an SM sees and by the values of A that it lays out; w4_umma_kernel's by the
 // steps of 128 x 128 an SM sees, in waves, whatever the rows. Over eight shapes from 6144 x 4096 to 65536 x 1024, groups, types and 1 to 8
 // rows the choice takes 0.3 % longer than the faster of both in the mean. Both sides, us (w4_kernel, the other):
-//  * 1024 x 1024, eight rows, groups of 128: 4.2, 5.0; 4096 x 4096: 7.9, 8.2 (one row 6.3, 8.1); 32768 x 4096: 22.9, 33.4
-//  * 16384 x 4096: one row 14.5, 16.9, eight 16.5, 17.0; groups of 64 in BF16 19.0, 19.1 and 20.4, 19.1; of 32 24.6, 23.3 and 26.0, 23.4
-//  * 4096 x 16384: one row 15.3, 17.9, eight 19.7, 18.1; groups of 64 in BF16 22.8, 20.1 and 26.9, 20.2
+//  * 1024 x 1024, eight rows, groups of 128: 3.9, 5.0; 4096 x 4096: 7.7, 8.2 (one row 6.1, 8.1); 32768 x 4096: 22.2, 33.4
+//  * 16384 x 4096: one row 14.3, 16.9, eight 15.8, 17.0; groups of 64 in BF16 18.7, 19.1 and 20.2, 19.1; of 32 24.5, 23.3 and 26.3, 23.4
+//  * 4096 x 16384: one row 15.1, 17.9, eight 17.9, 18.1; groups of 64 in BF16 22.5, 20.1 and 25.4, 20.2
 // Of sixteen rows (of an earlier w4_kernel that took them) 16384 x 4096 took 23.2, 17.0 and 1024 x 1024 5.1, 5.1.
 int64_t w4_kernel_ns(int dtype, int64_t group, int64_t tile_steps, int64_t a_steps)
 {
-    const int64_t per_step = dtype == GEMM_F16 ? (group == 128 ? 96 : group == 64 ? 122 : 174) : (group == 128 ? 106 : group == 64 ? 134 : 182);
-    return 3400 + tile_steps * per_step + a_steps * 16;
+    const int64_t per_step = dtype == GEMM_F16 ? (group == 128 ? 96 : group == 64 ? 122 : 178) : (group == 128 ? 106 : group == 64 ? 134 : 182);
+    return 3400 + tile_steps * per_step + a_steps * 12;
 }
 int64_t w4_umma_ns(int64_t group, int64_t waves, int64_t steps)
 {

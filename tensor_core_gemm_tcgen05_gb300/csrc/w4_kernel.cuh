@@ -15,10 +15,14 @@
 // sums of a round waits for another warp. These meet in shared and distributed shared memory in a fixed order.
 //
 // What bounds it: the chain of a step in its sixteen warps (issue 1.6 a cycle and SM, of which unpacking is a third; HBM at 22 %)
-// behind a start of about 3.5 us. Measured (captured, weights from HBM): 4096 x 4096 6.3 us for one row, 7.9 for eight, 16384 x 4096
-// 14.5 and 16.5 (33.5 MB: 5.2 at the copy rate), 32768 x 4096 21.0 and 22.9, 1024 x 1024 3.8. What it took there before:
+// behind a start of about 3 us. Measured (captured, weights from HBM): 4096 x 4096 6.1 us for one row, 7.7 for eight, 16384 x 4096
+// 14.3 and 15.8 (33.5 MB: 5.2 at the copy rate), 32768 x 4096 20.8 and 22.2, 1024 x 1024 3.7. What it took there before:
 // steps of 128 columns with a ring of four 25 (eight rows, 16384 x 4096); codes - zero unpacked for each row 24; 256 threads that
 // brought A anew for each 128 rows 23; two more barriers to a round 17.2.
+//
+// Laying A out is 1 of the 14.3 and 2.7 of the 15.8. Four pieces in flight whatever their number: 14.6 and 16.5; eight 15.0 and 15.6; sums
+// always as products with ones, which need a barrier and a look at all groups: 14.6 and 15.1 (4096 x 4096, one row 6.5 for 6.1);
+// asynchronous copies to the pieces' places, then a turn in place: 15.4 and 18.6.
 #pragma once
 
 #include <type_traits>
@@ -76,6 +80,7 @@ struct W4Codes;
 template <>
 struct W4Codes<__half> {
     static constexpr float UNIT = 16777216.0f, ODD_UNIT = 1048576.0f, BASE = 0.0f;
+    static constexpr uint32_t ONES = 0x3c003c00u;   // two of them
     static __device__ __forceinline__ void unpack(uint32_t w, uint32_t (&x)[4])
     {
         x[0] = w & 0x000f000fu;
@@ -88,6 +93,7 @@ struct W4Codes<__half> {
 template <>
 struct W4Codes<__nv_bfloat16> {
     static constexpr float UNIT = 1.0f, ODD_UNIT = 1.0f, BASE = 128.0f;
+    static constexpr uint32_t ONES = 0x3f803f80u;
     static __device__ __forceinline__ void unpack(uint32_t w, uint32_t (&x)[4])
     {
 #pragma unroll
@@ -140,6 +146,23 @@ struct W4Walk {
     }
     __device__ __forceinline__ int row_warp(int warp) const { return warp & ((1 << log_rows) - 1); }
     __device__ __forceinline__ int warps() const { return kW4Warps >> log_rows; }   // of a tile
+};
+
+// A warp's pieces of 256 columns of A's rows, `count` to a row: the warp-th of all and every kW4Warps-th from there on. (No division:
+// it would cost as much as the rest.)
+struct W4Pieces {
+    int row = 0, piece;
+    __device__ __forceinline__ W4Pieces(int warp, int count) : piece(warp) { settle(count); }
+    __device__ __forceinline__ void next(int count)
+    {
+        piece += kW4Warps;
+        settle(count);
+    }
+    __device__ __forceinline__ void settle(int count)
+    {
+        for (; piece >= count && row < kW4Rows; ++row)
+            piece -= count;
+    }
 };
 
 // Bytes of shared memory: A's columns of the slice and (by group) their sums, the rings, the partial sums and in clusters the
@@ -232,56 +255,73 @@ __global__ void __launch_bounds__(kW4Threads, 1) w4_kernel(const __grid_constant
 #pragma unroll
     for (int u = 0; u < kW4Ahead; ++u)
         load(u, scales[u]);
-    // ---- A's columns and their sums, a warp 256 columns of a row at a time, four rows or pieces of one in flight (what stands
-    // in rows past the last stays in columns of the products that are not written)
-    const int rows = min(p.M - m0, kW4Rows);
+    // ---- A's columns, each piece (eight columns of a row, one lane's word of W) to where the products take it, and the sums of the
+    // groups' columns: up to four pieces to a thread with shuffles, for more as products with ones once all are there
+    const int rows = min(p.M - m0, kW4Rows);   // (what stands in rows past the last stays in columns of the products that are not written)
+    const int k16 = lane % 16, of_lane = GW == 4 ? k16 / 4 : GW == 2 ? k16 / 2 % 4 : k16 % 4;
+    const int word = GW == 4 ? k16 % 4 : GW == 2 ? k16 / 8 * 2 + k16 % 2 : k16 / 4;
     bool finite = true;
-    int m = 0, piece = warp;   // (no division: it would cost as much as the rest)
-    auto settle = [&] {
-        while (piece >= count && m < rows) {
-            piece -= count;
-            ++m;
+    auto lay_out = [&](auto on_their_way, auto with_sums) {
+        constexpr int N = decltype(on_their_way)::value;
+#pragma unroll 1
+        for (W4Pieces at(warp, count); at.row < rows;) {
+            uint4 v[N];
+            int row[N], piece[N];
+#pragma unroll
+            for (int u = 0; u < N; ++u, at.next(count)) {
+                row[u] = at.row;
+                piece[u] = at.piece;
+                const int64_t k = (static_cast<int64_t>(step0) + at.piece) * 256 + 8 * lane;
+                v[u] = make_uint4(0, 0, 0, 0);
+                if (at.row < rows && k < p.K)
+                    v[u] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(p.a) + (m0 + at.row) * p.lda + k));
+            }
+#pragma unroll
+            for (int u = 0; u < N; ++u) {
+                float sum = 0.0f;
+                if constexpr (decltype(with_sums)::value) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 x = unpack2<T>(e == 0 ? v[u].x : e == 1 ? v[u].y : e == 2 ? v[u].z : v[u].w);
+                        sum += x.x + x.y;
+                    }
+#pragma unroll
+                    for (int o = GROUP / 16; o > 0; o /= 2)
+                        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                    finite = finite && fabsf(sum) < INFINITY;
+                }
+                if (row[u] < rows) {   // (the word's pairs are columns j and j + 4)
+                    const int k8 = piece[u] * 32 + lane;
+                    act[(k8 / 16 * 4 + word) * 32 + ((row[u] * 4 + of_lane) ^ turn(word))] =
+                        make_uint4(__byte_perm(v[u].x, v[u].z, 0x5410), __byte_perm(v[u].x, v[u].z, 0x7632),
+                                   __byte_perm(v[u].y, v[u].w, 0x5410), __byte_perm(v[u].y, v[u].w, 0x7632));
+                    if (decltype(with_sums)::value && k8 % (GROUP / 8) == 0)
+                        xsum[k8 / (GROUP / 8) * kW4Rows + row[u]] = sum;
+                }
+            }
         }
     };
-    settle();
-    while (m < rows) {
-        uint4 v[4];
-        int at_m[4], at_piece[4];
+    const int pieces = rows * count;
+    if (pieces <= 2 * kW4Warps) {
+        lay_out(std::integral_constant<int, 2>{}, std::true_type{});
+    } else if (pieces <= 4 * kW4Warps) {
+        lay_out(std::integral_constant<int, 4>{}, std::true_type{});
+    } else {
+        lay_out(std::integral_constant<int, 8>{}, std::false_type{});
+        __syncthreads();
+#pragma unroll 1
+        for (int q = warp; q < count * GROUPS; q += kW4Warps) {
+            constexpr uint32_t ONES = W4Codes<T>::ONES;
+            float sum[4] = {};
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            at_m[u] = m;
-            at_piece[u] = piece;
-            const int64_t k = (static_cast<int64_t>(step0) + piece) * 256 + 8 * lane;
-            v[u] = make_uint4(0, 0, 0, 0);
-            if (m < rows && k < p.K)
-                v[u] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(p.a) + (m0 + m) * p.lda + k));
-            piece += kW4Warps;
-            settle();
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int k8 = at_piece[u] * 32 + lane, at = lane % 16;
-            float sum = 0.0f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float2 x = unpack2<T>(e == 0 ? v[u].x : e == 1 ? v[u].y : e == 2 ? v[u].z : v[u].w);
-                sum += x.x + x.y;
+            for (int w = 0; w < GW; ++w) {
+                const uint4 x = act[(q * GW + w) * 32 + (lane ^ turn(w))];
+                mma_16x8x16<T>(sum, ONES, ONES, ONES, ONES, x.x, x.z);
+                mma_16x8x16<T>(sum, ONES, ONES, ONES, ONES, x.y, x.w);
             }
-#pragma unroll
-            for (int o = GROUP / 16; o > 0; o /= 2)
-                sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            finite = finite && fabsf(sum) < INFINITY;
-            if (at_m[u] < rows) {
-                const int row = at_m[u];
-                // eight columns belong to one lane's word; the word's pairs are columns j and j + 4
-                const int lane_t = GW == 4 ? at / 4 : GW == 2 ? at / 2 % 4 : at % 4;
-                const int word = GW == 4 ? at % 4 : GW == 2 ? at / 8 * 2 + at % 2 : at / 4;
-                act[(k8 / 16 * 4 + word) * 32 + ((row * 4 + lane_t) ^ turn(word))] =
-                    make_uint4(__byte_perm(v[u].x, v[u].z, 0x5410), __byte_perm(v[u].x, v[u].z, 0x7632),
-                               __byte_perm(v[u].y, v[u].w, 0x5410), __byte_perm(v[u].y, v[u].w, 0x7632));
-                if (k8 % (GROUP / 8) == 0)
-                    xsum[k8 / (GROUP / 8) * kW4Rows + row] = sum;
-            }
+            if (g == 0)
+                *reinterpret_cast<float2 *>(xsum + q * kW4Rows + 2 * t) = make_float2(sum[0], sum[1]);
+            finite = finite && (2 * t >= rows || fabsf(sum[0]) < INFINITY) && (2 * t + 1 >= rows || fabsf(sum[1]) < INFINITY);
         }
     }
     finite = __syncthreads_and(finite);
