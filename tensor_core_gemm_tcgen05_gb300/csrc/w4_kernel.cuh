@@ -14,7 +14,7 @@
 // of a tile; each lane copies its own codes of the next steps into a ring of its own, across rounds, so nothing but the
 // sums of a round waits for another warp. These meet in shared and distributed shared memory in a fixed order.
 //
-// What bounds it: the chain of a step in its sixteen warps (issue 1.6 a cycle and SM, of which unpacking is a third; HBM at 22 %)
+// What bounds it: the chain of a step in its sixteen warps (issue 1.6 a cycle and SM, of which unpacking is a third; HBM at 24 %)
 // behind a start of about 3 us. Measured (captured, weights from HBM): 4096 x 4096 6.1 us for one row, 7.7 for eight, 16384 x 4096
 // 14.3 and 15.8 (33.5 MB: 5.2 at the copy rate), 32768 x 4096 20.8 and 22.2, 1024 x 1024 3.7. What it took there before:
 // steps of 128 columns with a ring of four 25 (eight rows, 16384 x 4096); codes - zero unpacked for each row 24; 256 threads that
