@@ -100,14 +100,6 @@ __device__ __forceinline__ uint32_t cluster_ctarank()
     return r;
 }
 
-// CTAs of this cluster (1 in a launch without clusters).
-__device__ __forceinline__ uint32_t cluster_size()
-{
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-    return r;
-}
-
 // Address of the same shared-memory offset in CTA `rank` of this cluster.
 __device__ __forceinline__ uint32_t mapa_shared(uint32_t addr, uint32_t rank)
 {

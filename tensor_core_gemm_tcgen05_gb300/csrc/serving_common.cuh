@@ -40,6 +40,14 @@ __device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t v)
     return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
 }
 
+// CTAs of this cluster (1 in a launch without clusters).
+__device__ __forceinline__ uint32_t cluster_size()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+
 // BYTES (4, 8 or 16) from global to shared memory, on their way until the thread waits for its cp.async group.
 template <int BYTES>
 __device__ __forceinline__ void copy_async(uint32_t dst, const void *src)
