@@ -142,8 +142,9 @@ typedef struct gemm_w4 {
  * made for M up to 64. N a multiple of 8, K of the group, both up to 2^24 (K = 0: act(bias)). A and C have rows of lda and
  * ldc elements (multiples of 8, at least K and N), all pointers 16-byte aligned (scales 2, zeros 1). dtype: type of A, scales,
  * bias and C. No weight is rounded: codes enter the products exactly, each group is summed in FP32 before its scale is
- * applied, and the result is rounded once. (Up to eight rows, code A and zero A are summed apart, so that FP32's errors are
- * relative to 15 scale |A| - BF16: 143 - not to |W| |A|.) C may not overlap any other operand. One kernel launch. */
+ * applied, and the result is rounded once. (Up to eight rows, code A and zero A are summed apart where the |A| are below 2^113, so
+ * that FP32's errors are relative to 15 scale |A| - BF16: 143 - not to |W| |A|.) C may not overlap any other operand. One
+ * kernel launch. */
 int gemm_w4_run(gemm_ctx *ctx, int dtype, int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, const gemm_w4 *w,
                 const void *bias, void *C, int64_t ldc, int epilogue, void *stream);
 

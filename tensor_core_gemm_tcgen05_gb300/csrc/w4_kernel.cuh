@@ -5,8 +5,8 @@
 // the columns. With the zero z, the scale s and the columns of a group,
 //     s sum (code - z) x = s (sum code x - z sum x),
 // so the products are of the codes themselves, which cost a mask each (see W4Codes) and are exact, and sum x comes with A. Groups
-// are summed and scaled in FP32: no weight is rounded. Where a sum x is not finite the two terms would cancel to NaN: a CTA
-// that finds one takes code - zero itself to the products.
+// are summed and scaled in FP32: no weight is rounded. Where x is so large that code x or z sum x may leave FP32's range (BF16 from
+// 2^113 on, infinities, NaN) the two terms would cancel to NaN: a CTA that finds such a value takes code - zero itself to the products.
 //
 // A stays: a CTA (one to an SM, sixteen warps) brings its columns of A to shared memory once, in the order the products take
 // them, and then sees the tiles of 16 rows of W that are its cluster's, eight, four, two or one at a time (a round), the columns
@@ -75,12 +75,14 @@ __device__ __forceinline__ void w4_activate(int epilogue, float &x0, float &x1)
 //  * FP16: bits alone are subnormal numbers, code 2^-24; odd codes are left where they are, 16 code 2^-24.
 //  * BF16: in the mantissa of 128. (As subnormal numbers times x they would leave FP32's range.) The sums then lose
 //    5 of FP32's 24 bits to the base, of which the result keeps 8.
+// A group's sums, and what is taken off them, stay in FP32's range where all |x| are below LIMIT: FP16 128 15 2^16, BF16 128 143 2^113 < 2^128.
 template <typename T>
 struct W4Codes;
 template <>
 struct W4Codes<__half> {
     static constexpr float UNIT = 16777216.0f, ODD_UNIT = 1048576.0f, BASE = 0.0f;
     static constexpr uint32_t ONES = 0x3c003c00u;   // two of them
+    static constexpr float LIMIT = INFINITY;
     static __device__ __forceinline__ void unpack(uint32_t w, uint32_t (&x)[4])
     {
         x[0] = w & 0x000f000fu;
@@ -94,6 +96,7 @@ template <>
 struct W4Codes<__nv_bfloat16> {
     static constexpr float UNIT = 1.0f, ODD_UNIT = 1.0f, BASE = 128.0f;
     static constexpr uint32_t ONES = 0x3f803f80u;
+    static constexpr float LIMIT = 1.0384593717069655e34f;   // 2^113
     static __device__ __forceinline__ void unpack(uint32_t w, uint32_t (&x)[4])
     {
 #pragma unroll
@@ -102,12 +105,16 @@ struct W4Codes<__nv_bfloat16> {
     }
 };
 
-// The same with code - zero as the value, a zero for each row.
+// The same with code - zero (BF16: times 2^-11, so that a group's sum stays in FP32's range whatever the 128 values are) as the value, a
+// zero for each row. Times MINUS_ZERO_UNIT it is the value itself.
+template <typename T>
+constexpr float MINUS_ZERO_UNIT = std::is_same<T, __half>::value ? 1.0f : 2048.0f;
 template <typename T>
 __device__ __forceinline__ void w4_unpack_minus_zero(uint32_t w, uint32_t zero, uint32_t (&x)[4])
 {
     constexpr bool HALF = std::is_same<T, __half>::value;
-    const uint32_t base = HALF ? 0x64006400u : 0x43004300u, less = base | zero * 0x10001u;   // 1024 or 128, and with the zero
+    const uint32_t base = HALF ? 0x64006400u : 0x43004300u;   // 1024 or 128
+    const uint32_t less = (HALF ? base : 0xbd80bd80u) | zero * 0x10001u, times = 0x3a003a00u;   // with the zero; BF16: times -2^-11; 2^-11
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const uint32_t v = ((w >> (4 * j)) & 0x000f000fu) | base;
@@ -115,7 +122,8 @@ __device__ __forceinline__ void w4_unpack_minus_zero(uint32_t w, uint32_t zero, 
             const __half2 y = __hsub2(*reinterpret_cast<const __half2 *>(&v), *reinterpret_cast<const __half2 *>(&less));
             x[j] = *reinterpret_cast<const uint32_t *>(&y);
         } else {
-            const __nv_bfloat162 y = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&v), *reinterpret_cast<const __nv_bfloat162 *>(&less));
+            const __nv_bfloat162 y = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&v), *reinterpret_cast<const __nv_bfloat162 *>(&times),
+                                             *reinterpret_cast<const __nv_bfloat162 *>(&less));
             x[j] = *reinterpret_cast<const uint32_t *>(&y);
         }
     }
@@ -260,7 +268,8 @@ __global__ void __launch_bounds__(kW4Threads, 1) w4_kernel(const __grid_constant
     const int rows = min(p.M - m0, kW4Rows);   // (what stands in rows past the last stays in columns of the products that are not written)
     const int k16 = lane % 16, of_lane = GW == 4 ? k16 / 4 : GW == 2 ? k16 / 2 % 4 : k16 % 4;
     const int word = GW == 4 ? k16 % 4 : GW == 2 ? k16 / 8 * 2 + k16 % 2 : k16 / 4;
-    bool finite = true;
+    using Pair = std::conditional_t<std::is_same<T, __half>::value, __half2, __nv_bfloat162>;
+    uint32_t largest = 0;   // |x| of the thread's even and odd columns; NaN stays
     auto lay_out = [&](auto on_their_way, auto with_sums) {
         constexpr int N = decltype(on_their_way)::value;
 #pragma unroll 1
@@ -278,6 +287,12 @@ __global__ void __launch_bounds__(kW4Threads, 1) w4_kernel(const __grid_constant
             }
 #pragma unroll
             for (int u = 0; u < N; ++u) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t x = e == 0 ? v[u].x : e == 1 ? v[u].y : e == 2 ? v[u].z : v[u].w;
+                    const Pair y = __hmax2_nan(*reinterpret_cast<const Pair *>(&largest), __habs2(*reinterpret_cast<const Pair *>(&x)));
+                    largest = *reinterpret_cast<const uint32_t *>(&y);
+                }
                 float sum = 0.0f;
                 if constexpr (decltype(with_sums)::value) {
 #pragma unroll
@@ -288,7 +303,6 @@ __global__ void __launch_bounds__(kW4Threads, 1) w4_kernel(const __grid_constant
 #pragma unroll
                     for (int o = GROUP / 16; o > 0; o /= 2)
                         sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                    finite = finite && fabsf(sum) < INFINITY;
                 }
                 if (row[u] < rows) {   // (the word's pairs are columns j and j + 4)
                     const int k8 = piece[u] * 32 + lane;
@@ -321,10 +335,10 @@ __global__ void __launch_bounds__(kW4Threads, 1) w4_kernel(const __grid_constant
             }
             if (g == 0)
                 *reinterpret_cast<float2 *>(xsum + q * kW4Rows + 2 * t) = make_float2(sum[0], sum[1]);
-            finite = finite && (2 * t >= rows || fabsf(sum[0]) < INFINITY) && (2 * t + 1 >= rows || fabsf(sum[1]) < INFINITY);
         }
     }
-    finite = __syncthreads_and(finite);
+    const float2 top = unpack2<T>(largest);
+    const bool moderate = __syncthreads_and(top.x < W4Codes<T>::LIMIT && top.y < W4Codes<T>::LIMIT);   // (not of NaN)
     // ---- bias, activation and one rounding of a tile of sums (rows g and g + 8 of the tile, rows 2 t and 2 t + 1 of A)
     auto finish = [&](float4 y, int tile) {
         const int row = tile * 16 + g;
@@ -352,8 +366,8 @@ __global__ void __launch_bounds__(kW4Threads, 1) w4_kernel(const __grid_constant
         const int row_warp = now.row_warp(warp), k_warp = warp >> now.log_rows, k_warps = now.warps();
         float acc[4] = {};
         // codes of the turn's step (in slot `slot`) times A's columns
-        auto products = [&](int slot, int step, const Scales &mine, auto all_finite) {
-            constexpr bool FINITE = decltype(all_finite)::value;
+        auto products = [&](int slot, int step, const Scales &mine, auto all_moderate) {
+            constexpr bool MODERATE = decltype(all_moderate)::value;
             const uint4 *b = act + step * 256;
             const float *xs = xsum + step * (GROUPS * kW4Rows) + 2 * t;
             // s (UNIT sum + ODD_UNIT odd - (BASE + z) xsum), the unit with the scale
@@ -364,8 +378,8 @@ __global__ void __launch_bounds__(kW4Threads, 1) w4_kernel(const __grid_constant
 #pragma unroll
                 for (int j = 0; j < OWN; ++j) {
                     const float zero = static_cast<float>(mine.z[h][j] & 15);
-                    s[h][j] = unpack2<T>(mine.s[h][j]).x * (FINITE ? W4Codes<T>::UNIT : 1.0f);
-                    z[h][j] = FINITE ? (W4Codes<T>::BASE + zero) * (-1.0f / W4Codes<T>::UNIT) : zero;
+                    s[h][j] = unpack2<T>(mine.s[h][j]).x * (MODERATE ? W4Codes<T>::UNIT : 1.0f);
+                    z[h][j] = MODERATE ? (W4Codes<T>::BASE + zero) * (-1.0f / W4Codes<T>::UNIT) : zero;
                 }
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
@@ -380,7 +394,7 @@ __global__ void __launch_bounds__(kW4Threads, 1) w4_kernel(const __grid_constant
 #pragma unroll
                     for (int w = i * GW; w < (i + 1) * GW; ++w) {   // of the step's eight words
                         uint32_t a0[4], a1[4];
-                        if constexpr (FINITE) {
+                        if constexpr (MODERATE) {
                             W4Codes<T>::unpack(codes[0][w % 4], a0);
                             W4Codes<T>::unpack(codes[1][w % 4], a1);
                         } else {
@@ -391,7 +405,7 @@ __global__ void __launch_bounds__(kW4Threads, 1) w4_kernel(const __grid_constant
                         mma_16x8x16<T>(sum, a0[0], a1[0], a0[2], a1[2], x.x, x.z);
                         mma_16x8x16<T>(odd, a0[1], a1[1], a0[3], a1[3], x.y, x.w);
                     }
-                    if constexpr (FINITE) {
+                    if constexpr (MODERATE) {
                         const float2 x = *reinterpret_cast<const float2 *>(xs + i * kW4Rows);
                         acc[0] = fmaf(fmaf(z0, x.x, fmaf(odd[0], PER_ODD, sum[0])), s0, acc[0]);
                         acc[1] = fmaf(fmaf(z0, x.y, fmaf(odd[1], PER_ODD, sum[1])), s0, acc[1]);
@@ -400,7 +414,7 @@ __global__ void __launch_bounds__(kW4Threads, 1) w4_kernel(const __grid_constant
                     } else {
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            acc[e] = fmaf(sum[e] + odd[e], e < 2 ? s0 : s1, acc[e]);
+                            acc[e] = fmaf((sum[e] + odd[e]) * (e < 2 ? s0 : s1), MINUS_ZERO_UNIT<T>, acc[e]);
                     }
                 }
             }
@@ -411,7 +425,7 @@ __global__ void __launch_bounds__(kW4Threads, 1) w4_kernel(const __grid_constant
                 asm volatile("cp.async.wait_group %0;" ::"n"(kW4Ahead - 1) : "memory");   // (a lane reads only what it has copied)
                 const int step = now.step + (turn + u) * k_warps;
                 if (step < count) {
-                    if (finite)
+                    if (moderate)
                         products(u, step, scales[u], std::true_type{});
                     else
                         products(u, step, scales[u], std::false_type{});
