@@ -144,7 +144,8 @@ typedef struct gemm_w4 {
  * bias and C. No weight is rounded: codes enter the products exactly, each group is summed in FP32 before its scale is
  * applied, and the result is rounded once. (Up to eight rows, code A and zero A are summed apart where the |A| are below 2^113, so
  * that FP32's errors are relative to 15 scale |A| - BF16: 143 - not to |W| |A|.) C may not overlap any other operand. One
- * kernel launch. */
+ * kernel launch. Finite A and scales of any size: what leaves FP32's range is a scaled group's sum, or a sum of these, that does. (FP32's
+ * smallest step, 2^-149, may be one of 2^-137 for each group in BF16.) */
 int gemm_w4_run(gemm_ctx *ctx, int dtype, int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, const gemm_w4 *w,
                 const void *bias, void *C, int64_t ldc, int epilogue, void *stream);
 
