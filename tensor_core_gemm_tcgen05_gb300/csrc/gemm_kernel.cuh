@@ -406,7 +406,7 @@ __device__ __forceinline__ uint4 bias_fetch(const GemmParams &p, int n_tile0, in
     uint4 bv = make_uint4(0u, 0u, 0u, 0u);
     const int n = n_tile0 + 8 * lane;
     if (p.bias != nullptr && n < p.N)
-        bv = __ldg(reinterpret_cast<const uint4 *>(p.bias + n));
+        bv = *reinterpret_cast<const uint4 *>(p.bias + n);
     return bv;
 }
 
@@ -735,7 +735,7 @@ __device__ __forceinline__ void splitk_reduce_s(const GemmParams &p, uint32_t st
                     continue;
                 float v[4] = {a.x, a.y, a.z, a.w};
                 if (p.bias != nullptr) {
-                    const uint2 bv = __ldg(reinterpret_cast<const uint2 *>(p.bias + col));
+                    const uint2 bv = *reinterpret_cast<const uint2 *>(p.bias + col);
                     const float2 f0 = __half22float2(*reinterpret_cast<const __half2 *>(&bv.x));
                     const float2 f1 = __half22float2(*reinterpret_cast<const __half2 *>(&bv.y));
                     v[0] += f0.x;

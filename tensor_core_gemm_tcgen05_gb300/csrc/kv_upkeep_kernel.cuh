@@ -56,12 +56,12 @@ __global__ void __launch_bounds__(kTreeThreads) tree_mask_kernel(const TreeMaskP
     grid_dependency_wait();
     grid_dependents_launch();
     const int s = blockIdx.x;
-    const int raw0 = __ldg(p.q_start + s), raw1 = __ldg(p.q_start + s + 1), raw_kv = __ldg(p.kv_lens + s);
+    const int raw0 = load_start(p.q_start + s), raw1 = load_start(p.q_start + s + 1), raw_kv = p.kv_lens[s];
     const int q0 = min(max(raw0, 0), p.num_tokens), n = min(max(raw1, q0), p.num_tokens) - q0, kv = max(raw_kv, 0);
     const int nodes = min(n, 32 * p.mask_words);
     bool bad = q0 != raw0 || q0 + n != raw1 || kv != raw_kv || n > kv || nodes < n || kv > INT32_MAX - 1024 - p.prefix_len;
     for (int i = threadIdx.x; i < nodes; i += kTreeThreads) {
-        const int parent = __ldg(p.parents + q0 + i);
+        const int parent = p.parents[q0 + i];
         bad = bad || parent < -1 || parent >= i;
         up[i] = static_cast<int16_t>(parent < -1 || parent >= i ? -1 : parent);
     }
@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(kWeighThreads, 2) kv_weigh_kernel(const __grid
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
                 const int key = u.key0 + 16 * m;
-                u.page[m] = key < u.v.kv ? __ldg(p.batch.table + (s0 + lo) * p.batch.table_stride + (key >> p.batch.page_shift)) : -1;
+                u.page[m] = key < u.v.kv ? p.batch.table[(s0 + lo) * p.batch.table_stride + (key >> p.batch.page_shift)] : -1;
             }
             return u;
         };
@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kWeighThreads, 2) kv_weigh_kernel(const __grid
                     for (int half = 0; half < 2; ++half) {
 #pragma unroll
                         for (int c = 0; c < C; ++c)
-                            k[m][half][c] = __ldg(reinterpret_cast<const uint4 *>(src + half * 8 * p.row_stride + 32 * c));
+                            k[m][half][c] = *reinterpret_cast<const uint4 *>(src + half * 8 * p.row_stride + 32 * c);
                         if (t == 0 && p.decay != 0.0f && key + 8 * half + g < v.kv - v.n)
                             old[m][half] = weight[m][8 * half];
                     }
@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(kWeighThreads, 2) kv_weigh_kernel(const __grid
                 last = -1;
                 if (r < rows) {
                     const int token = divide(r, p.group, p.group_magic), i = v.n - tokens + token;   // of the sequence's new tokens
-                    const float l = __ldg(p.lse + (v.q0 + i) * p.lse_token + head * p.group + (r - token * p.group));
+                    const float l = p.lse[(v.q0 + i) * p.lse_token + head * p.group + (r - token * p.group)];
                     off = -l * 1.4426950408889634f;
                     last = l == -INFINITY ? -1 : v.kv - v.n + i;
                 }
@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(kWeighThreads, 2) kv_weigh_kernel(const __grid
                 int2 last;
 #pragma unroll
                 for (int c = 0; c < C; ++c)
-                    q[c] = g < rows ? __ldg(query_at(g, 4 * c + t)) : make_uint4(0, 0, 0, 0);
+                    q[c] = g < rows ? *query_at(g, 4 * c + t) : make_uint4(0, 0, 0, 0);
                 row_of(2 * t, off.x, last.x);
                 row_of(2 * t + 1, off.y, last.y);
                 next = find(b + gridDim.x);
@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(kSelectThreads) kv_select_kernel(const __grid_
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int ctas = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_ctarank());
     const int item = static_cast<int>(blockIdx.x) / ctas, s = item / p.kv_heads, head = item % p.kv_heads;
-    const int raw = __ldg(p.kv_lens + s), kv = min(max(raw, 0), p.table_width << p.page_shift);
+    const int raw = p.kv_lens[s], kv = min(max(raw, 0), p.table_width << p.page_shift);
     if (raw != kv && threadIdx.x == 0)
         report_index(p.err);
     int *index = p.index + s * p.seq_stride + head * p.head_stride;
@@ -384,12 +384,12 @@ __global__ void __launch_bounds__(kSelectThreads) kv_select_kernel(const __grid_
     const int a = static_cast<int>(min(static_cast<int64_t>(rank) * slice, static_cast<int64_t>(kv)));
     const int b = static_cast<int>(min(static_cast<int64_t>(a) + slice, static_cast<int64_t>(kv)));
     bool bad = false;
-    auto page_of = [&](int i) { return __ldg(p.table + s * p.table_stride + (i >> p.page_shift)); };
+    auto page_of = [&](int i) { return p.table[s * p.table_stride + (i >> p.page_shift)]; };
     auto weight_key = [&](int id, int i) -> uint32_t {   // of key i, whose page is id: as an integer that orders as the weights do
         // (no branch: several loads are in flight)
         const bool ok = id >= 0 && id < p.num_pages;
         bad = bad || !ok;
-        float x = __ldg(p.w + (ok ? id : 0) * p.w_page + head * p.w_head + (i & ((1 << p.page_shift) - 1))) + 0.0f;   // (-0 becomes 0)
+        float x = p.w[(ok ? id : 0) * p.w_page + head * p.w_head + (i & ((1 << p.page_shift) - 1))] + 0.0f;   // (-0 becomes 0)
         x = ok ? x : 0.0f;
         const uint32_t u = __float_as_uint(x);
         return x != x ? 0u : u ^ (u >> 31 ? 0xffffffffu : 0x80000000u);
@@ -577,9 +577,9 @@ __global__ void __launch_bounds__(kCompactThreads) kv_compact_kernel(const __gri
     const int ctas = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_ctarank());
     const int item = static_cast<int>(blockIdx.x) / ctas, s = item / p.groups, head0 = item % p.groups * p.heads;
     const int rows = PAIRS / p.heads;   // of each head in a CTA's round
-    const int raw_kv = __ldg(p.kv_lens + s), kv = min(max(raw_kv, 0), p.table_width << p.page_shift);
-    const int raw_start = p.start ? __ldg(p.start + s) : 0, start = min(max(raw_start, 0), kv);
-    const int raw_count = __ldg(p.counts + s), count = raw_start == start ? min(max(raw_count, 0), p.most) : 0;
+    const int raw_kv = p.kv_lens[s], kv = min(max(raw_kv, 0), p.table_width << p.page_shift);
+    const int raw_start = p.start ? p.start[s] : 0, start = min(max(raw_start, 0), kv);
+    const int raw_count = p.counts[s], count = raw_start == start ? min(max(raw_count, 0), p.most) : 0;
     if (threadIdx.x == 0 && rank == 0 && head0 == 0) {
         if (raw_kv != kv || raw_start != start || raw_count < 0 || raw_count > p.most)
             report_index(p.err);
@@ -598,14 +598,14 @@ __global__ void __launch_bounds__(kCompactThreads) kv_compact_kernel(const __gri
         int64_t src = -1, dst = 0;
         weight_to = nullptr;
         if (head < p.kv_heads && j < count) {
-            const int i = __ldg(p.index + s * p.seq_index + head * p.head_index + j);
+            const int i = p.index[s * p.seq_index + head * p.head_index + j];
             const int64_t row = static_cast<int64_t>(start) + i;
             if (i < j || row >= kv) {
                 report_index(p.err);
             } else if (i > j) {
                 const int to_row = start + static_cast<int>(j), from_row = static_cast<int>(row);
                 const int *table = p.table + s * p.table_stride;
-                const int a = __ldg(table + (from_row >> p.page_shift)), b = __ldg(table + (to_row >> p.page_shift));
+                const int a = table[from_row >> p.page_shift], b = table[to_row >> p.page_shift];
                 if (a < 0 || a >= p.num_pages || b < 0 || b >= p.num_pages) {
                     report_index(p.err);
                 } else {

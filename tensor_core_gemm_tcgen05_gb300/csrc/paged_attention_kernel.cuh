@@ -206,8 +206,8 @@ __host__ __device__ __noinline__ SeqItems seq_items(const PagedParams &p, int s)
 {
     SeqItems q;
     if (p.keys == KEYS_PREFIX || (p.keys == KEYS_BOTH && s == 0)) {
-        const int a = min(max(load_int(p.batch.q_start), 0), p.batch.num_tokens);
-        const int b = min(max(load_int(p.batch.q_start + p.batch.num_seqs), a), p.batch.num_tokens);
+        const int a = min(max(load_start(p.batch.q_start), 0), p.batch.num_tokens);
+        const int b = min(max(load_start(p.batch.q_start + p.batch.num_seqs), a), p.batch.num_tokens);
         q.q0 = a;
         q.n = b - a;
         q.kv = 0;
@@ -484,8 +484,8 @@ struct TreeRow {
     {
         at = p.mask + token * p.mask_stride;
         words = p.mask_words;
-        first[0] = on ? __ldg(at) : 0u;
-        first[1] = on && words > 1 ? __ldg(at + 1) : 0u;
+        first[0] = on ? *at : 0u;
+        first[1] = on && words > 1 ? at[1] : 0u;
     }
     // Bit e: whether the row sees the key `from` + e, counted from the first new token's (of n of them there are keys);
     // all keys before that one are seen.
@@ -495,7 +495,7 @@ struct TreeRow {
             return 0xffffffffu;
         auto word = [&](int i) -> uint32_t {
             const int left = n - 32 * i;
-            const uint32_t w = i >= words || left <= 0 ? 0u : i == 0 ? first[0] : i == 1 ? first[1] : __ldg(at + i);
+            const uint32_t w = i >= words || left <= 0 ? 0u : i == 0 ? first[0] : i == 1 ? first[1] : at[i];
             return left < 32 && left > 0 ? w & ((1u << left) - 1u) : w;
         };
         if (from < 0)
@@ -516,7 +516,7 @@ __device__ __noinline__ int prefix_seen(const BatchView &b, int token, bool on)
     int s = find_seq<32>(b.q_start, b.num_seqs, __shfl_sync(0xffffffffu, token, 0), threadIdx.x & 31);
     if (!on)
         return 0;
-    while (s + 1 < b.num_seqs && __ldg(b.q_start + s + 1) <= token)
+    while (s + 1 < b.num_seqs && load_start(b.q_start + s + 1) <= token)
         ++s;
     const SeqView v = load_seq(b, s);
     return min(b.prefix_len, max(0, b.prefix_len + v.kv - v.n + (token - v.q0) + 1));
@@ -614,8 +614,8 @@ __device__ __noinline__ void repair_stretches(const PagedParams &p, const Walk &
             if (j >= last)
                 return -1;
             const int key = key_base + j, lp = key >> p.batch.page_shift;
-            const int page = lp < p.n_prefix_pages ? __ldg(p.prefix_pages + lp)
-                                                   : __ldg(p.batch.table + g.s * p.batch.table_stride + (lp - p.n_prefix_pages));
+            const int page = lp < p.n_prefix_pages ? p.prefix_pages[lp]
+                                                   : p.batch.table[g.s * p.batch.table_stride + (lp - p.n_prefix_pages)];
             return page < 0 || page >= p.batch.num_pages
                        ? -1
                        : page * p.page_stride + g.head * p.head_stride + (key & ((1 << p.batch.page_shift) - 1)) * p.row_stride;
@@ -1344,9 +1344,9 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, Cfg::CTAS_PER_SM)
                 const int lp = (key_base + b * BKV + lane * box_rows) >> p.batch.page_shift;
                 int id;
                 if (lp < p.n_prefix_pages)
-                    id = __ldg(p.prefix_pages + lp);
+                    id = p.prefix_pages[lp];
                 else if (!g.prefix && lp - p.n_prefix_pages < own_pages)
-                    id = __ldg(p.batch.table + g.s * p.batch.table_stride + (lp - p.n_prefix_pages));
+                    id = p.batch.table[g.s * p.batch.table_stride + (lp - p.n_prefix_pages)];
                 else
                     return p.batch.num_pages;
                 if (id < 0 || id >= p.batch.num_pages) {
@@ -1823,7 +1823,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) paged_combine_kernel(const
             return;
         const int kv_head = head / p.group, g = head - kv_head * p.group;
         const int4 info[2] = {p.own[token * p.kv_heads + kv_head], p.prefix[token * p.kv_heads + kv_head]};
-        if (token < __ldg(p.q_start) || token >= __ldg(p.q_start + p.num_seqs))
+        if (token < load_start(p.q_start) || token >= load_start(p.q_start + p.num_seqs))
             return;   // of no sequence: nothing was written for it
         int n[2], tile[2], r[2];
 #pragma unroll

@@ -169,7 +169,9 @@ __device__ __forceinline__ void cluster_sync()
 // ---- programmatic dependent launch --------------------------------------------------------
 // Block until the grids this one depends on (the previous kernel in the stream, when it was
 // launched with programmatic stream serialisation) have completed and their memory is
-// visible. A no-op for a normal launch.
+// visible. A no-op for a normal launch. What the grid reads may be written while its own CTAs are
+// already here, so it is read with ordinary loads, not with ones for data that no one writes
+// while the kernel runs (__ldg).
 __device__ __forceinline__ void grid_dependency_wait()
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");

@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kRopeThreads, 8) rope_kernel(const __grid_cons
         if (kind != 0 && live) {
             int page = -1;
             if (place >= 0)   // place < kv <= the keys of table_width pages
-                page = __ldg(p.batch.table + s * p.batch.table_stride + (place >> p.batch.page_shift));
+                page = p.batch.table[s * p.batch.table_stride + (place >> p.batch.page_shift)];
             live = page >= 0 && page < p.batch.num_pages;
             bad = bad || !live;
             dst = static_cast<T *>(g.out) + page * g.out_token + (place & ((1 << p.batch.page_shift) - 1)) * p.row_stride;
@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kRopeThreads, 8) rope_kernel(const __grid_cons
         if (bad)
             atomicCAS(p.err, 0u, static_cast<uint32_t>(ERR_BATCH_INDEX));
     } else {
-        pos = __ldg(p.positions + token);
+        pos = p.positions[token];
     }
     dst += h0 * g.out_head + d0;
     const int64_t out_head = g.out_head;
@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kRopeThreads, 8) rope_kernel(const __grid_cons
             c4[e] = 1.0f;
             s4[e] = 0.0f;
             if (d0 < p.rotary_dim) {
-                const uint64_t turns = static_cast<uint64_t>(pos) * __ldg(p.table + pair0 + e);
+                const uint64_t turns = static_cast<uint64_t>(pos) * p.table[pair0 + e];
                 // the top 32 bits as a signed part of a turn, in half turns (2^-31 each)
                 sincospif(static_cast<float>(static_cast<int32_t>(turns >> 32)) * 4.656612873077393e-10f, &s4[e], &c4[e]);
                 c4[e] *= p.scale;
@@ -167,8 +167,8 @@ __global__ void __launch_bounds__(kRopeThreads, 8) rope_kernel(const __grid_cons
     const void *norm = kind == 0 ? p.q_norm : kind == 1 ? p.k_norm : nullptr;
     if (norm) {
         float w[8], wp[8];
-        unpack8<T>(__ldg(static_cast<const uint4 *>(norm) + sub), w);
-        unpack8<T>(__ldg(static_cast<const uint4 *>(norm) + partner % L), wp);
+        unpack8<T>(static_cast<const uint4 *>(norm)[sub], w);
+        unpack8<T>(static_cast<const uint4 *>(norm)[partner % L], wp);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             cs[e] *= w[e];

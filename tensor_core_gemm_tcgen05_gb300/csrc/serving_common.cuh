@@ -75,7 +75,9 @@ struct SeqView {
     bool bad;
 };
 
-__host__ __device__ __forceinline__ int load_int(const int *at)
+// A value of q_start. No operator writes it, so it may be read as data that no one writes while the kernel runs; kv_lens may come from
+// the kernel before (see grid_dependency_wait). With ordinary loads attention of drafts over heads of 64 took 94.4 us for 79.5.
+__host__ __device__ __forceinline__ int load_start(const int *at)
 {
 #ifdef __CUDA_ARCH__
     return __ldg(at);
@@ -86,7 +88,7 @@ __host__ __device__ __forceinline__ int load_int(const int *at)
 
 __host__ __device__ __forceinline__ SeqView load_seq(const BatchView &b, int s)
 {
-    const int q0 = load_int(b.q_start + s), q1 = load_int(b.q_start + s + 1), kv = load_int(b.kv_lens + s);
+    const int q0 = load_start(b.q_start + s), q1 = load_start(b.q_start + s + 1), kv = b.kv_lens[s];
     const int cap = b.table_width << b.page_shift;
     SeqView v;
     v.q0 = min(max(q0, 0), b.num_tokens);
@@ -107,7 +109,7 @@ __device__ __forceinline__ int find_seq(const int *q_start, int num_seqs, int to
     for (int width = num_seqs; width > 1;) {
         const int step = (width + L - 1) / L;
         const int at = lo + (sub + 1) * step;
-        const bool below = at < num_seqs && __ldg(q_start + at) <= token;
+        const bool below = at < num_seqs && load_start(q_start + at) <= token;
         const uint32_t votes = (__ballot_sync(0xffffffffu, below) >> first) & (0xffffffffu >> (32 - L));
         lo += __popc(votes) * step;
         width = step;

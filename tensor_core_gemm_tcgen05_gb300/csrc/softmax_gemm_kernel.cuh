@@ -493,7 +493,7 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
             const int n_first = j * BN + group * Cfg::WARP_COLS;
             uint4 bv = make_uint4(0u, 0u, 0u, 0u);
             if (p.bias != nullptr && lane < 8 && n_first + 8 * lane < p.N)
-                bv = __ldg(reinterpret_cast<const uint4 *>(p.bias + n_first + 8 * lane));
+                bv = *reinterpret_cast<const uint4 *>(p.bias + n_first + 8 * lane);
             if (!wait_warp(accf0 + 8u * acc, acc_phase, wc, ERR_EPILOGUE_ACCUMULATOR, lane))
                 return false;
             tc_fence_after_sync();

@@ -251,9 +251,9 @@ __global__ void __launch_bounds__(kW4Threads, 1) w4_kernel(const __grid_constant
                     x.s[h][j] = 0;
                     x.z[h][j] = 8;
                     if (t + 4 * j < min(GROUPS, have)) {
-                        x.s[h][j] = __ldg(scales_at[h] + step * GROUPS + 4 * j);
+                        x.s[h][j] = scales_at[h][step * GROUPS + 4 * j];
                         if (p.zeros)
-                            x.z[h][j] = __ldg(zeros_at[h] + step * GROUPS + 4 * j);
+                            x.z[h][j] = zeros_at[h][step * GROUPS + 4 * j];
                     }
                 }
             }
@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(kW4Threads, 1) w4_kernel(const __grid_constant
                 const int64_t k = (static_cast<int64_t>(step0) + at.piece) * 256 + 8 * lane;
                 v[u] = make_uint4(0, 0, 0, 0);
                 if (at.row < rows && k < p.K)
-                    v[u] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(p.a) + (m0 + at.row) * p.lda + k));
+                    v[u] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(p.a) + (m0 + at.row) * p.lda + k);
             }
 #pragma unroll
             for (int u = 0; u < N; ++u) {

@@ -160,7 +160,7 @@ __device__ __forceinline__ void w4_finish(const W4Params &p, const float *part, 
             }
         }
         if (p.bias) {
-            const float2 b = unpack2<T>(__ldg(reinterpret_cast<const uint32_t *>(static_cast<const T *>(p.bias) + n0 + r)));
+            const float2 b = unpack2<T>(*reinterpret_cast<const uint32_t *>(static_cast<const T *>(p.bias) + n0 + r));
             y.x += b.x;
             y.y += b.y;
         }
@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(Cfg::NUM_THREADS, 1)
                     const int r = (k0 + k * Cfg::LOADERS) * ROWS + lane / WIDE;
                     v[k] = static_cast<V>(none);
                     if (on && r < 128)
-                        v[k] = __ldg(src + static_cast<int64_t>(min(r, last)) * groups);
+                        v[k] = src[static_cast<int64_t>(min(r, last)) * groups];
                 }
 #pragma unroll
                 for (int k = 0; k < BATCH; ++k) {
