@@ -353,7 +353,8 @@ struct SelectParams {
 
 __global__ void __launch_bounds__(kSelectThreads) kv_select_kernel(const __grid_constant__ SelectParams p)
 {
-    extern __shared__ uint32_t held[];
+    extern __shared__ uint4 held_vectors[];   // (read four keys at a time: 16-byte aligned)
+    uint32_t *const held = reinterpret_cast<uint32_t *>(held_vectors);
     __shared__ uint4 histograms[3][kSelectThreads];   // of each digit, the highest value first, four to a thread
     __shared__ uint32_t warp_sum[2][kSelectThreads / 32];
     __shared__ uint32_t digit, above;

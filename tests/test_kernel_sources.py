@@ -31,3 +31,10 @@ def test_the_other_kernels_start_when_all_is_written():
     assert "grid_dependency_wait" not in FILES["softmax_kernel.cuh"]
     launches = re.findall(r"row_softmax\w*kernel[^;]*;", FILES["gemm_api.cu"])
     assert launches and not any("launch_serving" in x or "cudaLaunchKernelEx" in x for x in launches)
+
+
+@pytest.mark.parametrize("name", [f for f, text in FILES.items() if "extern __shared__" in text])
+def test_dynamic_shared_memory_is_aligned_for_vectors(name):
+    """It is read in vectors of 16 bytes (or written by TMA): declared as such, or aligned by the kernel itself."""
+    for kind, what in re.findall(r"extern __shared__ (\w+) (\w+)\[\]", FILES[name]):
+        assert kind == "uint4" or re.search(r"smem_u32\(" + what + r"\).*\+ 1023u\) & ~1023u", FILES[name], re.S), (kind, what)
