@@ -546,7 +546,7 @@ int gemm_w4_run(gemm_ctx *ctx, int dtype, int64_t M, int64_t N, int64_t K, const
     p.debug = ctx->debug & GEMM_DEBUG_WITHHOLD_FIRST_LOAD;
     // w4_kernel: A's columns have to fit the shared memory of a cluster.
     const int groups_128 = static_cast<int>(128 / w->group);
-    const int64_t blocks_m = (M + gb300::kW4Rows - 1) / gb300::kW4Rows;
+    const int64_t blocks_m = (M + gb300::kW4Rows - 1) / gb300::kW4Rows;   // (more than one only without columns: act(bias))
     p.tiles = static_cast<int>((N + 15) / 16);
     int cluster = 1;
     auto slice = [&] { return (p.steps + cluster - 1) / cluster; };
@@ -554,7 +554,7 @@ int gemm_w4_run(gemm_ctx *ctx, int dtype, int64_t M, int64_t N, int64_t K, const
     while (cluster < 8 && !fits())
         cluster *= 2;
     // Fewer tiles than CTAs: the columns shared by more of them, as long as every warp has a step.
-    while (cluster < 8 && int64_t(p.tiles) * blocks_m * cluster * 2 <= ctx->num_sms && p.steps >= 2 * cluster * gb300::kW4Warps)
+    while (cluster < 8 && int64_t(p.tiles) * cluster * 2 <= ctx->num_sms && p.steps >= 2 * cluster * gb300::kW4Warps)
         cluster *= 2;
     p.slice = slice();
     p.clusters = std::min(p.tiles, std::max(1, ctx->w4_clusters[cluster]));

@@ -129,12 +129,6 @@ __device__ __forceinline__ void w4_unpack_minus_zero(uint32_t w, uint32_t zero, 
     }
 }
 
-template <typename T>
-__device__ __forceinline__ float w4_scale(uint32_t sz)
-{
-    return unpack2<T>(sz & 0xffffu).x;
-}
-
 // A warp's way through the rounds of its cluster's tiles: 2^log_rows tiles from `tile` on; of a tile its steps w, w + warps, ...,
 // in `turns` turns, a multiple of kW4Ahead (so that a turn's slot of the ring is known when compiling; the last may be empty).
 struct W4Walk {
@@ -194,7 +188,7 @@ __global__ void __launch_bounds__(kW4Threads, 1) w4_kernel(const __grid_constant
     grid_dependents_launch();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const int ctas = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_ctarank());
-    const int cluster = static_cast<int>(blockIdx.x) / ctas, m0 = static_cast<int>(blockIdx.y) * kW4Rows;
+    const int cluster = static_cast<int>(blockIdx.x) / ctas, m0 = static_cast<int>(blockIdx.y) * kW4Rows;   // (0 unless K is)
     const int step0 = static_cast<int>(static_cast<int64_t>(p.steps) * rank / ctas);
     const int count = static_cast<int>(static_cast<int64_t>(p.steps) * (rank + 1) / ctas) - step0;
     const int groups = p.K / GROUP, my_groups = groups - step0 * GROUPS;   // of a row, in all and from this slice on

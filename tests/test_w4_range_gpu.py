@@ -199,3 +199,15 @@ def test_w4_prompts(ctx, dtype, m, n, k, group):
     got = g.w4_gemm(ctx, a.cuda(), codes.cuda(), scales.cuda(), zeros.cuda(), bias.cuda(), g.EPI_GELU)
     clean(ctx)
     ref.check_w4(got.cpu(), y, slack, (dtype, m, n, k, group))
+
+
+@pytest.mark.parametrize("m", [9, 70])
+@pytest.mark.parametrize("act", ["none", "gelu", "relu"])
+def test_w4_many_rows_without_columns(ctx, m, act):
+    """Without columns every row is act(bias)."""
+    bias = torch.linspace(-3, 3, 24).to(F16)
+    a, codes, scales = torch.empty(m, 0, dtype=F16), torch.empty(24, 0, dtype=torch.uint8), torch.empty(24, 0, dtype=F16)
+    got = g.w4_gemm(ctx, a.cuda(), codes.cuda(), scales.cuda(), None, bias.cuda(), {"none": g.EPI_NONE, "gelu": g.EPI_GELU, "relu": g.EPI_RELU}[act])
+    clean(ctx)
+    y, slack = ref.w4(a, codes, scales, None, bias, act)
+    ref.check_w4(got.cpu(), y.expand(m, 24), slack, (m, act))
