@@ -24,10 +24,10 @@ constexpr int kSelectHeldMax = 48 * 1024;   // keys: 192 KB of shared memory
 // Which of the two 4-bit products takes up to eight rows of A: the one that these estimates (ns) give less. w4_kernel's time goes by the
 // tiles of 16 rows of W and 256 columns that an SM sees and by the values of A that it lays out; w4_umma_kernel's by the
 // steps of 128 x 128 an SM sees, in waves, whatever the rows. Over eight shapes from 6144 x 4096 to 65536 x 1024, groups, types and 1 to 8
-// rows the choice takes 0.3 % longer than the faster of both in the mean. Both sides, us (w4_kernel, the other):
-//  * 1024 x 1024, eight rows, groups of 128: 3.9, 5.0; 4096 x 4096: 7.7, 8.2 (one row 6.1, 8.1); 32768 x 4096: 22.2, 33.4
-//  * 16384 x 4096: one row 14.3, 16.9, eight 15.8, 17.0; groups of 64 in BF16 18.7, 19.1 and 20.2, 19.1; of 32 24.5, 23.3 and 26.3, 23.4
-//  * 4096 x 16384: one row 15.1, 17.9, eight 17.9, 18.1; groups of 64 in BF16 22.5, 20.1 and 25.4, 20.2
+// rows the choice took 0.3 % longer than the faster of both in the mean. Both sides, us (w4_kernel, the other):
+//  * 1024 x 1024, eight rows, groups of 128: 3.8, 5.0; 4096 x 4096: 7.0, 8.3 (one row 6.1, 8.1); 32768 x 4096: 21.7, 33.3
+//  * 16384 x 4096: one row 14.3, 16.9, eight 15.4, 17.0; groups of 64 in BF16 19.0, 19.1 and 20.1, 19.2; of 32 25.2, 23.4 and 26.5, 23.4
+//  * 4096 x 16384: one row 14.8, 17.9, eight 17.8, 18.1; groups of 64 in BF16 22.6, 20.2 and 25.5, 20.3
 // Of sixteen rows (of an earlier w4_kernel that took them) 16384 x 4096 took 23.2, 17.0 and 1024 x 1024 5.1, 5.1.
 int64_t w4_kernel_ns(int dtype, int64_t group, int64_t tile_steps, int64_t a_steps)
 {
@@ -394,9 +394,13 @@ int gemm_kv_select(gemm_ctx *ctx, const gemm_kv_seqs *seqs, int64_t num_pages, i
     p.head_stride = head_stride;
     p.counts = counts;
     p.err = ctx->d_err;
-    // More CTAs for a long list, as long as they fit the GPU at once and have some thousand keys each (choice and compaction, us:
-    // 12 sequences of up to 16 000 keys, 8 heads, 59.0, with half as many CTAs 62.8; 16 of up to 40 000 109, 114, with twice as
-    // many 165; one sequence, 1090 keys, 12.4, with a CTA's keys down to 512 16.0).
+    // More CTAs for a long list, up to four an SM in all (fewer run at once where their keys take much shared memory) and with some thousand
+    // keys each. Us with two, four and eight an SM at most, 8 heads, evictions one after the other: 12 sequences of up to 16 000 keys,
+    // choice and compaction 66.6, 60.6, 60.7, the choice alone 21.5, 23.0, 23.2; 16 of up to 40 000 116, 105, 164 and 39.9, 41.3, 102; 32
+    // of up to 6000 142, 146, 146 and 23.5, 27.4, 27.5. So two would be better for choices alone and short lists, four for evictions
+    // of long ones. Why the pair takes longer than its parts with two is not known: with 16 sequences the compaction's CTAs, there early, are the
+    // reason (116 -> 104 when they come after the choice), with 12 they are not (66.6 -> 67.3), and a single eviction of those takes 60.5 either
+    // way. One sequence of 1090 keys, with a CTA's keys down to 512: 16.0 for 12.4.
     const int64_t room = seqs->table_width * page_size;
     int cluster = 1;
     while (cluster < 8 && items * cluster * 2 <= 4 * static_cast<int64_t>(ctx->num_sms) && room >= 4096 * cluster)
@@ -475,8 +479,8 @@ int gemm_kv_compact(gemm_ctx *ctx, const gemm_kv_cache *cache, const gemm_kv_seq
     p.counts = counts;
     p.new_lens = new_lens;
     p.err = ctx->d_err;
-    // A CTA takes several heads where their rows fit its round (accepted drafts: 4.2 us for 200 sequences x 16 heads x 12 rows, a CTA to
-    // each head 15.4); several CTAs take the rows of one head where there are more of them than fit (12 sequences x 8 heads x 2048 rows
+    // A CTA takes several heads where their rows fit its round (accepted drafts, rows in L2: 4.2 us for 200 sequences x 16 heads x 12 rows, a
+    // CTA to each head 15.4); several CTAs take the rows of one head where there are more of them than fit (12 sequences x 8 heads x 2048 rows
     // 39.4 us, half as many CTAs 55.0, one to a head 66.4, twice as many 40.9).
     const int pairs = cache->head_dim == 64 ? gb300::CompactShape<64>::PAIRS : gb300::CompactShape<128>::PAIRS;
     p.heads = 1;

@@ -8,9 +8,8 @@
 
 namespace gb300 {
 
-// Words of the shared memory of a CTA of this cluster. `addr` is what mapa_shared returned, with nothing added
-// to it: such loads take 64-bit addresses, and where the compiler splits a 32-bit sum into a register that
-// has wrapped below zero and a positive offset, the sum ends up outside shared memory (a fault).
+// Words of the shared memory of a CTA of this cluster. `addr` is what mapa_shared returned, with nothing added to it. (With an
+// index below zero added to a mapped address these loads faulted; since they take mapa's own results they have not.)
 __device__ __forceinline__ uint2 ld_shared_cluster_u2(uint32_t addr)
 {
     uint2 v;
@@ -334,7 +333,7 @@ __global__ void __launch_bounds__(kWeighThreads, 2) kv_weigh_kernel(const __grid
 // border and the first of those on it. A cluster of CTAs per sequence and key head, each with a
 // slice of the keys, which it holds in shared memory; the histograms are summed over distributed
 // shared memory. Reads each weight once. Bound by the chain of its passes, each with a barrier of the cluster: 1090 keys of 8
-// heads 7.6 us, 12 sequences of 3000 to 16 000 about 18.
+// heads 7.9 us, 12 sequences of 3000 to 16 000 22.9 (captured, weights from HBM).
 constexpr int kSelectThreads = 512, kSelectBins = 2048, kSelectBatch = 8;
 
 struct SelectParams {
@@ -541,7 +540,7 @@ __global__ void __launch_bounds__(kSelectThreads) kv_select_kernel(const __grid_
 // earlier ones are read already. A cluster of CTAs takes a round together (loads into registers, a
 // cluster barrier, stores); each CTA moves keys and values of a few heads. Bound by HBM for long lists (12 sequences x 8 heads x
 // 2048 rows, 101 MB read and as much written: 39.4 us, 53 % of HBM's time busy; reads a round ahead, which took
-// 117 registers, 55), by the chain of lookups for a few accepted drafts (3.1).
+// 117 registers, 55), by the chain of lookups for a few accepted drafts (3.9; 2.7 on rows that are in L2).
 constexpr int kCompactThreads = 256, kCompactVecs = 8;   // 16-byte pieces a thread holds
 
 struct CompactParams {

@@ -15,14 +15,14 @@
 // sums of a round waits for another warp. These meet in shared and distributed shared memory in a fixed order.
 //
 // What bounds it: the chain of a step in its sixteen warps (issue 1.6 a cycle and SM, of which unpacking is a third; HBM at 24 %)
-// behind a start of about 3 us. Measured (captured, weights from HBM): 4096 x 4096 6.1 us for one row, 7.7 for eight, 16384 x 4096
-// 14.3 and 15.8 (33.5 MB: 5.2 at the copy rate), 32768 x 4096 20.8 and 22.2, 1024 x 1024 3.7. What it took there before:
+// behind a start of about 3 us. Measured (captured, weights from HBM): 4096 x 4096 6.1 us for one row, 7.0 for eight, 16384 x 4096
+// 14.3 and 15.4 (33.5 MB: 5.2 at the copy rate), 32768 x 4096 20.7 and 21.7, 1024 x 1024 3.7 and 3.8. What it took there before:
 // steps of 128 columns with a ring of four 25 (eight rows, 16384 x 4096); codes - zero unpacked for each row 24; 256 threads that
 // brought A anew for each 128 rows 23; two more barriers to a round 17.2.
 //
-// Laying A out is 1 of the 14.3 and 2.7 of the 15.8. Four pieces in flight whatever their number: 14.6 and 16.5; eight 15.0 and 15.6; sums
-// always as products with ones, which need a barrier and a look at all groups: 14.6 and 15.1 (4096 x 4096, one row 6.5 for 6.1);
-// asynchronous copies to the pieces' places, then a turn in place: 15.4 and 18.6.
+// Laying A out is 1 of the 14.3 and about 2.5 of the 15.4. While the eight rows took 15.8: four pieces in flight whatever their number 14.6 and
+// 16.5; eight 15.0 and 15.6; sums always as products with ones, which need a barrier and a look at all groups, 14.6 and 15.1 (4096 x
+// 4096, one row 6.5 for 6.1); asynchronous copies to the pieces' places, then a turn in place, 15.4 and 18.6.
 #pragma once
 
 #include <type_traits>
